@@ -85,7 +85,9 @@ std::atomic<uint32_t> g_epoch{0};
 const char *const kKernelNames[kKernelCount] = {"seg_table", "prefill_fused", "recurrent_step",
                                                 "recurrent_step_indexed", "output_norm_gate",
                                                 "qk_prologue", "gdn_step", "gdn_fwd",
-                                                "gdn_newv", "prefill_pair"};
+                                                "gdn_newv", "prefill_pair",
+                                                "verify_drafts", "draft_step", "pool_plan",
+                                                "pool_copy"};
 struct TimingRecord {
     int id;
     cudaEvent_t start, stop;
@@ -187,6 +189,25 @@ void prefill_fault_knobs(uint64_t *wait_ns, int64_t *withhold) {
 
 using namespace sala;
 
+namespace {
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+struct Range {
+    const void *p;
+    size_t bytes;
+};
+// An output overlaps one of the other arguments.
+template <int N>
+bool overlaps_any(const Range &out, const Range (&others)[N]) {
+    for (const Range &r : others)
+        if (overlaps(out.p, out.bytes, r.p, r.bytes)) return true;
+    return false;
+}
+
+constexpr int64_t kMaxRows = int64_t(1) << 31;   // CTAs of a launch, exclusive
+constexpr int64_t kMaxUnits = int64_t(1) << 40;  // (layer, slot, head) states of a pool
+}  // namespace
+
 extern "C" {
 
 int sala_gla_set_prefill_kernel(int kernel) {
@@ -247,7 +268,7 @@ const char *sala_gla_status_string(int status) {
     case SALA_ERR_BAD_SEQLENS: return "cu_seqlens is not monotone from 0 to T";
     case SALA_ERR_TOO_LARGE:
         return "problem needs more scratch than the no-allocation entry point's fixed buffer";
-    case SALA_ERR_BAD_INDEX: return "a state index is at or past the pool size";
+    case SALA_ERR_BAD_INDEX: return "an index or count lies outside its range (a state slot past the pool)";
     case SALA_ERR_DEBUG_CHECK: return "debug build: a device-side index check failed (access skipped)";
     default: return "unknown status";
     }
@@ -576,6 +597,181 @@ int sala_gla_chunk_fwd(const void *q, const void *k, const void *v, const float 
         rc = SALA_ERR_CUDA;
     if (cudaFreeAsync(ws, st) != cudaSuccess) rc = SALA_ERR_CUDA;
     return rc;
+}
+
+int sala_gla_verify_drafts(const void *target_probs, int64_t target_stride, const void *draft_probs,
+                           int64_t draft_stride, int32_t prob_dtype, const int32_t *draft_tokens,
+                           const int32_t *num_drafts, const float *accept_u, const float *sample_u,
+                           int32_t *tokens, int32_t *accepted, int64_t N, int32_t K, int64_t V,
+                           void *stream) {
+    if (N < 0 || K < 0 || V < 1 || V > SALA_VERIFY_MAX_VOCAB) return SALA_ERR_INVALID_ARG;
+    if (prob_dtype != SALA_PROB_F32 && prob_dtype != SALA_PROB_BF16) return SALA_ERR_INVALID_ARG;
+    if (N == 0) return SALA_OK;
+    if (N >= kMaxRows || K > (1 << 20) || target_stride < V || target_stride > (int64_t(1) << 32))
+        return SALA_ERR_INVALID_ARG;
+    if (!target_probs || !sample_u || !tokens || !accepted) return SALA_ERR_INVALID_ARG;
+    if (K > 0 && (!draft_tokens || !accept_u)) return SALA_ERR_INVALID_ARG;
+    const bool drafter = K > 0 && draft_probs;
+    if (drafter && (draft_stride < V || draft_stride > (int64_t(1) << 32))) return SALA_ERR_INVALID_ARG;
+    const bool bf16 = prob_dtype == SALA_PROB_BF16;
+    const uintptr_t odd = bf16 ? 1u : 3u;
+    if ((reinterpret_cast<uintptr_t>(target_probs) & odd) ||
+        (drafter && (reinterpret_cast<uintptr_t>(draft_probs) & odd)) || !aligned4(draft_tokens) ||
+        !aligned4(num_drafts) || !aligned4(accept_u) || !aligned4(sample_u) || !aligned4(tokens) ||
+        !aligned4(accepted))
+        return SALA_ERR_MISALIGNED;
+    const size_t es = bf16 ? 2 : 4, n = static_cast<size_t>(N), k = static_cast<size_t>(K);
+    const Range out{tokens, 4 * n * (k + 1)}, count{accepted, 4 * n};
+    const Range ins[6] = {{target_probs, es * ((n * (k + 1) - 1) * target_stride + V)},
+                          {drafter ? draft_probs : nullptr, drafter ? es * ((n * k - 1) * draft_stride + V) : 0},
+                          {draft_tokens, 4 * n * k}, {num_drafts, 4 * n}, {accept_u, 4 * n * k},
+                          {sample_u, 4 * n}};
+    if (overlaps_any(out, ins) || overlaps_any(count, ins) ||
+        overlaps(out.p, out.bytes, count.p, count.bytes))
+        return SALA_ERR_INVALID_ARG;
+    int err = SALA_OK;
+    DeviceState *d = device_state(&err);
+    if (!d) return err;
+    if (launch_verify_drafts(target_probs, target_stride, drafter ? draft_probs : nullptr, draft_stride, bf16,
+                             draft_tokens, K > 0 ? num_drafts : nullptr, accept_u, sample_u, tokens,
+                             accepted, N, K, V, d->status, static_cast<cudaStream_t>(stream)) !=
+        cudaSuccess)
+        return SALA_ERR_CUDA;
+    return SALA_OK;
+}
+
+int sala_gla_recurrent_draft_step(const void *q, const void *k, const void *v, const float *g,
+                                  const int32_t *num_tokens, const void *pend_k, const void *pend_v,
+                                  const float *pend_g, const int32_t *accepted, float scale,
+                                  void *state_pool, int32_t state_dtype, const int32_t *state_indices,
+                                  int64_t P, void *o, int64_t N, int64_t T, int64_t T_pend, int32_t H,
+                                  void *stream) {
+    if (N < 0 || T < 0 || T_pend < 0 || H < 1 || P < 1) return SALA_ERR_INVALID_ARG;
+    if (state_dtype != SALA_STATE_F32 && state_dtype != SALA_STATE_BF16) return SALA_ERR_INVALID_ARG;
+    if (N == 0 || (T == 0 && T_pend == 0)) return SALA_OK;
+    if (N > (kMaxRows - 1) / H || P > kMaxUnits / H || P > kMaxRows || T > kMaxRows / N ||
+        T_pend > kMaxRows / N)
+        return SALA_ERR_INVALID_ARG;
+    if (!state_pool || !state_indices) return SALA_ERR_INVALID_ARG;
+    if (T > 0 && (!q || !k || !v || !g || !o)) return SALA_ERR_INVALID_ARG;
+    if (T_pend > 0 && (!pend_k || !pend_v || !pend_g || !accepted)) return SALA_ERR_INVALID_ARG;
+    if (!aligned16(state_pool) || !aligned4(state_indices)) return SALA_ERR_MISALIGNED;
+    if (T > 0 && (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned4(g) || !aligned16(o) ||
+                  !aligned4(num_tokens)))
+        return SALA_ERR_MISALIGNED;
+    if (T_pend > 0 && (!aligned16(pend_k) || !aligned16(pend_v) || !aligned4(pend_g) || !aligned4(accepted)))
+        return SALA_ERR_MISALIGNED;
+    const size_t n = static_cast<size_t>(N), units = n * H;
+    const size_t vec = units * T * kD * 2, pvec = units * T_pend * kD * 2;
+    const Range pool{state_pool, static_cast<size_t>(P) * H * kD * kD * (state_dtype == SALA_STATE_BF16 ? 2 : 4)};
+    const Range out{T > 0 ? o : nullptr, vec};
+    const Range ins[10] = {{q, vec}, {k, vec}, {v, vec}, {g, units * T * 4}, {num_tokens, T > 0 ? 4 * n : 0},
+                           {pend_k, pvec}, {pend_v, pvec}, {pend_g, units * T_pend * 4},
+                           {accepted, T_pend > 0 ? 4 * n : 0}, {state_indices, 4 * n}};
+    if (overlaps_any(pool, ins) || overlaps_any(out, ins) || overlaps(pool.p, pool.bytes, out.p, out.bytes))
+        return SALA_ERR_INVALID_ARG;
+    int err = SALA_OK;
+    DeviceState *d = device_state(&err);
+    if (!d) return err;
+    if (launch_draft_step(q, k, v, g, T > 0 ? num_tokens : nullptr, pend_k, pend_v, pend_g, accepted, scale,
+                          state_pool, state_dtype == SALA_STATE_BF16, state_indices, P, o, N, T, T_pend,
+                          H, d->status, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SALA_ERR_CUDA;
+    return SALA_OK;
+}
+
+namespace {
+// Sizes, type and pointer of a pool [L, P, H, 128, 128]; *bytes its size.
+int check_pool(const void *pool, int32_t dtype, int64_t L, int64_t P, int32_t H, size_t *bytes) {
+    if (L < 1 || P < 1 || H < 1) return SALA_ERR_INVALID_ARG;
+    if (dtype != SALA_STATE_F32 && dtype != SALA_STATE_BF16) return SALA_ERR_INVALID_ARG;
+    if (L > (int64_t(1) << 30) / H || P >= kMaxRows || P > kMaxUnits / (L * H)) return SALA_ERR_INVALID_ARG;
+    if (!pool) return SALA_ERR_INVALID_ARG;
+    if (!aligned16(pool)) return SALA_ERR_MISALIGNED;
+    *bytes = static_cast<size_t>(L) * P * H * kD * kD * (dtype == SALA_STATE_BF16 ? 2 : 4);
+    return SALA_OK;
+}
+}  // namespace
+
+int sala_gla_state_pool_copy(const void *src_pool, int32_t src_dtype, int64_t src_P, void *dst_pool,
+                             int32_t dst_dtype, int64_t dst_P, const int32_t *src, const int32_t *dst,
+                             int64_t n, int64_t L, int32_t H, void *stream) {
+    size_t sb = 0, db = 0;
+    if (const int e = check_pool(src_pool, src_dtype, L, src_P, H, &sb)) return e;
+    if (const int e = check_pool(dst_pool, dst_dtype, L, dst_P, H, &db)) return e;
+    if (n < 0 || n >= kMaxRows) return SALA_ERR_INVALID_ARG;
+    if (src_pool == dst_pool ? (src_dtype != dst_dtype || src_P != dst_P)
+                             : overlaps(src_pool, sb, dst_pool, db))
+        return SALA_ERR_INVALID_ARG;
+    if (n == 0) return SALA_OK;
+    if (!src || !dst) return SALA_ERR_INVALID_ARG;
+    if (!aligned4(src) || !aligned4(dst)) return SALA_ERR_MISALIGNED;
+    const size_t nb = static_cast<size_t>(n) * 4;
+    const Range ins[2] = {{src, nb}, {dst, nb}};
+    if (overlaps_any(Range{dst_pool, db}, ins)) return SALA_ERR_INVALID_ARG;
+    int err = SALA_OK;
+    DeviceState *d = device_state(&err);
+    if (!d) return err;
+    if (launch_state_pool_copy(src_pool, src_dtype == SALA_STATE_BF16, src_P, dst_pool,
+                               dst_dtype == SALA_STATE_BF16, dst_P, src, dst, n, L, H, d->status,
+                               static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SALA_ERR_CUDA;
+    return SALA_OK;
+}
+
+int sala_gla_state_pool_fork(void *pool, int32_t dtype, int64_t L, int64_t P, int32_t H, int32_t *used,
+                             const int32_t *parents, int32_t *children, int64_t n, void *stream) {
+    size_t pb = 0;
+    if (const int e = check_pool(pool, dtype, L, P, H, &pb)) return e;
+    if (n < 0 || n >= kMaxRows) return SALA_ERR_INVALID_ARG;
+    if (n == 0) return SALA_OK;
+    if (!used || !parents || !children) return SALA_ERR_INVALID_ARG;
+    if (!aligned4(used) || !aligned4(parents) || !aligned4(children)) return SALA_ERR_MISALIGNED;
+    const size_t nb = static_cast<size_t>(n) * 4, ub = static_cast<size_t>(P) * 4;
+    const Range others[3] = {{used, ub}, {parents, nb}, {children, nb}};
+    if (overlaps_any(Range{pool, pb}, others) || overlaps(used, ub, parents, nb) ||
+        overlaps(used, ub, children, nb) || overlaps(parents, nb, children, nb))
+        return SALA_ERR_INVALID_ARG;
+    int err = SALA_OK;
+    DeviceState *d = device_state(&err);
+    if (!d) return err;
+    if (launch_state_pool_fork(pool, dtype == SALA_STATE_BF16, L, P, H, used, parents, children, n, d->status,
+                               static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SALA_ERR_CUDA;
+    return SALA_OK;
+}
+
+int sala_gla_state_pool_free(int32_t *used, int64_t P, const int32_t *slots, int64_t n, void *stream) {
+    if (P < 1 || P >= kMaxRows || n < 0 || n >= kMaxRows) return SALA_ERR_INVALID_ARG;
+    if (n == 0) return SALA_OK;
+    if (!used || !slots) return SALA_ERR_INVALID_ARG;
+    if (!aligned4(used) || !aligned4(slots)) return SALA_ERR_MISALIGNED;
+    if (overlaps(used, static_cast<size_t>(P) * 4, slots, static_cast<size_t>(n) * 4)) return SALA_ERR_INVALID_ARG;
+    int err = SALA_OK;
+    DeviceState *d = device_state(&err);
+    if (!d) return err;
+    if (launch_state_pool_free(used, P, slots, n, d->status, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SALA_ERR_CUDA;
+    return SALA_OK;
+}
+
+int sala_gla_state_pool_compact(void *pool, int32_t dtype, int64_t L, int64_t P, int32_t H, int32_t *used,
+                                int32_t *mapping, int32_t *live, int32_t *work, void *stream) {
+    size_t pb = 0;
+    if (const int e = check_pool(pool, dtype, L, P, H, &pb)) return e;
+    if (!used || !mapping || !live || !work) return SALA_ERR_INVALID_ARG;
+    if (!aligned4(used) || !aligned4(mapping) || !aligned4(live) || !aligned4(work)) return SALA_ERR_MISALIGNED;
+    const size_t ub = static_cast<size_t>(P) * 4;
+    const Range all[5] = {{pool, pb}, {used, ub}, {mapping, ub}, {live, 4}, {work, ub + 16}};
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlaps(all[i].p, all[i].bytes, all[j].p, all[j].bytes)) return SALA_ERR_INVALID_ARG;
+    int err = SALA_OK;
+    if (!device_state(&err)) return err;
+    if (launch_state_pool_compact(pool, dtype == SALA_STATE_BF16, L, P, H, used, mapping, live, work,
+                                  static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SALA_ERR_CUDA;
+    return SALA_OK;
 }
 
 }  // extern "C"

@@ -55,10 +55,10 @@ __device__ __forceinline__ void dependent_start() {
 // Launch as a programmatic dependent of the work before it on the stream: only the launch
 // latency overlaps the previous grid's last wave (the kernel begins with dependent_start).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kern)(KArgs...), unsigned grid, unsigned block, cudaStream_t st,
+cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, unsigned block, cudaStream_t st,
                              Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = 0;
     cfg.stream = st;

@@ -19,6 +19,10 @@ enum KernelId {
     kKGdnFwd,
     kKGdnNewv,
     kKPrefillPair,
+    kKVerifyDrafts,
+    kKDraftStep,
+    kKPoolPlan,
+    kKPoolCopy,
     kKernelCount
 };
 
@@ -120,6 +124,37 @@ cudaError_t setup_gdn_chunk_kernel();
 cudaError_t launch_gdn_newv(const void *k, const void *v, const float *g, const float *beta,
                             const float *h0, const SegTable &t, int64_t T_total, void *nv, int H,
                             int *status, cudaStream_t st);
+
+// Drafted tokens against the target's probabilities (fp32, or bf16 if `bf16`): rows of V
+// probabilities, `p_stride` / `q_stride` elements apart; q and num_drafts may be null.
+cudaError_t launch_verify_drafts(const void *p, int64_t p_stride, const void *q, int64_t q_stride,
+                                 bool bf16, const int32_t *x, const int32_t *num_drafts,
+                                 const float *u, const float *s, int32_t *tokens,
+                                 int32_t *accepted, int64_t N, int K, int64_t V, int *status,
+                                 cudaStream_t stream);
+
+// Decode step over T drafted tokens on pooled states, after committing accepted[n] + 1 of the
+// T_pend tokens of the step before (T or T_pend may be 0).
+cudaError_t launch_draft_step(const void *q, const void *k, const void *v, const float *g,
+                              const int32_t *num_tokens, const void *pend_k, const void *pend_v,
+                              const float *pend_g, const int32_t *accepted, float scale, void *pool,
+                              bool bf16, const int32_t *slots, int64_t P, void *o, int64_t N,
+                              int64_t T, int64_t T_pend, int H, int *status, cudaStream_t stream);
+
+// States of a pool [L, P, H, 128, 128]: n pairs of slots copied (source < 0: zeros, destination
+// < 0: skipped), n requests forked into the lowest free slots, n slots freed, the used slots
+// moved to the front (`work`: P + 4 words).
+cudaError_t launch_state_pool_copy(const void *src_pool, bool src_bf16, int64_t src_P, void *dst_pool,
+                                   bool dst_bf16, int64_t dst_P, const int32_t *src,
+                                   const int32_t *dst, int64_t n, int64_t L, int H, int *status,
+                                   cudaStream_t st);
+cudaError_t launch_state_pool_fork(void *pool, bool bf16, int64_t L, int64_t P, int H, int32_t *used,
+                                   const int32_t *parents, int32_t *children, int64_t n, int *status,
+                                   cudaStream_t st);
+cudaError_t launch_state_pool_free(int32_t *used, int64_t P, const int32_t *slots, int64_t n, int *status,
+                                   cudaStream_t st);
+cudaError_t launch_state_pool_compact(void *pool, bool bf16, int64_t L, int64_t P, int H, int32_t *used,
+                                      int32_t *mapping, int32_t *live, int32_t *work, cudaStream_t st);
 
 // Nonzero tag of one prefill call for the hand-off flags (differs from the previous call's).
 uint32_t next_prefill_epoch();

@@ -1,0 +1,267 @@
+// The states of a pool as a serving engine manages them: copies between slots and between
+// pools, forks into free slots, freeing, and compaction. A slot holds a request's states of all
+// layers: pool [L, P, H, 128, 128], slot s of layer l at ((l * P) + s) * H * 128 * 128.
+//
+// Which slots move is decided on the device (a mask of the used slots, one int32 each), so a
+// server needs no host round trip and a captured graph serves every occupancy. The decisions
+// are one CTA's prefix counts over the mask; the moving is a plain stream of 16-byte accesses,
+// bounded by the memory bandwidth.
+#include <type_traits>
+
+#include "launch.h"
+
+namespace sala {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kCopyThreads = 256;
+constexpr int kUnit = kD * kD;   // elements of one head's state
+
+// Exclusive prefix count of `flag` over the CTA (kPlanThreads threads); *total the count.
+__device__ int block_rank(bool flag, int *total) {
+    __shared__ int warp_count[kPlanWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned m = __ballot_sync(0xffffffffu, flag);
+    if (lane == 0) warp_count[warp] = __popc(m);
+    __syncthreads();
+    int c = warp_count[lane], before = 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, c, off);
+        if (lane >= off) c += y;
+    }
+    *total = __shfl_sync(0xffffffffu, c, 31);
+    if (warp) before = __shfl_sync(0xffffffffu, c, warp - 1);
+    __syncthreads();
+    return before + __popc(m & ((1u << lane) - 1));
+}
+
+// children[i] of every request i: the lowest free slots, in order, to the requests whose parent
+// is a used slot or -1 (a new state); -1 to the others and once the pool is full.
+__global__ void __launch_bounds__(kPlanThreads)
+pool_fork_plan_kernel(int32_t *used, int64_t P, const int32_t *parents, int32_t *children, int64_t n,
+                      int *status) {
+    dependent_start();
+    const int tid = threadIdx.x;
+    // 1. children[r] = the r-th free slot, for r < n
+    int64_t found = 0;
+    for (int64_t s0 = 0; s0 < P && found < n; s0 += kPlanThreads) {
+        const int64_t s = s0 + tid;
+        const bool is_free = s < P && used[s] == 0;
+        int total;
+        const int64_t r = found + block_rank(is_free, &total);
+        if (is_free && r < n) children[r] = static_cast<int32_t>(s);
+        found += total;
+    }
+    if (found > n) found = n;
+    // 2. how many requests want a slot
+    int64_t wanted = 0;
+    auto wants = [&](int64_t i) {
+        if (i >= n) return false;
+        const int32_t p = parents[i];
+        if (p < 0) return p == -1;
+        if (p < P && used[p] != 0) return true;
+        record_status(status, SALA_ERR_BAD_INDEX);   // past the pool, or of a slot that is free
+        return false;
+    };
+    for (int64_t i0 = 0; i0 < n; i0 += kPlanThreads) {
+        int total;
+        block_rank(wants(i0 + tid), &total);
+        wanted += total;
+    }
+    // 3. request i takes the slot of its rank among those: ranks do not exceed i, so from the
+    // last tile down every entry is read before it is overwritten. Slots are marked at the end:
+    // one of them may be the (refused) parent of a request still to be looked at.
+    int64_t left = wanted;
+    for (int64_t i0 = ((n - 1) / kPlanThreads) * kPlanThreads; i0 >= 0; i0 -= kPlanThreads) {
+        const int64_t i = i0 + tid;
+        const bool w = wants(i);
+        int total;
+        const int rank = block_rank(w, &total);
+        left -= total;
+        const int64_t r = left + rank;
+        const int32_t child = w && r < found ? children[r] : -1;
+        __syncthreads();
+        if (i < n) children[i] = child;
+        __syncthreads();
+    }
+    for (int64_t i = tid; i < n; i += kPlanThreads)
+        if (children[i] >= 0) used[children[i]] = 1;
+}
+
+// used[s] = 0 for every named slot; a slot that is not in use (or named twice) is reported.
+__global__ void pool_free_kernel(int32_t *used, int64_t P, const int32_t *slots, int64_t n, int *status) {
+    dependent_start();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= n) return;
+    const int32_t s = slots[i];
+    if (s < 0) return;
+    if (s >= P || atomicExch(used + s, 0) == 0) record_status(status, SALA_ERR_BAD_INDEX);
+}
+
+// With m used slots: the r-th used slot at or past m moves to the r-th free slot below m.
+// work: [0] the number of moves, [4 ..] their sources, [4 + P / 2 ..] their destinations.
+__global__ void __launch_bounds__(kPlanThreads)
+pool_compact_plan_kernel(int32_t *used, int64_t P, int32_t *mapping, int32_t *live, int32_t *work) {
+    dependent_start();
+    const int tid = threadIdx.x;
+    int32_t *src = work + 4, *dst = src + P / 2;
+    int64_t m = 0;
+    for (int64_t s0 = 0; s0 < P; s0 += kPlanThreads) {
+        int total;
+        block_rank(s0 + tid < P && used[s0 + tid] != 0, &total);
+        m += total;
+    }
+    int64_t nsrc = 0, ndst = 0;
+    for (int64_t s0 = 0; s0 < P; s0 += kPlanThreads) {
+        const int64_t s = s0 + tid;
+        const bool in = s < P, u = in && used[s] != 0;
+        const bool mover = u && s >= m, hole = in && !u && s < m;
+        int nm, nh;
+        const int64_t rm = nsrc + block_rank(mover, &nm), rh = ndst + block_rank(hole, &nh);
+        if (mover) src[rm] = static_cast<int32_t>(s);
+        if (hole) dst[rh] = static_cast<int32_t>(s);
+        if (in && !mover) mapping[s] = u ? static_cast<int32_t>(s) : -1;
+        nsrc += nm;
+        ndst += nh;
+    }
+    __syncthreads();
+    for (int64_t r = tid; r < nsrc; r += kPlanThreads) mapping[src[r]] = dst[r];
+    for (int64_t s = tid; s < P; s += kPlanThreads) used[s] = s < m;
+    if (tid == 0) {
+        *live = static_cast<int32_t>(m);
+        work[0] = static_cast<int32_t>(nsrc);
+    }
+}
+
+__device__ __forceinline__ uint4 to_bf16x8(float4 a, float4 b) {
+    return make_uint4(float2_to_bf16x2(a.x, a.y), float2_to_bf16x2(a.z, a.w), float2_to_bf16x2(b.x, b.y),
+                      float2_to_bf16x2(b.z, b.w));
+}
+
+struct CopyArgs {
+    const void *src_pool;
+    void *dst_pool;
+    int64_t src_P, dst_P;
+    const int32_t *src, *dst;
+    const int32_t *count;   // pairs in use (null: n)
+    int64_t n;
+    int units, H;           // L * H
+    bool check;             // pairs come from the caller
+    bool same;              // source and destination are one pool
+    int *status;
+};
+
+// One pair per blockIdx.x, its L * H states dealt over blockIdx.y.
+template <typename S, typename T>
+__global__ void __launch_bounds__(kCopyThreads) pool_copy_kernel(CopyArgs a) {
+    dependent_start();
+    const int64_t i = blockIdx.x;
+    if (a.count && i >= *a.count) return;
+    const int32_t from = a.src[i], to = a.dst[i];
+    if (to < 0) return;
+    if (a.check) {
+        bool bad = from >= a.src_P || to >= a.dst_P;
+        if (!bad)   // a destination belongs to one pair, and no pair reads what another writes
+            for (int64_t j = threadIdx.x; j < a.n; j += kCopyThreads)
+                bad |= (j < i && a.dst[j] == to) || (a.same && j != i && a.dst[j] >= 0 && a.src[j] == to);
+        if (__syncthreads_or(bad)) {
+            if (threadIdx.x == 0 && blockIdx.y == 0) record_status(a.status, SALA_ERR_BAD_INDEX);
+            return;
+        }
+    }
+    if (a.same && from == to) return;
+    for (int unit = blockIdx.y; unit < a.units; unit += gridDim.y) {
+        const int l = unit / a.H, h = unit - l * a.H;
+        T *d = static_cast<T *>(a.dst_pool) + ((l * a.dst_P + to) * a.H + h) * kUnit;
+        const S *s = from < 0 ? nullptr
+                              : static_cast<const S *>(a.src_pool) + ((l * a.src_P + from) * a.H + h) * kUnit;
+#pragma unroll 4
+        for (int e = 8 * threadIdx.x; e < kUnit; e += 8 * kCopyThreads) {
+            if constexpr (std::is_same<S, uint16_t>::value && std::is_same<T, uint16_t>::value) {
+                const uint4 x = s ? __ldcs(reinterpret_cast<const uint4 *>(s + e)) : make_uint4(0, 0, 0, 0);
+                __stcs(reinterpret_cast<uint4 *>(d + e), x);
+            } else {
+                float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
+                if (s) {
+                    if constexpr (std::is_same<S, float>::value) {
+                        x0 = __ldcs(reinterpret_cast<const float4 *>(s + e));
+                        x1 = __ldcs(reinterpret_cast<const float4 *>(s + e) + 1);
+                    } else {
+                        const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(s + e));
+                        const float2 f0 = bf16x2_to_float2(b.x), f1 = bf16x2_to_float2(b.y),
+                                     f2 = bf16x2_to_float2(b.z), f3 = bf16x2_to_float2(b.w);
+                        x0 = make_float4(f0.x, f0.y, f1.x, f1.y);
+                        x1 = make_float4(f2.x, f2.y, f3.x, f3.y);
+                    }
+                }
+                if constexpr (std::is_same<T, float>::value) {
+                    __stcs(reinterpret_cast<float4 *>(d + e), x0);
+                    __stcs(reinterpret_cast<float4 *>(d + e) + 1, x1);
+                } else {
+                    __stcs(reinterpret_cast<uint4 *>(d + e), to_bf16x8(x0, x1));
+                }
+            }
+        }
+    }
+}
+
+cudaError_t copy_pairs(const CopyArgs &a, bool src_bf16, bool dst_bf16, int64_t pairs, cudaStream_t st) {
+    if (pairs == 0) return cudaSuccess;
+    LaunchTimer timer(kKPoolCopy, st);
+    const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(a.units < 65535 ? a.units : 65535));
+    void (*kern)(CopyArgs) = src_bf16 ? (dst_bf16 ? pool_copy_kernel<uint16_t, uint16_t>
+                                                  : pool_copy_kernel<uint16_t, float>)
+                                      : (dst_bf16 ? pool_copy_kernel<float, uint16_t>
+                                                  : pool_copy_kernel<float, float>);
+    return launch_dependent(kern, grid, kCopyThreads, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_state_pool_copy(const void *src_pool, bool src_bf16, int64_t src_P, void *dst_pool,
+                                   bool dst_bf16, int64_t dst_P, const int32_t *src,
+                                   const int32_t *dst, int64_t n, int64_t L, int H, int *status,
+                                   cudaStream_t st) {
+    const CopyArgs a{src_pool, dst_pool, src_P, dst_P, src, dst, nullptr, n, static_cast<int>(L * H), H,
+                     true, src_pool == dst_pool, status};
+    return copy_pairs(a, src_bf16, dst_bf16, n, st);
+}
+
+cudaError_t launch_state_pool_fork(void *pool, bool bf16, int64_t L, int64_t P, int H, int32_t *used,
+                                   const int32_t *parents, int32_t *children, int64_t n, int *status,
+                                   cudaStream_t st) {
+    {
+        LaunchTimer timer(kKPoolPlan, st);
+        const cudaError_t e = launch_dependent(pool_fork_plan_kernel, 1, kPlanThreads, st, used, P, parents,
+                                               children, n, status);
+        if (e != cudaSuccess) return e;
+    }
+    const CopyArgs a{pool, pool, P, P, parents, children, nullptr, n, static_cast<int>(L * H), H,
+                     false, true, status};
+    return copy_pairs(a, bf16, bf16, n, st);
+}
+
+cudaError_t launch_state_pool_free(int32_t *used, int64_t P, const int32_t *slots, int64_t n, int *status,
+                                   cudaStream_t st) {
+    LaunchTimer timer(kKPoolPlan, st);
+    return launch_dependent(pool_free_kernel, static_cast<unsigned>((n + 255) / 256), 256, st, used, P, slots,
+                            n, status);
+}
+
+cudaError_t launch_state_pool_compact(void *pool, bool bf16, int64_t L, int64_t P, int H, int32_t *used,
+                                      int32_t *mapping, int32_t *live, int32_t *work, cudaStream_t st) {
+    {
+        LaunchTimer timer(kKPoolPlan, st);
+        const cudaError_t e = launch_dependent(pool_compact_plan_kernel, 1, kPlanThreads, st, used, P, mapping,
+                                               live, work);
+        if (e != cudaSuccess) return e;
+    }
+    const CopyArgs a{pool, pool, P, P, work + 4, work + 4 + P / 2, work, P / 2, static_cast<int>(L * H), H,
+                     false, true, nullptr};
+    return copy_pairs(a, bf16, bf16, P / 2, st);
+}
+
+}  // namespace sala

@@ -24,6 +24,7 @@ STATUS_NAMES = {
     9: "SALA_ERR_DEBUG_CHECK",
 }
 SALA_STATE_F32, SALA_STATE_BF16 = 0, 1
+SALA_PROB_F32, SALA_PROB_BF16 = 0, 1
 
 class QkPrologue(ctypes.Structure):
     """``sala_qk_prologue``: RMSNorm weights of q and k (bf16 [128] device pointers), eps,
@@ -60,6 +61,15 @@ SIGNATURES = {
     "sala_gla_kernel_name": ([ctypes.c_int], ctypes.c_char_p),
     "sala_gla_debug_prefill_knobs": ([ctypes.c_uint64, _i64], ctypes.c_int),
     "sala_gla_set_prefill_kernel": ([_i32], ctypes.c_int),
+    "sala_gla_verify_drafts": ([_p, _i64, _p, _i64, _i32, _p, _p, _p, _p, _p, _p, _i64, _i32, _i64,
+                                _p], ctypes.c_int),
+    "sala_gla_recurrent_draft_step": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _f32, _p, _i32, _p, _i64,
+                                       _p, _i64, _i64, _i64, _i32, _p], ctypes.c_int),
+    "sala_gla_state_pool_copy": ([_p, _i32, _i64, _p, _i32, _i64, _p, _p, _i64, _i64, _i32, _p],
+                                 ctypes.c_int),
+    "sala_gla_state_pool_fork": ([_p, _i32, _i64, _i64, _i32, _p, _p, _p, _i64, _p], ctypes.c_int),
+    "sala_gla_state_pool_free": ([_p, _i64, _p, _i64, _p], ctypes.c_int),
+    "sala_gla_state_pool_compact": ([_p, _i32, _i64, _i64, _i32, _p, _p, _p, _p, _p], ctypes.c_int),
 }
 
 
@@ -362,6 +372,206 @@ def gdn_recurrent_step(q, k, v, g, beta, scale, S, o=None, stream=None):
                                             float(scale), _ptr(S), _ptr(o), N, H, _stream(stream))
     _check(rc, "sala_gla_gdn_recurrent_step")
     return o
+
+
+def _empty(shape, dtype, like, stream):
+    """An uninitialised tensor that is safe to use on ``stream`` (None: the current stream)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _probs(t, name, dtype, shape):
+    """Checks probabilities [N, R, V] whose rows may be apart; returns the elements between rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    N, R, V = t.shape
+    if t.is_contiguous():
+        return V
+    ld = t.stride(1) if R > 1 else t.stride(0) if N > 1 else V
+    if (V > 1 and t.stride(2) != 1) or ld < V or (N > 1 and t.stride(0) != R * ld):
+        raise ValueError(f"{name} must have contiguous rows at equal distances")
+    return ld
+
+
+def verify_drafts(target_probs, draft_probs, draft_tokens, accept_u, sample_u, num_drafts=None,
+                  tokens=None, accepted=None, stream=None):
+    """Drafted tokens against the target's probabilities, ``sala_gla_verify_drafts``.
+    target_probs: fp32 or bf16 [N, K + 1, V]; draft_probs: the same type [N, K, V], or None for a
+    drafter without probabilities; draft_tokens: int32 [N, K]; accept_u: fp32 [N, K]; sample_u:
+    fp32 [N]; num_drafts: int32 [N] or None (K each). Rows of probabilities may be apart (a padded
+    vocabulary). Returns (tokens int32 [N, K + 1]: accepted tokens, next token, then -1;
+    accepted int32 [N])."""
+    if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 3 or target_probs.shape[1] < 1:
+        raise ValueError("target_probs must be [N, K + 1, V]")
+    N, K, V = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2]
+    dt = target_probs.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"target_probs must be float32 or bfloat16, got {dt}")
+    p_ld = _probs(target_probs, "target_probs", dt, (N, K + 1, V))
+    q_ld = _probs(draft_probs, "draft_probs", dt, (N, K, V)) if draft_probs is not None else 0
+    _need(draft_tokens, "draft_tokens", torch.int32, (N, K))
+    _need(accept_u, "accept_u", torch.float32, (N, K))
+    _need(sample_u, "sample_u", torch.float32, (N,))
+    if num_drafts is not None:
+        _need(num_drafts, "num_drafts", torch.int32, (N,))
+    if tokens is None:
+        tokens = _empty((N, K + 1), torch.int32, target_probs, stream)
+    else:
+        _need(tokens, "tokens", torch.int32, (N, K + 1))
+    if accepted is None:
+        accepted = _empty((N,), torch.int32, target_probs, stream)
+    else:
+        _need(accepted, "accepted", torch.int32, (N,))
+    rc = load().sala_gla_verify_drafts(_ptr(target_probs), p_ld, _ptr(draft_probs), q_ld,
+                                       SALA_PROB_BF16 if dt == torch.bfloat16 else SALA_PROB_F32,
+                                       _ptr(draft_tokens), _ptr(num_drafts), _ptr(accept_u),
+                                       _ptr(sample_u), _ptr(tokens), _ptr(accepted), N, K, V,
+                                       _stream(stream))
+    _check(rc, "sala_gla_verify_drafts")
+    return tokens, accepted
+
+
+def _pool(pool, name="pool"):
+    """Checks a pool [P, H, 128, 128] (one layer) or [L, P, H, 128, 128]; returns L, P, H, dtype."""
+    if not isinstance(pool, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if pool.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {pool.dtype}")
+    _need(pool, name, pool.dtype)
+    if pool.dim() not in (4, 5) or tuple(pool.shape[-2:]) != (128, 128):
+        raise ValueError(f"{name} has shape {tuple(pool.shape)}, expected (P, H, 128, 128) or "
+                         "(L, P, H, 128, 128)")
+    L = pool.shape[0] if pool.dim() == 5 else 1
+    return L, pool.shape[-4], pool.shape[-3], \
+        SALA_STATE_BF16 if pool.dtype == torch.bfloat16 else SALA_STATE_F32
+
+
+def recurrent_draft_step(q, k, v, g, scale, pool, indices, pending=None, accepted=None,
+                         num_tokens=None, o=None, stream=None):
+    """Decode step over several drafted tokens on pooled states, ``sala_gla_recurrent_draft_step``.
+    First commits ``accepted[n] + 1`` tokens of ``pending = (k, v, g)`` (bf16, bf16 [N, T', H, 128],
+    fp32 [N, T', H]: those of the step before) to ``pool[indices[n]]``, in place; then runs the T
+    new tokens (q, k, v: bf16 [N, T, H, 128], g: fp32 [N, T, H]) from there without storing their
+    states. ``accepted``: int32 [N], as from :func:`verify_drafts` (negative: commit nothing);
+    ``num_tokens``: int32 [N] or None (T each); pool: fp32 or bf16 [P, H, 128, 128]; indices:
+    int32 [N], negative for padding. q = k = v = g = None only commits. Returns o (bf16
+    [N, T, H, 128], zeros past a row's tokens), None if there are no new tokens."""
+    L, P, H, dt = _pool(pool)
+    if pool.dim() != 4:
+        raise ValueError("pool must be one layer's (P, H, 128, 128)")
+    if not isinstance(indices, torch.Tensor) or indices.dim() != 1:
+        raise ValueError("indices must be a tensor [N]")
+    N, T, Tp = indices.shape[0], 0, 0
+    _need(indices, "indices", torch.int32)
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("q must be [N, T, H, 128]")
+        T = q.shape[1]
+        _need(q, "q", torch.bfloat16, (N, T, H, 128))
+        _need(k, "k", torch.bfloat16, q.shape)
+        _need(v, "v", torch.bfloat16, q.shape)
+        _need(g, "g", torch.float32, (N, T, H))
+        if num_tokens is not None:
+            _need(num_tokens, "num_tokens", torch.int32, (N,))
+        if o is None:
+            o = _empty((N, T, H, 128), torch.bfloat16, q, stream)
+        else:
+            _need(o, "o", torch.bfloat16, q.shape)
+    elif k is not None or v is not None or g is not None or num_tokens is not None or o is not None:
+        raise ValueError("k, v, g, num_tokens and o need q")
+    pk = pv = pg = None
+    if pending is not None:
+        pk, pv, pg = pending
+        if not isinstance(pk, torch.Tensor) or pk.dim() != 4:
+            raise ValueError("pending k must be [N, T, H, 128]")
+        Tp = pk.shape[1]
+        _need(pk, "pending k", torch.bfloat16, (N, Tp, H, 128))
+        _need(pv, "pending v", torch.bfloat16, pk.shape)
+        _need(pg, "pending g", torch.float32, (N, Tp, H))
+        _need(accepted, "accepted", torch.int32, (N,))
+    rc = load().sala_gla_recurrent_draft_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(num_tokens),
+                                              _ptr(pk), _ptr(pv), _ptr(pg),
+                                              _ptr(accepted) if pending is not None else None,
+                                              float(scale), _ptr(pool), dt, _ptr(indices), P,
+                                              _ptr(o), N, T, Tp, H, _stream(stream))
+    _check(rc, "sala_gla_recurrent_draft_step")
+    return o
+
+
+def state_pool_copy(dst_pool, src_pool, dst, src, stream=None):
+    """``sala_gla_state_pool_copy``: dst_pool[:, dst[i]] = src_pool[:, src[i]] (int32 [n] each) in
+    all layers. Pools: fp32 or bf16 [L, P, H, 128, 128] or [P, H, 128, 128], one pool or two that
+    may differ in P and type. A negative source clears the destination, a negative destination
+    skips the pair."""
+    L, Ps, H, ds = _pool(src_pool, "src_pool")
+    Ld, Pd, Hd, dd = _pool(dst_pool, "dst_pool")
+    if (L, H) != (Ld, Hd):
+        raise ValueError("src_pool and dst_pool differ in layers or heads")
+    n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else -1
+    _need(src, "src", torch.int32, (n,))
+    _need(dst, "dst", torch.int32, (n,))
+    rc = load().sala_gla_state_pool_copy(_ptr(src_pool), ds, Ps, _ptr(dst_pool), dd, Pd, _ptr(src),
+                                         _ptr(dst), n, L, H, _stream(stream))
+    _check(rc, "sala_gla_state_pool_copy")
+
+
+def state_pool_fork(pool, used, parents, children=None, stream=None):
+    """``sala_gla_state_pool_fork``: takes the lowest free slots of ``used`` (int32 [P], nonzero:
+    in use; updated) for the requests ``parents`` (int32 [n]: a used slot whose states are copied,
+    -1 for zero states, below -1 for padding). Returns the slots, int32 [n], -1 where there is
+    none."""
+    L, P, H, dt = _pool(pool)
+    _need(used, "used", torch.int32, (P,))
+    n = parents.shape[0] if isinstance(parents, torch.Tensor) and parents.dim() == 1 else -1
+    _need(parents, "parents", torch.int32, (n,))
+    if children is None:
+        children = _empty((n,), torch.int32, parents, stream)
+    else:
+        _need(children, "children", torch.int32, (n,))
+    rc = load().sala_gla_state_pool_fork(_ptr(pool), dt, L, P, H, _ptr(used), _ptr(parents),
+                                         _ptr(children), n, _stream(stream))
+    _check(rc, "sala_gla_state_pool_fork")
+    return children
+
+
+def state_pool_free(used, slots, stream=None):
+    """``sala_gla_state_pool_free``: used[slots[i]] = 0 (int32; negative slots are skipped)."""
+    _need(used, "used", torch.int32)
+    _need(slots, "slots", torch.int32)
+    if used.dim() != 1 or slots.dim() != 1:
+        raise ValueError("used and slots must be [P] and [n]")
+    rc = load().sala_gla_state_pool_free(_ptr(used), used.shape[0], _ptr(slots), slots.shape[0],
+                                         _stream(stream))
+    _check(rc, "sala_gla_state_pool_free")
+
+
+def state_pool_compact(pool, used, mapping=None, live=None, stream=None):
+    """``sala_gla_state_pool_compact``: moves the used slots to the front with the fewest copies and
+    updates ``used``. Returns (mapping int32 [P]: where each slot went, -1 for a free one; live
+    int32 [1]: the number of used slots)."""
+    L, P, H, dt = _pool(pool)
+    _need(used, "used", torch.int32, (P,))
+    if mapping is None:
+        mapping = _empty((P,), torch.int32, used, stream)
+    else:
+        _need(mapping, "mapping", torch.int32, (P,))
+    if live is None:
+        live = _empty((1,), torch.int32, used, stream)
+    else:
+        _need(live, "live", torch.int32, (1,))
+    work = _empty((P + 4,), torch.int32, used, stream)
+    rc = load().sala_gla_state_pool_compact(_ptr(pool), dt, L, P, H, _ptr(used), _ptr(mapping),
+                                            _ptr(live), _ptr(work), _stream(stream))
+    _check(rc, "sala_gla_state_pool_compact")
+    return mapping, live
 
 
 def get_device_status(stream=None) -> int:

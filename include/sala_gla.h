@@ -50,7 +50,8 @@ typedef enum {
     SALA_ERR_TIMEOUT = 5,     /* a bounded device-side wait gave up */
     SALA_ERR_BAD_SEQLENS = 6, /* device-detected: cu_seqlens not monotone or last != T */
     SALA_ERR_TOO_LARGE = 7,   /* sala_gla_chunk_fwd_noalloc: problem exceeds its fixed scratch */
-    SALA_ERR_BAD_INDEX = 8,   /* device-detected: a state index at or past the pool size */
+    SALA_ERR_BAD_INDEX = 8,   /* device-detected: a state index at or past the pool size, or
+                                 another index or count outside its range */
     SALA_ERR_DEBUG_CHECK = 9  /* debug build only (SALA_GLA_DEBUG): a device-side index check
                                  failed; the access it guards was skipped */
 } sala_status;
@@ -307,6 +308,130 @@ int sala_gla_chunk_fwd_noalloc(const void *q, const void *k, const void *v, cons
                                float scale, const float *h0, const int64_t *cu_seqlens, void *o,
                                float *hT, int64_t B, int64_t T, int32_t H, int64_t num_seqs,
                                void *stream);
+
+/* Type of the probabilities of sala_gla_verify_drafts. */
+typedef enum { SALA_PROB_F32 = 0, SALA_PROB_BF16 = 1 } sala_prob_dtype;
+
+#define SALA_VERIFY_MAX_VOCAB (1 << 20)
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given random numbers
+ * (speculative sampling). Row n holds K_n = num_drafts[n] drafted tokens x_0 .. x_{K_n - 1}, the
+ * target's distributions p_0 .. p_{K_n} after 0 .. K_n of them, and the distributions q_i that
+ * the tokens were drawn from:
+ *     token i is accepted if u_i q_i(x_i) < p_i(x_i); a = the first that is not, or K_n
+ *     w = max(p_a - q_a, 0) if token a was rejected (p_a where that is all zero), p_a if none was
+ *     the next token is the first x with  sum_{y <= x} w(y) > s sum(w)
+ * With u and s uniform in [0, 1) the emitted tokens are distributed as the target's own samples.
+ * The pages name speculative decoding for this model ("MiniCPM-SALA — Complete Blueprint",
+ * "Optimization Vectors") and no kernel for it.
+ *
+ *   target_probs  [N, K + 1, V] of prob_dtype, rows target_stride elements apart (>= V)
+ *   draft_probs   [N, K, V] of prob_dtype, rows draft_stride elements apart, or NULL: a drafter
+ *                 without probabilities (its token has probability 1)
+ *   draft_tokens  int32 [N, K]. A negative token ends its row's drafts; one >= V does too and is
+ *                 recorded as SALA_ERR_BAD_INDEX.
+ *   num_drafts    int32 [N] drafts of each row, or NULL: K each. A count outside [0, K] is
+ *                 recorded as SALA_ERR_BAD_INDEX and taken as the nearer end.
+ *   accept_u      fp32 [N, K];  sample_u  fp32 [N]; sample_u outside [0, 1) is taken as the
+ *                 nearest value inside
+ *   tokens        int32 [N, K + 1] output: the accepted tokens, the next token, then -1. The next
+ *                 token is -1 where all of p_a is zero.
+ *   accepted      int32 [N] output: the number a of accepted tokens
+ *   N, K, V       N >= 0 (0 is a no-op), K >= 0 (0: one token is drawn from each target row;
+ *                 the drafter's arguments are ignored), 1 <= V <= SALA_VERIFY_MAX_VOCAB
+ * Probabilities count as whole numbers of 2^-43 (rounded to nearest; NaN and negative values as
+ * 0, values above 1 as 1) and need not sum to 1; the sums are exact, so the result does not
+ * depend on how the work is split. Pointers need the alignment of their element type only.
+ * Errors: SALA_ERR_INVALID_ARG, SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED, SALA_ERR_CUDA.
+ */
+int sala_gla_verify_drafts(const void *target_probs, int64_t target_stride, const void *draft_probs,
+                           int64_t draft_stride, int32_t prob_dtype, const int32_t *draft_tokens,
+                           const int32_t *num_drafts, const float *accept_u, const float *sample_u,
+                           int32_t *tokens, int32_t *accepted, int64_t N, int32_t K, int64_t V,
+                           void *stream);
+
+/*
+ * Decode step over several drafted tokens on states kept in a pool, with the commit of the step
+ * before. A recurrent state has no history to roll back to, so the states of drafted tokens are
+ * not stored; the next step, which knows how many were accepted, adds those to the pool's state
+ * first. For each sequence n and head h, with i = state_indices[n] and c = accepted[n] + 1:
+ *     S = state_pool[i, h]
+ *     for j < c:              S = exp(pend_g[n,j,h]) S + pend_k[n,j,h]^T pend_v[n,j,h]
+ *     state_pool[i, h] = S    (if c > 0)
+ *     for t < num_tokens[n]:  S = exp(g[n,t,h]) S + k[n,t,h]^T v[n,t,h];  o[n,t,h] = scale q[n,t,h] S
+ * The new tokens' k, v and g are the pending ones of the next call. With the tokens of a step
+ * laid out as [the last emitted token, draft 0, .., draft K - 1] the accepted counts of
+ * sala_gla_verify_drafts are `accepted` here: the last emitted token is always kept.
+ *
+ *   q, k, v        bf16 [N, T, H, 128];  g fp32 [N, T, H]  (NULL with T = 0: commit only)
+ *   num_tokens     int32 [N] tokens of each row, or NULL: T each. Later rows of o are zeros.
+ *   pend_k, pend_v bf16 [N, T_pend, H, 128];  pend_g fp32 [N, T_pend, H]  (NULL with T_pend = 0:
+ *                  nothing is committed and the pool is only read)
+ *   accepted       int32 [N]; accepted[n] + 1 pending tokens are committed, a negative value
+ *                  commits none (required with T_pend > 0)
+ *   state_pool     [P, H, 128, 128] of state_dtype, as for sala_gla_recurrent_step_indexed. The
+ *                  arithmetic is fp32; a bf16 state is rounded once, when the commit is stored,
+ *                  and o reads the values before that rounding.
+ *   state_indices  int32 [N] slots, negative: padding row (o = 0, no state touched). Two rows that
+ *                  commit to one slot race; the caller must not do that.
+ *   o              bf16 [N, T, H, 128] output
+ * A slot >= P, more commits than T_pend or a token count outside [0, T] is recorded as
+ * SALA_ERR_BAD_INDEX and its row is treated as padding. q, k, v, pend_k, pend_v, o and the pool
+ * are 16-byte aligned, the other arrays 4-byte aligned. o and the pool overlap nothing else.
+ * Errors: SALA_ERR_INVALID_ARG, SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED, SALA_ERR_CUDA.
+ */
+int sala_gla_recurrent_draft_step(const void *q, const void *k, const void *v, const float *g,
+                                  const int32_t *num_tokens, const void *pend_k, const void *pend_v,
+                                  const float *pend_g, const int32_t *accepted, float scale,
+                                  void *state_pool, int32_t state_dtype, const int32_t *state_indices,
+                                  int64_t P, void *o, int64_t N, int64_t T, int64_t T_pend, int32_t H,
+                                  void *stream);
+
+/*
+ * Management of the states of a pool [L, P, H, 128, 128] ("MiniCPM-SALA — Complete Blueprint",
+ * "Memory Architecture": MambaPool temporal states of all layers, one slot per request). A slot
+ * is the states of one request in all L layers. `used` (int32 [P]) marks the slots in use with
+ * nonzero values; the calls read and update it on the device, in stream order, so that the host
+ * never waits and a captured graph serves every occupancy. Slot and mask arrays are 4-byte
+ * aligned; the pool is 16-byte aligned and overlaps none of them.
+ * Errors: SALA_ERR_INVALID_ARG, SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED, SALA_ERR_CUDA.
+ *
+ * sala_gla_state_pool_copy: dst_pool[:, dst[i]] = src_pool[:, src[i]] for i < n. The pools may be
+ * one (same type and P) or may not overlap; they may differ in P and in type (fp32 to bf16 rounds
+ * to nearest even). src[i] < 0 fills the destination with zeros; dst[i] < 0 skips the pair. A
+ * pair is recorded as SALA_ERR_BAD_INDEX and not copied if one of its slots is past its pool, if
+ * an earlier pair names the same destination, or if its destination is another pair's source in
+ * the same pool.
+ */
+int sala_gla_state_pool_copy(const void *src_pool, int32_t src_dtype, int64_t src_P, void *dst_pool,
+                             int32_t dst_dtype, int64_t dst_P, const int32_t *src, const int32_t *dst,
+                             int64_t n, int64_t L, int32_t H, void *stream);
+
+/*
+ * sala_gla_state_pool_fork: a free slot for each of n requests, filled with a copy of its parent's
+ * states. parents[i] >= 0: a used slot; -1: a new request (zero states); below -1: a padding
+ * entry. children[i] (int32 [n] output) is the slot: the lowest free ones in the order of the
+ * requests, or -1 for a padding entry, for a parent that is past the pool or not in use (recorded
+ * as SALA_ERR_BAD_INDEX) and once no slot is free. The slots given out are marked in `used`.
+ */
+int sala_gla_state_pool_fork(void *pool, int32_t dtype, int64_t L, int64_t P, int32_t H, int32_t *used,
+                             const int32_t *parents, int32_t *children, int64_t n, void *stream);
+
+/*
+ * sala_gla_state_pool_free: used[slots[i]] = 0 for i < n; negative slots are skipped. A slot past
+ * the pool, not in use or named twice is recorded as SALA_ERR_BAD_INDEX.
+ */
+int sala_gla_state_pool_free(int32_t *used, int64_t P, const int32_t *slots, int64_t n, void *stream);
+
+/*
+ * sala_gla_state_pool_compact: moves the m used slots to the slots 0 .. m - 1 with the fewest
+ * copies: the r-th used slot at or past m goes to the r-th free slot below m. mapping[s] (int32
+ * [P] output) is where slot s went, -1 for a free one; live[0] = m; `used` becomes 1 for the first
+ * m slots and 0 for the others. work: int32 [P + 4] scratch.
+ */
+int sala_gla_state_pool_compact(void *pool, int32_t dtype, int64_t L, int64_t P, int32_t H, int32_t *used,
+                                int32_t *mapping, int32_t *live, int32_t *work, void *stream);
 
 /*
  * Failure-path test settings of the chunked prefill (process-wide; for tests and diagnosis,
