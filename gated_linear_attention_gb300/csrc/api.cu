@@ -58,6 +58,8 @@ DeviceState *device_state(int *err) {
         d.init_error = setup_pair_kernel();
         if (d.init_error != cudaSuccess) return;
         d.init_error = setup_gdn_chunk_kernel();
+        if (d.init_error != cudaSuccess) return;
+        d.init_error = setup_draft_step_kernel();
     });
     if (d.init_error != cudaSuccess) {
         *err = SALA_ERR_CUDA;
@@ -607,7 +609,7 @@ int sala_gla_verify_drafts(const void *target_probs, int64_t target_stride, cons
     if (N < 0 || K < 0 || V < 1 || V > SALA_VERIFY_MAX_VOCAB) return SALA_ERR_INVALID_ARG;
     if (prob_dtype != SALA_PROB_F32 && prob_dtype != SALA_PROB_BF16) return SALA_ERR_INVALID_ARG;
     if (N == 0) return SALA_OK;
-    if (N >= kMaxRows || K > (1 << 20) || target_stride < V || target_stride > (int64_t(1) << 32))
+    if (N >= kMaxRows / 8 || K > (1 << 20) || target_stride < V || target_stride > (int64_t(1) << 32))
         return SALA_ERR_INVALID_ARG;
     if (!target_probs || !sample_u || !tokens || !accepted) return SALA_ERR_INVALID_ARG;
     if (K > 0 && (!draft_tokens || !accept_u)) return SALA_ERR_INVALID_ARG;
@@ -634,7 +636,7 @@ int sala_gla_verify_drafts(const void *target_probs, int64_t target_stride, cons
     if (!d) return err;
     if (launch_verify_drafts(target_probs, target_stride, drafter ? draft_probs : nullptr, draft_stride, bf16,
                              draft_tokens, K > 0 ? num_drafts : nullptr, accept_u, sample_u, tokens,
-                             accepted, N, K, V, d->status, static_cast<cudaStream_t>(stream)) !=
+                             accepted, N, K, V, d->sm_count, d->status, static_cast<cudaStream_t>(stream)) !=
         cudaSuccess)
         return SALA_ERR_CUDA;
     return SALA_OK;
@@ -649,7 +651,7 @@ int sala_gla_recurrent_draft_step(const void *q, const void *k, const void *v, c
     if (N < 0 || T < 0 || T_pend < 0 || H < 1 || P < 1) return SALA_ERR_INVALID_ARG;
     if (state_dtype != SALA_STATE_F32 && state_dtype != SALA_STATE_BF16) return SALA_ERR_INVALID_ARG;
     if (N == 0 || (T == 0 && T_pend == 0)) return SALA_OK;
-    if (N > (kMaxRows - 1) / H || P > kMaxUnits / H || P > kMaxRows || T > kMaxRows / N ||
+    if (N > (kMaxRows - 1) / 2 / H || P > kMaxUnits / H || P > kMaxRows || T > kMaxRows / N ||
         T_pend > kMaxRows / N)
         return SALA_ERR_INVALID_ARG;
     if (!state_pool || !state_indices) return SALA_ERR_INVALID_ARG;

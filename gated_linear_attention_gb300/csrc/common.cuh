@@ -54,20 +54,29 @@ __device__ __forceinline__ void dependent_start() {
 
 // Launch as a programmatic dependent of the work before it on the stream: only the launch
 // latency overlaps the previous grid's last wave (the kernel begins with dependent_start).
+// `cluster`: CTAs per cluster along x (0: no clusters); `smem`: dynamic shared memory.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, unsigned block, cudaStream_t st,
-                             Args... args) {
+cudaError_t launch_dependent_cluster(void (*kern)(KArgs...), dim3 grid, unsigned cluster, unsigned block,
+                                     size_t smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, unsigned block, cudaStream_t st,
+                             Args... args) {
+    return launch_dependent_cluster(kern, grid, 0, block, 0, st, args...);
 }
 
 }  // namespace sala

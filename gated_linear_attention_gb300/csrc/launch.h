@@ -130,8 +130,8 @@ cudaError_t launch_gdn_newv(const void *k, const void *v, const float *g, const 
 cudaError_t launch_verify_drafts(const void *p, int64_t p_stride, const void *q, int64_t q_stride,
                                  bool bf16, const int32_t *x, const int32_t *num_drafts,
                                  const float *u, const float *s, int32_t *tokens,
-                                 int32_t *accepted, int64_t N, int K, int64_t V, int *status,
-                                 cudaStream_t stream);
+                                 int32_t *accepted, int64_t N, int K, int64_t V, int sm_count,
+                                 int *status, cudaStream_t stream);
 
 // Decode step over T drafted tokens on pooled states, after committing accepted[n] + 1 of the
 // T_pend tokens of the step before (T or T_pend may be 0).
@@ -140,6 +140,8 @@ cudaError_t launch_draft_step(const void *q, const void *k, const void *v, const
                               const float *pend_g, const int32_t *accepted, float scale, void *pool,
                               bool bf16, const int32_t *slots, int64_t P, void *o, int64_t N,
                               int64_t T, int64_t T_pend, int H, int *status, cudaStream_t stream);
+
+cudaError_t setup_draft_step_kernel();
 
 // States of a pool [L, P, H, 128, 128]: n pairs of slots copied (source < 0: zeros, destination
 // < 0: skipped), n requests forked into the lowest free slots, n slots freed, the used slots

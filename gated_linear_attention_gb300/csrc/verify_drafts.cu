@@ -15,8 +15,11 @@
 //
 // Only the rows p_a and q_a are read in full; the accept test gathers two values per draft.
 //
-// One CTA per row: warp w sums the w-th of equal parts of the vocabulary, the warp whose part
-// holds the drawn number walks through it again.
+// A cluster of CTAs reads one row. The vocabulary is cut into one part per warp of the cluster, in
+// order; every warp sums its part, the CTAs read each other's sums through distributed shared
+// memory, and the CTA whose part holds the drawn number goes through that part again (from L2).
+#include <cooperative_groups.h>
+
 #include <type_traits>
 
 #include "launch.h"
@@ -25,20 +28,49 @@ namespace sala {
 
 namespace {
 
-constexpr int kVerifyThreads = 512;
-constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr float kProbScale = 8796093022208.f;   // 2^43: 2^20 tokens of probability 1 stay below 2^63
+namespace cg = cooperative_groups;
 
-// A probability in units of 2^-43 (NaN and negative values as 0, values above 1 as 1).
-__device__ __forceinline__ long long prob_units(float p) {
-    return p > 0.f ? __float2ll_rn(fminf(p, 1.f) * kProbScale) : 0ll;
-}
+constexpr int kVerifyThreads = 256;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kMaxCluster = 8;
 
 template <typename T>
 __device__ __forceinline__ float prob_load(const T *p) {
     if constexpr (std::is_same<T, float>::value) return __ldg(p);
     else return bf16_bits_to_float(__ldg(p));
 }
+
+// A probability in [0, 1] in units of 2^-43, rounded to nearest even, as hi * 2^21 + lo:
+// adding 2 to p rounds it to a multiple of 2^-22, adding
+// 3 * 2^-21 to the (exact) remainder rounds that to a multiple of 2^-43, and either sum's bits
+// hold the multiple in the low mantissa. Both parts carry a constant, which differences lose.
+// (A conversion to a 64-bit integer gives the same value but goes through the fp64 units, of
+// which this GPU has few.)
+struct Units {
+    int hi, lo;
+};
+__device__ __forceinline__ Units prob_units(float p) {
+    const float a = __fadd_rn(p, 2.f);
+    const float r = __fsub_rn(p, __fsub_rn(a, 2.f));
+    return {__float_as_int(a), __float_as_int(__fadd_rn(r, 1.430511474609375e-6f))};
+}
+constexpr Units kZeroUnits = {0x40000000, 0x35c00000};   // bits of 2 and of 3 * 2^-21
+
+// Sum of max(p - q, 0) over some tokens, in two 32-bit parts: 256 tokens of probability 1 fit.
+struct PartSum {
+    int hi = 0, lo = 0;
+    __device__ __forceinline__ void add_units(Units p, Units q) {
+        hi += p.hi - q.hi;
+        lo += p.lo - q.lo;
+    }
+    // rounding keeps the order, so the larger of p and q has the larger units
+    __device__ __forceinline__ void add(float p, float q) {
+        q = __saturatef(q);
+        add_units(prob_units(fmaxf(__saturatef(p), q)), prob_units(q));
+    }
+    __device__ __forceinline__ void add(float p) { add_units(prob_units(__saturatef(p)), kZeroUnits); }
+    __device__ __forceinline__ long long units() const { return static_cast<long long>(hi) * (1 << 21) + lo; }
+};
 
 struct VerifyArgs {
     const void *p, *q;                 // target rows [N * (K + 1)], drafter rows [N * K] or null
@@ -65,51 +97,182 @@ __device__ int first_rejected(const VerifyArgs &a, int64_t n, bool *rejected) {
         }
     }
     *rejected = false;
-    for (int base = 0; base < drafts; base += 32) {
+    for (int base = 0; base < a.K; base += 32) {
         const int i = base + lane;
-        bool stop = i >= drafts, no = false;
-        if (!stop) {
-            const int32_t x = __ldg(a.x + n * a.K + i);
-            if (x < 0 || x >= a.V) {   // the row's drafts end here
-                if (x >= 0) record_status(a.status, SALA_ERR_BAD_INDEX);
-                stop = true;
-            } else {
-                const T *p = static_cast<const T *>(a.p) + (n * (a.K + 1) + i) * a.p_stride;
-                const T *q = static_cast<const T *>(a.q) + (n * a.K + i) * a.q_stride;
-                // two 24-bit factors: the product is exact in 64 bits
-                const double qx = a.q ? static_cast<double>(prob_load(q + x)) : 1.0;
-                no = !(static_cast<double>(__ldg(a.u + n * a.K + i)) * qx <
-                       static_cast<double>(prob_load(p + x)));
-                stop = no;
-            }
+        // all loads that need no other go out together
+        const int32_t x = i < a.K ? __ldg(a.x + n * a.K + i) : -1;
+        const float u = i < a.K ? __ldg(a.u + n * a.K + i) : 0.f;
+        bool stop = true, no = false;   // a negative token ends the row's drafts
+        if (x >= 0 && x < a.V) {
+            const T *p = static_cast<const T *>(a.p) + (n * (a.K + 1) + i) * a.p_stride;
+            const T *q = static_cast<const T *>(a.q) + (n * a.K + i) * a.q_stride;
+            // two 24-bit factors: the product is exact in 64 bits
+            const double qx = a.q ? static_cast<double>(prob_load(q + x)) : 1.0;
+            no = !(static_cast<double>(u) * qx < static_cast<double>(prob_load(p + x)));
+            stop = no;
         }
+        if (i >= drafts) stop = true, no = false;
         const unsigned stops = __ballot_sync(0xffffffffu, stop);
         if (stops) {
             const int first = __ffs(stops) - 1;
             *rejected = __shfl_sync(0xffffffffu, no, first);
+            if (lane == first && i < drafts && x >= a.V) record_status(a.status, SALA_ERR_BAD_INDEX);
             return base + first;
         }
     }
     return drafts;
 }
 
-// The weight of token x in the draw, in units of 2^-43.
+// The distribution that a row's next token is drawn from: the target's row p, less the drafter's
+// row q or less a certain token (a drafter without probabilities) where a draft was rejected.
 template <typename T>
-__device__ __forceinline__ long long weight(const T *p, const T *q, int64_t one_at, int64_t x) {
-    long long w = prob_units(prob_load(p + x));
-    if (q) w -= prob_units(prob_load(q + x));
-    else if (x == one_at) w -= static_cast<long long>(kProbScale);   // a drafter without probabilities
-    return w > 0 ? w : 0;
+struct Weights {
+    const T *p, *q;
+    int64_t one_at;
+
+    __device__ __forceinline__ long long at(int64_t x) const {
+        PartSum s;
+        if (q) s.add(prob_load(p + x), prob_load(q + x));
+        else if (x != one_at) s.add(prob_load(p + x));
+        return s.units();
+    }
+};
+
+// 16 bytes of probabilities
+template <typename T>
+struct Vec {
+    static constexpr int kN = 16 / sizeof(T);
+    uint4 w;
+    __device__ __forceinline__ void load(const T *p) { w = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void keep(bool ok) {
+        const uint32_t m = ok ? ~0u : 0u;
+        w = make_uint4(w.x & m, w.y & m, w.z & m, w.w & m);
+    }
+    __device__ __forceinline__ float at(int i) const {
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (sizeof(T) == 4) return __uint_as_float(ws[i]);
+        const float2 f = bf16x2_to_float2(ws[i / 2]);
+        return i & 1 ? f.y : f.x;
+    }
+};
+
+// One lane's share of the sum over tokens [lo, hi), `lo` aligned for 16-byte loads of p and, with
+// kQ (subtract the drafter's row), of q.
+template <typename T, bool kQ>
+__device__ __forceinline__ long long sum_vectors(const Weights<T> &w, int64_t lo, int64_t hi, int lane) {
+    constexpr int kN = Vec<T>::kN, kAhead = 4;   // vectors of a lane in flight
+    long long sum = 0;
+    const T *p = w.p + lo + lane * kN, *q = kQ ? w.q + lo + lane * kN : nullptr;
+    const int vectors = static_cast<int>((hi - lo) / kN);
+    auto add = [&](const Vec<T> (&x)[kAhead], const Vec<T> (&y)[kAhead]) {
+        PartSum s;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                if constexpr (kQ) s.add(x[i].at(e), y[i].at(e));
+                else s.add(x[i].at(e));
+            }
+        sum += s.units();
+    };
+    Vec<T> x[kAhead], y[kAhead];
+    int v = 0;
+    for (; v + 32 * kAhead <= vectors; v += 32 * kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            x[i].load(p + static_cast<int64_t>(v + 32 * i) * kN);
+            if constexpr (kQ) y[i].load(q + static_cast<int64_t>(v + 32 * i) * kN);
+        }
+        add(x, y);
+    }
+    if (v + lane < vectors) {
+        // the last round: a vector past the end is read from the lane's first place and dropped
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t at = static_cast<int64_t>(v + 32 * i + lane < vectors ? v + 32 * i : v) * kN;
+            x[i].load(p + at);
+            if constexpr (kQ) y[i].load(q + at);
+        }
+#pragma unroll
+        for (int i = 1; i < kAhead; ++i) {
+            x[i].keep(v + 32 * i + lane < vectors);
+            if constexpr (kQ) y[i].keep(v + 32 * i + lane < vectors);
+        }
+        add(x, y);
+    }
+    // fewer than a vector's tokens, where the part ends the row
+    const int64_t rest = lo + static_cast<int64_t>(vectors) * kN + lane;
+    if (rest < hi) {
+        PartSum s;
+        if constexpr (kQ) s.add(prob_load(w.p + rest), prob_load(w.q + rest));
+        else s.add(prob_load(w.p + rest));
+        sum += s.units();
+    }
+    return sum;
+}
+
+// The sum of the weights of tokens [lo, hi) by one warp; every lane returns it.
+template <typename T>
+__device__ __forceinline__ long long sum_part(const Weights<T> &w, int64_t lo, int64_t hi, int lane) {
+    long long sum = 0;
+    const uintptr_t bp = reinterpret_cast<uintptr_t>(w.p), bq = reinterpret_cast<uintptr_t>(w.q);
+    if (!w.q || ((bp ^ bq) & 15) == 0) {
+        // tokens before the first aligned one (only where the part begins the row)
+        const int64_t start = min(hi, lo + static_cast<int64_t>((-(bp + lo * sizeof(T)) & 15) / sizeof(T)));
+        PartSum s;
+        if (lo + lane < start) {
+            if (w.q) s.add(prob_load(w.p + lo + lane), prob_load(w.q + lo + lane));
+            else s.add(prob_load(w.p + lo + lane));
+        }
+        sum = s.units() + (w.q ? sum_vectors<T, true>(w, start, hi, lane) : sum_vectors<T, false>(w, start, hi, lane));
+        // the certain token was summed with its whole probability
+        if (lane == 0 && w.one_at >= lo && w.one_at < hi) {
+            PartSum one;
+            one.add(prob_load(w.p + w.one_at));
+            sum -= one.units();
+        }
+    } else {
+        // rows whose starts differ modulo 16 bytes: one token at a time, eight in flight
+        for (int64_t x = lo + lane; x - lane < hi; x += 8 * 32) {
+            float p[8], q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool ok = x + 32 * i < hi;
+                p[i] = ok ? prob_load(w.p + x + 32 * i) : 0.f;
+                q[i] = ok ? prob_load(w.q + x + 32 * i) : 0.f;
+            }
+            PartSum s;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s.add(p[i], q[i]);
+            sum += s.units();
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    return sum;
+}
+
+// Inclusive prefix sum over the lanes of a warp.
+__device__ __forceinline__ long long warp_prefix(long long c, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, c, off);
+        if (lane >= off) c += y;
+    }
+    return c;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArgs a) {
     dependent_start();
-    const int64_t n = blockIdx.x;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const int64_t n = blockIdx.x / ranks;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ int first_s;
-    __shared__ bool rejected_s;
-    __shared__ long long sums[kVerifyWarps];
+    __shared__ int first_s, rejected_s;
+    __shared__ long long mine[2][kVerifyWarps];                   // this CTA's sums, one row a pass
+    __shared__ long long all[kMaxCluster * kVerifyWarps];         // the cluster's
+    __shared__ long long scan[kVerifyWarps];
 
     if (warp == 0) {
         bool rejected;
@@ -121,62 +284,102 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
     }
     __syncthreads();
     const int first = first_s;
-    const T *p = static_cast<const T *>(a.p) + (n * (a.K + 1) + first) * a.p_stride;
-    const T *q = nullptr;
-    int64_t one_at = -1;
+    Weights<T> w{static_cast<const T *>(a.p) + (n * (a.K + 1) + first) * a.p_stride, nullptr, -1};
     if (rejected_s) {
-        if (a.q) q = static_cast<const T *>(a.q) + (n * a.K + first) * a.q_stride;
-        else one_at = __ldg(a.x + n * a.K + first);
+        if (a.q) w.q = static_cast<const T *>(a.q) + (n * a.K + first) * a.q_stride;
+        else w.one_at = __ldg(a.x + n * a.K + first);
     }
-    const int64_t part = (a.V + kVerifyWarps - 1) / kVerifyWarps;
-    const int64_t lo = min(a.V, part * warp), hi = min(a.V, lo + part);
 
-    long long total = 0, before = 0;
+    // parts: from the second on they begin at 16-byte boundaries of the target's row
+    constexpr int kN = Vec<T>::kN;
+    const int parts = ranks * kVerifyWarps;
+    const int64_t head = (-reinterpret_cast<uintptr_t>(w.p) & 15) / sizeof(T);
+    const int64_t len = (a.V / kN + parts) / parts * kN;
+    auto part_begin = [&](int i) { return i == 0 ? 0 : min(a.V, head + len * i); };
+
+    long long total = 0;
     for (int pass = 0; pass < 2; ++pass) {
-        long long sum = 0;
-        for (int64_t x = lo + lane; x < hi; x += 32) sum += weight(p, q, one_at, x);
+        const int i = rank * kVerifyWarps + warp;
+        const long long sum = sum_part(w, part_begin(i), part_begin(i + 1), lane);
+        if (lane == 0) mine[pass][warp] = sum;
+        cluster.sync();
+        if (threadIdx.x < parts)
+            all[threadIdx.x] = cluster.map_shared_rank(&mine[pass][0], threadIdx.x / kVerifyWarps)[threadIdx.x % kVerifyWarps];
+        __syncthreads();
+        total = 0;
+        for (int j = lane; j < parts; j += 32) total += all[j];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) sums[warp] = sum;
+        for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+        if (total > 0 || (!w.q && w.one_at < 0)) break;
+        w.q = nullptr;   // nothing is left of the target after the drafter's part: draw from the target
+        w.one_at = -1;
         __syncthreads();
-        total = before = 0;
-        for (int w = 0; w < kVerifyWarps; ++w) {
-            if (w == warp) before = total;
-            total += sums[w];
-        }
-        __syncthreads();
-        if (total > 0 || (!q && one_at < 0)) break;
-        q = nullptr;   // nothing is left of the target after the drafter's part: draw from the target
-        one_at = -1;
     }
+    cluster.barrier_arrive();   // the others may still be reading this CTA's sums
 
     int32_t *out = a.tokens + n * (a.K + 1);
-    for (int i = threadIdx.x; i <= a.K; i += kVerifyThreads)
-        if (i != first || total == 0) out[i] = i < first ? __ldg(a.x + n * a.K + i) : -1;
-    if (threadIdx.x == 0) a.accepted[n] = first;
-    if (total == 0) return;
-
-    // the number drawn, in the same units, at most total - 1
-    float s = __ldg(a.s + n);
-    s = s >= 0.f ? fminf(s, 0.99999994f) : 0.f;
-    const long long at = static_cast<long long>(static_cast<double>(s) * static_cast<double>(total));
-    if (at < before || at >= before + sums[warp]) return;
-    long long run = before;
-    for (int64_t x0 = lo; x0 < hi; x0 += 32) {
-        const int64_t x = x0 + lane;
-        long long c = x < hi ? weight(p, q, one_at, x) : 0;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, c, off);
-            if (lane >= off) c += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, run + c > at);
-        if (past) {
-            if (lane == 0) out[first] = static_cast<int32_t>(x0 + __ffs(past) - 1);
-            return;
-        }
-        run += __shfl_sync(0xffffffffu, c, 31);
+    if (rank == 0) {
+        for (int i = threadIdx.x; i <= a.K; i += kVerifyThreads)
+            if (i != first || total == 0) out[i] = i < first ? __ldg(a.x + n * a.K + i) : -1;
+        if (threadIdx.x == 0) a.accepted[n] = first;
     }
+    if (total > 0) {
+        // the number drawn, in the same units: the whole part of s * total (s is a whole number of
+        // 2^-64, or closer to 0 than that)
+        float s = __ldg(a.s + n);
+        s = s >= 0.f ? fminf(s, 0.99999994f) : 0.f;
+        const long long at = __umul64hi(__float2ull_rz(s * 18446744073709551616.f), total);
+        // the part that holds it: every warp finds the same one
+        long long before = 0;
+        int part = -1;
+        for (int j0 = 0; j0 < parts; j0 += 32) {
+            const long long own = j0 + lane < parts ? all[j0 + lane] : 0;
+            const long long c = before + warp_prefix(own, lane);
+            const unsigned past = __ballot_sync(0xffffffffu, c > at);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                part = j0 + l;
+                before = __shfl_sync(0xffffffffu, c - own, l);
+                break;
+            }
+            before = __shfl_sync(0xffffffffu, c, 31);
+        }
+        if (part / kVerifyWarps == rank) {
+            // each thread sums consecutive tokens of the part, then the one that passes `at` looks
+            // for its token
+            const int64_t lo = part_begin(part), hi = part_begin(part + 1);
+            const int64_t per = (hi - lo + kVerifyThreads - 1) / kVerifyThreads;
+            const int64_t x0 = min(hi, lo + per * threadIdx.x), x1 = min(hi, x0 + per);
+            long long sum = 0;
+#pragma unroll 8
+            for (int64_t x = x0; x < x1; ++x) sum += w.at(x);
+            const long long c = warp_prefix(sum, lane);
+            if (lane == 31) scan[warp] = c;
+            __syncthreads();
+            long long run = before + c - sum;
+            for (int i = 0; i < warp; ++i) run += scan[i];
+            if (run <= at && at < run + sum) {
+                for (int64_t x = x0; x < x1; ++x) {
+                    run += w.at(x);
+                    if (run > at) {
+                        out[first] = static_cast<int32_t>(x);
+                        break;
+                    }
+                }
+            }
+        }
+    }
+    cluster.barrier_wait();
+}
+
+// CTAs that share a row: 8 while the rows are few, so that every SM reads and each CTA's part is
+// short; fewer where the rows alone are four CTAs for every SM, since each CTA pays about 5 us of
+// dependent steps (accept test, sums of the cluster, second look). 1024 rows of 65536 bf16: 8 CTAs
+// 123 us, 2 CTAs 66 us; 256 rows of 131072 fp32: 8 CTAs 56 us, 2 CTAs 73 us.
+int cluster_size(int64_t N, int sm_count) {
+    int c = kMaxCluster;
+    while (c > 1 && N * c > 16 * sm_count) c /= 2;
+    return c;
 }
 
 }  // namespace
@@ -184,14 +387,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
 cudaError_t launch_verify_drafts(const void *p, int64_t p_stride, const void *q, int64_t q_stride,
                                  bool bf16, const int32_t *x, const int32_t *num_drafts,
                                  const float *u, const float *s, int32_t *tokens,
-                                 int32_t *accepted, int64_t N, int K, int64_t V, int *status,
-                                 cudaStream_t stream) {
+                                 int32_t *accepted, int64_t N, int K, int64_t V, int sm_count,
+                                 int *status, cudaStream_t stream) {
     LaunchTimer timer(kKVerifyDrafts, stream);
+    const int c = cluster_size(N, sm_count);
     const VerifyArgs a{p, q, p_stride, q_stride, x, num_drafts, u, s, tokens, accepted, K, V, status};
-    return bf16 ? launch_dependent(verify_drafts_kernel<uint16_t>, static_cast<unsigned>(N),
-                                   kVerifyThreads, stream, a)
-                : launch_dependent(verify_drafts_kernel<float>, static_cast<unsigned>(N),
-                                   kVerifyThreads, stream, a);
+    return launch_dependent_cluster(bf16 ? verify_drafts_kernel<uint16_t> : verify_drafts_kernel<float>,
+                                    static_cast<unsigned>(N * c), c, kVerifyThreads, 0, stream, a);
 }
 
 }  // namespace sala
