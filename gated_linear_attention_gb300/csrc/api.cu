@@ -677,7 +677,7 @@ int sala_gla_recurrent_draft_step(const void *q, const void *k, const void *v, c
     if (!d) return err;
     if (launch_draft_step(q, k, v, g, T > 0 ? num_tokens : nullptr, pend_k, pend_v, pend_g, accepted, scale,
                           state_pool, state_dtype == SALA_STATE_BF16, state_indices, P, o, N, T, T_pend,
-                          H, d->status, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+                          H, d->sm_count, d->status, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SALA_ERR_CUDA;
     return SALA_OK;
 }

@@ -139,7 +139,8 @@ cudaError_t launch_draft_step(const void *q, const void *k, const void *v, const
                               const int32_t *num_tokens, const void *pend_k, const void *pend_v,
                               const float *pend_g, const int32_t *accepted, float scale, void *pool,
                               bool bf16, const int32_t *slots, int64_t P, void *o, int64_t N,
-                              int64_t T, int64_t T_pend, int H, int *status, cudaStream_t stream);
+                              int64_t T, int64_t T_pend, int H, int sm_count, int *status,
+                              cudaStream_t stream);
 
 cudaError_t setup_draft_step_kernel();
 
