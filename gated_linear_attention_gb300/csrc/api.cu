@@ -758,19 +758,19 @@ int sala_gla_state_pool_free(int32_t *used, int64_t P, const int32_t *slots, int
 }
 
 int sala_gla_state_pool_compact(void *pool, int32_t dtype, int64_t L, int64_t P, int32_t H, int32_t *used,
-                                int32_t *mapping, int32_t *live, int32_t *work, void *stream) {
+                                int32_t *mapping, int32_t *live, void *stream) {
     size_t pb = 0;
     if (const int e = check_pool(pool, dtype, L, P, H, &pb)) return e;
-    if (!used || !mapping || !live || !work) return SALA_ERR_INVALID_ARG;
-    if (!aligned4(used) || !aligned4(mapping) || !aligned4(live) || !aligned4(work)) return SALA_ERR_MISALIGNED;
+    if (!used || !mapping || !live) return SALA_ERR_INVALID_ARG;
+    if (!aligned4(used) || !aligned4(mapping) || !aligned4(live)) return SALA_ERR_MISALIGNED;
     const size_t ub = static_cast<size_t>(P) * 4;
-    const Range all[5] = {{pool, pb}, {used, ub}, {mapping, ub}, {live, 4}, {work, ub + 16}};
-    for (int i = 0; i < 5; ++i)
+    const Range all[4] = {{pool, pb}, {used, ub}, {mapping, ub}, {live, 4}};
+    for (int i = 0; i < 4; ++i)
         for (int j = 0; j < i; ++j)
             if (overlaps(all[i].p, all[i].bytes, all[j].p, all[j].bytes)) return SALA_ERR_INVALID_ARG;
     int err = SALA_OK;
     if (!device_state(&err)) return err;
-    if (launch_state_pool_compact(pool, dtype == SALA_STATE_BF16, L, P, H, used, mapping, live, work,
+    if (launch_state_pool_compact(pool, dtype == SALA_STATE_BF16, L, P, H, used, mapping, live,
                                   static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SALA_ERR_CUDA;
     return SALA_OK;

@@ -146,7 +146,7 @@ cudaError_t setup_draft_step_kernel();
 
 // States of a pool [L, P, H, 128, 128]: n pairs of slots copied (source < 0: zeros, destination
 // < 0: skipped), n requests forked into the lowest free slots, n slots freed, the used slots
-// moved to the front (`work`: P + 4 words).
+// moved to the front.
 cudaError_t launch_state_pool_copy(const void *src_pool, bool src_bf16, int64_t src_P, void *dst_pool,
                                    bool dst_bf16, int64_t dst_P, const int32_t *src,
                                    const int32_t *dst, int64_t n, int64_t L, int H, int *status,
@@ -157,7 +157,7 @@ cudaError_t launch_state_pool_fork(void *pool, bool bf16, int64_t L, int64_t P, 
 cudaError_t launch_state_pool_free(int32_t *used, int64_t P, const int32_t *slots, int64_t n, int *status,
                                    cudaStream_t st);
 cudaError_t launch_state_pool_compact(void *pool, bool bf16, int64_t L, int64_t P, int H, int32_t *used,
-                                      int32_t *mapping, int32_t *live, int32_t *work, cudaStream_t st);
+                                      int32_t *mapping, int32_t *live, cudaStream_t st);
 
 // Nonzero tag of one prefill call for the hand-off flags (differs from the previous call's).
 uint32_t next_prefill_epoch();

@@ -17,6 +17,7 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kCopyThreads = 256;
+constexpr int64_t kCopyCtas = 131072;   // CTAs of a launch where pairs are many (compaction: most of them idle)
 constexpr int kUnit = kD * kD;   // elements of one head's state
 
 // Exclusive prefix count of `flag` over the CTA (kPlanThreads threads); *total the count.
@@ -102,51 +103,79 @@ __global__ void pool_free_kernel(int32_t *used, int64_t P, const int32_t *slots,
 }
 
 // With m used slots: the r-th used slot at or past m moves to the r-th free slot below m.
-// work: [0] the number of moves, [4 ..] their sources, [4 + P / 2 ..] their destinations.
 __global__ void __launch_bounds__(kPlanThreads)
-pool_compact_plan_kernel(int32_t *used, int64_t P, int32_t *mapping, int32_t *live, int32_t *work) {
+pool_compact_plan_kernel(int32_t *used, int64_t P, int32_t *mapping, int32_t *live) {
     dependent_start();
     const int tid = threadIdx.x;
-    int32_t *src = work + 4, *dst = src + P / 2;
+    auto in_use = [&](int64_t s) { return s < P && used[s] != 0; };
     int64_t m = 0;
     for (int64_t s0 = 0; s0 < P; s0 += kPlanThreads) {
         int total;
-        block_rank(s0 + tid < P && used[s0 + tid] != 0, &total);
+        block_rank(in_use(s0 + tid), &total);
         m += total;
     }
-    int64_t nsrc = 0, ndst = 0;
-    for (int64_t s0 = 0; s0 < P; s0 += kPlanThreads) {
+    // 1. slots below m; mapping[m + r] = the r-th free one of them (there are as many as used slots
+    // past m, so at most P - m)
+    int64_t holes = 0;
+    for (int64_t s0 = 0; s0 < m; s0 += kPlanThreads) {
         const int64_t s = s0 + tid;
-        const bool in = s < P, u = in && used[s] != 0;
-        const bool mover = u && s >= m, hole = in && !u && s < m;
-        int nm, nh;
-        const int64_t rm = nsrc + block_rank(mover, &nm), rh = ndst + block_rank(hole, &nh);
-        if (mover) src[rm] = static_cast<int32_t>(s);
-        if (hole) dst[rh] = static_cast<int32_t>(s);
-        if (in && !mover) mapping[s] = u ? static_cast<int32_t>(s) : -1;
-        nsrc += nm;
-        ndst += nh;
+        const bool hole = s < m && !in_use(s);
+        int total;
+        const int64_t r = holes + block_rank(hole, &total);
+        if (hole) mapping[m + r] = static_cast<int32_t>(s);
+        if (s < m) mapping[s] = hole ? -1 : static_cast<int32_t>(s);
+        holes += total;
     }
     __syncthreads();
-    for (int64_t r = tid; r < nsrc; r += kPlanThreads) mapping[src[r]] = dst[r];
-    for (int64_t s = tid; s < P; s += kPlanThreads) used[s] = s < m;
-    if (tid == 0) {
-        *live = static_cast<int32_t>(m);
-        work[0] = static_cast<int32_t>(nsrc);
+    // 2. slots from m: the rank r of used slot s is at most s - m, so from the last tile down every
+    // entry of the list is read before it is overwritten
+    int64_t left = holes;
+    for (int64_t s0 = m + (P - m - 1) / kPlanThreads * kPlanThreads; P > m && s0 >= m; s0 -= kPlanThreads) {
+        const int64_t s = s0 + tid;
+        const bool mover = in_use(s);
+        int total;
+        const int rank = block_rank(mover, &total);
+        left -= total;
+        const int32_t to = mover ? mapping[m + left + rank] : -1;
+        __syncthreads();
+        if (s < P) mapping[s] = to;
+        __syncthreads();
     }
+    for (int64_t s = tid; s < P; s += kPlanThreads) used[s] = s < m;
+    if (tid == 0) *live = static_cast<int32_t>(m);
 }
 
-__device__ __forceinline__ uint4 to_bf16x8(float4 a, float4 b) {
-    return make_uint4(float2_to_bf16x2(a.x, a.y), float2_to_bf16x2(a.z, a.w), float2_to_bf16x2(b.x, b.y),
-                      float2_to_bf16x2(b.z, b.w));
-}
+// What a thread moves at a time: 16 bytes of the wider type (8 bf16 elements, else 4 of both), so
+// that each warp access is contiguous on both sides.
+template <typename S, typename T>
+struct Mover {
+    static constexpr bool kSame16 = std::is_same<S, uint16_t>::value && std::is_same<T, uint16_t>::value;
+    static constexpr int kN = kSame16 ? 8 : 4;
+    using Word = typename std::conditional<kSame16, uint4, float4>::type;
+
+    // (no streaming hint: children of one parent read it from L2, and evict-first loads made a fork
+    // of 40 slots from 5 parents 200 us instead of 175)
+    static __device__ __forceinline__ Word load(const S *p) {
+        if constexpr (std::is_same<S, uint16_t>::value && !kSame16) {
+            const uint2 b = __ldg(reinterpret_cast<const uint2 *>(p));
+            const float2 f0 = bf16x2_to_float2(b.x), f1 = bf16x2_to_float2(b.y);
+            return make_float4(f0.x, f0.y, f1.x, f1.y);
+        } else {
+            return __ldg(reinterpret_cast<const Word *>(p));
+        }
+    }
+    static __device__ __forceinline__ void store(T *p, Word x) {
+        if constexpr (std::is_same<T, uint16_t>::value && !kSame16)
+            __stcs(reinterpret_cast<uint2 *>(p), make_uint2(float2_to_bf16x2(x.x, x.y), float2_to_bf16x2(x.z, x.w)));
+        else __stcs(reinterpret_cast<Word *>(p), x);
+    }
+};
 
 struct CopyArgs {
     const void *src_pool;
     void *dst_pool;
     int64_t src_P, dst_P;
-    const int32_t *src, *dst;
-    const int32_t *count;   // pairs in use (null: n)
+    const int32_t *src, *dst;   // src null: pair i reads slot i
     int64_t n;
     int units, H;           // L * H
     bool check;             // pairs come from the caller
@@ -159,8 +188,7 @@ template <typename S, typename T>
 __global__ void __launch_bounds__(kCopyThreads) pool_copy_kernel(CopyArgs a) {
     dependent_start();
     const int64_t i = blockIdx.x;
-    if (a.count && i >= *a.count) return;
-    const int32_t from = a.src[i], to = a.dst[i];
+    const int32_t from = a.src ? a.src[i] : static_cast<int32_t>(i), to = a.dst[i];
     if (to < 0) return;
     if (a.check) {
         bool bad = from >= a.src_P || to >= a.dst_P;
@@ -178,40 +206,29 @@ __global__ void __launch_bounds__(kCopyThreads) pool_copy_kernel(CopyArgs a) {
         T *d = static_cast<T *>(a.dst_pool) + ((l * a.dst_P + to) * a.H + h) * kUnit;
         const S *s = from < 0 ? nullptr
                               : static_cast<const S *>(a.src_pool) + ((l * a.src_P + from) * a.H + h) * kUnit;
-#pragma unroll 4
-        for (int e = 8 * threadIdx.x; e < kUnit; e += 8 * kCopyThreads) {
-            if constexpr (std::is_same<S, uint16_t>::value && std::is_same<T, uint16_t>::value) {
-                const uint4 x = s ? __ldcs(reinterpret_cast<const uint4 *>(s + e)) : make_uint4(0, 0, 0, 0);
-                __stcs(reinterpret_cast<uint4 *>(d + e), x);
-            } else {
-                float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
-                if (s) {
-                    if constexpr (std::is_same<S, float>::value) {
-                        x0 = __ldcs(reinterpret_cast<const float4 *>(s + e));
-                        x1 = __ldcs(reinterpret_cast<const float4 *>(s + e) + 1);
-                    } else {
-                        const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(s + e));
-                        const float2 f0 = bf16x2_to_float2(b.x), f1 = bf16x2_to_float2(b.y),
-                                     f2 = bf16x2_to_float2(b.z), f3 = bf16x2_to_float2(b.w);
-                        x0 = make_float4(f0.x, f0.y, f1.x, f1.y);
-                        x1 = make_float4(f2.x, f2.y, f3.x, f3.y);
-                    }
-                }
-                if constexpr (std::is_same<T, float>::value) {
-                    __stcs(reinterpret_cast<float4 *>(d + e), x0);
-                    __stcs(reinterpret_cast<float4 *>(d + e) + 1, x1);
-                } else {
-                    __stcs(reinterpret_cast<uint4 *>(d + e), to_bf16x8(x0, x1));
-                }
-            }
+        using M = Mover<S, T>;
+        constexpr int kAhead = 8;   // loads in flight
+#pragma unroll 1
+        for (int e = M::kN * threadIdx.x; e < kUnit; e += kAhead * M::kN * kCopyThreads) {
+            typename M::Word x[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) x[i] = s ? M::load(s + e + i * M::kN * kCopyThreads) : typename M::Word{};
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) M::store(d + e + i * M::kN * kCopyThreads, x[i]);
         }
     }
+}
+
+// CTAs that share a pair: one per head's state, fewer where the pairs are many.
+int64_t copy_slices(int64_t pairs, int64_t units) {
+    const int64_t most = (kCopyCtas + pairs - 1) / pairs;
+    return units < most ? units : most;
 }
 
 cudaError_t copy_pairs(const CopyArgs &a, bool src_bf16, bool dst_bf16, int64_t pairs, cudaStream_t st) {
     if (pairs == 0) return cudaSuccess;
     LaunchTimer timer(kKPoolCopy, st);
-    const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(a.units < 65535 ? a.units : 65535));
+    const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(copy_slices(pairs, a.units)));
     void (*kern)(CopyArgs) = src_bf16 ? (dst_bf16 ? pool_copy_kernel<uint16_t, uint16_t>
                                                   : pool_copy_kernel<uint16_t, float>)
                                       : (dst_bf16 ? pool_copy_kernel<float, uint16_t>
@@ -225,7 +242,7 @@ cudaError_t launch_state_pool_copy(const void *src_pool, bool src_bf16, int64_t 
                                    bool dst_bf16, int64_t dst_P, const int32_t *src,
                                    const int32_t *dst, int64_t n, int64_t L, int H, int *status,
                                    cudaStream_t st) {
-    const CopyArgs a{src_pool, dst_pool, src_P, dst_P, src, dst, nullptr, n, static_cast<int>(L * H), H,
+    const CopyArgs a{src_pool, dst_pool, src_P, dst_P, src, dst, n, static_cast<int>(L * H), H,
                      true, src_pool == dst_pool, status};
     return copy_pairs(a, src_bf16, dst_bf16, n, st);
 }
@@ -239,7 +256,7 @@ cudaError_t launch_state_pool_fork(void *pool, bool bf16, int64_t L, int64_t P, 
                                                children, n, status);
         if (e != cudaSuccess) return e;
     }
-    const CopyArgs a{pool, pool, P, P, parents, children, nullptr, n, static_cast<int>(L * H), H,
+    const CopyArgs a{pool, pool, P, P, parents, children, n, static_cast<int>(L * H), H,
                      false, true, status};
     return copy_pairs(a, bf16, bf16, n, st);
 }
@@ -252,16 +269,15 @@ cudaError_t launch_state_pool_free(int32_t *used, int64_t P, const int32_t *slot
 }
 
 cudaError_t launch_state_pool_compact(void *pool, bool bf16, int64_t L, int64_t P, int H, int32_t *used,
-                                      int32_t *mapping, int32_t *live, int32_t *work, cudaStream_t st) {
+                                      int32_t *mapping, int32_t *live, cudaStream_t st) {
     {
         LaunchTimer timer(kKPoolPlan, st);
         const cudaError_t e = launch_dependent(pool_compact_plan_kernel, 1, kPlanThreads, st, used, P, mapping,
-                                               live, work);
+                                               live);
         if (e != cudaSuccess) return e;
     }
-    const CopyArgs a{pool, pool, P, P, work + 4, work + 4 + P / 2, work, P / 2, static_cast<int>(L * H), H,
-                     false, true, nullptr};
-    return copy_pairs(a, bf16, bf16, P / 2, st);
+    const CopyArgs a{pool, pool, P, P, nullptr, mapping, P, static_cast<int>(L * H), H, false, true, nullptr};
+    return copy_pairs(a, bf16, bf16, P, st);
 }
 
 }  // namespace sala

@@ -428,10 +428,10 @@ int sala_gla_state_pool_free(int32_t *used, int64_t P, const int32_t *slots, int
  * sala_gla_state_pool_compact: moves the m used slots to the slots 0 .. m - 1 with the fewest
  * copies: the r-th used slot at or past m goes to the r-th free slot below m. mapping[s] (int32
  * [P] output) is where slot s went, -1 for a free one; live[0] = m; `used` becomes 1 for the first
- * m slots and 0 for the others. work: int32 [P + 4] scratch.
+ * m slots and 0 for the others.
  */
 int sala_gla_state_pool_compact(void *pool, int32_t dtype, int64_t L, int64_t P, int32_t H, int32_t *used,
-                                int32_t *mapping, int32_t *live, int32_t *work, void *stream);
+                                int32_t *mapping, int32_t *live, void *stream);
 
 /*
  * Failure-path test settings of the chunked prefill (process-wide; for tests and diagnosis,

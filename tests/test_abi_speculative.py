@@ -112,15 +112,15 @@ def test_state_pool_free_argument_errors(lib, args, want):
     assert lib.sala_gla_state_pool_free(_p(used), Pn, _p(slots), n, None) == want
 
 
-def _compact(lib, pool=0x10000000, dt=0, L=2, Pn=8, H=2, used=0x1000, m=0x2000, live=0x3000, work=0x4000):
-    return lib.sala_gla_state_pool_compact(_p(pool), dt, L, Pn, H, _p(used), _p(m), _p(live), _p(work), None)
+def _compact(lib, pool=0x10000000, dt=0, L=2, Pn=8, H=2, used=0x1000, m=0x2000, live=0x3000):
+    return lib.sala_gla_state_pool_compact(_p(pool), dt, L, Pn, H, _p(used), _p(m), _p(live), None)
 
 
 @no_gpu
 @pytest.mark.parametrize("kw,want", [
     (dict(pool=0), INVALID), (dict(used=0), INVALID), (dict(m=0), INVALID), (dict(live=0), INVALID),
-    (dict(work=0), INVALID), (dict(m=0x1004), INVALID), (dict(live=0x4008), INVALID),
-    (dict(work=0x10000000), INVALID), (dict(H=0), INVALID), (dict(work=0x4002), MISALIGNED), (dict(), CUDA)])
+    (dict(m=0x1004), INVALID), (dict(live=0x2008), INVALID), (dict(live=0x10000000), INVALID),
+    (dict(H=0), INVALID), (dict(live=0x4002), MISALIGNED), (dict(), CUDA)])
 def test_state_pool_compact_argument_errors(lib, kw, want):
     assert _compact(lib, **kw) == want
 
