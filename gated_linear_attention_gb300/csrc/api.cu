@@ -21,6 +21,7 @@ struct DeviceState {
     cudaError_t init_error = cudaSuccess;
     bool supported = false;
     int sm_count = 0;
+    int verify_fits[kVerifyFits] = {};   // see setup_verify_drafts_kernel
     int *status = nullptr;         // device address of g_device_status
     cudaMemPool_t pool = nullptr;  // the library's own stream-ordered pool for scratch
 };
@@ -60,6 +61,8 @@ DeviceState *device_state(int *err) {
         d.init_error = setup_gdn_chunk_kernel();
         if (d.init_error != cudaSuccess) return;
         d.init_error = setup_draft_step_kernel();
+        if (d.init_error != cudaSuccess) return;
+        d.init_error = setup_verify_drafts_kernel(d.verify_fits);
     });
     if (d.init_error != cudaSuccess) {
         *err = SALA_ERR_CUDA;
@@ -636,7 +639,7 @@ int sala_gla_verify_drafts(const void *target_probs, int64_t target_stride, cons
     if (!d) return err;
     if (launch_verify_drafts(target_probs, target_stride, drafter ? draft_probs : nullptr, draft_stride, bf16,
                              draft_tokens, K > 0 ? num_drafts : nullptr, accept_u, sample_u, tokens,
-                             accepted, N, K, V, d->sm_count, d->status, static_cast<cudaStream_t>(stream)) !=
+                             accepted, N, K, V, d->sm_count, d->verify_fits, d->status, static_cast<cudaStream_t>(stream)) !=
         cudaSuccess)
         return SALA_ERR_CUDA;
     return SALA_OK;

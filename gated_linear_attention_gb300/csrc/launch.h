@@ -131,7 +131,10 @@ cudaError_t launch_verify_drafts(const void *p, int64_t p_stride, const void *q,
                                  bool bf16, const int32_t *x, const int32_t *num_drafts,
                                  const float *u, const float *s, int32_t *tokens,
                                  int32_t *accepted, int64_t N, int K, int64_t V, int sm_count,
-                                 int *status, cudaStream_t stream);
+                                 const int *fits, int *status, cudaStream_t stream);
+// fits[i]: clusters that run at once with at most i + 1 CTAs on an SM.
+constexpr int kVerifyFits = 6;
+cudaError_t setup_verify_drafts_kernel(int *fits);
 
 // Decode step over T drafted tokens on pooled states, after committing accepted[n] + 1 of the
 // T_pend tokens of the step before (T or T_pend may be 0).

@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "launch.h"
+#include "tc.cuh"
 
 namespace sala {
 
@@ -128,9 +129,9 @@ __device__ int first_rejected(const VerifyArgs &a, int64_t n, bool *rejected) {
 template <typename T>
 struct Weights {
     const T *p, *q;
-    int64_t one_at;
+    int one_at;
 
-    __device__ __forceinline__ long long at(int64_t x) const {
+    __device__ __forceinline__ long long at(int x) const {
         PartSum s;
         if (q) s.add(prob_load(p + x), prob_load(q + x));
         else if (x != one_at) s.add(prob_load(p + x));
@@ -138,16 +139,16 @@ struct Weights {
     }
 };
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
 // 16 bytes of probabilities
 template <typename T>
 struct Vec {
     static constexpr int kN = 16 / sizeof(T);
     uint4 w;
     __device__ __forceinline__ void load(const T *p) { w = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void keep(bool ok) {
-        const uint32_t m = ok ? ~0u : 0u;
-        w = make_uint4(w.x & m, w.y & m, w.z & m, w.w & m);
-    }
     __device__ __forceinline__ float at(int i) const {
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
         if constexpr (sizeof(T) == 4) return __uint_as_float(ws[i]);
@@ -156,52 +157,53 @@ struct Vec {
     }
 };
 
+// Loads run ahead of the sums through shared memory, kAhead vectors of p and of q per lane. Each
+// lane copies (cp.async) and reads its own slots, so no barrier is needed.
+constexpr int kAhead = 4;
+struct Ring {
+    uint4 v[2][kAhead][kVerifyThreads];   // p, q
+};
+
 // One lane's share of the sum over tokens [lo, hi), `lo` aligned for 16-byte loads of p and, with
 // kQ (subtract the drafter's row), of q.
 template <typename T, bool kQ>
-__device__ __forceinline__ long long sum_vectors(const Weights<T> &w, int64_t lo, int64_t hi, int lane) {
-    constexpr int kN = Vec<T>::kN, kAhead = 4;   // vectors of a lane in flight
+__device__ __forceinline__ long long sum_vectors(const Weights<T> &w, int lo, int hi, int lane, Ring &ring) {
+    constexpr int kN = Vec<T>::kN;
     long long sum = 0;
     const T *p = w.p + lo + lane * kN, *q = kQ ? w.q + lo + lane * kN : nullptr;
-    const int vectors = static_cast<int>((hi - lo) / kN);
-    auto add = [&](const Vec<T> (&x)[kAhead], const Vec<T> (&y)[kAhead]) {
-        PartSum s;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
-                if constexpr (kQ) s.add(x[i].at(e), y[i].at(e));
-                else s.add(x[i].at(e));
-            }
-        sum += s.units();
+    const int vectors = (hi - lo) / kN - lane;   // of this lane: 0, 32, 64, ..
+    uint4 *mine[2] = {&ring.v[0][0][threadIdx.x], &ring.v[1][0][threadIdx.x]};
+    auto load = [&](int v, int slot) {
+        const bool ok = v < vectors;   // zeros past the end
+        const int at = ok ? v * kN : 0;
+        cp_async16(mine[0] + slot * kVerifyThreads, p + at, ok);
+        if constexpr (kQ) cp_async16(mine[1] + slot * kVerifyThreads, q + at, ok);
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    Vec<T> x[kAhead], y[kAhead];
-    int v = 0;
-    for (; v + 32 * kAhead <= vectors; v += 32 * kAhead) {
+    if (vectors > 0) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            x[i].load(p + static_cast<int64_t>(v + 32 * i) * kN);
-            if constexpr (kQ) y[i].load(q + static_cast<int64_t>(v + 32 * i) * kN);
-        }
-        add(x, y);
-    }
-    if (v + lane < vectors) {
-        // the last round: a vector past the end is read from the lane's first place and dropped
+        for (int i = 0; i < kAhead; ++i) load(32 * i, i);
+        for (int v = 0; v < vectors; v += 32 * kAhead) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int64_t at = static_cast<int64_t>(v + 32 * i + lane < vectors ? v + 32 * i : v) * kN;
-            x[i].load(p + at);
-            if constexpr (kQ) y[i].load(q + at);
-        }
+            for (int i = 0; i < kAhead; ++i) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+                Vec<T> x, y;
+                x.w = mine[0][i * kVerifyThreads];
+                if constexpr (kQ) y.w = mine[1][i * kVerifyThreads];
+                load(v + 32 * (i + kAhead), i);
+                PartSum s;
 #pragma unroll
-        for (int i = 1; i < kAhead; ++i) {
-            x[i].keep(v + 32 * i + lane < vectors);
-            if constexpr (kQ) y[i].keep(v + 32 * i + lane < vectors);
+                for (int e = 0; e < kN; ++e) {
+                    if constexpr (kQ) s.add(x.at(e), y.at(e));
+                    else s.add(x.at(e));
+                }
+                sum += s.units();
+            }
         }
-        add(x, y);
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     // fewer than a vector's tokens, where the part ends the row
-    const int64_t rest = lo + static_cast<int64_t>(vectors) * kN + lane;
+    const int rest = lo + (hi - lo) / kN * kN + lane;
     if (rest < hi) {
         PartSum s;
         if constexpr (kQ) s.add(prob_load(w.p + rest), prob_load(w.q + rest));
@@ -213,18 +215,19 @@ __device__ __forceinline__ long long sum_vectors(const Weights<T> &w, int64_t lo
 
 // The sum of the weights of tokens [lo, hi) by one warp; every lane returns it.
 template <typename T>
-__device__ __forceinline__ long long sum_part(const Weights<T> &w, int64_t lo, int64_t hi, int lane) {
+__device__ __forceinline__ long long sum_part(const Weights<T> &w, int lo, int hi, int lane, Ring &ring) {
     long long sum = 0;
     const uintptr_t bp = reinterpret_cast<uintptr_t>(w.p), bq = reinterpret_cast<uintptr_t>(w.q);
     if (!w.q || ((bp ^ bq) & 15) == 0) {
         // tokens before the first aligned one (only where the part begins the row)
-        const int64_t start = min(hi, lo + static_cast<int64_t>((-(bp + lo * sizeof(T)) & 15) / sizeof(T)));
+        const int start = min(hi, lo + static_cast<int>((-(bp + lo * sizeof(T)) & 15) / sizeof(T)));
         PartSum s;
         if (lo + lane < start) {
             if (w.q) s.add(prob_load(w.p + lo + lane), prob_load(w.q + lo + lane));
             else s.add(prob_load(w.p + lo + lane));
         }
-        sum = s.units() + (w.q ? sum_vectors<T, true>(w, start, hi, lane) : sum_vectors<T, false>(w, start, hi, lane));
+        sum = s.units() + (w.q ? sum_vectors<T, true>(w, start, hi, lane, ring)
+                               : sum_vectors<T, false>(w, start, hi, lane, ring));
         // the certain token was summed with its whole probability
         if (lane == 0 && w.one_at >= lo && w.one_at < hi) {
             PartSum one;
@@ -233,7 +236,7 @@ __device__ __forceinline__ long long sum_part(const Weights<T> &w, int64_t lo, i
         }
     } else {
         // rows whose starts differ modulo 16 bytes: one token at a time, eight in flight
-        for (int64_t x = lo + lane; x - lane < hi; x += 8 * 32) {
+        for (int x = lo + lane; x - lane < hi; x += 8 * 32) {
             float p[8], q[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -269,6 +272,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int64_t n = blockIdx.x / ranks;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ Ring ring;
     __shared__ int first_s, rejected_s;
     __shared__ long long mine[2][kVerifyWarps];                   // this CTA's sums, one row a pass
     __shared__ long long all[kMaxCluster * kVerifyWarps];         // the cluster's
@@ -293,14 +297,14 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
     // parts: from the second on they begin at 16-byte boundaries of the target's row
     constexpr int kN = Vec<T>::kN;
     const int parts = ranks * kVerifyWarps;
-    const int64_t head = (-reinterpret_cast<uintptr_t>(w.p) & 15) / sizeof(T);
-    const int64_t len = (a.V / kN + parts) / parts * kN;
-    auto part_begin = [&](int i) { return i == 0 ? 0 : min(a.V, head + len * i); };
+    const int V = static_cast<int>(a.V), head = static_cast<int>((-reinterpret_cast<uintptr_t>(w.p) & 15) / sizeof(T));
+    const int len = (V / kN + parts) / parts * kN;
+    auto part_begin = [&](int i) { return i == 0 ? 0 : min(V, head + len * i); };
 
     long long total = 0;
     for (int pass = 0; pass < 2; ++pass) {
         const int i = rank * kVerifyWarps + warp;
-        const long long sum = sum_part(w, part_begin(i), part_begin(i + 1), lane);
+        const long long sum = sum_part(w, part_begin(i), part_begin(i + 1), lane, ring);
         if (lane == 0) mine[pass][warp] = sum;
         cluster.sync();
         if (threadIdx.x < parts)
@@ -345,24 +349,43 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
             before = __shfl_sync(0xffffffffu, c, 31);
         }
         if (part / kVerifyWarps == rank) {
-            // each thread sums consecutive tokens of the part, then the one that passes `at` looks
-            // for its token
-            const int64_t lo = part_begin(part), hi = part_begin(part + 1);
-            const int64_t per = (hi - lo + kVerifyThreads - 1) / kVerifyThreads;
-            const int64_t x0 = min(hi, lo + per * threadIdx.x), x1 = min(hi, x0 + per);
+            // each thread sums consecutive vectors of the part (the first thread also what lies before
+            // the first whole one), then the one that passes `at` looks for its token
+            const int lo = part_begin(part), hi = part_begin(part + 1);
+            const int start = part == 0 ? min(hi, head) : lo;
+            const int per = ((hi - start + kN - 1) / kN + kVerifyThreads - 1) / kVerifyThreads * kN;
+            const int tid = threadIdx.x, x0 = tid == 0 ? lo : min(hi, start + per * tid);
+            const int x1 = min(hi, start + per * (tid + 1));
+            const bool wide = !w.q || ((reinterpret_cast<uintptr_t>(w.p) ^ reinterpret_cast<uintptr_t>(w.q)) & 15) == 0;
             long long sum = 0;
+            int x = x0;
+            if (wide) {
+                for (; x < min(start, x1); ++x) sum += w.at(x);
+                for (; x + kN <= x1; x += kN) {
+                    Vec<T> p, q;
+                    p.load(w.p + x);
+                    if (w.q) q.load(w.q + x);
+                    PartSum s;
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) {
+                        if (w.q) s.add(p.at(e), q.at(e));
+                        else s.add(x + e == w.one_at ? 0.f : p.at(e));
+                    }
+                    sum += s.units();
+                }
+            }
 #pragma unroll 8
-            for (int64_t x = x0; x < x1; ++x) sum += w.at(x);
+            for (; x < x1; ++x) sum += w.at(x);
             const long long c = warp_prefix(sum, lane);
             if (lane == 31) scan[warp] = c;
             __syncthreads();
             long long run = before + c - sum;
             for (int i = 0; i < warp; ++i) run += scan[i];
             if (run <= at && at < run + sum) {
-                for (int64_t x = x0; x < x1; ++x) {
+                for (x = x0; x < x1; ++x) {
                     run += w.at(x);
                     if (run > at) {
-                        out[first] = static_cast<int32_t>(x);
+                        out[first] = x;
                         break;
                     }
                 }
@@ -382,18 +405,57 @@ int cluster_size(int64_t N, int sm_count) {
     return c;
 }
 
+// Shared memory asked for beyond a CTA's own so that at most `per_sm` of them share an SM.
+constexpr size_t kSmSmem = 227 * 1024, kStaticSmem = sizeof(Ring) + 2048;
+size_t room_for(int per_sm) { return kSmSmem / per_sm - kStaticSmem; }
+static_assert(kSmSmem / kVerifyFits >= kStaticSmem, "a CTA's own memory fits so often");
+
+// A cluster's CTAs are packed onto as few SMs as hold them, so a small launch would leave most SMs
+// idle: it asks for the most memory per CTA with which all its clusters still run at once (32 rows of
+// 131072 fp32: 16.5 us packed, 11.3 us spread).
+size_t spread(int64_t N, int c, const int *fits) {
+    for (int i = 0; c == kMaxCluster && i < kVerifyFits; ++i)
+        if (N <= fits[i]) return room_for(i + 1);
+    return 0;
+}
+
 }  // namespace
+
+cudaError_t setup_verify_drafts_kernel(int *fits) {
+    void (*kernels[2])(VerifyArgs) = {verify_drafts_kernel<float>, verify_drafts_kernel<uint16_t>};
+    for (auto kern : kernels) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(room_for(1)));
+        if (e != cudaSuccess) return e;
+    }
+    for (int i = 0; i < kVerifyFits; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kMaxCluster);
+        cfg.blockDim = dim3(kVerifyThreads);
+        cfg.dynamicSmemBytes = room_for(i + 1);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kMaxCluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&fits[i], verify_drafts_kernel<float>, &cfg);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
 
 cudaError_t launch_verify_drafts(const void *p, int64_t p_stride, const void *q, int64_t q_stride,
                                  bool bf16, const int32_t *x, const int32_t *num_drafts,
                                  const float *u, const float *s, int32_t *tokens,
                                  int32_t *accepted, int64_t N, int K, int64_t V, int sm_count,
-                                 int *status, cudaStream_t stream) {
+                                 const int *fits, int *status, cudaStream_t stream) {
     LaunchTimer timer(kKVerifyDrafts, stream);
     const int c = cluster_size(N, sm_count);
+    const size_t room = spread(N, c, fits);
     const VerifyArgs a{p, q, p_stride, q_stride, x, num_drafts, u, s, tokens, accepted, K, V, status};
     return launch_dependent_cluster(bf16 ? verify_drafts_kernel<uint16_t> : verify_drafts_kernel<float>,
-                                    static_cast<unsigned>(N * c), c, kVerifyThreads, 0, stream, a);
+                                    static_cast<unsigned>(N * c), c, kVerifyThreads, room, stream, a);
 }
 
 }  // namespace sala
