@@ -654,7 +654,7 @@ int sala_gla_recurrent_draft_step(const void *q, const void *k, const void *v, c
     if (N < 0 || T < 0 || T_pend < 0 || H < 1 || P < 1) return SALA_ERR_INVALID_ARG;
     if (state_dtype != SALA_STATE_F32 && state_dtype != SALA_STATE_BF16) return SALA_ERR_INVALID_ARG;
     if (N == 0 || (T == 0 && T_pend == 0)) return SALA_OK;
-    if (N > (kMaxRows - 1) / 2 / H || P > kMaxUnits / H || P > kMaxRows || T > kMaxRows / N ||
+    if (N > (kMaxRows - 1) / 2 / H || P > (kMaxRows - 1) / H || T > kMaxRows / N ||
         T_pend > kMaxRows / N)
         return SALA_ERR_INVALID_ARG;
     if (!state_pool || !state_indices) return SALA_ERR_INVALID_ARG;

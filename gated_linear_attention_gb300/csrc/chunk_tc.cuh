@@ -101,6 +101,12 @@ struct TcMaps {
     CUtensorMap o;         // stores: box 32 x 1 x 64, no swizzle or (o_sw64) 64-byte swizzle
 };
 
+// host: tensor map of a tensor in device memory (innermost dimension contiguous, strides in bytes of
+// the others; zeros outside)
+cudaError_t encode_tiled(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base,
+                         const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                         CUtensorMapSwizzle swizzle);
+
 // host: 3-D tensor maps over q, k, v and o viewed as [T_total, H, 128] bf16
 cudaError_t make_maps(TcMaps *m, const void *q, const void *k, const void *v, const void *o,
                       int64_t T_total, int H, bool o_sw64 = false);

@@ -12,9 +12,9 @@
 // of minus infinity (forget everything) gives exact zeros.
 //
 // Steps of up to 16 new and 16 pending tokens (draft_step_kernel): one persistent CTA per SM. An
-// item of work is one (sequence, head, half of the value columns). Two producer warps stage items
-// ahead of use in a ring of shared-memory stages (cp.async); each of the groups of 4 consumer warps
-// takes every kGroups-th item. The two products with the state run on the tensor cores as
+// item of work is one (sequence, head, half of the value columns). A producer warp stages items ahead
+// of use in a ring of shared-memory stages (TMA); each of the groups of 4 consumer warps takes every
+// kGroups-th item and sends the state back from its stage (TMA). The two products with the state run on the tensor cores as
 // mma.m16n8k16, 16 (or 8) being the tokens:
 //     commit   D[16 dv x 8 dk] = (w V)^T K     with w_j v_j in fp32 split into three bf16 parts
 //     read     O[16 t x 8 dv]  = Q S           with S in bf16
@@ -22,13 +22,13 @@
 // state in shared memory, 16 key rows at a time, feeds both. An fp32 state is read after the
 // commit, split into two bf16 parts. A bf16 state is read as it was stored, an operand without any
 // arithmetic, and what the commit adds to it enters as the pending tokens' own term (Q K^T w) V.
-// A token that is not there (past the counts) is zero in shared memory; the products among the new
-// tokens are taken in fp32 over j <= t only, so nothing of a masked place reaches a result.
+// Places past the counts hold anything: pending tokens there are masked out of every operand, and the
+// products among the new tokens are taken in fp32 over j <= t only, so nothing of a masked place
+// reaches a result.
 // Longer steps (draft_step_long_kernel) run the plain form below.
 #include <type_traits>
 
-#include "launch.h"
-#include "tc.cuh"
+#include "chunk_tc.cuh"
 
 namespace sala {
 
@@ -72,29 +72,35 @@ __device__ __forceinline__ Row read_row(const DraftArgs &a, int n, bool report) 
 
 constexpr int kHalf = kD / 2;         // value columns of an item
 constexpr int kGroupThreads = 128;    // warp w: columns [32 (w % 2), + 32) of the half, key rows [64 (w / 2), + 64)
-constexpr int kLoaders = 128;          // threads of the producer warps
-constexpr uint64_t kWaitNs = 2000000000ull;   // limit of every wait
+constexpr int kOctBytes = 8 * 128;     // 8 tokens x 64 columns: a copy takes 8 tokens, of both halves of the columns or of one
 
-// Shared memory (offsets in bytes). Rows are cut into 16-byte chunks whose places are permuted by the
-// row so that the 8 rows of a matrix fragment (and the 4 even or odd state rows that a quarter-warp
-// reads) fall into different banks. kTok: tokens of an operand, 8 or 16.
 struct Item {
     int32_t slot, n, h, half, commits, tokens, pad[2];
 };
+
+// Shared memory (offsets in bytes). Every tile has rows of 128 bytes as TMA lays them out with 128-byte
+// swizzle: the 16-byte chunk c of row r is at place c ^ (r % 8), so that the 8 rows of a matrix
+// fragment, and the even or odd state rows that a quarter-warp reads, fall into different banks.
+// kTok: tokens of an operand, 8 or 16.
 template <bool kBf16, int kTok>
 struct StepSmem {
     // a stage
-    static constexpr int kStateRow = kHalf * (kBf16 ? 2 : 4);
+    static constexpr int kBoxCols = kBf16 ? 64 : 32;         // state columns of a tile
+    static constexpr int kBoxes = kHalf / kBoxCols;
+    static constexpr int kStateTile = kD * 128;
     static constexpr int kState = 0;
-    static constexpr int kPk = kState + kD * kStateRow;      // [kTok][128] bf16
-    static constexpr int kQ = kPk + kTok * kD * 2;
-    static constexpr int kK = kQ + kTok * kD * 2;
-    static constexpr int kPv = kK + kTok * kD * 2;           // [kTok][64] bf16
-    static constexpr int kV = kPv + kTok * kHalf * 2;
-    static constexpr int kPg = kV + kTok * kHalf * 2;        // [kTok] fp32
+    static constexpr int kPk = kState + kBoxes * kStateTile; // keys and queries: [kTok / 8][8 tokens][2 halves][64]
+    static constexpr int kQ = kPk + kTok / 8 * 2 * kOctBytes;
+    static constexpr int kK = kQ + kTok / 8 * 2 * kOctBytes;
+    static constexpr int kPv = kK + kTok / 8 * 2 * kOctBytes;   // values of the item's half: [kTok][64]
+    static constexpr int kV = kPv + kTok / 8 * kOctBytes;
+    static constexpr int kStage = kV + kTok / 8 * kOctBytes;
+    static_assert(kStage % 1024 == 0, "tiles begin with their swizzle");
+    // beside each stage
+    static constexpr int kPg = 0;                            // [kTok] fp32
     static constexpr int kG = kPg + kTok * 4;
     static constexpr int kHead = kG + kTok * 4;              // struct Item
-    static constexpr int kStage = (kHead + 32 + 255) / 256 * 256;
+    static constexpr int kSide = kHead + 32;
     // a group's own
     static constexpr int kScore = 0;                         // [kTok][kTok] fp32: q_t . k_j
     static constexpr int kPend = kScore + kTok * kTok * 4;   // [kTok][kTok] fp32: q_t . pk_j
@@ -103,30 +109,42 @@ struct StepSmem {
     static constexpr int kOwn = kSwap + 4 * kTok / 2 * 32 * 4;
     // groups as far as registers go, stages as far as memory goes
     static constexpr int kGroups = kBf16 ? 4 : 3;
-    static constexpr int kStages = (232448 - 1024 - kGroups * kOwn) / kStage;
-    static constexpr int kBytes = kStages * kStage + kGroups * kOwn;
-    static constexpr int kThreads = kGroups * kGroupThreads + kLoaders;
+    static constexpr int kStages = (232448 - 1024 - kGroups * kOwn) / (kStage + kSide);
+    // "Full" barriers: a multiple of the groups, so that a barrier's phases are all one group's. Were they
+    // as many as the stages, the phases of one would go round the groups, and a group could ask for phase
+    // p + 1 before phase p of another group had come, which the parity cannot tell from its end.
+    static constexpr int kFulls = (kStages + kGroups - 1) / kGroups * kGroups;
+    static constexpr int kSides = kStages * kStage;
+    static constexpr int kOwns = kSides + kStages * kSide;
+    static constexpr int kBytes = kOwns + kGroups * kOwn;
+    static constexpr int kThreads = kGroups * kGroupThreads + 32;
     static_assert(kStages > kGroups, "the loads run ahead");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+// pool [P * H, 128, 128]: boxes of one state's 128 rows x 128 bytes; tokens [N, T, H, 2, 64]: boxes of
+// 8 tokens of one head (zeros past T), all columns of keys and queries, half of them of values. (A
+// copy costs the copy engine about 90 ns whatever its size: boxes of 4 tokens x 64 columns bounded
+// 256 bf16 rows of 5 tokens by their number, at 159 us.)
+struct StepMaps {
+    CUtensorMap pool, pk, pv, q, k, v;
+};
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 // This thread's copies so far count as one arrival on `bar` once they have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void group_sync(int group) {
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kGroupThreads) : "memory");
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
+                                            int32_t c3, int32_t c4, uint64_t *bar) {
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1),
+                 "r"(c2), "r"(c3), "r"(c4), "r"(tc::smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ bool group_any(int group, bool p) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(static_cast<uint32_t>(p)), "r"(group + 1), "n"(kGroupThreads) : "memory");
-    return r != 0;
+__device__ __forceinline__ void group_sync(int group) {
+    __syncwarp();
+    tck::named_sync(group + 9, kGroupThreads);
 }
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -192,24 +210,12 @@ __device__ __forceinline__ void sts_f32(uint32_t addr, float x) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
 
-// Chunk c of row r: rows of 16 chunks (tokens' 128 keys), rows of 8 chunks (64 values in bf16).
-__device__ __forceinline__ uint32_t chunk256(int r, int c) { return r * 256 + ((c ^ (r & 7)) << 4); }
-__device__ __forceinline__ uint32_t chunk128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
-// fp32 state half: rows of 16 chunks.
-__device__ __forceinline__ uint32_t chunk_f32(int r, int c) { return r * 256 + ((c ^ (((r >> 1) & 3) << 1)) << 4); }
-
-// kTok token rows of [tokens, H, 128] bf16 (kWide: all of a row, else 64 values), zeros past `count`.
-template <int kTok, bool kWide>
-__device__ __forceinline__ void stage_tokens(uint32_t dst, const uint16_t *src, int64_t row0, int H, int count, int lane) {
-    constexpr int kChunks = kWide ? 16 : 8;
-#pragma unroll
-    for (int i = 0; i < (kTok * kChunks + kLoaders - 1) / kLoaders; ++i) {
-        const int e = lane + i * kLoaders, t = e / kChunks, c = e % kChunks;
-        if (kTok * kChunks % kLoaders && e >= kTok * kChunks) break;
-        const bool ok = t < count;
-        const uint16_t *p = src + (row0 + (ok ? static_cast<int64_t>(t) * H : 0)) * kD + 8 * c;
-        cp_async16(dst + (kWide ? chunk256(t, c) : chunk128(t, c)), p, ok);
-    }
+// Chunk c of row r of a tile.
+__device__ __forceinline__ uint32_t chunk(int r, int c) { return tck::sw(r, c); }
+// Chunk c of column half `half` of token t's keys or queries. (Token rows are two rows apart, so the 8
+// rows of a fragment meet in pairs in the banks; that is a tenth of an item's shared-memory reads.)
+__device__ __forceinline__ uint32_t wide_chunk(int t, int half, int c) {
+    return (t >> 3) * 2 * kOctBytes + tck::sw(2 * (t & 7) + half, c);
 }
 
 // Lane t holds exp(g_1 + .. + g_t) (head) and exp(g_{t+1} + .. + g_count) (tail) of kTok gates, 0 past the count.
@@ -219,7 +225,7 @@ struct Gates {
 template <int kTok>
 __device__ __forceinline__ Gates gate_scan(const uint8_t *at, int count, int lane) {
     Gates s;
-    s.g = lane < kTok ? reinterpret_cast<const float *>(at)[lane] : 0.f;   // zeros past the count
+    s.g = lane < kTok && lane < count ? reinterpret_cast<const float *>(at)[lane] : 0.f;
     float pre = s.g, suf = s.g;
 #pragma unroll
     for (int off = 1; off < kTok; off <<= 1) {
@@ -242,41 +248,43 @@ __device__ __forceinline__ uint32_t split_bf16(float &x0, float &x1) {
     return w;
 }
 
+// Queues an item's copies into its stage (by a whole warp). The barrier takes one arrival of every
+// lane, one of lane 0 for the item itself and the bytes of the tiles.
 template <bool kBf16, int kTok>
-__device__ __forceinline__ void stage_item(const DraftArgs &a, uint32_t st, const Item &it, int lane) {
+__device__ __forceinline__ void stage_item(const DraftArgs &a, const StepMaps &maps, uint8_t *smem, uint8_t *side, const Item &it,
+                                           uint64_t *bar, int lane) {
     using Sm = StepSmem<kBf16, kTok>;
-    const int64_t n = it.n;
     const int h = it.h, half = it.half, commits = it.commits, tokens = it.tokens;
-    if (commits == 0 && tokens == 0) return;
-    const int64_t at = (static_cast<int64_t>(it.slot) * a.H + h) * kD * kD + half * kHalf;
-    constexpr int kChunks = Sm::kStateRow / 16;   // of a state row
-#pragma unroll 8
-    for (int i = 0; i < kD * kChunks / kLoaders; ++i) {
-        const int e = lane + i * kLoaders, r = e / kChunks, c = e % kChunks;
-        if constexpr (kBf16)
-            cp_async16(st + Sm::kState + chunk128(r, c), static_cast<const uint16_t *>(a.pool) + at + r * kD + 8 * c, true);
-        else
-            cp_async16(st + Sm::kState + chunk_f32(r, c), static_cast<const float *>(a.pool) + at + r * kD + 4 * c, true);
+    const int states = commits || tokens ? Sm::kBoxes : 0;
+    const int pend = (commits + 7) / 8, fresh = (tokens + 7) / 8;
+    if (lane == 0) {
+        *reinterpret_cast<Item *>(side + Sm::kHead) = it;
+        tc::mbar_arrive_expect_tx(bar, states * Sm::kStateTile + (3 * pend + 5 * fresh) * kOctBytes);
     }
-    const int64_t pend0 = n * a.T_pend * a.H + h, new0 = n * a.T * a.H + h;   // token rows of this head
-    if (commits) {
-        stage_tokens<kTok, true>(st + Sm::kPk, a.pk, pend0, a.H, commits, lane);
-        stage_tokens<kTok, false>(st + Sm::kPv, a.pv + half * kHalf, pend0, a.H, commits, lane);
-        if (lane < kTok)
-            cp_async4(st + Sm::kPg + 4 * lane, a.pg + pend0 + (lane < commits ? static_cast<int64_t>(lane) * a.H : 0), lane < commits);
+    __syncwarp();
+    if (lane < states)
+        tc::tma_load_3d(smem + Sm::kState + lane * Sm::kStateTile, &maps.pool, half * kHalf + lane * Sm::kBoxCols, 0,
+                        static_cast<int32_t>(static_cast<int64_t>(it.slot) * a.H + h), bar);
+    // lanes 4 to 13: 8 tokens each of the pending keys and values and the new queries, keys and values
+    const int i = lane - 4, kind = i >> 1, oct = i & 1;
+    if (i >= 0 && kind < 5 && oct < (kind < 2 ? pend : fresh)) {
+        const CUtensorMap *map = kind == 0 ? &maps.pk : kind == 1 ? &maps.pv : kind == 2 ? &maps.q : kind == 3 ? &maps.k : &maps.v;
+        const bool values = kind == 1 || kind == 4;
+        const int at = (kind == 0 ? Sm::kPk : kind == 1 ? Sm::kPv : kind == 2 ? Sm::kQ : kind == 3 ? Sm::kK : Sm::kV) +
+                       oct * (values ? 1 : 2) * kOctBytes;
+        tma_load_5d(tc::smem_u32(smem + at), map, 0, values ? half : 0, h, 8 * oct, it.n, bar);
     }
-    if (tokens) {
-        stage_tokens<kTok, true>(st + Sm::kQ, a.q, new0, a.H, tokens, lane);
-        stage_tokens<kTok, true>(st + Sm::kK, a.k, new0, a.H, tokens, lane);
-        stage_tokens<kTok, false>(st + Sm::kV, a.v + half * kHalf, new0, a.H, tokens, lane);
-        if (lane < kTok)
-            cp_async4(st + Sm::kG + 4 * lane, a.g + new0 + (lane < tokens ? static_cast<int64_t>(lane) * a.H : 0), lane < tokens);
-    }
+    const int64_t pend0 = it.n * a.T_pend * a.H + h, new0 = it.n * a.T * a.H + h;   // token rows of this head
+    if (lane < commits) cp_async4(tc::smem_u32(side + Sm::kPg) + 4 * lane, a.pg + pend0 + static_cast<int64_t>(lane) * a.H);
+    if (lane < tokens) cp_async4(tc::smem_u32(side + Sm::kG) + 4 * lane, a.g + new0 + static_cast<int64_t>(lane) * a.H);
+    cp_async_arrive(bar);
 }
 
-// One item by a group of 4 warps, from its stage `smem` (address `st`); `own`: the group's memory.
+// One item by a group of 4 warps, from its stage `smem` and what stands beside it; `own`: the group's
+// memory. Thread 0 of the group leaves a store of the state in flight that still reads the stage.
 template <bool kBf16, int kTok>
-__device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint32_t st, uint8_t *own, const Item &it, int group) {
+__device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &maps, uint8_t *smem, const uint8_t *side, uint8_t *own,
+                                         const Item &it, int group) {
     using Sm = StepSmem<kBf16, kTok>;
     constexpr int kParts = 3;   // of w_j v_j in fp32: what three bf16 parts leave out is below 2^-26 of it
     constexpr int kOct = kTok / 8;
@@ -285,10 +293,10 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint
     const int gr = lane >> 2, tq = lane & 3;      // row and column pair of a lane in a fragment
     const int mi = lane >> 3, mr = lane & 7;      // matrix and row whose address a lane gives
     const int commits = it.commits, tokens = it.tokens;
-    const uint32_t own_at = tc::smem_u32(own);
+    const uint32_t st = tc::smem_u32(smem), own_at = tc::smem_u32(own);
     Gates pg{0.f, 0.f, 0.f}, ng{0.f, 0.f, 0.f};
-    if (commits) pg = gate_scan<kTok>(smem + Sm::kPg, commits, lane);
-    if (tokens) ng = gate_scan<kTok>(smem + Sm::kG, tokens, lane);
+    if (commits) pg = gate_scan<kTok>(side + Sm::kPg, commits, lane);
+    if (tokens) ng = gate_scan<kTok>(side + Sm::kG, tokens, lane);
 
     // 1. products of the new tokens' queries with 8 keys at a time, one warp each: with the new tokens
     // (first warps), with the pending ones (next warps); decays by warp 3
@@ -298,18 +306,19 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint
         float d[4] = {0.f, 0.f, 0.f, 0.f};
         const uint32_t keys = st + (pending ? Sm::kPk : Sm::kK);
 #pragma unroll
-        for (int c = 0; c < 8; c += 2) {
+        for (int c = 0; c < 8; c += 2) {   // 32 columns: chunks 2 c .. 2 c + 3, of half c / 4
             uint32_t qa[4], qb[4], kb[4];
+            const int cols = c / 4, first = 2 * (c & 3);
             if constexpr (kTok == 16) {
-                ldmatrix_x4(qa, st + Sm::kQ + chunk256(mr + 8 * (mi & 1), 2 * c + (mi >> 1)));
-                ldmatrix_x4(qb, st + Sm::kQ + chunk256(mr + 8 * (mi & 1), 2 * c + 2 + (mi >> 1)));
+                ldmatrix_x4(qa, st + Sm::kQ + wide_chunk(mr + 8 * (mi & 1), cols, first + (mi >> 1)));
+                ldmatrix_x4(qb, st + Sm::kQ + wide_chunk(mr + 8 * (mi & 1), cols, first + 2 + (mi >> 1)));
             } else {
                 uint32_t q4[4];
-                ldmatrix_x4(q4, st + Sm::kQ + chunk256(mr, 2 * c + mi));
+                ldmatrix_x4(q4, st + Sm::kQ + wide_chunk(mr, cols, first + mi));
                 qa[0] = q4[0], qa[2] = q4[1], qb[0] = q4[2], qb[2] = q4[3];
                 qa[1] = qa[3] = qb[1] = qb[3] = 0u;
             }
-            ldmatrix_x4(kb, keys + chunk256(mr + 8 * oct, 2 * c + mi));
+            ldmatrix_x4(kb, keys + wide_chunk(mr + 8 * oct, cols, first + mi));
             mma(d, qa, kb[0], kb[1]);
             mma(d, qb, kb[2], kb[3]);
         }
@@ -333,13 +342,17 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint
     const float fade = commits ? __shfl_sync(0xffffffffu, pg.head, commits - 1) : 1.f;
     // the lane's columns 4 gr .. + 3 of pending token t's values
     auto pend_values = [&](int t) {
-        return lds_u32x2(st + Sm::kPv + chunk128(t, 4 * col + (gr >> 1)) + (gr & 1) * 8);
+        return lds_u32x2(st + Sm::kPv + chunk(t, 4 * col + (gr >> 1)) + (gr & 1) * 8);
     };
+    uint32_t there[kOct];   // mask of the pending tokens 2 tq + 8 i, + 1 of a packed pair
     if (commits) {
 #pragma unroll
         for (int i = 0; i < kOct; ++i) {   // tokens 2 tq + 8 i, + 1
             const int t = 2 * tq + 8 * i;
-            const uint2 a0 = pend_values(t), a1 = pend_values(t + 1);
+            uint2 a0 = pend_values(t), a1 = pend_values(t + 1);
+            if (t >= commits) a0 = make_uint2(0u, 0u);
+            if (t + 1 >= commits) a1 = make_uint2(0u, 0u);
+            there[i] = (t < commits ? 0xffffu : 0u) | (t + 1 < commits ? 0xffff0000u : 0u);
             const float w0 = __shfl_sync(0xffffffffu, pg.tail, t), w1 = __shfl_sync(0xffffffffu, pg.tail, t + 1);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
@@ -356,21 +369,19 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint
     float o[4][4] = {};   // tile j: rows gr, gr + 8; columns 8 tq + j, 8 tq + 4 + j
     // the lane's first state row (even) and the next one, and its rows of the token operands; 16 key
     // rows on, the places of the state repeat and those of the tokens differ by an exclusive or
-    const uint32_t st0 = st + Sm::kState + (kBf16 ? chunk128(64 * rows + 2 * tq, 4 * col + (gr >> 1)) + (gr & 1) * 8
-                                                  : chunk_f32(64 * rows + 2 * tq, 8 * col + gr));
-    const uint32_t st1 = st + Sm::kState + (kBf16 ? chunk128(64 * rows + 2 * tq + 1, 4 * col + (gr >> 1)) + (gr & 1) * 8
-                                                  : chunk_f32(64 * rows + 2 * tq + 1, 8 * col + gr));
-    const uint32_t frag = kTok == 16 ? (mr + 8 * (mi & 1)) * 256 + (((mi >> 1) ^ mr) << 4)
-                                     : mr * 256 + (((mi & 1) ^ mr) << 4);
+    const uint32_t tile = st + Sm::kState + (kBf16 ? 0 : col * Sm::kStateTile), odd = kBf16 ? (gr & 1) * 8 : 0;
+    const int at_chunk = kBf16 ? 4 * col + (gr >> 1) : gr;
+    const uint32_t st0 = tile + chunk(64 * rows + 2 * tq, at_chunk) + odd, st1 = tile + chunk(64 * rows + 2 * tq + 1, at_chunk) + odd;
+    const uint32_t frag = kTok == 16 ? wide_chunk(mr + 8 * (mi & 1), rows, mi >> 1) : wide_chunk(mr, rows, mi & 1);
 #pragma unroll
     for (int ci = 0; ci < 4; ++ci) {
-        const uint32_t tok_at = frag ^ ((4 * rows + ci) << 5);
+        const uint32_t tok_at = frag ^ (ci << 5);
         float x[2][2][4];      // rows 8 i + 2 tq + e, column j
         uint32_t hi[2][4];     // the same as B operands: rows 8 i + 2 tq, + 1 of column j
         [[maybe_unused]] uint32_t lo[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint32_t at_row = (16 * ci + 8 * i) * Sm::kStateRow;
+            const uint32_t at_row = (16 * ci + 8 * i) * 128;
             if constexpr (kBf16) {
                 const uint2 w0 = lds_u32x2(st0 + at_row), w1 = lds_u32x2(st1 + at_row);
 #pragma unroll
@@ -399,6 +410,10 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint
                 kb[0][1] = kb[1][1] = 0u;
             }
 #pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < kOct; ++e) kb[i][e] &= there[e];
+#pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
@@ -417,7 +432,7 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint32_t at_row = (e ? st1 : st0) + (16 * ci + 8 * i) * Sm::kStateRow;
+                    const uint32_t at_row = (e ? st1 : st0) + (16 * ci + 8 * i) * 128;
                     const float *y = x[i][e];
                     if constexpr (kBf16) sts_u32x2(at_row, float2_to_bf16x2(y[0], y[1]), float2_to_bf16x2(y[2], y[3]));
                     else sts_f32x4(at_row, y[0], y[1], y[2], y[3]);
@@ -459,21 +474,15 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint
             if constexpr (kTok == 16) swap[(warp * 8 + 4 + j) * 32 + lane] = rows ? o[j][2] : o[j][3];
         }
     }
+    if (commits) tc::fence_proxy_async_smem();
     group_sync(group);
 
     // 3. the state goes back
-    if (commits) {
-        const int64_t at = (static_cast<int64_t>(it.slot) * a.H + it.h) * kD * kD + it.half * kHalf;
-        constexpr int kChunks = Sm::kStateRow / 16;
-#pragma unroll 8
-        for (int i = 0; i < kD * kChunks / kGroupThreads; ++i) {
-            const int e = tid + i * kGroupThreads, r = e / kChunks, c = e % kChunks;
-            const uint4 w = *reinterpret_cast<const uint4 *>(smem + Sm::kState + (kBf16 ? chunk128(r, c) : chunk_f32(r, c)));
-            if constexpr (kBf16)
-                __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.pool) + at + r * kD + 8 * c), w);
-            else
-                __stcs(reinterpret_cast<uint4 *>(static_cast<float *>(a.pool) + at + r * kD + 4 * c), w);
-        }
+    if (commits && tid == 0) {
+        for (int b = 0; b < Sm::kBoxes; ++b)
+            tc::tma_store_3d(&maps.pool, it.half * kHalf + b * Sm::kBoxCols, 0,
+                             static_cast<int32_t>(static_cast<int64_t>(it.slot) * a.H + it.h), smem + Sm::kState + b * Sm::kStateTile);
+        tc::tma_store_commit();
     }
 
     // 4. o_t = scale ( head_t (Q S)_t + sum_{j <= t} decay_tj score_tj v_j ), rows gr, gr + 8; bf16: with
@@ -499,18 +508,18 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint
                 const float w0 = __shfl_sync(0xffffffffu, pg.tail, t), w1 = __shfl_sync(0xffffffffu, pg.tail, t + 1);
                 float2 s0 = lds_f32x2(pend + 32 * i), s1 = lds_f32x2(pend + 32 * i + (kTok == 16 ? 8 * kTok * 4 : 0));
                 if (kTok == 8) s1 = make_float2(0.f, 0.f);
-                if (8 * i >= commits) s0 = s1 = make_float2(0.f, 0.f);   // was not computed
-                s0.x *= w0, s0.y *= w1, s1.x *= w0, s1.y *= w1;
+                s0.x = t < commits ? s0.x * w0 : 0.f, s1.x = t < commits ? s1.x * w0 : 0.f;
+                s0.y = t + 1 < commits ? s0.y * w1 : 0.f, s1.y = t + 1 < commits ? s1.y * w1 : 0.f;
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     pa[p][2 * i] = split_bf16(s0.x, s0.y);
                     pa[p][2 * i + 1] = split_bf16(s1.x, s1.y);
                 }
                 const uint2 a0 = pend_values(t), a1 = pend_values(t + 1);
-                bv[0][i] = __byte_perm(a0.x, a1.x, 0x5410);
-                bv[1][i] = __byte_perm(a0.x, a1.x, 0x7632);
-                bv[2][i] = __byte_perm(a0.y, a1.y, 0x5410);
-                bv[3][i] = __byte_perm(a0.y, a1.y, 0x7632);
+                bv[0][i] = __byte_perm(a0.x, a1.x, 0x5410) & there[i];
+                bv[1][i] = __byte_perm(a0.x, a1.x, 0x7632) & there[i];
+                bv[2][i] = __byte_perm(a0.y, a1.y, 0x5410) & there[i];
+                bv[3][i] = __byte_perm(a0.y, a1.y, 0x7632) & there[i];
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -527,7 +536,7 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint
             if constexpr (kTok == 16) y1[j] *= h1;
         }
         for (int j = 0; j < tokens; ++j) {
-            const uint2 w = lds_u32x2(st + Sm::kV + chunk128(j, first / 8) + rows * 8);
+            const uint2 w = lds_u32x2(st + Sm::kV + chunk(j, first / 8) + rows * 8);
             const float2 v0 = bf16x2_to_float2(w.x), v1 = bf16x2_to_float2(w.y);
             if (j <= gr) {
                 const float s = score[gr * kTok + j] * decay[gr * kTok + j];
@@ -560,25 +569,26 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, uint8_t *smem, uint
 }
 
 template <bool kBf16, int kTok>
-__global__ void __launch_bounds__(StepSmem<kBf16, kTok>::kThreads, 1) draft_step_kernel(DraftArgs a, unsigned items) {
+__global__ void __launch_bounds__(StepSmem<kBf16, kTok>::kThreads, 1) 
+draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned items) {
     using Sm = StepSmem<kBf16, kTok>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ uint64_t full[Sm::kStages], empty[Sm::kStages];
+    __shared__ uint64_t full[Sm::kFulls], empty[Sm::kStages];
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Sm::kStages; ++s) {
-            tc::mbar_init(&full[s], kLoaders + 1);
-            tc::mbar_init(&empty[s], kGroupThreads / 32);
-        }
+        for (int s = 0; s < Sm::kFulls; ++s) tc::mbar_init(&full[s], 32 + 1);
+        for (int s = 0; s < Sm::kStages; ++s) tc::mbar_init(&empty[s], kGroupThreads / 32);
         tc::fence_barrier_init();
     }
     __syncthreads();
     dependent_start();
 
-    // item i: unit i / 2 (n * H + h), column half i % 2; this CTA's k-th goes through stage k % kStages
+    // item i: unit i / 2 (n * H + h), column half i % 2; this CTA's k-th goes through stage k % kStages and
+    // is announced on full[k % kFulls]; group k % kGroups takes it. Item k is staged once item k - kStages
+    // was taken, so neither kind of barrier is ever two phases ahead of who waits for it.
     const unsigned step = gridDim.x;
     if (threadIdx.x >= Sm::kGroups * kGroupThreads) {
-        const int lane = threadIdx.x - Sm::kGroups * kGroupThreads;
-        int stage = 0;
+        const int lane = threadIdx.x & 31;
+        int stage = 0, next_full = 0;
         uint32_t parity = 1;   // of the wait for an empty stage: the first round passes at once
         auto read = [&](unsigned item) {
             Item it{};
@@ -591,46 +601,50 @@ __global__ void __launch_bounds__(StepSmem<kBf16, kTok>::kThreads, 1) draft_step
             return it;
         };
         Item next = read(blockIdx.x);
+        unsigned staged = 0;
         for (unsigned item = blockIdx.x; item < items; item += step) {
             const Item it = next;
             next = read(item + step);   // its latency hides behind this item's copies
-            if (!tc::mbar_wait(&empty[stage], parity, kWaitNs)) {
-                record_status(a.status, SALA_ERR_TIMEOUT);
+            if (__any_sync(0xffffffffu, !tc::mbar_wait(&empty[stage], parity, tck::kWaitNs))) {
+                if (lane == 0) record_status(a.status, SALA_ERR_TIMEOUT);
                 break;
             }
-            uint8_t *at = smem + stage * Sm::kStage;
-            stage_item<kBf16, kTok>(a, tc::smem_u32(at), it, lane);
-            if (lane == 0) {
-                *reinterpret_cast<Item *>(at + Sm::kHead) = it;
-                tc::mbar_arrive(&full[stage]);
-            }
-            cp_async_arrive(&full[stage]);
+            stage_item<kBf16, kTok>(a, maps, smem + stage * Sm::kStage, smem + Sm::kSides + stage * Sm::kSide, it,
+                                    &full[next_full], lane);
+            ++staged;
+            if (++next_full == Sm::kFulls) next_full = 0;
             if (++stage == Sm::kStages) stage = 0, parity ^= 1;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");   // none of this thread's copies outlives it
+        // no copy outlives the CTA, however it ends: the last ones of every stage have landed
+        for (unsigned k = staged > Sm::kStages ? staged - Sm::kStages : 0; k < staged; ++k)
+            if (!tc::mbar_wait(&full[k % Sm::kFulls], (k / Sm::kFulls) & 1, tck::kWaitNs)) break;
         return;
     }
 
     const int group = threadIdx.x / kGroupThreads, tid = threadIdx.x & (kGroupThreads - 1);
-    uint8_t *own = smem + Sm::kStages * Sm::kStage + group * Sm::kOwn;
-    int stage = group;
+    uint8_t *own = smem + Sm::kOwns + group * Sm::kOwn;
+    int stage = group, mine = group;
     uint32_t parity = 0;
     for (unsigned item = blockIdx.x + group * step; item < items; item += Sm::kGroups * step) {
-        const bool late = !tc::mbar_wait(&full[stage], parity, kWaitNs);
+        const bool late = !tc::mbar_wait(&full[mine], parity, tck::kWaitNs);
         if (late) record_status(a.status, SALA_ERR_TIMEOUT);
+        __syncwarp();
         // also: the group's memory of the item before is free
-        if (group_any(group, late)) break;
-        uint8_t *at = smem + stage * Sm::kStage;
-        const Item it = *reinterpret_cast<const Item *>(at + Sm::kHead);
+        if (tck::named_any(group + 1, kGroupThreads, late)) break;
+        uint8_t *at = smem + stage * Sm::kStage, *side = smem + Sm::kSides + stage * Sm::kSide;
+        const Item it = *reinterpret_cast<const Item *>(side + Sm::kHead);
         for (int e = it.tokens * 8 + tid; e < static_cast<int>(a.T) * 8; e += kGroupThreads)   // rows past the count
             *reinterpret_cast<uint4 *>(a.o + ((it.n * a.T + e / 8) * a.H + it.h) * kD + it.half * kHalf + 8 * (e % 8)) =
                 make_uint4(0, 0, 0, 0);
-        if (it.commits || it.tokens) run_item<kBf16, kTok>(a, at, tc::smem_u32(at), own, it, group);
+        if (it.commits || it.tokens) run_item<kBf16, kTok>(a, maps, at, side, own, it, group);
+        if (tid == 0) tc::tma_store_wait_read<0>();
         __syncwarp();
         if ((tid & 31) == 0) tc::mbar_arrive(&empty[stage]);
-        stage += Sm::kGroups;
-        if (stage >= Sm::kStages) stage -= Sm::kStages, parity ^= 1;
+        stage = (stage + Sm::kGroups) % Sm::kStages;
+        mine += Sm::kGroups;
+        if (mine >= Sm::kFulls) mine = group, parity ^= 1;
     }
+    if (tid == 0) tc::tma_store_wait_all<0>();
 }
 
 // ---- longer steps ----------------------------------------------------------------------------
@@ -823,6 +837,27 @@ __global__ void __launch_bounds__(kThreads) draft_step_long_kernel(DraftArgs a) 
     }
 }
 
+cudaError_t pool_map(CUtensorMap *map, const void *pool, bool bf16, int64_t states) {
+    const cuuint64_t dims[3] = {kD, kD, static_cast<cuuint64_t>(states)};
+    const cuuint64_t row = kD * (bf16 ? 2 : 4), strides[2] = {row, kD * row};
+    const cuuint32_t box[3] = {bf16 ? 64u : 32u, kD, 1};
+    return tck::encode_tiled(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, pool, dims, strides,
+                             box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t token_map(CUtensorMap *map, const void *tokens, int64_t N, int64_t T, int H, bool values) {
+    const cuuint64_t dims[5] = {64, 2, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(N)};
+    const cuuint64_t strides[4] = {128, 256, dims[2] * 256, dims[3] * dims[2] * 256};
+    const cuuint32_t box[5] = {64, values ? 1u : 2u, 1, 8, 1};
+    return tck::encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, tokens, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <bool kBf16, int kTok>
+cudaError_t launch_step(const DraftArgs &a, const StepMaps &maps, unsigned items, unsigned grid, cudaStream_t stream) {
+    using Sm = StepSmem<kBf16, kTok>;
+    return launch_dependent_cluster(draft_step_kernel<kBf16, kTok>, grid, 0, Sm::kThreads, Sm::kBytes, stream, a, maps, items);
+}
+
 }  // namespace
 
 cudaError_t launch_draft_step(const void *q, const void *k, const void *v, const float *g,
@@ -837,18 +872,19 @@ cudaError_t launch_draft_step(const void *q, const void *k, const void *v, const
                       pend_g, accepted, scale, pool, slots, P, static_cast<uint16_t *>(o), T, T_pend, H,
                       status};
     if (T <= 16 && T_pend <= 16) {
+        StepMaps maps{};
+        cudaError_t e = pool_map(&maps.pool, pool, bf16, P * H);
+        if (e == cudaSuccess && T_pend) e = token_map(&maps.pk, pend_k, N, T_pend, H, false);
+        if (e == cudaSuccess && T_pend) e = token_map(&maps.pv, pend_v, N, T_pend, H, true);
+        if (e == cudaSuccess && T) e = token_map(&maps.q, q, N, T, H, false);
+        if (e == cudaSuccess && T) e = token_map(&maps.k, k, N, T, H, false);
+        if (e == cudaSuccess && T) e = token_map(&maps.v, v, N, T, H, true);
+        if (e != cudaSuccess) return e;
+        const bool few = T <= 8 && T_pend <= 8;
         const unsigned items = static_cast<unsigned>(2 * N * H);
         const unsigned grid = items < static_cast<unsigned>(sm_count) ? items : sm_count;
-        const bool few = T <= 8 && T_pend <= 8;
-        if (bf16)
-            return few ? launch_dependent_cluster(draft_step_kernel<true, 8>, grid, 0, StepSmem<true, 8>::kThreads,
-                                                  StepSmem<true, 8>::kBytes, stream, a, items)
-                       : launch_dependent_cluster(draft_step_kernel<true, 16>, grid, 0, StepSmem<true, 16>::kThreads,
-                                                  StepSmem<true, 16>::kBytes, stream, a, items);
-        return few ? launch_dependent_cluster(draft_step_kernel<false, 8>, grid, 0, StepSmem<false, 8>::kThreads,
-                                              StepSmem<false, 8>::kBytes, stream, a, items)
-                   : launch_dependent_cluster(draft_step_kernel<false, 16>, grid, 0, StepSmem<false, 16>::kThreads,
-                                              StepSmem<false, 16>::kBytes, stream, a, items);
+        return bf16 ? (few ? launch_step<true, 8>(a, maps, items, grid, stream) : launch_step<true, 16>(a, maps, items, grid, stream))
+                    : (few ? launch_step<false, 8>(a, maps, items, grid, stream) : launch_step<false, 16>(a, maps, items, grid, stream));
     }
     return launch_dependent(bf16 ? draft_step_long_kernel<true> : draft_step_long_kernel<false>,
                             static_cast<unsigned>(N * H), kThreads, stream, a);

@@ -1185,9 +1185,11 @@ namespace {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 cudaError_t g_encode_err = cudaSuccess;
 std::once_flag g_encode_once;
+}  // namespace
 
-cudaError_t encode_map(CUtensorMap *map, const void *base, int64_t T_total, int H, bool store,
-                       bool sw64 = false) {
+cudaError_t encode_tiled(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base,
+                         const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                         CUtensorMapSwizzle swizzle) {
     std::call_once(g_encode_once, []() {
         cudaDriverEntryPointQueryResult q;
         g_encode_err = cudaGetDriverEntryPointByVersion(
@@ -1197,18 +1199,23 @@ cudaError_t encode_map(CUtensorMap *map, const void *base, int64_t T_total, int 
             g_encode_err = cudaErrorNotSupported;
     });
     if (g_encode_err != cudaSuccess) return g_encode_err;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(H),
-                          static_cast<cuuint64_t>(T_total)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(H) * kD * 2};
-    cuuint32_t box_load[3] = {64, 1, 64}, box_store[3] = {32, 1, 64};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
-                          strides, store ? box_store : box_load, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          store ? (sw64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE)
-                                : CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    CUresult r = g_encode(map, type, rank, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+namespace {
+cudaError_t encode_map(CUtensorMap *map, const void *base, int64_t T_total, int H, bool store,
+                       bool sw64 = false) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(H),
+                                static_cast<cuuint64_t>(T_total)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(H) * kD * 2};
+    const cuuint32_t box_load[3] = {64, 1, 64}, box_store[3] = {32, 1, 64};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, store ? box_store : box_load,
+                        store ? (sw64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE)
+                              : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 }  // namespace
 
