@@ -12,8 +12,8 @@
 // of minus infinity (forget everything) gives exact zeros.
 //
 // Steps of up to 16 new and 16 pending tokens (draft_step_kernel): one persistent CTA per SM. An
-// item of work is one (sequence, head, half of the value columns). A producer warp stages items ahead
-// of use in a ring of shared-memory stages (TMA); each of the groups of 4 consumer warps takes every
+// item of work is one (sequence, head, half of the value columns). Two producer warps stage items
+// ahead of use in a ring of shared-memory stages (TMA); each of the groups of 4 consumer warps takes every
 // kGroups-th item and sends the state back from its stage (TMA). The two products with the state run on the tensor cores as
 // mma.m16n8k16, 16 (or 8) being the tokens:
 //     commit   D[16 dv x 8 dk] = (w V)^T K     with w_j v_j in fp32 split into three bf16 parts
@@ -109,7 +109,10 @@ struct StepSmem {
     static constexpr int kOwn = kSwap + 4 * kTok / 2 * 32 * 4;
     // groups as far as registers go, stages as far as memory goes
     static constexpr int kGroups = kBf16 ? 4 : 3;
-    static constexpr int kStages = (232448 - 1024 - kGroups * kOwn) / (kStage + kSide);
+    // (fp32: 4 stages of 33 KB states; with 5 the loads run so far ahead of the stores that the memory
+    // serves both more slowly, 256 rows of 5 tokens in 186 us instead of 178)
+    static constexpr int kFit = (232448 - 1024 - kGroups * kOwn) / (kStage + kSide);
+    static constexpr int kStages = !kBf16 && kFit > 4 ? 4 : kFit;
     // "Full" barriers: a multiple of the groups, so that a barrier's phases are all one group's. Were they
     // as many as the stages, the phases of one would go round the groups, and a group could ask for phase
     // p + 1 before phase p of another group had come, which the parity cannot tell from its end.
@@ -117,13 +120,13 @@ struct StepSmem {
     static constexpr int kSides = kStages * kStage;
     static constexpr int kOwns = kSides + kStages * kSide;
     static constexpr int kBytes = kOwns + kGroups * kOwn;
-    static constexpr int kThreads = kGroups * kGroupThreads + 32;
+    static constexpr int kThreads = kGroups * kGroupThreads + 64;   // and two producer warps
     static_assert(kStages > kGroups, "the loads run ahead");
 };
 
 // pool [P * H, 128, 128]: boxes of one state's 128 rows x 128 bytes; tokens [N, T, H, 2, 64]: boxes of
 // 8 tokens of one head (zeros past T), all columns of keys and queries, half of them of values. (A
-// copy costs the copy engine about 90 ns whatever its size: boxes of 4 tokens x 64 columns bounded
+// copy costs its issuing warp about 90 ns whatever its size: boxes of 4 tokens x 64 columns bounded
 // 256 bf16 rows of 5 tokens by their number, at 159 us.)
 struct StepMaps {
     CUtensorMap pool, pk, pv, q, k, v;
@@ -248,36 +251,53 @@ __device__ __forceinline__ uint32_t split_bf16(float &x0, float &x1) {
     return w;
 }
 
-// Queues an item's copies into its stage (by a whole warp). The barrier takes one arrival of every
-// lane, one of lane 0 for the item itself and the bytes of the tiles.
+// An item's copies into its stage, by two warps: the state and the item itself, and the tokens. The
+// barrier takes one arrival from each with the bytes of its tiles, and one from every lane of the
+// second for the gates, which are too narrow for the copy engine.
 template <bool kBf16, int kTok>
-__device__ __forceinline__ void stage_item(const DraftArgs &a, const StepMaps &maps, uint8_t *smem, uint8_t *side, const Item &it,
-                                           uint64_t *bar, int lane) {
+__device__ __forceinline__ void stage_state(const DraftArgs &a, const StepMaps &maps, uint8_t *smem, uint8_t *side, const Item &it,
+                                            uint64_t *bar, int lane) {
     using Sm = StepSmem<kBf16, kTok>;
-    const int h = it.h, half = it.half, commits = it.commits, tokens = it.tokens;
-    const int states = commits || tokens ? Sm::kBoxes : 0;
-    const int pend = (commits + 7) / 8, fresh = (tokens + 7) / 8;
+    if (lane != 0) return;
+    const int states = it.commits || it.tokens ? Sm::kBoxes : 0;
+    *reinterpret_cast<Item *>(side + Sm::kHead) = it;
+    tc::mbar_arrive_expect_tx(bar, states * Sm::kStateTile);
+    for (int b = 0; b < states; ++b)
+        tc::tma_load_3d(smem + Sm::kState + b * Sm::kStateTile, &maps.pool, it.half * kHalf + b * Sm::kBoxCols, 0,
+                        static_cast<int32_t>(static_cast<int64_t>(it.slot) * a.H + it.h), bar);
+}
+template <bool kBf16, int kTok>
+__device__ __forceinline__ void stage_tokens(const DraftArgs &a, const StepMaps &maps, uint8_t *smem, uint8_t *side, const Item &it,
+                                             uint64_t *bar, int lane) {
+    using Sm = StepSmem<kBf16, kTok>;
+    const int commits = it.commits, tokens = it.tokens;
     if (lane == 0) {
-        *reinterpret_cast<Item *>(side + Sm::kHead) = it;
-        tc::mbar_arrive_expect_tx(bar, states * Sm::kStateTile + (3 * pend + 5 * fresh) * kOctBytes);
+        const uint32_t at = tc::smem_u32(smem);
+        tc::mbar_arrive_expect_tx(bar, (3 * ((commits + 7) / 8) + 5 * ((tokens + 7) / 8)) * kOctBytes);
+#pragma unroll
+        for (int oct = 0; oct < kTok / 8; ++oct) {
+            if (8 * oct < commits) {
+                tma_load_5d(at + Sm::kPk + oct * 2 * kOctBytes, &maps.pk, 0, 0, it.h, 8 * oct, it.n, bar);
+                tma_load_5d(at + Sm::kPv + oct * kOctBytes, &maps.pv, 0, it.half, it.h, 8 * oct, it.n, bar);
+            }
+            if (8 * oct < tokens) {
+                tma_load_5d(at + Sm::kQ + oct * 2 * kOctBytes, &maps.q, 0, 0, it.h, 8 * oct, it.n, bar);
+                tma_load_5d(at + Sm::kK + oct * 2 * kOctBytes, &maps.k, 0, 0, it.h, 8 * oct, it.n, bar);
+                tma_load_5d(at + Sm::kV + oct * kOctBytes, &maps.v, 0, it.half, it.h, 8 * oct, it.n, bar);
+            }
+        }
     }
     __syncwarp();
-    if (lane < states)
-        tc::tma_load_3d(smem + Sm::kState + lane * Sm::kStateTile, &maps.pool, half * kHalf + lane * Sm::kBoxCols, 0,
-                        static_cast<int32_t>(static_cast<int64_t>(it.slot) * a.H + h), bar);
-    // lanes 4 to 13: 8 tokens each of the pending keys and values and the new queries, keys and values
-    const int i = lane - 4, kind = i >> 1, oct = i & 1;
-    if (i >= 0 && kind < 5 && oct < (kind < 2 ? pend : fresh)) {
-        const CUtensorMap *map = kind == 0 ? &maps.pk : kind == 1 ? &maps.pv : kind == 2 ? &maps.q : kind == 3 ? &maps.k : &maps.v;
-        const bool values = kind == 1 || kind == 4;
-        const int at = (kind == 0 ? Sm::kPk : kind == 1 ? Sm::kPv : kind == 2 ? Sm::kQ : kind == 3 ? Sm::kK : Sm::kV) +
-                       oct * (values ? 1 : 2) * kOctBytes;
-        tma_load_5d(tc::smem_u32(smem + at), map, 0, values ? half : 0, h, 8 * oct, it.n, bar);
-    }
-    const int64_t pend0 = it.n * a.T_pend * a.H + h, new0 = it.n * a.T * a.H + h;   // token rows of this head
+    const int64_t pend0 = it.n * a.T_pend * a.H + it.h, new0 = it.n * a.T * a.H + it.h;   // token rows of this head
     if (lane < commits) cp_async4(tc::smem_u32(side + Sm::kPg) + 4 * lane, a.pg + pend0 + static_cast<int64_t>(lane) * a.H);
     if (lane < tokens) cp_async4(tc::smem_u32(side + Sm::kG) + 4 * lane, a.g + new0 + static_cast<int64_t>(lane) * a.H);
     cp_async_arrive(bar);
+}
+
+// p = a b of four neighbours
+__device__ __forceinline__ void weights4(float (&p)[4], const float *a, const float *b) {
+    const float4 x = *reinterpret_cast<const float4 *>(a), y = *reinterpret_cast<const float4 *>(b);
+    p[0] = x.x * y.x, p[1] = x.y * y.y, p[2] = x.z * y.z, p[3] = x.w * y.w;
 }
 
 // One item by a group of 4 warps, from its stage `smem` and what stands beside it; `own`: the group's
@@ -299,7 +319,7 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
     if (tokens) ng = gate_scan<kTok>(side + Sm::kG, tokens, lane);
 
     // 1. products of the new tokens' queries with 8 keys at a time, one warp each: with the new tokens
-    // (first warps), with the pending ones (next warps); decays by warp 3
+    // (first warps), with the pending ones (next warps)
     const bool pending = warp >= kOct;
     const int oct = pending ? warp - kOct : warp;
     if (tokens && oct < kOct && 8 * oct < (!pending ? tokens : kBf16 ? commits : 0)) {
@@ -326,12 +346,21 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
         sts_f32x2(s, d[0], d[1]);
         if constexpr (kTok == 16) sts_f32x2(s + 8 * kTok * 4, d[2], d[3]);
     }
-    if (tokens && warp == 3) {
-        float sum = 0.f;   // lane j: g_{j+1} + .. + g_t
-        for (int t = 0; t < tokens; ++t) {
+    if (tokens) {
+        // decays of rows t = kOct * 2 * warp + r, lanes j and j + 16 taking turns; sums of g_{j+1} .. g_t
+        constexpr int kRows = kTok / 4;
+        const int j = lane & 15, turn = lane >> 4;
+        float sum = 0.f;
+        for (int i = 1; i < kRows * warp; ++i) {
+            const float g = __shfl_sync(0xffffffffu, ng.g, i);
+            if (i > j) sum += g;
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int t = kRows * warp + r;
             const float g = __shfl_sync(0xffffffffu, ng.g, t);
-            if (t > lane) sum += g;
-            if (lane <= t) sts_f32(own_at + Sm::kDecay + (t * kTok + lane) * 4, expf(sum));
+            if (t > j) sum += g;
+            if ((r & 1) == turn && j <= t) sts_f32(own_at + Sm::kDecay + (t * kTok + j) * 4, expf(sum));
         }
     }
 
@@ -535,23 +564,30 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
             y0[j] *= h0;
             if constexpr (kTok == 16) y1[j] *= h1;
         }
-        for (int j = 0; j < tokens; ++j) {
-            const uint2 w = lds_u32x2(st + Sm::kV + chunk(j, first / 8) + rows * 8);
-            const float2 v0 = bf16x2_to_float2(w.x), v1 = bf16x2_to_float2(w.y);
-            if (j <= gr) {
-                const float s = score[gr * kTok + j] * decay[gr * kTok + j];
-                y0[0] = fmaf(s, v0.x, y0[0]);
-                y0[1] = fmaf(s, v0.y, y0[1]);
-                y0[2] = fmaf(s, v1.x, y0[2]);
-                y0[3] = fmaf(s, v1.y, y0[3]);
-            }
-            if constexpr (kTok == 16) {
-                if (j <= gr + 8) {
-                    const float s = score[(gr + 8) * kTok + j] * decay[(gr + 8) * kTok + j];
-                    y1[0] = fmaf(s, v0.x, y1[0]);
-                    y1[1] = fmaf(s, v0.y, y1[1]);
-                    y1[2] = fmaf(s, v1.x, y1[2]);
-                    y1[3] = fmaf(s, v1.y, y1[3]);
+#pragma unroll
+        for (int j0 = 0; j0 < kTok; j0 += 4) {
+            if (j0 >= tokens) break;
+            // of rows gr (which ends before token 8) and gr + 8
+            float p0[4], p1[4];
+            if (j0 < 8) weights4(p0, score + gr * kTok + j0, decay + gr * kTok + j0);
+            if constexpr (kTok == 16) weights4(p1, score + (gr + 8) * kTok + j0, decay + (gr + 8) * kTok + j0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = j0 + i;
+                if (j >= tokens) break;
+                const uint2 w = lds_u32x2(st + Sm::kV + chunk(j, first / 8) + rows * 8);
+                const float2 v0 = bf16x2_to_float2(w.x), v1 = bf16x2_to_float2(w.y);
+                if (j0 < 8 && j <= gr) {
+                    y0[0] = fmaf(p0[i], v0.x, y0[0]);
+                    y0[1] = fmaf(p0[i], v0.y, y0[1]);
+                    y0[2] = fmaf(p0[i], v1.x, y0[2]);
+                    y0[3] = fmaf(p0[i], v1.y, y0[3]);
+                }
+                if (kTok == 16 && j <= gr + 8) {
+                    y1[0] = fmaf(p1[i], v0.x, y1[0]);
+                    y1[1] = fmaf(p1[i], v0.y, y1[1]);
+                    y1[2] = fmaf(p1[i], v1.x, y1[2]);
+                    y1[3] = fmaf(p1[i], v1.y, y1[3]);
                 }
             }
         }
@@ -575,7 +611,7 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[Sm::kFulls], empty[Sm::kStages];
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Sm::kFulls; ++s) tc::mbar_init(&full[s], 32 + 1);
+        for (int s = 0; s < Sm::kFulls; ++s) tc::mbar_init(&full[s], 32 + 2);
         for (int s = 0; s < Sm::kStages; ++s) tc::mbar_init(&empty[s], kGroupThreads / 32);
         tc::fence_barrier_init();
     }
@@ -588,13 +624,14 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
     const unsigned step = gridDim.x;
     if (threadIdx.x >= Sm::kGroups * kGroupThreads) {
         const int lane = threadIdx.x & 31;
+        const bool states = threadIdx.x < Sm::kGroups * kGroupThreads + 32;   // or the tokens
         int stage = 0, next_full = 0;
         uint32_t parity = 1;   // of the wait for an empty stage: the first round passes at once
         auto read = [&](unsigned item) {
             Item it{};
             if (item < items) {
                 const unsigned unit = item >> 1, n = unit / static_cast<unsigned>(a.H);
-                const Row row = read_row(a, static_cast<int>(n), lane == 0);
+                const Row row = read_row(a, static_cast<int>(n), states && lane == 0);
                 it = {row.slot, static_cast<int32_t>(n), static_cast<int32_t>(unit - n * a.H), static_cast<int32_t>(item & 1),
                       static_cast<int32_t>(row.commits), static_cast<int32_t>(row.tokens), {0, 0}};
             }
@@ -609,8 +646,9 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
                 if (lane == 0) record_status(a.status, SALA_ERR_TIMEOUT);
                 break;
             }
-            stage_item<kBf16, kTok>(a, maps, smem + stage * Sm::kStage, smem + Sm::kSides + stage * Sm::kSide, it,
-                                    &full[next_full], lane);
+            uint8_t *at = smem + stage * Sm::kStage, *side = smem + Sm::kSides + stage * Sm::kSide;
+            if (states) stage_state<kBf16, kTok>(a, maps, at, side, it, &full[next_full], lane);
+            else stage_tokens<kBf16, kTok>(a, maps, at, side, it, &full[next_full], lane);
             ++staged;
             if (++next_full == Sm::kFulls) next_full = 0;
             if (++stage == Sm::kStages) stage = 0, parity ^= 1;
