@@ -16,8 +16,8 @@
 // Only the rows p_a and q_a are read in full; the accept test gathers two values per draft.
 //
 // A cluster of CTAs reads one row. The vocabulary is cut into one part per warp of the cluster, in
-// order; every warp sums its part, the CTAs read each other's sums through distributed shared
-// memory, and the CTA whose part holds the drawn number goes through that part again (from L2).
+// order; every warp sums its part and hands the sum to the first CTA through distributed shared
+// memory, which finds the part that holds the drawn number and goes through it again (from L2).
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -274,9 +274,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ Ring ring;
     __shared__ int first_s, rejected_s;
-    __shared__ long long mine[2][kVerifyWarps];                   // this CTA's sums, one row a pass
-    __shared__ long long all[kMaxCluster * kVerifyWarps];         // the cluster's
+    __shared__ long long all[kMaxCluster * kVerifyWarps];   // sums of the parts, in the first CTA
     __shared__ long long scan[kVerifyWarps];
+    cluster.barrier_arrive();   // waited for before the first CTA's memory is written
 
     if (warp == 0) {
         bool rejected;
@@ -301,32 +301,41 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
     const int len = (V / kN + parts) / parts * kN;
     auto part_begin = [&](int i) { return i == 0 ? 0 : min(V, head + len * i); };
 
-    long long total = 0;
-    for (int pass = 0; pass < 2; ++pass) {
+    // every warp hands its sum to the first CTA, which goes on alone: the others make room
+    {
         const int i = rank * kVerifyWarps + warp;
         const long long sum = sum_part(w, part_begin(i), part_begin(i + 1), lane, ring);
-        if (lane == 0) mine[pass][warp] = sum;
-        cluster.sync();
-        if (threadIdx.x < parts)
-            all[threadIdx.x] = cluster.map_shared_rank(&mine[pass][0], threadIdx.x / kVerifyWarps)[threadIdx.x % kVerifyWarps];
-        __syncthreads();
-        total = 0;
-        for (int j = lane; j < parts; j += 32) total += all[j];
+        cluster.barrier_wait();
+        if (lane == 0) *cluster.map_shared_rank(&all[i], 0) = sum;
+        cluster.barrier_arrive();
+        if (rank != 0) return;
+        cluster.barrier_wait();
+    }
+    auto sum_all = [&] {
+        long long t = 0;
+        for (int j = lane; j < parts; j += 32) t += all[j];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-        if (total > 0 || (!w.q && w.one_at < 0)) break;
-        w.q = nullptr;   // nothing is left of the target after the drafter's part: draw from the target
+        for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+        return t;
+    };
+    long long total = sum_all();
+    if (total == 0 && rejected_s) {
+        // nothing is left of the target after the drafter's part: draw from the target
+        w.q = nullptr;
         w.one_at = -1;
         __syncthreads();
+        for (int i = warp; i < parts; i += kVerifyWarps) {
+            const long long sum = sum_part(w, part_begin(i), part_begin(i + 1), lane, ring);
+            if (lane == 0) all[i] = sum;
+        }
+        __syncthreads();
+        total = sum_all();
     }
-    cluster.barrier_arrive();   // the others may still be reading this CTA's sums
 
     int32_t *out = a.tokens + n * (a.K + 1);
-    if (rank == 0) {
-        for (int i = threadIdx.x; i <= a.K; i += kVerifyThreads)
-            if (i != first || total == 0) out[i] = i < first ? __ldg(a.x + n * a.K + i) : -1;
-        if (threadIdx.x == 0) a.accepted[n] = first;
-    }
+    for (int i = threadIdx.x; i <= a.K; i += kVerifyThreads)
+        if (i != first || total == 0) out[i] = i < first ? __ldg(a.x + n * a.K + i) : -1;
+    if (threadIdx.x == 0) a.accepted[n] = first;
     if (total > 0) {
         // the number drawn, in the same units: the whole part of s * total (s is a whole number of
         // 2^-64, or closer to 0 than that)
@@ -348,7 +357,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
             }
             before = __shfl_sync(0xffffffffu, c, 31);
         }
-        if (part / kVerifyWarps == rank) {
+        {
             // each thread sums consecutive vectors of the part (the first thread also what lies before
             // the first whole one), then the one that passes `at` looks for its token
             const int lo = part_begin(part), hi = part_begin(part + 1);
@@ -392,13 +401,12 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
             }
         }
     }
-    cluster.barrier_wait();
 }
 
 // CTAs that share a row: 8 while the rows are few, so that every SM reads and each CTA's part is
-// short; fewer where the rows alone are four CTAs for every SM, since each CTA pays about 5 us of
-// dependent steps (accept test, sums of the cluster, second look). 1024 rows of 65536 bf16: 8 CTAs
-// 123 us, 2 CTAs 66 us; 256 rows of 131072 fp32: 8 CTAs 56 us, 2 CTAs 73 us.
+// short; fewer where the rows alone are two CTAs for every SM, since each CTA pays some 5 us of
+// dependent steps (the accept test, the hand-over of its sums). 1024 rows of 65536 bf16: 4 CTAs
+// 65 us, 2 CTAs 56 us; 256 rows of 131072 fp32: 8 CTAs 48 us, 4 CTAs 51 us.
 int cluster_size(int64_t N, int sm_count) {
     int c = kMaxCluster;
     while (c > 1 && N * c > 16 * sm_count) c /= 2;
@@ -412,7 +420,7 @@ static_assert(kSmSmem / kVerifyFits >= kStaticSmem, "a CTA's own memory fits so 
 
 // A cluster's CTAs are packed onto as few SMs as hold them, so a small launch would leave most SMs
 // idle: it asks for the most memory per CTA with which all its clusters still run at once (32 rows of
-// 131072 fp32: 16.5 us packed, 11.3 us spread).
+// 131072 fp32: 16.5 us packed, 12.4 us spread).
 size_t spread(int64_t N, int c, const int *fits) {
     for (int i = 0; c == kMaxCluster && i < kVerifyFits; ++i)
         if (N <= fits[i]) return room_for(i + 1);
