@@ -23,7 +23,7 @@
 // commit, split into two bf16 parts. A bf16 state is read as it was stored, an operand without any
 // arithmetic, and what the commit adds to it enters as the pending tokens' own term (Q K^T w) V.
 // Places past the counts hold anything: pending tokens there are masked out of every operand, and the
-// products among the new tokens are taken in fp32 over j <= t only, so nothing of a masked place
+// products among the new tokens go one by one where a value is not finite, so nothing of a masked place
 // reaches a result.
 // Longer steps (draft_step_long_kernel) run the plain form below.
 #include <type_traits>
@@ -102,13 +102,19 @@ struct StepSmem {
     static constexpr int kHead = kG + kTok * 4;              // struct Item
     static constexpr int kSide = kHead + 32;
     // a group's own
-    static constexpr int kScore = 0;                         // [kTok][kTok] fp32: q_t . k_j
-    static constexpr int kPend = kScore + kTok * kTok * 4;   // [kTok][kTok] fp32: q_t . pk_j
-    static constexpr int kDecay = kPend + kTok * kTok * 4;   // [kTok][kTok] fp32: exp(g_{j+1} + .. + g_t)
-    static constexpr int kSwap = kDecay + kTok * kTok * 4;   // [4 warps][kTok / 2][32 lanes] fp32: halves of Q S
-    static constexpr int kOwn = kSwap + 4 * kTok / 2 * 32 * 4;
-    // groups as far as registers go, stages as far as memory goes
-    static constexpr int kGroups = kBf16 ? 4 : 3;
+    static constexpr int kPitch = kTok + 4;                  // of rows t, so that 8 of them fill the banks
+    static constexpr int kRect = kTok * kPitch * 4;          // [t][j] fp32
+    static constexpr int kScore = 0;                         // q_t . k_j, over either half of the keys' columns
+    static constexpr int kPend = kScore + 2 * kRect;         // q_t . pk_j, the same (bf16 states)
+    static constexpr int kDecay = kPend + (kBf16 ? 2 : 0) * kRect;   // exp(g_{j+1} + .. + g_t)
+    static constexpr int kOwn = kDecay + kRect;
+    // halves of Q S, [4 warps][kTok / 2][32 lanes] fp32, in the place of the queries once they are read
+    static constexpr int kSwap = kQ;
+    static_assert(4 * kTok / 2 * 32 * 4 <= kK - kQ, "the halves fit");
+    // Groups: three keep the memory busy with fp32 states; four with bf16 states and 8 tokens (256 rows of
+    // 5 tokens: 109 us, with three 116); with 16 tokens the registers of four do not suffice (201 ragged
+    // rows: 111 us with three, 115 with four). Stages as far as memory goes.
+    static constexpr int kGroups = kBf16 && kTok == 8 ? 4 : 3;
     // (fp32: 4 stages of 33 KB states; with 5 the loads run so far ahead of the stores that the memory
     // serves both more slowly, 256 rows of 5 tokens in 186 us instead of 178)
     static constexpr int kFit = (232448 - 1024 - kGroups * kOwn) / (kStage + kSide);
@@ -251,6 +257,15 @@ __device__ __forceinline__ uint32_t split_bf16(float &x0, float &x1) {
     return w;
 }
 
+// Wait for a phase of `bar`, at most tck::kWaitNs, asleep in the barrier between tries.
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = tc::global_timer_ns();
+    while (!tc::mbar_try_wait_sleep(bar, parity, 20000))
+        if (tc::global_timer_ns() - t0 > tck::kWaitNs) return false;
+    return true;
+}
+
 // An item's copies into its stage, by two warps: the state and the item itself, and the tokens. The
 // barrier takes one arrival from each with the bytes of its tiles, and one from every lane of the
 // second for the gates, which are too narrow for the copy engine.
@@ -294,15 +309,29 @@ __device__ __forceinline__ void stage_tokens(const DraftArgs &a, const StepMaps 
     cp_async_arrive(bar);
 }
 
-// p = a b of four neighbours
-__device__ __forceinline__ void weights4(float (&p)[4], const float *a, const float *b) {
-    const float4 x = *reinterpret_cast<const float4 *>(a), y = *reinterpret_cast<const float4 *>(b);
-    p[0] = x.x * y.x, p[1] = x.y * y.y, p[2] = x.z * y.z, p[3] = x.w * y.w;
+// Two neighbouring weights of a row in two bf16 parts, as word i of an A operand.
+template <int kWords>
+__device__ __forceinline__ void split_row(uint32_t (&pa)[2][kWords], int i, float2 w) {
+    pa[0][i] = split_bf16(w.x, w.y);
+    pa[1][i] = float2_to_bf16x2(w.x, w.y);
+}
+// Four columns of two neighbouring tokens' values as words i of four B operands.
+template <int kWords>
+__device__ __forceinline__ void pack_values(uint32_t (&bv)[4][kWords], int i, uint2 a0, uint2 a1, uint32_t mask) {
+    bv[0][i] = __byte_perm(a0.x, a1.x, 0x5410) & mask;
+    bv[1][i] = __byte_perm(a0.x, a1.x, 0x7632) & mask;
+    bv[2][i] = __byte_perm(a0.y, a1.y, 0x5410) & mask;
+    bv[3][i] = __byte_perm(a0.y, a1.y, 0x7632) & mask;
+}
+// Nonzero if either bf16 of the pair is an infinity or NaN: its exponent, all ones, carries.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u);
 }
 
 // One item by a group of 4 warps, from its stage `smem` and what stands beside it; `own`: the group's
 // memory. Thread 0 of the group leaves a store of the state in flight that still reads the stage.
-template <bool kBf16, int kTok>
+// kC, kT: there is something to commit, there are new tokens.
+template <bool kBf16, int kTok, bool kC, bool kT>
 __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &maps, uint8_t *smem, const uint8_t *side, uint8_t *own,
                                          const Item &it, int group) {
     using Sm = StepSmem<kBf16, kTok>;
@@ -315,38 +344,11 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
     const int commits = it.commits, tokens = it.tokens;
     const uint32_t st = tc::smem_u32(smem), own_at = tc::smem_u32(own);
     Gates pg{0.f, 0.f, 0.f}, ng{0.f, 0.f, 0.f};
-    if (commits) pg = gate_scan<kTok>(side + Sm::kPg, commits, lane);
-    if (tokens) ng = gate_scan<kTok>(side + Sm::kG, tokens, lane);
+    if (kC) pg = gate_scan<kTok>(side + Sm::kPg, commits, lane);
+    if (kT) ng = gate_scan<kTok>(side + Sm::kG, tokens, lane);
 
-    // 1. products of the new tokens' queries with 8 keys at a time, one warp each: with the new tokens
-    // (first warps), with the pending ones (next warps)
-    const bool pending = warp >= kOct;
-    const int oct = pending ? warp - kOct : warp;
-    if (tokens && oct < kOct && 8 * oct < (!pending ? tokens : kBf16 ? commits : 0)) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t keys = st + (pending ? Sm::kPk : Sm::kK);
-#pragma unroll
-        for (int c = 0; c < 8; c += 2) {   // 32 columns: chunks 2 c .. 2 c + 3, of half c / 4
-            uint32_t qa[4], qb[4], kb[4];
-            const int cols = c / 4, first = 2 * (c & 3);
-            if constexpr (kTok == 16) {
-                ldmatrix_x4(qa, st + Sm::kQ + wide_chunk(mr + 8 * (mi & 1), cols, first + (mi >> 1)));
-                ldmatrix_x4(qb, st + Sm::kQ + wide_chunk(mr + 8 * (mi & 1), cols, first + 2 + (mi >> 1)));
-            } else {
-                uint32_t q4[4];
-                ldmatrix_x4(q4, st + Sm::kQ + wide_chunk(mr, cols, first + mi));
-                qa[0] = q4[0], qa[2] = q4[1], qb[0] = q4[2], qb[2] = q4[3];
-                qa[1] = qa[3] = qb[1] = qb[3] = 0u;
-            }
-            ldmatrix_x4(kb, keys + wide_chunk(mr + 8 * oct, cols, first + mi));
-            mma(d, qa, kb[0], kb[1]);
-            mma(d, qb, kb[2], kb[3]);
-        }
-        const uint32_t s = own_at + (pending ? Sm::kPend : Sm::kScore) + (gr * kTok + 8 * oct + 2 * tq) * 4;
-        sts_f32x2(s, d[0], d[1]);
-        if constexpr (kTok == 16) sts_f32x2(s + 8 * kTok * 4, d[2], d[3]);
-    }
-    if (tokens) {
+    // 1. decays
+    if (kT) {
         // decays of rows t = kOct * 2 * warp + r, lanes j and j + 16 taking turns; sums of g_{j+1} .. g_t
         constexpr int kRows = kTok / 4;
         const int j = lane & 15, turn = lane >> 4;
@@ -360,25 +362,25 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
             const int t = kRows * warp + r;
             const float g = __shfl_sync(0xffffffffu, ng.g, t);
             if (t > j) sum += g;
-            if ((r & 1) == turn && j <= t) sts_f32(own_at + Sm::kDecay + (t * kTok + j) * 4, expf(sum));
+            if ((r & 1) == turn && j <= t) sts_f32(own_at + Sm::kDecay + (t * Sm::kPitch + j) * 4, expf(sum));
         }
     }
 
-    // 2. the state, 16 key rows at a time. The 8 columns of an mma tile are every fourth one, so that
+    // 2. the state, 16 key rows at a time, and on the way the products of queries and keys over those 16
+    // columns: with the new keys in the warps of the first 32 values, with the pending ones in the
+    // others. The 8 columns of an mma tile are every fourth one, so that
     // a lane's columns 4 gr .. 4 gr + 3 of the four tiles are neighbours: tile j holds column 4 gr + j
     // of lane row gr, and a state row of the lane is one 16-byte (fp32) or 8-byte (bf16) access.
     uint32_t wv[kParts][2][2 * kOct];   // (w V)^T: row gr is column 4 gr + 2 m, row gr + 8 column 4 gr + 2 m + 1
-    const float fade = commits ? __shfl_sync(0xffffffffu, pg.head, commits - 1) : 1.f;
-    // the lane's columns 4 gr .. + 3 of pending token t's values
-    auto pend_values = [&](int t) {
-        return lds_u32x2(st + Sm::kPv + chunk(t, 4 * col + (gr >> 1)) + (gr & 1) * 8);
-    };
+    const float fade = kC ? __shfl_sync(0xffffffffu, pg.head, commits - 1) : 1.f;
+    // columns 4 gr .. + 3 of the warp's 32 of token t's values
+    auto values = [&](uint32_t tile, int t) { return lds_u32x2(st + tile + chunk(t, 4 * col + (gr >> 1)) + (gr & 1) * 8); };
     uint32_t there[kOct];   // mask of the pending tokens 2 tq + 8 i, + 1 of a packed pair
-    if (commits) {
+    if (kC) {
 #pragma unroll
         for (int i = 0; i < kOct; ++i) {   // tokens 2 tq + 8 i, + 1
             const int t = 2 * tq + 8 * i;
-            uint2 a0 = pend_values(t), a1 = pend_values(t + 1);
+            uint2 a0 = values(Sm::kPv, t), a1 = values(Sm::kPv, t + 1);
             if (t >= commits) a0 = make_uint2(0u, 0u);
             if (t + 1 >= commits) a1 = make_uint2(0u, 0u);
             there[i] = (t < commits ? 0xffffu : 0u) | (t + 1 < commits ? 0xffff0000u : 0u);
@@ -402,6 +404,9 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
     const int at_chunk = kBf16 ? 4 * col + (gr >> 1) : gr;
     const uint32_t st0 = tile + chunk(64 * rows + 2 * tq, at_chunk) + odd, st1 = tile + chunk(64 * rows + 2 * tq + 1, at_chunk) + odd;
     const uint32_t frag = kTok == 16 ? wide_chunk(mr + 8 * (mi & 1), rows, mi >> 1) : wide_chunk(mr, rows, mi & 1);
+    const uint32_t key_frag = st + (col ? Sm::kPk : Sm::kK) + (kTok == 16 ? wide_chunk(mr + 8 * (mi >> 1), rows, mi & 1) : frag);
+    const bool scores = kT && (col == 0 || (kBf16 && kC));
+    float sc[kOct][4] = {};   // keys 8 i + 2 tq, + 1; rows gr, gr + 8
 #pragma unroll
     for (int ci = 0; ci < 4; ++ci) {
         const uint32_t tok_at = frag ^ (ci << 5);
@@ -428,7 +433,7 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
                 x[i][1][0] = f1.x, x[i][1][1] = f1.y, x[i][1][2] = f1.z, x[i][1][3] = f1.w;
             }
         }
-        if (commits) {
+        if (kC) {
             uint32_t kb[2][2];   // K: [dk, dk + 8][tok, tok + 8]
             if constexpr (kTok == 16) {
                 uint32_t k4[4];
@@ -468,7 +473,7 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
                 }
             }
         }
-        if (tokens) {
+        if (kT) {
             if constexpr (!kBf16) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -491,65 +496,66 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
                 if constexpr (!kBf16) mma(o[j], qa, lo[0][j], lo[1][j]);
                 mma(o[j], qa, hi[0][j], hi[1][j]);
             }
-        }
-    }
-    // each warp finishes the first (rows = 0) or second four of a lane's 8 columns and hands the sums
-    // of the others to the warp with the other key rows
-    float *swap = reinterpret_cast<float *>(own + Sm::kSwap);
-    if (tokens) {
+            if (scores) {
+                uint32_t k4[4];
+                if constexpr (kTok == 16) ldmatrix_x4(k4, key_frag ^ (ci << 5));
+                else ldmatrix_x2(k4[0], k4[1], key_frag ^ (ci << 5));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            swap[(warp * kTok / 2 + j) * 32 + lane] = rows ? o[j][0] : o[j][1];
-            if constexpr (kTok == 16) swap[(warp * 8 + 4 + j) * 32 + lane] = rows ? o[j][2] : o[j][3];
+                for (int i = 0; i < kOct; ++i) mma(sc[i], qa, k4[2 * i], k4[2 * i + 1]);
+            }
         }
     }
-    if (commits) tc::fence_proxy_async_smem();
+    if (scores) {
+        const uint32_t at = own_at + (col ? Sm::kPend : Sm::kScore) + rows * Sm::kRect + (gr * Sm::kPitch + 2 * tq) * 4;
+#pragma unroll
+        for (int i = 0; i < kOct; ++i) {
+            sts_f32x2(at + 32 * i, sc[i][0], sc[i][1]);
+            if constexpr (kTok == 16) sts_f32x2(at + 32 * i + 8 * Sm::kPitch * 4, sc[i][2], sc[i][3]);
+        }
+    }
+    if (kC) tc::fence_proxy_async_smem();
     group_sync(group);
 
     // 3. the state goes back
-    if (commits && tid == 0) {
+    if (kC && tid == 0) {
         for (int b = 0; b < Sm::kBoxes; ++b)
             tc::tma_store_3d(&maps.pool, it.half * kHalf + b * Sm::kBoxCols, 0,
                              static_cast<int32_t>(static_cast<int64_t>(it.slot) * a.H + it.h), smem + Sm::kState + b * Sm::kStateTile);
         tc::tma_store_commit();
     }
 
+    // each warp finishes the first (rows = 0) or second four of a lane's 8 columns and hands the sums
+    // of the others to the warp with the other key rows
+    float *swap = reinterpret_cast<float *>(smem + Sm::kSwap);
+    if (kT) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            swap[(warp * kTok / 2 + j) * 32 + lane] = rows ? o[j][0] : o[j][1];
+            if constexpr (kTok == 16) swap[(warp * 8 + 4 + j) * 32 + lane] = rows ? o[j][2] : o[j][3];
+        }
+    }
+    if (kT) group_sync(group);
+
     // 4. o_t = scale ( head_t (Q S)_t + sum_{j <= t} decay_tj score_tj v_j ), rows gr, gr + 8; bf16: with
     // fade (Q S)_t + sum_j w_j (q_t . pk_j) pv_j in place of (Q S)_t
-    if (tokens) {
-        const float *score = reinterpret_cast<const float *>(own + Sm::kScore);
-        const float *decay = reinterpret_cast<const float *>(own + Sm::kDecay);
+    if (kT) {
         const float h0 = __shfl_sync(0xffffffffu, ng.head, gr), h1 = __shfl_sync(0xffffffffu, ng.head, gr + 8);
         const int first = 32 * col + 8 * tq + 4 * rows;   // the lane's 4 columns
+        // products of the lane's rows with tokens t, t + 1, from the two halves of the keys' columns
+        auto product = [&](uint32_t rect, int r, int t) {
+            const uint32_t at = own_at + rect + (r * Sm::kPitch + t) * 4;
+            const float2 x = lds_f32x2(at), y = lds_f32x2(at + Sm::kRect);
+            return make_float2(x.x + y.x, x.y + y.y);
+        };
         float y0[4], y1[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            y0[j] = (kBf16 ? fade : 1.f) * ((rows ? o[j][1] : o[j][0]) + swap[((warp ^ 2) * kTok / 2 + j) * 32 + lane]);
-            if constexpr (kTok == 16) y1[j] = (kBf16 ? fade : 1.f) * ((rows ? o[j][3] : o[j][2]) + swap[((warp ^ 2) * 8 + 4 + j) * 32 + lane]);
+            y0[j] = h0 * (kBf16 ? fade : 1.f) * ((rows ? o[j][1] : o[j][0]) + swap[(warp ^ 2) * kTok / 2 * 32 + j * 32 + lane]);
+            if constexpr (kTok == 16)
+                y1[j] = h1 * (kBf16 ? fade : 1.f) * ((rows ? o[j][3] : o[j][2]) + swap[((warp ^ 2) * 8 + 4 + j) * 32 + lane]);
         }
-        if (kBf16 && commits) {
-            const uint32_t pend = own_at + Sm::kPend + (gr * kTok + 2 * tq) * 4;
-            uint32_t pa[2][2 * kOct];   // w_j (q_t . pk_j) in two bf16 parts
-            uint32_t bv[4][2];          // pv: column 4 gr + j of tokens 2 tq, + 1, + 8, + 9
-#pragma unroll
-            for (int i = 0; i < kOct; ++i) {
-                const int t = 2 * tq + 8 * i;
-                const float w0 = __shfl_sync(0xffffffffu, pg.tail, t), w1 = __shfl_sync(0xffffffffu, pg.tail, t + 1);
-                float2 s0 = lds_f32x2(pend + 32 * i), s1 = lds_f32x2(pend + 32 * i + (kTok == 16 ? 8 * kTok * 4 : 0));
-                if (kTok == 8) s1 = make_float2(0.f, 0.f);
-                s0.x = t < commits ? s0.x * w0 : 0.f, s1.x = t < commits ? s1.x * w0 : 0.f;
-                s0.y = t + 1 < commits ? s0.y * w1 : 0.f, s1.y = t + 1 < commits ? s1.y * w1 : 0.f;
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    pa[p][2 * i] = split_bf16(s0.x, s0.y);
-                    pa[p][2 * i + 1] = split_bf16(s1.x, s1.y);
-                }
-                const uint2 a0 = pend_values(t), a1 = pend_values(t + 1);
-                bv[0][i] = __byte_perm(a0.x, a1.x, 0x5410) & there[i];
-                bv[1][i] = __byte_perm(a0.x, a1.x, 0x7632) & there[i];
-                bv[2][i] = __byte_perm(a0.y, a1.y, 0x5410) & there[i];
-                bv[3][i] = __byte_perm(a0.y, a1.y, 0x7632) & there[i];
-            }
+        // tokens' weights (A operand, two bf16 parts) times their values, 8 or 16 tokens
+        auto add_tokens = [&](const uint32_t (&pa)[2][2 * kOct], const uint32_t (&bv)[4][kOct]) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float d[4];
@@ -558,36 +564,60 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
                 y0[j] += rows ? d[1] : d[0];
                 if constexpr (kTok == 16) y1[j] += rows ? d[3] : d[2];
             }
+        };
+        if (kBf16 && kC) {
+            uint32_t pa[2][2 * kOct], bv[4][kOct];
+#pragma unroll
+            for (int i = 0; i < kOct; ++i) {
+                const int t = 2 * tq + 8 * i;
+                const float w0 = __shfl_sync(0xffffffffu, pg.tail, t), w1 = __shfl_sync(0xffffffffu, pg.tail, t + 1);
+                float2 s0 = product(Sm::kPend, gr, t), s1 = make_float2(0.f, 0.f);
+                if constexpr (kTok == 16) s1 = product(Sm::kPend, gr + 8, t);
+                s0.x = t < commits ? s0.x * w0 * h0 : 0.f, s1.x = t < commits ? s1.x * w0 * h1 : 0.f;
+                s0.y = t + 1 < commits ? s0.y * w1 * h0 : 0.f, s1.y = t + 1 < commits ? s1.y * w1 * h1 : 0.f;
+                split_row(pa, 2 * i, s0);
+                split_row(pa, 2 * i + 1, s1);
+                pack_values(bv, i, values(Sm::kPv, t), values(Sm::kPv, t + 1), there[i]);
+            }
+            add_tokens(pa, bv);
         }
+        uint32_t bv[4][kOct], odd_values = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            y0[j] *= h0;
-            if constexpr (kTok == 16) y1[j] *= h1;
+        for (int i = 0; i < kOct; ++i) {
+            const int t = 2 * tq + 8 * i;
+            const uint32_t in = (t < tokens ? 0xffffu : 0u) | (t + 1 < tokens ? 0xffff0000u : 0u);
+            pack_values(bv, i, values(Sm::kV, t), values(Sm::kV, t + 1), in);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) odd_values |= not_finite(bv[j][i]);
         }
+        if (!__any_sync(0xffffffffu, odd_values != 0)) {
+            uint32_t pa[2][2 * kOct];
 #pragma unroll
-        for (int j0 = 0; j0 < kTok; j0 += 4) {
-            if (j0 >= tokens) break;
-            // of rows gr (which ends before token 8) and gr + 8
-            float p0[4], p1[4];
-            if (j0 < 8) weights4(p0, score + gr * kTok + j0, decay + gr * kTok + j0);
-            if constexpr (kTok == 16) weights4(p1, score + (gr + 8) * kTok + j0, decay + (gr + 8) * kTok + j0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = j0 + i;
-                if (j >= tokens) break;
+            for (int i = 0; i < kOct; ++i) {
+                const int t = 2 * tq + 8 * i;
+                auto weights = [&](int r) {   // 0 for the tokens after token r
+                    const float2 s = product(Sm::kScore, r, t), d = lds_f32x2(own_at + Sm::kDecay + (r * Sm::kPitch + t) * 4);
+                    return make_float2(t <= r ? s.x * d.x : 0.f, t + 1 <= r ? s.y * d.y : 0.f);
+                };
+                split_row(pa, 2 * i, weights(gr));
+                split_row(pa, 2 * i + 1, kTok == 16 ? weights(gr + 8) : make_float2(0.f, 0.f));
+            }
+            add_tokens(pa, bv);
+        } else {
+            // an infinity or NaN among the values: one product at a time, so that it reaches no token
+            // before its own
+            for (int j = 0; j < tokens; ++j) {
                 const uint2 w = lds_u32x2(st + Sm::kV + chunk(j, first / 8) + rows * 8);
                 const float2 v0 = bf16x2_to_float2(w.x), v1 = bf16x2_to_float2(w.y);
-                if (j0 < 8 && j <= gr) {
-                    y0[0] = fmaf(p0[i], v0.x, y0[0]);
-                    y0[1] = fmaf(p0[i], v0.y, y0[1]);
-                    y0[2] = fmaf(p0[i], v1.x, y0[2]);
-                    y0[3] = fmaf(p0[i], v1.y, y0[3]);
-                }
-                if (kTok == 16 && j <= gr + 8) {
-                    y1[0] = fmaf(p1[i], v0.x, y1[0]);
-                    y1[1] = fmaf(p1[i], v0.y, y1[1]);
-                    y1[2] = fmaf(p1[i], v1.x, y1[2]);
-                    y1[3] = fmaf(p1[i], v1.y, y1[3]);
+                const float v[4] = {v0.x, v0.y, v1.x, v1.y};
+#pragma unroll
+                for (int r = 0; r < kOct; ++r) {
+                    const int t = gr + 8 * r;
+                    if (j > t) continue;
+                    const float s = product(Sm::kScore, t, j & ~1).x, s1 = product(Sm::kScore, t, j & ~1).y;
+                    const float p = (j & 1 ? s1 : s) * reinterpret_cast<const float *>(own + Sm::kDecay)[t * Sm::kPitch + j];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) (r ? y1 : y0)[c] = fmaf(p, v[c], (r ? y1 : y0)[c]);
                 }
             }
         }
@@ -642,7 +672,7 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
         for (unsigned item = blockIdx.x; item < items; item += step) {
             const Item it = next;
             next = read(item + step);   // its latency hides behind this item's copies
-            if (__any_sync(0xffffffffu, !tc::mbar_wait(&empty[stage], parity, tck::kWaitNs))) {
+            if (__any_sync(0xffffffffu, !ring_wait(&empty[stage], parity))) {
                 if (lane == 0) record_status(a.status, SALA_ERR_TIMEOUT);
                 break;
             }
@@ -655,7 +685,7 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
         }
         // no copy outlives the CTA, however it ends: the last ones of every stage have landed
         for (unsigned k = staged > Sm::kStages ? staged - Sm::kStages : 0; k < staged; ++k)
-            if (!tc::mbar_wait(&full[k % Sm::kFulls], (k / Sm::kFulls) & 1, tck::kWaitNs)) break;
+            if (!ring_wait(&full[k % Sm::kFulls], (k / Sm::kFulls) & 1)) break;
         return;
     }
 
@@ -664,7 +694,7 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
     int stage = group, mine = group;
     uint32_t parity = 0;
     for (unsigned item = blockIdx.x + group * step; item < items; item += Sm::kGroups * step) {
-        const bool late = !tc::mbar_wait(&full[mine], parity, tck::kWaitNs);
+        const bool late = !ring_wait(&full[mine], parity);
         if (late) record_status(a.status, SALA_ERR_TIMEOUT);
         __syncwarp();
         // also: the group's memory of the item before is free
@@ -674,8 +704,11 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
         for (int e = it.tokens * 8 + tid; e < static_cast<int>(a.T) * 8; e += kGroupThreads)   // rows past the count
             *reinterpret_cast<uint4 *>(a.o + ((it.n * a.T + e / 8) * a.H + it.h) * kD + it.half * kHalf + 8 * (e % 8)) =
                 make_uint4(0, 0, 0, 0);
-        if (it.commits || it.tokens) run_item<kBf16, kTok>(a, maps, at, side, own, it, group);
+        if (it.commits && it.tokens) run_item<kBf16, kTok, true, true>(a, maps, at, side, own, it, group);
+        else if (it.commits) run_item<kBf16, kTok, true, false>(a, maps, at, side, own, it, group);
+        else if (it.tokens) run_item<kBf16, kTok, false, true>(a, maps, at, side, own, it, group);
         if (tid == 0) tc::tma_store_wait_read<0>();
+        tc::fence_proxy_async_smem();   // the stage was written to, and TMA writes to it next
         __syncwarp();
         if ((tid & 31) == 0) tc::mbar_arrive(&empty[stage]);
         stage = (stage + Sm::kGroups) % Sm::kStages;

@@ -218,3 +218,35 @@ def test_graph_and_side_stream(sg):
     torch.cuda.synchronize()
     assert torch.equal(out.cpu(), o.cpu())
     _check(c, out.cpu(), d["pool"].cpu(), 0.125)
+
+
+@pytest.mark.parametrize("storage", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,Tp", [(5, 5), (8, 3), (13, 16), (20, 19)])
+def test_masked_places_hold_anything(sg, T, Tp, storage):
+    # NaN in tokens past the counts (and in their gates) changes nothing
+    c = _case(6, T, Tp, 2, 9, storage, seed=T + Tp)
+    c["accepted"][0], c["counts"][0] = -1, 0
+    o, pool = _run(sg, c, 0.125)
+    for n in range(6):
+        for t in c["pending"]:
+            t[n, int(c["accepted"][n]) + 1:] = float("nan")
+        for name in ("q", "k", "v", "g"):
+            c[name][n, int(c["counts"][n]):] = float("nan")
+    o2, pool2 = _run(sg, c, 0.125)
+    assert torch.equal(o, o2) and torch.equal(pool, pool2)
+
+
+@pytest.mark.parametrize("storage", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,at", [(6, 3), (16, 11), (12, 0)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_bad_value_reaches_only_the_tokens_from_its_own_on(sg, T, at, bad, storage):
+    c = _case(2, T, 2, 2, 3, storage, seed=T, ragged=False)
+    o, pool = _run(sg, c, 0.125)
+    c["v"][1, at, 0, 77] = bad
+    o2, pool2 = _run(sg, c, 0.125)
+    assert torch.equal(pool, pool2)
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[1, at:, 0, 77] = True
+    assert not o2[hit].isfinite().any()
+    near = (o.double() - o2.double()).abs() <= 2 * E16 * o.double().abs() + 1e-6
+    assert torch.all(near | hit)
