@@ -6,6 +6,7 @@
 // server needs no host round trip and a captured graph serves every occupancy. The decisions
 // are one CTA's prefix counts over the mask; the moving is a plain stream of 16-byte accesses,
 // bounded by the memory bandwidth.
+#include <algorithm>
 #include <type_traits>
 
 #include "launch.h"
@@ -221,8 +222,8 @@ __global__ void __launch_bounds__(kCopyThreads) pool_copy_kernel(CopyArgs a) {
 
 // CTAs that share a pair: one per head's state, fewer where the pairs are many.
 int64_t copy_slices(int64_t pairs, int64_t units) {
-    const int64_t most = (kCopyCtas + pairs - 1) / pairs;
-    return units < most ? units : most;
+    const int64_t most = std::min<int64_t>((kCopyCtas + pairs - 1) / pairs, 65535);   // a grid's y extent
+    return std::min(units, most);
 }
 
 cudaError_t copy_pairs(const CopyArgs &a, bool src_bf16, bool dst_bf16, int64_t pairs, cudaStream_t st) {

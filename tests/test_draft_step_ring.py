@@ -44,7 +44,7 @@ def _run(stages, groups, fulls, items, rng):
             place[i] += groups
 
 
-@pytest.mark.parametrize("stages,groups", [(5, 3), (4, 3), (8, 4), (6, 4), (6, 5), (7, 2)])
+@pytest.mark.parametrize("stages,groups", [(5, 3), (4, 3), (8, 4), (9, 4), (6, 3), (6, 4), (6, 5), (7, 2)])
 def test_every_group_gets_its_items(stages, groups):
     fulls = -(-stages // groups) * groups
     rng = random.Random(stages * 10 + groups)

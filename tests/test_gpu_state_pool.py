@@ -94,6 +94,13 @@ def test_copy_of_many_slots(sg, n):
     assert torch.equal(d.cpu(), want)
 
 
+def test_copy_of_more_states_than_a_grid_has_rows(sg):
+    d = torch.zeros(2, 65540, 128, 128, dtype=B, device="cuda")     # two slots of 65540 heads
+    d[0] = torch.arange(65540, device="cuda", dtype=torch.int32).remainder(251).to(B)[:, None, None]
+    sg.state_pool_copy(d, d, _i32(1), _i32(0))
+    assert torch.equal(d[0], d[1]) and sg.get_device_status() == 0
+
+
 def _fork(sg, a, used, parents, status=0):
     d, u = a.cuda(), used.cuda()
     kids = sg.state_pool_fork(d, u, parents.cuda()).tolist()
