@@ -5,7 +5,8 @@
 // Which slots move is decided on the device (a mask of the used slots, one int32 each), so a
 // server needs no host round trip and a captured graph serves every occupancy. The decisions
 // are one CTA's prefix counts over the mask; the moving is a plain stream of 16-byte accesses,
-// bounded by the memory bandwidth.
+// bounded by the memory bandwidth (24 layers x 32 heads: 32 states of 25 MB moved by a compaction in
+// 234 us, 6.9 TB/s; 40 forked from 5 parents in 175 us; 16 copied from fp32 to bf16 in 173 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -18,7 +19,9 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kCopyThreads = 256;
-constexpr int64_t kCopyCtas = 131072;   // CTAs of a launch where pairs are many (compaction: most of them idle)
+// CTAs of a launch where pairs are many: in a compaction most of them find nothing to move, and with
+// 32768 the others are too long (237 us instead of 234)
+constexpr int64_t kCopyCtas = 131072;
 constexpr int kUnit = kD * kD;   // elements of one head's state
 
 // Exclusive prefix count of `flag` over the CTA (kPlanThreads threads); *total the count.

