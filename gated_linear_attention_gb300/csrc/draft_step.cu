@@ -26,7 +26,7 @@
 // Places past the counts hold anything: pending tokens there are masked out of every operand, and the
 // products among the new tokens go one by one where a value is not finite, so nothing of a masked place
 // reaches a result.
-// Longer steps (draft_step_long_kernel) run the plain form below.
+// Longer steps (draft_step_long_kernel) take 16 tokens at a time over a state held in shared memory.
 //
 // Bound by the memory with fp32 states: 256 rows of 5 tokens, 32 heads, 181 us, 6.2 TB/s of what has to
 // move; 16 tokens, 195 us. With bf16 states the same tokens come with half the bytes and the
@@ -336,10 +336,11 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 
 // One item by a group of 4 warps, from its stage `smem` and what stands beside it; `own`: the group's
 // memory. Thread 0 of the group leaves a store of the state in flight that still reads the stage.
-// kC, kT: there is something to commit, there are new tokens.
-template <bool kBf16, int kTok, bool kC, bool kT>
-__device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &maps, uint8_t *smem, const uint8_t *side, uint8_t *own,
-                                         const Item &it, int group) {
+// kC, kT: there is something to commit, there are new tokens; kStore: what was committed goes to `pool`
+// from here (else it stays in the stage). t0: place of the first new token in its row.
+template <bool kBf16, int kTok, bool kC, bool kT, bool kStore = kC>
+__device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *pool, uint8_t *smem, const uint8_t *side,
+                                         uint8_t *own, const Item &it, int group, int64_t t0 = 0) {
     using Sm = StepSmem<kBf16, kTok>;
     constexpr int kParts = 3;   // of w_j v_j in fp32: what three bf16 parts leave out is below 2^-26 of it
     constexpr int kOct = kTok / 8;
@@ -519,13 +520,13 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
             if constexpr (kTok == 16) sts_f32x2(at + 32 * i + 8 * Sm::kPitch * 4, sc[i][2], sc[i][3]);
         }
     }
-    if (kC) tc::fence_proxy_async_smem();
+    if (kStore) tc::fence_proxy_async_smem();
     group_sync(group);
 
     // 3. the state goes back
-    if (kC && tid == 0) {
+    if (kStore && tid == 0) {
         for (int b = 0; b < Sm::kBoxes; ++b)
-            tc::tma_store_3d(&maps.pool, it.half * kHalf + b * Sm::kBoxCols, 0,
+            tc::tma_store_3d(pool, it.half * kHalf + b * Sm::kBoxCols, 0,
                              static_cast<int32_t>(static_cast<int64_t>(it.slot) * a.H + it.h), smem + Sm::kState + b * Sm::kStateTile);
         tc::tma_store_commit();
     }
@@ -627,7 +628,7 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const StepMaps &map
                 }
             }
         }
-        uint16_t *out = a.o + ((it.n * a.T + gr) * a.H + it.h) * kD + it.half * kHalf + first;
+        uint16_t *out = a.o + ((it.n * a.T + t0 + gr) * a.H + it.h) * kD + it.half * kHalf + first;
         if (gr < tokens)
             *reinterpret_cast<uint2 *>(out) = make_uint2(float2_to_bf16x2(a.scale * y0[0], a.scale * y0[1]),
                                                          float2_to_bf16x2(a.scale * y0[2], a.scale * y0[3]));
@@ -710,9 +711,9 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
         for (int e = it.tokens * 8 + tid; e < static_cast<int>(a.T) * 8; e += kGroupThreads)   // rows past the count
             *reinterpret_cast<uint4 *>(a.o + ((it.n * a.T + e / 8) * a.H + it.h) * kD + it.half * kHalf + 8 * (e % 8)) =
                 make_uint4(0, 0, 0, 0);
-        if (it.commits && it.tokens) run_item<kBf16, kTok, true, true>(a, maps, at, side, own, it, group);
-        else if (it.commits) run_item<kBf16, kTok, true, false>(a, maps, at, side, own, it, group);
-        else if (it.tokens) run_item<kBf16, kTok, false, true>(a, maps, at, side, own, it, group);
+        if (it.commits && it.tokens) run_item<kBf16, kTok, true, true>(a, &maps.pool, at, side, own, it, group);
+        else if (it.commits) run_item<kBf16, kTok, true, false>(a, &maps.pool, at, side, own, it, group);
+        else if (it.tokens) run_item<kBf16, kTok, false, true>(a, &maps.pool, at, side, own, it, group);
         if (tid == 0) tc::tma_store_wait_read<0>();
         tc::fence_proxy_async_smem();   // the stage was written to, and TMA writes to it next
         __syncwarp();
@@ -726,191 +727,101 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
 
 // ---- longer steps ----------------------------------------------------------------------------
 //
-// One CTA of 256 threads per (sequence, head); thread (w, l) holds rows [16 w, 16 w + 16) and
-// columns [4 l, 4 l + 4) of the state in fp32. Tokens are taken in blocks of 8.
+// One CTA of 4 warps per item. The state half stays in shared memory in fp32, whatever the pool's
+// type, and 16 tokens at a time go over it: the accepted ones, then (the state stored) the new ones,
+// each 16 of which are read and then added for the next. The blocks are loaded as they are needed;
+// four CTAs on an SM hide that from each other.
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kRows = kD / kWarps;   // state rows of a warp
-constexpr int kBlock = 8;            // tokens in flight
-
-struct Tile {
-    float q[kBlock][kD], k[kBlock][kD], v[kBlock][kD];
-    float part[kWarps][kBlock][kD];
-    float score[kBlock][kBlock];   // exp(g_{j+1} + .. + g_t) (q_t . k_j)
-    float gate[kBlock];
-    float tail[kBlock];            // exp(g_{j+1} + .. + g_last)
-    float head[kBlock];            // exp(g_1 + .. + g_t)
-};
-
-// `m` rows of [tokens, H, 128] bf16 into a tile, from token t0 of row n.
-__device__ __forceinline__ void load_rows(float (*dst)[kD], const uint16_t *src, int64_t row0, int H, int m) {
-    for (int e = threadIdx.x; e < m * (kD / 2); e += kThreads) {
-        const int t = e / (kD / 2), c = e % (kD / 2);
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(src + (row0 + static_cast<int64_t>(t) * H) * kD) + c);
-        const float2 f = bf16x2_to_float2(w);
-        dst[t][2 * c] = f.x;
-        dst[t][2 * c + 1] = f.y;
+// m token rows of [tokens, H, 128]: all of a row (kWide) or the item's half.
+template <bool kWide>
+__device__ __forceinline__ void put_tokens(uint8_t *dst, const uint16_t *src, int64_t row0, int H, int m) {
+    constexpr int kChunks = kWide ? 16 : 8;
+    for (int e = threadIdx.x; e < m * kChunks; e += kGroupThreads) {
+        const int t = e / kChunks, c = e % kChunks;
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + (row0 + static_cast<int64_t>(t) * H) * kD) + c);
+        *reinterpret_cast<uint4 *>(dst + (kWide ? wide_chunk(t, c >> 3, c & 7) : chunk(t, c))) = w;
     }
 }
-
-// head and tail of the m gates in the tile (thread 0; at most kBlock of them).
-__device__ __forceinline__ void gate_sums(Tile &s, int m) {
-    if (threadIdx.x == 0) {
-        float sum = 0.f;
-        for (int t = 0; t < m; ++t) {
-            sum += s.gate[t];
-            s.head[t] = expf(sum);
-        }
-        sum = 0.f;
-        for (int t = m - 1; t >= 0; --t) {
-            s.tail[t] = expf(sum);
-            sum += s.gate[t];
-        }
-    }
-}
-
-// S = exp(all gates) S + sum_j tail_j k_j^T v_j over the m tokens of the tile.
-__device__ __forceinline__ void advance(float4 *x, const Tile &s, int m, int row0, int lane) {
-    const float a = s.head[m - 1];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        x[r].x *= a;
-        x[r].y *= a;
-        x[r].z *= a;
-        x[r].w *= a;
-    }
-    for (int j = 0; j < m; ++j) {
-        float4 v = *reinterpret_cast<const float4 *>(&s.v[j][4 * lane]);
-        const float w = s.tail[j];
-        v.x *= w;
-        v.y *= w;
-        v.z *= w;
-        v.w *= w;
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const float k = s.k[j][row0 + r];
-            x[r].x = fmaf(k, v.x, x[r].x);
-            x[r].y = fmaf(k, v.y, x[r].y);
-            x[r].z = fmaf(k, v.z, x[r].z);
-            x[r].w = fmaf(k, v.w, x[r].w);
-        }
-    }
+__device__ __forceinline__ void put_gates(uint8_t *dst, const float *g, int64_t row0, int H, int m) {
+    const int t = threadIdx.x;
+    if (t < m) reinterpret_cast<float *>(dst)[t] = __ldg(g + row0 + static_cast<int64_t>(t) * H);
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) draft_step_long_kernel(DraftArgs a) {
+__global__ void __launch_bounds__(kGroupThreads) draft_step_long_kernel(DraftArgs a) {
     dependent_start();
-    __shared__ Tile s;
-    const int unit = blockIdx.x, n = unit / a.H, h = unit - n * a.H;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row0 = warp * kRows;
-    const Row row = read_row(a, n, threadIdx.x == 0);
-    const int64_t commits = row.commits, tokens = row.tokens;
-    for (int64_t e = tokens * (kD / 8) + threadIdx.x; e < a.T * (kD / 8); e += kThreads) {
-        const int64_t t = e / (kD / 8);
-        uint16_t *row = a.o + ((n * a.T + t) * a.H + h) * kD;
-        reinterpret_cast<uint4 *>(row)[e % (kD / 8)] = make_uint4(0, 0, 0, 0);
-    }
-    if (commits == 0 && tokens == 0) return;
+    using Sm = StepSmem<false, 16>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *side = smem + Sm::kStage, *own = side + Sm::kSide;
+    const int unit = blockIdx.x >> 1, half = blockIdx.x & 1, n = unit / a.H, h = unit - n * a.H, tid = threadIdx.x;
+    const Row row = read_row(a, n, tid == 0);
+    for (int64_t e = row.tokens * 8 + tid; e < a.T * 8; e += kGroupThreads)   // rows past the count
+        *reinterpret_cast<uint4 *>(a.o + ((n * a.T + e / 8) * a.H + h) * kD + half * kHalf + 8 * (e % 8)) = make_uint4(0, 0, 0, 0);
+    if (row.commits == 0 && row.tokens == 0) return;
 
-    const int64_t at = (static_cast<int64_t>(row.slot) * a.H + h) * kD * kD;
-    float4 x[kRows];
-    if constexpr (kBf16) {
-        const uint16_t *S = static_cast<const uint16_t *>(a.pool) + at;
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(S + (row0 + r) * kD) + lane);
+    // four neighbouring values of the state half: row r, columns 4 c .. 4 c + 3
+    const int64_t at = (static_cast<int64_t>(row.slot) * a.H + h) * kD * kD + half * kHalf;
+    auto place = [&](int r, int c) {
+        return reinterpret_cast<float4 *>(smem + Sm::kState + (c >> 3) * Sm::kStateTile + chunk(r, c & 7));
+    };
+    for (int e = tid; e < kD * kHalf / 4; e += kGroupThreads) {
+        const int r = e / 16, c = e % 16;
+        if constexpr (kBf16) {
+            const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.pool) + at + r * kD) + c);
             const float2 f0 = bf16x2_to_float2(w.x), f1 = bf16x2_to_float2(w.y);
-            x[r] = make_float4(f0.x, f0.y, f1.x, f1.y);
+            *place(r, c) = make_float4(f0.x, f0.y, f1.x, f1.y);
+        } else {
+            *place(r, c) = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(a.pool) + at + r * kD) + c);
         }
-    } else {
-        const float *S = static_cast<const float *>(a.pool) + at;
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) x[r] = __ldcs(reinterpret_cast<const float4 *>(S + (row0 + r) * kD) + lane);
     }
-
-    // 1. commit the accepted tokens of the step before
-    for (int64_t j0 = 0; j0 < commits; j0 += kBlock) {
-        const int m = static_cast<int>(min(static_cast<int64_t>(kBlock), commits - j0));
+    Item it{row.slot, n, h, half, 0, 0, {0, 0}};
+    for (int64_t j0 = 0; j0 < row.commits; j0 += 16) {
+        const int m = static_cast<int>(min(static_cast<int64_t>(16), row.commits - j0));
         const int64_t first = (n * a.T_pend + j0) * a.H + h;
         __syncthreads();
-        load_rows(s.k, a.pk, first, a.H, m);
-        load_rows(s.v, a.pv, first, a.H, m);
-        if (threadIdx.x < m) s.gate[threadIdx.x] = __ldg(a.pg + first + static_cast<int64_t>(threadIdx.x) * a.H);
+        put_tokens<true>(smem + Sm::kPk, a.pk, first, a.H, m);
+        put_tokens<false>(smem + Sm::kPv, a.pv + half * kHalf, first, a.H, m);
+        put_gates(side + Sm::kPg, a.pg, first, a.H, m);
         __syncthreads();
-        gate_sums(s, m);
-        __syncthreads();
-        advance(x, s, m, row0, lane);
+        it.commits = m;
+        run_item<false, 16, true, false, false>(a, nullptr, smem, side, own, it, 0);
     }
-    if (commits) {
-        if constexpr (kBf16) {
-            uint16_t *S = static_cast<uint16_t *>(a.pool) + at;
-#pragma unroll
-            for (int r = 0; r < kRows; ++r)
-                __stcs(reinterpret_cast<uint2 *>(S + (row0 + r) * kD) + lane,
-                       make_uint2(float2_to_bf16x2(x[r].x, x[r].y), float2_to_bf16x2(x[r].z, x[r].w)));
-        } else {
-            float *S = static_cast<float *>(a.pool) + at;
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) __stcs(reinterpret_cast<float4 *>(S + (row0 + r) * kD) + lane, x[r]);
+    it.commits = 0;
+    __syncthreads();
+    if (row.commits) {
+        for (int e = tid; e < kD * kHalf / 4; e += kGroupThreads) {
+            const int r = e / 16, c = e % 16;
+            const float4 f = *place(r, c);
+            if constexpr (kBf16)
+                __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.pool) + at + r * kD) + c,
+                       make_uint2(float2_to_bf16x2(f.x, f.y), float2_to_bf16x2(f.z, f.w)));
+            else
+                __stcs(reinterpret_cast<float4 *>(static_cast<float *>(a.pool) + at + r * kD) + c, f);
         }
     }
-
-    // 2. the new tokens
-    for (int64_t t0 = 0; t0 < tokens; t0 += kBlock) {
-        const int m = static_cast<int>(min(static_cast<int64_t>(kBlock), tokens - t0));
+    for (int64_t t0 = 0; t0 < row.tokens; t0 += 16) {
+        const int m = static_cast<int>(min(static_cast<int64_t>(16), row.tokens - t0));
+        const bool more = t0 + 16 < row.tokens;
         const int64_t first = (n * a.T + t0) * a.H + h;
         __syncthreads();
-        load_rows(s.q, a.q, first, a.H, m);
-        load_rows(s.k, a.k, first, a.H, m);
-        load_rows(s.v, a.v, first, a.H, m);
-        if (threadIdx.x < m) s.gate[threadIdx.x] = __ldg(a.g + first + static_cast<int64_t>(threadIdx.x) * a.H);
-        __syncthreads();
-        gate_sums(s, m);
-        for (int i = warp; i < m * m; i += kWarps) {
-            const int t = i / m, j = i - t * m;
-            if (j > t) continue;
-            float d = 0.f;
-#pragma unroll
-            for (int c = lane; c < kD; c += 32) d = fmaf(s.q[t][c], s.k[j][c], d);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-            float sum = 0.f;
-            for (int i2 = j + 1; i2 <= t; ++i2) sum += s.gate[i2];
-            if (lane == 0) s.score[t][j] = expf(sum) * d;
-        }
-        for (int t = 0; t < m; ++t) {
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const float q = s.q[t][row0 + r];
-                acc.x = fmaf(q, x[r].x, acc.x);
-                acc.y = fmaf(q, x[r].y, acc.y);
-                acc.z = fmaf(q, x[r].z, acc.z);
-                acc.w = fmaf(q, x[r].w, acc.w);
-            }
-            *reinterpret_cast<float4 *>(&s.part[warp][t][4 * lane]) = acc;
+        put_tokens<true>(smem + Sm::kQ, a.q, first, a.H, m);
+        put_tokens<true>(smem + Sm::kK, a.k, first, a.H, m);
+        put_tokens<false>(smem + Sm::kV, a.v + half * kHalf, first, a.H, m);
+        put_gates(side + Sm::kG, a.g, first, a.H, m);
+        if (more) {   // and once more as the tokens to add
+            put_tokens<true>(smem + Sm::kPk, a.k, first, a.H, m);
+            put_tokens<false>(smem + Sm::kPv, a.v + half * kHalf, first, a.H, m);
+            put_gates(side + Sm::kPg, a.g, first, a.H, m);
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < m * (kD / 2); e += kThreads) {
-            const int t = e / (kD / 2), c = 2 * (e % (kD / 2));
-            float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                a0 += s.part[w][t][c];
-                a1 += s.part[w][t][c + 1];
-            }
-            a0 *= s.head[t];
-            a1 *= s.head[t];
-            for (int j = 0; j <= t; ++j) {
-                a0 = fmaf(s.score[t][j], s.v[j][c], a0);
-                a1 = fmaf(s.score[t][j], s.v[j][c + 1], a1);
-            }
-            reinterpret_cast<uint32_t *>(a.o + (first + static_cast<int64_t>(t) * a.H) * kD)[c / 2] =
-                float2_to_bf16x2(a.scale * a0, a.scale * a1);
+        it.tokens = m;
+        run_item<false, 16, false, true, false>(a, nullptr, smem, side, own, it, 0, t0);
+        if (more) {
+            __syncthreads();
+            it.commits = m, it.tokens = 0;
+            run_item<false, 16, true, false, false>(a, nullptr, smem, side, own, it, 0);
+            it.commits = 0;
         }
-        if (t0 + kBlock < tokens) advance(x, s, m, row0, lane);
     }
 }
 
@@ -928,6 +839,8 @@ cudaError_t token_map(CUtensorMap *map, const void *tokens, int64_t N, int64_t T
     const cuuint32_t box[5] = {64, values ? 1u : 2u, 1, 8, 1};
     return tck::encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, tokens, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
+
+constexpr size_t kLongBytes = StepSmem<false, 16>::kStage + StepSmem<false, 16>::kSide + StepSmem<false, 16>::kOwn;
 
 template <bool kBf16, int kTok>
 cudaError_t launch_step(const DraftArgs &a, const StepMaps &maps, unsigned items, unsigned grid, cudaStream_t stream) {
@@ -965,9 +878,8 @@ cudaError_t launch_draft_step(const void *q, const void *k, const void *v, const
         return bf16 ? (few ? launch_step<true, 8>(a, maps, items, grid, stream) : launch_step<true, 16>(a, maps, items, grid, stream))
                     : (few ? launch_step<false, 8>(a, maps, items, grid, stream) : launch_step<false, 16>(a, maps, items, grid, stream));
     }
-    // (256 fp32 rows of 5 tokens: 308 us this way, 180 us above)
-    return launch_dependent(bf16 ? draft_step_long_kernel<true> : draft_step_long_kernel<false>,
-                            static_cast<unsigned>(N * H), kThreads, stream, a);
+    return launch_dependent_cluster(bf16 ? draft_step_long_kernel<true> : draft_step_long_kernel<false>,
+                                    static_cast<unsigned>(2 * N * H), 0, kGroupThreads, kLongBytes, stream, a);
 }
 
 namespace {
@@ -983,6 +895,10 @@ cudaError_t setup_draft_step_kernel() {
     if (e == cudaSuccess) e = allow_smem<true, 16>();
     if (e == cudaSuccess) e = allow_smem<false, 8>();
     if (e == cudaSuccess) e = allow_smem<false, 16>();
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(draft_step_long_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLongBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(draft_step_long_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLongBytes);
     return e;
 }
 
