@@ -728,9 +728,10 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
 // ---- longer steps ----------------------------------------------------------------------------
 //
 // One CTA of 4 warps per item. The state half stays in shared memory in fp32, whatever the pool's
-// type, and 16 tokens at a time go over it: the accepted ones, then (the state stored) the new ones,
-// each 16 of which are read and then added for the next. The blocks are loaded as they are needed;
-// four CTAs on an SM hide that from each other.
+// type, and blocks of up to 16 tokens go over it: a pass adds one block and reads the state for
+// another. The accepted tokens are added first, the last of them in the pass that reads for the first
+// new tokens; then the state is stored, and each pass adds the block that the one before read for. The
+// blocks are loaded as they are needed; four CTAs on an SM hide that from each other.
 
 // m token rows of [tokens, H, 128]: all of a row (kWide) or the item's half.
 template <bool kWide>
@@ -775,52 +776,44 @@ __global__ void __launch_bounds__(kGroupThreads) draft_step_long_kernel(DraftArg
         }
     }
     Item it{row.slot, n, h, half, 0, 0, {0, 0}};
-    for (int64_t j0 = 0; j0 < row.commits; j0 += 16) {
-        const int m = static_cast<int>(min(static_cast<int64_t>(16), row.commits - j0));
-        const int64_t first = (n * a.T_pend + j0) * a.H + h;
+    const int64_t pend0 = n * a.T_pend * a.H + h, new0 = n * a.T * a.H + h;   // token rows of this head
+    const int64_t before = (row.commits + 15) / 16, reads = (row.tokens + 15) / 16;   // blocks of either
+    const int64_t first_read = before > 1 ? before - 1 : 0;
+    for (int64_t p = 0; p < before || p < first_read + reads; ++p) {
+        const bool pending = p < before;
+        const int64_t t0 = 16 * (p - first_read);         // of the tokens that are read for
+        const int64_t j0 = pending ? 16 * p : t0 - 16;    // of those that are added
+        it.tokens = t0 >= 0 ? static_cast<int>(min(static_cast<int64_t>(16), row.tokens - t0)) : 0;
+        it.commits = j0 >= 0 ? static_cast<int>(min(static_cast<int64_t>(16), (pending ? row.commits : row.tokens) - j0)) : 0;
         __syncthreads();
-        put_tokens<true>(smem + Sm::kPk, a.pk, first, a.H, m);
-        put_tokens<false>(smem + Sm::kPv, a.pv + half * kHalf, first, a.H, m);
-        put_gates(side + Sm::kPg, a.pg, first, a.H, m);
-        __syncthreads();
-        it.commits = m;
-        run_item<false, 16, true, false, false>(a, nullptr, smem, side, own, it, 0);
-    }
-    it.commits = 0;
-    __syncthreads();
-    if (row.commits) {
-        for (int e = tid; e < kD * kHalf / 4; e += kGroupThreads) {
-            const int r = e / 16, c = e % 16;
-            const float4 f = *place(r, c);
-            if constexpr (kBf16)
-                __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.pool) + at + r * kD) + c,
-                       make_uint2(float2_to_bf16x2(f.x, f.y), float2_to_bf16x2(f.z, f.w)));
-            else
-                __stcs(reinterpret_cast<float4 *>(static_cast<float *>(a.pool) + at + r * kD) + c, f);
+        if (it.commits) {
+            const int64_t first = (pending ? pend0 : new0) + j0 * a.H;
+            put_tokens<true>(smem + Sm::kPk, pending ? a.pk : a.k, first, a.H, it.commits);
+            put_tokens<false>(smem + Sm::kPv, (pending ? a.pv : a.v) + half * kHalf, first, a.H, it.commits);
+            put_gates(side + Sm::kPg, pending ? a.pg : a.g, first, a.H, it.commits);
         }
-    }
-    for (int64_t t0 = 0; t0 < row.tokens; t0 += 16) {
-        const int m = static_cast<int>(min(static_cast<int64_t>(16), row.tokens - t0));
-        const bool more = t0 + 16 < row.tokens;
-        const int64_t first = (n * a.T + t0) * a.H + h;
-        __syncthreads();
-        put_tokens<true>(smem + Sm::kQ, a.q, first, a.H, m);
-        put_tokens<true>(smem + Sm::kK, a.k, first, a.H, m);
-        put_tokens<false>(smem + Sm::kV, a.v + half * kHalf, first, a.H, m);
-        put_gates(side + Sm::kG, a.g, first, a.H, m);
-        if (more) {   // and once more as the tokens to add
-            put_tokens<true>(smem + Sm::kPk, a.k, first, a.H, m);
-            put_tokens<false>(smem + Sm::kPv, a.v + half * kHalf, first, a.H, m);
-            put_gates(side + Sm::kPg, a.g, first, a.H, m);
+        if (it.tokens) {
+            const int64_t first = new0 + t0 * a.H;
+            put_tokens<true>(smem + Sm::kQ, a.q, first, a.H, it.tokens);
+            put_tokens<true>(smem + Sm::kK, a.k, first, a.H, it.tokens);
+            put_tokens<false>(smem + Sm::kV, a.v + half * kHalf, first, a.H, it.tokens);
+            put_gates(side + Sm::kG, a.g, first, a.H, it.tokens);
         }
         __syncthreads();
-        it.tokens = m;
-        run_item<false, 16, false, true, false>(a, nullptr, smem, side, own, it, 0, t0);
-        if (more) {
+        if (it.commits && it.tokens) run_item<false, 16, true, true, false>(a, nullptr, smem, side, own, it, 0, t0);
+        else if (it.commits) run_item<false, 16, true, false, false>(a, nullptr, smem, side, own, it, 0);
+        else run_item<false, 16, false, true, false>(a, nullptr, smem, side, own, it, 0, t0);
+        if (p == before - 1) {   // the commit is complete
             __syncthreads();
-            it.commits = m, it.tokens = 0;
-            run_item<false, 16, true, false, false>(a, nullptr, smem, side, own, it, 0);
-            it.commits = 0;
+            for (int e = tid; e < kD * kHalf / 4; e += kGroupThreads) {
+                const int r = e / 16, c = e % 16;
+                const float4 f = *place(r, c);
+                if constexpr (kBf16)
+                    __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.pool) + at + r * kD) + c,
+                           make_uint2(float2_to_bf16x2(f.x, f.y), float2_to_bf16x2(f.z, f.w)));
+                else
+                    __stcs(reinterpret_cast<float4 *>(static_cast<float *>(a.pool) + at + r * kD) + c, f);
+            }
         }
     }
 }
