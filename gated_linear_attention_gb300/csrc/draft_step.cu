@@ -730,26 +730,33 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
 // One CTA of 4 warps per item. The state half stays in shared memory in fp32, whatever the pool's
 // type, and blocks of up to 16 tokens go over it: a pass adds one block and reads the state for
 // another. The accepted tokens are added first, the last of them in the pass that reads for the first
-// new tokens; then the state is stored, and each pass adds the block that the one before read for. The
-// blocks are loaded as they are needed; four CTAs on an SM hide that from each other.
+// new tokens; then the state is stored, and each pass adds the block that the one before read for. All
+// copies are asynchronous, a block's at the start of its pass: four CTAs on an SM, which 128 registers a
+// thread allow, hide that from each other (with a second buffer for the blocks, which leaves room for
+// three, 256 fp32 rows of 17 take a fourteenth longer; with plain loads 617 us). Bound by the passes, about
+// 1 us of an SM's time each whatever the block holds: 256 rows of 17, 32 heads, 3 passes, 328 us with fp32
+// states (floor 185), 320 with bf16 (106); 16 rows of 200 bf16 161 us.
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
 // m token rows of [tokens, H, 128]: all of a row (kWide) or the item's half.
 template <bool kWide>
 __device__ __forceinline__ void put_tokens(uint8_t *dst, const uint16_t *src, int64_t row0, int H, int m) {
     constexpr int kChunks = kWide ? 16 : 8;
-    for (int e = threadIdx.x; e < m * kChunks; e += kGroupThreads) {
-        const int t = e / kChunks, c = e % kChunks;
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + (row0 + static_cast<int64_t>(t) * H) * kD) + c);
-        *reinterpret_cast<uint4 *>(dst + (kWide ? wide_chunk(t, c >> 3, c & 7) : chunk(t, c))) = w;
-    }
+    const int c = threadIdx.x % kChunks;
+    for (int t = threadIdx.x / kChunks; t < m; t += kGroupThreads / kChunks)
+        cp_async16(dst + (kWide ? wide_chunk(t, c >> 3, c & 7) : chunk(t, c)), src + (row0 + static_cast<int64_t>(t) * H) * kD + 8 * c);
 }
 __device__ __forceinline__ void put_gates(uint8_t *dst, const float *g, int64_t row0, int H, int m) {
     const int t = threadIdx.x;
-    if (t < m) reinterpret_cast<float *>(dst)[t] = __ldg(g + row0 + static_cast<int64_t>(t) * H);
+    if (t < m) cp_async4(tc::smem_u32(dst) + 4 * t, g + row0 + static_cast<int64_t>(t) * H);
 }
 
+constexpr size_t kLongBytes = StepSmem<false, 16>::kStage + StepSmem<false, 16>::kSide + StepSmem<false, 16>::kOwn;
+
 template <bool kBf16>
-__global__ void __launch_bounds__(kGroupThreads) draft_step_long_kernel(DraftArgs a) {
+__global__ void __launch_bounds__(kGroupThreads, 4) draft_step_long_kernel(DraftArgs a) {
     dependent_start();
     using Sm = StepSmem<false, 16>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -765,54 +772,74 @@ __global__ void __launch_bounds__(kGroupThreads) draft_step_long_kernel(DraftArg
     auto place = [&](int r, int c) {
         return reinterpret_cast<float4 *>(smem + Sm::kState + (c >> 3) * Sm::kStateTile + chunk(r, c & 7));
     };
-    for (int e = tid; e < kD * kHalf / 4; e += kGroupThreads) {
-        const int r = e / 16, c = e % 16;
-        if constexpr (kBf16) {
-            const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.pool) + at + r * kD) + c);
-            const float2 f0 = bf16x2_to_float2(w.x), f1 = bf16x2_to_float2(w.y);
-            *place(r, c) = make_float4(f0.x, f0.y, f1.x, f1.y);
-        } else {
-            *place(r, c) = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(a.pool) + at + r * kD) + c);
-        }
-    }
-    Item it{row.slot, n, h, half, 0, 0, {0, 0}};
     const int64_t pend0 = n * a.T_pend * a.H + h, new0 = n * a.T * a.H + h;   // token rows of this head
-    const int64_t before = (row.commits + 15) / 16, reads = (row.tokens + 15) / 16;   // blocks of either
-    const int64_t first_read = before > 1 ? before - 1 : 0;
-    for (int64_t p = 0; p < before || p < first_read + reads; ++p) {
-        const bool pending = p < before;
-        const int64_t t0 = 16 * (p - first_read);         // of the tokens that are read for
-        const int64_t j0 = pending ? 16 * p : t0 - 16;    // of those that are added
-        it.tokens = t0 >= 0 ? static_cast<int>(min(static_cast<int64_t>(16), row.tokens - t0)) : 0;
-        it.commits = j0 >= 0 ? static_cast<int>(min(static_cast<int64_t>(16), (pending ? row.commits : row.tokens) - j0)) : 0;
-        __syncthreads();
+    const int commits = static_cast<int>(row.commits), tokens = static_cast<int>(row.tokens);   // of one row: fewer than fill the memory
+    const int before = (commits + 15) / 16, first_read = before > 1 ? before - 1 : 0;   // passes that add accepted tokens; that do nothing else
+    const int passes = max(before, first_read + (tokens + 15) / 16);
+    Item it{row.slot, n, h, half, 0, 0, {0, 0}};
+    // What pass p adds and reads for: places (negative: nothing) and counts of up to 16 tokens.
+    auto plan = [&](int p, int &j0, int &t0) {
+        t0 = 16 * (p - first_read), j0 = p < before ? 16 * p : t0 - 16;
+        it.tokens = t0 >= 0 ? min(16, tokens - t0) : 0;
+        it.commits = j0 >= 0 ? min(16, (p < before ? commits : tokens) - j0) : 0;
+    };
+    auto load = [&](int p) {
+        int j0, t0;
+        plan(p, j0, t0);
         if (it.commits) {
-            const int64_t first = (pending ? pend0 : new0) + j0 * a.H;
+            const bool pending = p < before;
+            const int64_t first = (pending ? pend0 : new0) + static_cast<int64_t>(j0) * a.H;
             put_tokens<true>(smem + Sm::kPk, pending ? a.pk : a.k, first, a.H, it.commits);
             put_tokens<false>(smem + Sm::kPv, (pending ? a.pv : a.v) + half * kHalf, first, a.H, it.commits);
             put_gates(side + Sm::kPg, pending ? a.pg : a.g, first, a.H, it.commits);
         }
         if (it.tokens) {
-            const int64_t first = new0 + t0 * a.H;
+            const int64_t first = new0 + static_cast<int64_t>(t0) * a.H;
             put_tokens<true>(smem + Sm::kQ, a.q, first, a.H, it.tokens);
             put_tokens<true>(smem + Sm::kK, a.k, first, a.H, it.tokens);
             put_tokens<false>(smem + Sm::kV, a.v + half * kHalf, first, a.H, it.tokens);
             put_gates(side + Sm::kG, a.g, first, a.H, it.tokens);
         }
+    };
+    load(0);   // on its way while the state comes
+    const int r0 = tid / 16, c0 = tid % 16;   // every eighth row is this thread's
+    if constexpr (kBf16) {
+        uint2 w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            w[i] = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.pool) + at + (8 * i + r0) * kD) + c0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 f0 = bf16x2_to_float2(w[i].x), f1 = bf16x2_to_float2(w[i].y);
+            *place(8 * i + r0, c0) = make_float4(f0.x, f0.y, f1.x, f1.y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            cp_async16(place(8 * i + r0, c0), static_cast<const float *>(a.pool) + at + (8 * i + r0) * kD + 4 * c0);
+    }
+    for (int p = 0; p < passes; ++p) {
+        if (p) {
+            __syncthreads();   // all are through with the tokens before
+            load(p);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
+        int j0, t0;
+        plan(p, j0, t0);
         if (it.commits && it.tokens) run_item<false, 16, true, true, false>(a, nullptr, smem, side, own, it, 0, t0);
         else if (it.commits) run_item<false, 16, true, false, false>(a, nullptr, smem, side, own, it, 0);
         else run_item<false, 16, false, true, false>(a, nullptr, smem, side, own, it, 0, t0);
         if (p == before - 1) {   // the commit is complete
             __syncthreads();
-            for (int e = tid; e < kD * kHalf / 4; e += kGroupThreads) {
-                const int r = e / 16, c = e % 16;
-                const float4 f = *place(r, c);
+#pragma unroll 8
+            for (int i = 0; i < 16; ++i) {
+                const float4 f = *place(8 * i + r0, c0);
                 if constexpr (kBf16)
-                    __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.pool) + at + r * kD) + c,
+                    __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.pool) + at + (8 * i + r0) * kD) + c0,
                            make_uint2(float2_to_bf16x2(f.x, f.y), float2_to_bf16x2(f.z, f.w)));
                 else
-                    __stcs(reinterpret_cast<float4 *>(static_cast<float *>(a.pool) + at + r * kD) + c, f);
+                    __stcs(reinterpret_cast<float4 *>(static_cast<float *>(a.pool) + at + (8 * i + r0) * kD) + c0, f);
             }
         }
     }
@@ -833,8 +860,6 @@ cudaError_t token_map(CUtensorMap *map, const void *tokens, int64_t N, int64_t T
     return tck::encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, tokens, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-constexpr size_t kLongBytes = StepSmem<false, 16>::kStage + StepSmem<false, 16>::kSide + StepSmem<false, 16>::kOwn;
-
 template <bool kBf16, int kTok>
 cudaError_t launch_step(const DraftArgs &a, const StepMaps &maps, unsigned items, unsigned grid, cudaStream_t stream) {
     using Sm = StepSmem<kBf16, kTok>;
@@ -854,6 +879,8 @@ cudaError_t launch_draft_step(const void *q, const void *k, const void *v, const
                       static_cast<const uint16_t *>(pend_k), static_cast<const uint16_t *>(pend_v),
                       pend_g, accepted, scale, pool, slots, P, static_cast<uint16_t *>(o), T, T_pend, H,
                       status};
+    // the persistent kernel where a step is one pass: 256 rows of 16, bf16, in 141 us, 197 by the kernel
+    // for longer ones; fp32 195 and 208; one row of 5, 4.3 and 5.4
     if (T <= 16 && T_pend <= 16) {
         StepMaps maps{};
         cudaError_t e = pool_map(&maps.pool, pool, bf16, P * H);

@@ -363,7 +363,7 @@ int sala_gla_verify_drafts(const void *target_probs, int64_t target_stride, cons
  * The new tokens' k, v and g are the pending ones of the next call. With the tokens of a step
  * laid out as [the last emitted token, draft 0, .., draft K - 1] the accepted counts of
  * sala_gla_verify_drafts are `accepted` here: the last emitted token is always kept. Made for up to
- * 16 new and 16 pending tokens (tensor cores); longer steps run in fp32 multiply-adds.
+ * 16 new and 16 pending tokens; longer steps take 16 at a time.
  *
  *   q, k, v        bf16 [N, T, H, 128];  g fp32 [N, T, H]  (NULL with T = 0: commit only)
  *   num_tokens     int32 [N] tokens of each row, or NULL: T each. Later rows of o are zeros.

@@ -250,3 +250,43 @@ def test_a_bad_value_reaches_only_the_tokens_from_its_own_on(sg, T, at, bad, sto
     assert not o2[hit].isfinite().any()
     near = (o.double() - o2.double()).abs() <= 2 * E16 * o.double().abs() + 1e-6
     assert torch.all(near | hit)
+
+
+@pytest.mark.parametrize("storage", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,Tp", [(17, 1), (1, 17), (31, 32), (33, 47), (48, 16), (0, 40), (16, 64)])
+def test_counts_around_the_edges_of_longer_steps(sg, T, Tp, storage):
+    # more than 16 tokens go over the state in blocks: counts at, before and after a block's end
+    c = _case(6, T, Tp, 2, 8, storage, seed=900 + T + 100 * Tp, gate="wild", pad=(1,))
+    for n, x in enumerate((0, 0, 15, 16, 17, 33)):
+        c["accepted"][n] = min(x, Tp) - 1
+        if T:
+            c["counts"][5 - n] = min(x, T)
+    o, pool = _run(sg, c, 0.125)
+    assert sg.get_device_status() == 0
+    _check(c, o, pool, 0.125)
+
+
+def test_a_longer_call_equals_commit_then_step(sg):
+    c = _case(4, 37, 35, 2, 6, torch.float32, seed=71, ragged=True)
+    o, pool = _run(sg, c, 0.125)
+    commit = dict(c, q=c["q"][:, :0], k=c["k"][:, :0], v=c["v"][:, :0], g=c["g"][:, :0])
+    none, pool2 = _run(sg, commit, 0.125)
+    assert none is None and torch.equal(pool, pool2)
+    o2, pool3 = _run(sg, dict(c, pool=pool2, pending=None, accepted=None), 0.125)
+    assert torch.equal(pool3, pool2) and torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("storage", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("at", [3, 16, 20, 39])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_bad_value_of_a_longer_step(sg, at, bad, storage):
+    c = _case(2, 40, 2, 2, 3, storage, seed=at, ragged=False)
+    o, pool = _run(sg, c, 0.125)
+    c["v"][1, at, 0, 77] = bad
+    o2, pool2 = _run(sg, c, 0.125)
+    assert torch.equal(pool, pool2)
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[1, at:, 0, 77] = True
+    assert not o2[hit].isfinite().any()
+    near = (o.double() - o2.double()).abs() <= 2 * E16 * o.double().abs() + 1e-6
+    assert torch.all(near | hit)
