@@ -20,8 +20,10 @@
 // memory, which finds the part that holds the drawn number and goes through it again (from L2).
 //
 // Bound by the memory for large batches, short of the copy rate by the dependent steps at both ends
-// of a row: 256 rows of 131072 fp32 take 48 us where the bytes of p_a and (for the 76 % of rows with a
-// rejection) q_a need 35 us; one row of 65536 takes 5.9 us, which is latency.
+// of a row: 256 rows of 131072 fp32 take 46.4 us where the bytes of p_a and (for the 76 % of rows with a
+// rejection) q_a need 35 us, 1024 rows 145 us (floor 140); one row of 65536 takes 5.7 us, which is latency.
+// With bf16 the arithmetic on twice as many values in the same bytes shows: 512 rows of 131072 take 56 us
+// (floor 35).
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -47,8 +49,9 @@ __device__ __forceinline__ float prob_load(const T *p) {
 
 // A probability in [0, 1] in units of 2^-43, rounded to nearest even, as hi * 2^21 + lo:
 // adding 2 to p rounds it to a multiple of 2^-22, adding
-// 3 * 2^-21 to the (exact) remainder rounds that to a multiple of 2^-43, and either sum's bits
+// 3 * 2^-21 to the remainder rounds that to a multiple of 2^-43, and either sum's bits
 // hold the multiple in the low mantissa. Both parts carry a constant, which differences lose.
+// The second sum is p less (2 + p rounded, less 2 + 3 * 2^-21), a difference that is exact.
 // (A conversion to a 64-bit integer gives the same value but goes through the fp64 units, of
 // which this GPU has few.)
 struct Units {
@@ -56,8 +59,28 @@ struct Units {
 };
 __device__ __forceinline__ Units prob_units(float p) {
     const float a = __fadd_rn(p, 2.f);
-    const float r = __fsub_rn(p, __fsub_rn(a, 2.f));
-    return {__float_as_int(a), __float_as_int(__fadd_rn(r, 1.430511474609375e-6f))};
+    return {__float_as_int(a), __float_as_int(__fsub_rn(p, __fsub_rn(a, 2.000001430511474609375f)))};
+}
+// The same of two probabilities at a time, in half the instructions (with the packed clamps of bf16 and a
+// 64-bit sum per four vectors: 512 rows of 131072 bf16 75 -> 64 us at 8 CTAs a row).
+struct Units2 {
+    int hi[2], lo[2];
+};
+__device__ __forceinline__ Units2 prob_units2(float p0, float p1) {
+    Units2 u;
+    asm("{\n\t.reg .b64 p, a, b;\n\t.reg .b64 two, shift, minus;\n\t"
+        "mov.b64 p, {%4, %5};\n\t"
+        "mov.b64 two, {%6, %6};\n\t"
+        "mov.b64 shift, {%7, %7};\n\t"
+        "mov.b64 minus, {%8, %8};\n\t"
+        "add.rn.f32x2 a, p, two;\n\t"
+        "fma.rn.f32x2 b, a, minus, shift;\n\t"
+        "add.rn.f32x2 b, p, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t"
+        "mov.b64 {%2, %3}, b;\n\t}"
+        : "=r"(u.hi[0]), "=r"(u.hi[1]), "=r"(u.lo[0]), "=r"(u.lo[1])
+        : "f"(p0), "f"(p1), "f"(2.f), "f"(2.000001430511474609375f), "f"(-1.f));
+    return u;
 }
 constexpr Units kZeroUnits = {0x40000000, 0x35c00000};   // bits of 2 and of 3 * 2^-21
 
@@ -74,6 +97,17 @@ struct PartSum {
         add_units(prob_units(fmaxf(__saturatef(p), q)), prob_units(q));
     }
     __device__ __forceinline__ void add(float p) { add_units(prob_units(__saturatef(p)), kZeroUnits); }
+    // two tokens whose larger m = max(p, q) and q are in [0, 1]
+    __device__ __forceinline__ void add2(float m0, float m1, float q0, float q1) {
+        const Units2 m = prob_units2(m0, m1), q = prob_units2(q0, q1);
+        add_units({m.hi[0], m.lo[0]}, {q.hi[0], q.lo[0]});
+        add_units({m.hi[1], m.lo[1]}, {q.hi[1], q.lo[1]});
+    }
+    __device__ __forceinline__ void add2(float p0, float p1) {
+        const Units2 p = prob_units2(p0, p1);
+        add_units({p.hi[0], p.lo[0]}, kZeroUnits);
+        add_units({p.hi[1], p.lo[1]}, kZeroUnits);
+    }
     __device__ __forceinline__ long long units() const { return static_cast<long long>(hi) * (1 << 21) + lo; }
 };
 
@@ -161,6 +195,45 @@ struct Vec {
     }
 };
 
+// Pairs of bf16, the larger or smaller of each (a NaN yields to the other).
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// s += max(p - q, 0), or p, over 16 bytes of probabilities.
+template <typename T, bool kQ>
+__device__ __forceinline__ void add_vector(PartSum &s, uint4 p, uint4 q) {
+    const uint32_t ps[4] = {p.x, p.y, p.z, p.w}, qs[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const float p0 = __saturatef(__uint_as_float(ps[i])), p1 = __saturatef(__uint_as_float(ps[i + 1]));
+            if constexpr (kQ) {
+                const float q0 = __saturatef(__uint_as_float(qs[i])), q1 = __saturatef(__uint_as_float(qs[i + 1]));
+                s.add2(fmaxf(p0, q0), fmaxf(p1, q1), q0, q1);
+            } else {
+                s.add2(p0, p1);
+            }
+        }
+    } else {
+        constexpr uint32_t kOnes = 0x3f803f80u;   // 1, 1
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 y = bf16x2_to_float2(kQ ? min2(max2(qs[i], 0u), kOnes) : 0u);
+            const float2 x = bf16x2_to_float2(min2(max2(ps[i], kQ ? min2(max2(qs[i], 0u), kOnes) : 0u), kOnes));
+            if constexpr (kQ) s.add2(x.x, x.y, y.x, y.y);
+            else s.add2(x.x, x.y);
+        }
+    }
+}
+
 // Loads run ahead of the sums through shared memory, kAhead vectors of p and of q per lane. Each
 // lane copies (cp.async) and reads its own slots, so no barrier is needed.
 constexpr int kAhead = 4;
@@ -188,21 +261,18 @@ __device__ __forceinline__ long long sum_vectors(const Weights<T> &w, int lo, in
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) load(32 * i, i);
         for (int v = 0; v < vectors; v += 32 * kAhead) {
+            PartSum s;
+            static_assert(kN * kAhead <= 256, "a part's sum holds them");
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-                Vec<T> x, y;
-                x.w = mine[0][i * kVerifyThreads];
-                if constexpr (kQ) y.w = mine[1][i * kVerifyThreads];
+                const uint4 x = mine[0][i * kVerifyThreads];
+                uint4 y{};
+                if constexpr (kQ) y = mine[1][i * kVerifyThreads];
                 load(v + 32 * (i + kAhead), i);
-                PartSum s;
-#pragma unroll
-                for (int e = 0; e < kN; ++e) {
-                    if constexpr (kQ) s.add(x.at(e), y.at(e));
-                    else s.add(x.at(e));
-                }
-                sum += s.units();
+                add_vector<T, kQ>(s, x, y);
             }
+            sum += s.units();
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -407,13 +477,14 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
     }
 }
 
-// CTAs that share a row: 8 while the rows are few, so that every SM reads and each CTA's part is
-// short; fewer where the rows alone are two CTAs for every SM, since each CTA pays some 5 us of
-// dependent steps (the accept test, the hand-over of its sums). 1024 rows of 65536 bf16: 4 CTAs
-// 65 us, 2 CTAs 56 us; 256 rows of 131072 fp32: 8 CTAs 48 us, 4 CTAs 51 us.
-int cluster_size(int64_t N, int sm_count) {
+// CTAs that share a row. Each pays some 5 us of dependent steps (the accept test, the hand-over of its
+// sums), so it gets at least 12 KB of the row's target probabilities (32 rows of 8000 bf16: 8 CTAs 7.3 us,
+// 1 CTA 5.9) and, where the launch fills the SMs anyway, 48 KB (2048 rows of 32000 bf16: 8 CTAs 130 us, 2
+// CTAs 60, 1 CTA 53; 1024 rows of 131072 bf16: 8 CTAs 115, 4 CTAs 96). More CTAs where there is more to
+// read: their ends overlap better (1024 rows of 131072 fp32: 8 CTAs 144 us, 2 CTAs 195).
+int cluster_size(int64_t N, int64_t row_bytes, int sm_count) {
     int c = kMaxCluster;
-    while (c > 1 && N * c > 16 * sm_count) c /= 2;
+    while (c > 1 && (row_bytes < c * (12 << 10) || (N * c > 8 * sm_count && row_bytes < c * (48 << 10)))) c /= 2;
     return c;
 }
 
@@ -465,7 +536,7 @@ cudaError_t launch_verify_drafts(const void *p, int64_t p_stride, const void *q,
                                  int32_t *accepted, int64_t N, int K, int64_t V, int sm_count,
                                  const int *fits, int *status, cudaStream_t stream) {
     LaunchTimer timer(kKVerifyDrafts, stream);
-    const int c = cluster_size(N, sm_count);
+    const int c = cluster_size(N, V * (bf16 ? 2 : 4), sm_count);
     const size_t room = spread(N, c, fits);
     const VerifyArgs a{p, q, p_stride, q_stride, x, num_drafts, u, s, tokens, accepted, K, V, status};
     return launch_dependent_cluster(bf16 ? verify_drafts_kernel<uint16_t> : verify_drafts_kernel<float>,

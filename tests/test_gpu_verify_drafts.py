@@ -137,3 +137,18 @@ def test_graph_and_side_stream(sg):
     graph.replay()
     want = sp.verify_drafts(c2["p"], c2["q"], c2["x"], c2["u"], c2["s"])
     assert tokens.tolist() == want[0].tolist() and accepted.tolist() == want[1].tolist()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,V", [(3, 3000), (3, 17001), (3, 40008), (3, 70001), (700, 20000), (400, 60001)])
+@pytest.mark.parametrize("drafter", [True, False])
+def test_values_of_every_kind(sg, N, V, dtype, drafter):
+    # probabilities that are none, borders between two units, and rows cut into one to eight parts of a cluster
+    c = _case(N, 1, V, dtype, drafter, False, seed=N + V, sharp=6.0)
+    gen = torch.Generator().manual_seed(V)
+    for t in (c["p"], c["q"]) if drafter else (c["p"],):
+        flat = t.view(N, -1)
+        for value in (float("nan"), float("inf"), -1.0, -0.0, 2.0 ** -44, 3 * 2.0 ** -44, 5 * 2.0 ** -44, 2.0 ** -130):
+            flat.scatter_(1, torch.randint(0, flat.shape[1], (N, 6), generator=gen), value)
+        flat[:, 7] = 1.5
+    _check(sg, c)
