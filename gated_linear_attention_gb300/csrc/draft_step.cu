@@ -17,11 +17,14 @@
 // every kGroups-th item and sends the state back from its stage (TMA). The two products with the
 // state run on the tensor cores as mma.m16n8k16, 16 (or 8) being the tokens, which are too few for
 // the rows of a tcgen05 tile:
-//     commit   D[16 dv x 8 dk] = (w V)^T K     with w_j v_j in fp32 split into three bf16 parts
-//     read     O[16 t x 8 dv]  = Q S           with S in bf16
+//     commit   D[16 dv x 8 dk] = (w V)^T K
+//     read     O[16 t x 8 dv]  = Q S
 // The accumulators of the first are laid out like the B operand of the second, so one pass over the
-// state in shared memory, 16 key rows at a time, feeds both. An fp32 state is read after the
-// commit, split into two bf16 parts. A bf16 state is read as it was stored, an operand without any
+// state in shared memory, 16 key rows at a time, feeds both. Operands that are fp32 (w_j v_j, the state, the
+// tokens' weights) go in three bf16 parts that sum to them, so every product is exact and the sums are
+// fp32 (with two parts of the state and the weights, 17 of 24 bits, o had three times as many elements on
+// the wrong side of a bf16 rounding; 256 rows of 5, fp32, took as long). An fp32 state is read after the
+// commit. A bf16 state is read as it was stored, an operand without any
 // arithmetic, and what the commit adds to it enters as the pending tokens' own term (Q K^T w) V.
 // Places past the counts hold anything: pending tokens there are masked out of every operand, and the
 // products among the new tokens go one by one where a value is not finite, so nothing of a masked place
@@ -254,13 +257,15 @@ __device__ __forceinline__ Gates gate_scan(const uint8_t *at, int count, int lan
     return s;
 }
 
-// x split into bf16 parts that sum to it: packed pairs (x0 in the low half).
+// Products of fp32 values on the tensor cores: a value is the sum of three bf16 parts, 8 of its 24 bits each.
+constexpr int kParts = 3;
+// The next part of x0 and of x1, a packed pair (x0 in the low half), and what it leaves of them. The bits
+// are cut, not rounded, so no part is larger than the value.
 __device__ __forceinline__ uint32_t split_bf16(float &x0, float &x1) {
-    const uint32_t w = float2_to_bf16x2(x0, x1);
-    const float2 f = bf16x2_to_float2(w);
-    x0 -= f.x;
-    x1 -= f.y;
-    return w;
+    const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
+    x0 -= __uint_as_float(u0 & 0xffff0000u);
+    x1 -= __uint_as_float(u1 & 0xffff0000u);
+    return __byte_perm(u0, u1, 0x7632);
 }
 
 // Wait for a phase of `bar`, at most tck::kWaitNs, asleep in the barrier between tries.
@@ -315,11 +320,11 @@ __device__ __forceinline__ void stage_tokens(const DraftArgs &a, const StepMaps 
     cp_async_arrive(bar);
 }
 
-// Two neighbouring weights of a row in two bf16 parts, as word i of an A operand.
+// Two neighbouring weights of a row as word i of an A operand in parts.
 template <int kWords>
-__device__ __forceinline__ void split_row(uint32_t (&pa)[2][kWords], int i, float2 w) {
-    pa[0][i] = split_bf16(w.x, w.y);
-    pa[1][i] = float2_to_bf16x2(w.x, w.y);
+__device__ __forceinline__ void split_row(uint32_t (&pa)[kParts][kWords], int i, float2 w) {
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) pa[p][i] = split_bf16(w.x, w.y);
 }
 // Four columns of two neighbouring tokens' values as words i of four B operands.
 template <int kWords>
@@ -342,7 +347,6 @@ template <bool kBf16, int kTok, bool kC, bool kT, bool kStore = kC>
 __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *pool, uint8_t *smem, const uint8_t *side,
                                          uint8_t *own, const Item &it, int group, int64_t t0 = 0) {
     using Sm = StepSmem<kBf16, kTok>;
-    constexpr int kParts = 3;   // of w_j v_j in fp32: what three bf16 parts leave out is below 2^-26 of it
     constexpr int kOct = kTok / 8;
     const int tid = threadIdx.x & (kGroupThreads - 1), warp = tid >> 5, lane = tid & 31;
     const int col = warp & 1, rows = warp >> 1;   // the warp's 32 columns and 64 key rows
@@ -418,8 +422,7 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
     for (int ci = 0; ci < 4; ++ci) {
         const uint32_t tok_at = frag ^ (ci << 5);
         float x[2][2][4];      // rows 8 i + 2 tq + e, column j
-        uint32_t hi[2][4];     // the same as B operands: rows 8 i + 2 tq, + 1 of column j
-        [[maybe_unused]] uint32_t lo[2][4];
+        [[maybe_unused]] uint32_t xb[2][4];   // bf16: the same as B operands, rows 8 i + 2 tq, + 1 of column j
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t at_row = (16 * ci + 8 * i) * 128;
@@ -431,8 +434,8 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
                     const float2 f0 = bf16x2_to_float2(u0), f1 = bf16x2_to_float2(u1);
                     x[i][0][2 * m] = f0.x, x[i][0][2 * m + 1] = f0.y;
                     x[i][1][2 * m] = f1.x, x[i][1][2 * m + 1] = f1.y;
-                    hi[i][2 * m] = __byte_perm(u0, u1, 0x5410);
-                    hi[i][2 * m + 1] = __byte_perm(u0, u1, 0x7632);
+                    xb[i][2 * m] = __byte_perm(u0, u1, 0x5410);
+                    xb[i][2 * m + 1] = __byte_perm(u0, u1, 0x7632);
                 }
             } else {
                 const float4 f0 = lds_f32x4(st0 + at_row), f1 = lds_f32x4(st1 + at_row);
@@ -481,16 +484,6 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
             }
         }
         if (kT) {
-            if constexpr (!kBf16) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float x0 = x[i][0][j], x1 = x[i][1][j];
-                        hi[i][j] = split_bf16(x0, x1);
-                        lo[i][j] = float2_to_bf16x2(x0, x1);
-                    }
-            }
             uint32_t qa[4];   // (t, dk), (t + 8, dk), (t, dk + 8), (t + 8, dk + 8)
             if constexpr (kTok == 16) {
                 ldmatrix_x4(qa, st + Sm::kQ + tok_at);
@@ -500,8 +493,17 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if constexpr (!kBf16) mma(o[j], qa, lo[0][j], lo[1][j]);
-                mma(o[j], qa, hi[0][j], hi[1][j]);
+                if constexpr (kBf16) {
+                    mma(o[j], qa, xb[0][j], xb[1][j]);
+                } else {
+                    uint32_t part[kParts][2];
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) part[p][i] = split_bf16(x[i][0][j], x[i][1][j]);
+#pragma unroll
+                    for (int p = kParts - 1; p >= 0; --p) mma(o[j], qa, part[p][0], part[p][1]);
+                }
             }
             if (scores) {
                 uint32_t k4[4];
@@ -561,19 +563,20 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
             if constexpr (kTok == 16)
                 y1[j] = h1 * (kBf16 ? fade : 1.f) * ((rows ? o[j][3] : o[j][2]) + swap[((warp ^ 2) * 8 + 4 + j) * 32 + lane]);
         }
-        // tokens' weights (A operand, two bf16 parts) times their values, 8 or 16 tokens
-        auto add_tokens = [&](const uint32_t (&pa)[2][2 * kOct], const uint32_t (&bv)[4][kOct]) {
+        // tokens' weights (A operand, in parts) times their values, 8 or 16 tokens
+        auto add_tokens = [&](const uint32_t (&pa)[kParts][2 * kOct], const uint32_t (&bv)[4][kOct]) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float d[4];
-                mma_tok<kTok>(d, pa[1], bv[j][0], bv[j][kOct - 1], 0.f, 0.f, 0.f, 0.f);
-                mma_tok<kTok>(d, pa[0], bv[j][0], bv[j][kOct - 1], d[0], d[1], d[2], d[3]);
+                mma_tok<kTok>(d, pa[kParts - 1], bv[j][0], bv[j][kOct - 1], 0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int p = kParts - 2; p >= 0; --p) mma_tok<kTok>(d, pa[p], bv[j][0], bv[j][kOct - 1], d[0], d[1], d[2], d[3]);
                 y0[j] += rows ? d[1] : d[0];
                 if constexpr (kTok == 16) y1[j] += rows ? d[3] : d[2];
             }
         };
         if (kBf16 && kC) {
-            uint32_t pa[2][2 * kOct], bv[4][kOct];
+            uint32_t pa[kParts][2 * kOct], bv[4][kOct];
 #pragma unroll
             for (int i = 0; i < kOct; ++i) {
                 const int t = 2 * tq + 8 * i;
@@ -598,7 +601,7 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
             for (int j = 0; j < 4; ++j) odd_values |= not_finite(bv[j][i]);
         }
         if (!__any_sync(0xffffffffu, odd_values != 0)) {
-            uint32_t pa[2][2 * kOct];
+            uint32_t pa[kParts][2 * kOct];
 #pragma unroll
             for (int i = 0; i < kOct; ++i) {
                 const int t = 2 * tq + 8 * i;
