@@ -26,6 +26,8 @@
 // the wrong side of a bf16 rounding; 256 rows of 5, fp32, took as long). An fp32 state is read after the
 // commit. A bf16 state is read as it was stored, an operand without any
 // arithmetic, and what the commit adds to it enters as the pending tokens' own term (Q K^T w) V.
+// Infinities and NaN: a commit that has them is taken one product at a time (commit_by_one), so that the stored
+// state has the recurrence's; o is infinite or NaN where the recurrence's is.
 // Places past the counts hold anything: pending tokens there are masked out of every operand, and the
 // products among the new tokens go one by one where a value is not finite, so nothing of a masked place
 // reaches a result.
@@ -339,12 +341,61 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
     return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u);
 }
 
+// x + 0 w for a pair of bf16: a mark of NaN where one of them is an infinity or NaN.
+__device__ __forceinline__ void mark_not_finite(uint32_t &x, uint32_t w) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(x) : "r"(w), "r"(0u));
+}
+
+// Columns 4 c .. 4 c + 3 of row r of a state half that begins at element `at` of the pool.
+template <bool kBf16>
+__device__ __forceinline__ void store_state(void *pool, int64_t at, int r, int c, float4 x) {
+    if constexpr (kBf16)
+        __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(pool) + at + r * kD) + c,
+               make_uint2(float2_to_bf16x2(x.x, x.y), float2_to_bf16x2(x.z, x.w)));
+    else
+        __stcs(reinterpret_cast<float4 *>(static_cast<float *>(pool) + at + r * kD) + c, x);
+}
+
+// A thread's part of the commit of an item (as they are numbered in the kernels) where infinities or NaN are
+// committed, whose parts do not sum to them: the recurrence as it stands, in fp32, from the pool to the pool.
+// Every eighth row from `row` to `end`, columns 4 c .. 4 c + 3 of the item's half with c = thread % 16.
+template <bool kBf16>
+__device__ __forceinline__ void commit_by_one(const DraftArgs &a, unsigned item, int row, int end) {
+    const unsigned unit = item >> 1, n = unit / static_cast<unsigned>(a.H), h = unit - n * a.H, half = item & 1;
+    const int c = threadIdx.x & 15;
+    const Row what = read_row(a, static_cast<int>(n), false);
+    const int64_t at = (static_cast<int64_t>(what.slot) * a.H + h) * kD * kD + half * kHalf, pend0 = n * a.T_pend * a.H + h;
+    const uint16_t *k = a.pk + pend0 * kD, *v = a.pv + pend0 * kD + half * kHalf;
+    const float *g = a.pg + pend0;
+    void *pool = a.pool;
+#pragma unroll 1
+    for (int r = row; r < end; r += 8) {
+        float4 x;
+        if constexpr (kBf16) {
+            const uint2 w = *(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(pool) + at + r * kD) + c);
+            const float2 f0 = bf16x2_to_float2(w.x), f1 = bf16x2_to_float2(w.y);
+            x = make_float4(f0.x, f0.y, f1.x, f1.y);
+        } else {
+            x = *(reinterpret_cast<const float4 *>(static_cast<const float *>(pool) + at + r * kD) + c);
+        }
+#pragma unroll 1
+        for (int64_t t = 0; t < what.commits; ++t) {
+            const float fade = expf(__ldg(g + t * a.H)), key = bf16_bits_to_float(__ldg(k + t * a.H * kD + r));
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(v + t * a.H * kD) + c);
+            const float2 f0 = bf16x2_to_float2(w.x), f1 = bf16x2_to_float2(w.y);
+            x = make_float4(fmaf(fade, x.x, key * f0.x), fmaf(fade, x.y, key * f0.y), fmaf(fade, x.z, key * f1.x), fmaf(fade, x.w, key * f1.y));
+        }
+        store_state<kBf16>(pool, at, r, c, x);
+    }
+}
+
 // One item by a group of 4 warps, from its stage `smem` and what stands beside it; `own`: the group's
 // memory. Thread 0 of the group leaves a store of the state in flight that still reads the stage.
 // kC, kT: there is something to commit, there are new tokens; kStore: what was committed goes to `pool`
-// from here (else it stays in the stage). t0: place of the first new token in its row.
+// from here (else it stays in the stage). t0: place of the first new token in its row. Returns, to the whole
+// group, whether the commit has infinities or NaN (kStore): it is then not sent, NaN stand for both in it.
 template <bool kBf16, int kTok, bool kC, bool kT, bool kStore = kC>
-__device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *pool, uint8_t *smem, const uint8_t *side,
+__device__ __forceinline__ bool run_item(const DraftArgs &a, const CUtensorMap *pool, uint8_t *smem, const uint8_t *side,
                                          uint8_t *own, const Item &it, int group, int64_t t0 = 0) {
     using Sm = StepSmem<kBf16, kTok>;
     constexpr int kOct = kTok / 8;
@@ -387,6 +438,9 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
     // columns 4 gr .. + 3 of the warp's 32 of token t's values
     auto values = [&](uint32_t tile, int t) { return lds_u32x2(st + tile + chunk(t, 4 * col + (gr >> 1)) + (gr & 1) * 8); };
     uint32_t there[kOct];   // mask of the pending tokens 2 tq + 8 i, + 1 of a packed pair
+    // infinities and NaN to commit show in the sums where an fp32 state is read next; else the operands are marked
+    constexpr bool kMark = kStore && (kBf16 || !kT);
+    [[maybe_unused]] uint32_t mark = 0;
     if (kC) {
 #pragma unroll
         for (int i = 0; i < kOct; ++i) {   // tokens 2 tq + 8 i, + 1
@@ -405,6 +459,10 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
                     wv[p][m][2 * i] = split_bf16(x0, x1);
                     wv[p][m][2 * i + 1] = split_bf16(y0, y1);
                 }
+                if constexpr (kMark) {
+                    mark_not_finite(mark, wv[0][m][2 * i]);
+                    mark_not_finite(mark, wv[0][m][2 * i + 1]);
+                }
             }
         }
     }
@@ -415,10 +473,12 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
     const int at_chunk = kBf16 ? 4 * col + (gr >> 1) : gr;
     const uint32_t st0 = tile + chunk(64 * rows + 2 * tq, at_chunk) + odd, st1 = tile + chunk(64 * rows + 2 * tq + 1, at_chunk) + odd;
     const uint32_t frag = kTok == 16 ? wide_chunk(mr + 8 * (mi & 1), rows, mi >> 1) : wide_chunk(mr, rows, mi & 1);
-    const uint32_t key_frag = st + (col ? Sm::kPk : Sm::kK) + (kTok == 16 ? wide_chunk(mr + 8 * (mi >> 1), rows, mi & 1) : frag);
+    const uint32_t key_frag = st + (kBf16 && col ? Sm::kPk : Sm::kK) + (kTok == 16 ? wide_chunk(mr + 8 * (mi >> 1), rows, mi & 1) : frag);
     const bool scores = kT && (col == 0 || (kBf16 && kC));
     float sc[kOct][4] = {};   // keys 8 i + 2 tq, + 1; rows gr, gr + 8
-#pragma unroll
+    // (16 tokens and fp32 states fill the registers: unrolled four times, 256 rows of 16 spill and take 207 us,
+    // twice 192)
+#pragma unroll (kBf16 || kTok == 8 || !kStore ? 4 : 2)
     for (int ci = 0; ci < 4; ++ci) {
         const uint32_t tok_at = frag ^ (ci << 5);
         float x[2][2][4];      // rows 8 i + 2 tq + e, column j
@@ -456,7 +516,10 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int e = 0; e < kOct; ++e) kb[i][e] &= there[e];
+                for (int e = 0; e < kOct; ++e) {
+                    kb[i][e] &= there[e];
+                    if constexpr (kMark) mark_not_finite(mark, kb[i][e]);
+                }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -523,10 +586,21 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
         }
     }
     if (kStore) tc::fence_proxy_async_smem();
-    group_sync(group);
+    bool not_finite_commit = false;
+    if (kStore) {
+        bool odd_sum = mark & 0x7fff7fffu;
+        if constexpr (!kMark) {
+#pragma unroll
+            for (int i = 0; i < 8 * kOct; ++i) odd_sum |= !isfinite(o[i & 3][i >> 2]) && gr + 8 * (i >> 3) < tokens;
+        }
+        __syncwarp();
+        not_finite_commit = tck::named_any(group + 9, kGroupThreads, odd_sum);
+    } else {
+        group_sync(group);
+    }
 
     // 3. the state goes back
-    if (kStore && tid == 0) {
+    if (kStore && tid == 0 && !not_finite_commit) {
         for (int b = 0; b < Sm::kBoxes; ++b)
             tc::tma_store_3d(pool, it.half * kHalf + b * Sm::kBoxCols, 0,
                              static_cast<int32_t>(static_cast<int64_t>(it.slot) * a.H + it.h), smem + Sm::kState + b * Sm::kStateTile);
@@ -642,6 +716,7 @@ __device__ __forceinline__ void run_item(const DraftArgs &a, const CUtensorMap *
                                float2_to_bf16x2(a.scale * y1[2], a.scale * y1[3]));
         }
     }
+    return not_finite_commit;
 }
 
 template <bool kBf16, int kTok>
@@ -714,9 +789,11 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
         for (int e = it.tokens * 8 + tid; e < static_cast<int>(a.T) * 8; e += kGroupThreads)   // rows past the count
             *reinterpret_cast<uint4 *>(a.o + ((it.n * a.T + e / 8) * a.H + it.h) * kD + it.half * kHalf + 8 * (e % 8)) =
                 make_uint4(0, 0, 0, 0);
-        if (it.commits && it.tokens) run_item<kBf16, kTok, true, true>(a, &maps.pool, at, side, own, it, group);
-        else if (it.commits) run_item<kBf16, kTok, true, false>(a, &maps.pool, at, side, own, it, group);
+        bool odd = false;
+        if (it.commits && it.tokens) odd = run_item<kBf16, kTok, true, true>(a, &maps.pool, at, side, own, it, group);
+        else if (it.commits) odd = run_item<kBf16, kTok, true, false>(a, &maps.pool, at, side, own, it, group);
         else if (it.tokens) run_item<kBf16, kTok, false, true>(a, &maps.pool, at, side, own, it, group);
+        if (odd) commit_by_one<kBf16>(a, item, tid >> 4, kD);
         if (tid == 0) tc::tma_store_wait_read<0>();
         tc::fence_proxy_async_smem();   // the stage was written to, and TMA writes to it next
         __syncwarp();
@@ -835,14 +912,21 @@ __global__ void __launch_bounds__(kGroupThreads, 4) draft_step_long_kernel(Draft
         else run_item<false, 16, false, true, false>(a, nullptr, smem, side, own, it, 0, t0);
         if (p == before - 1) {   // the commit is complete
             __syncthreads();
-#pragma unroll 8
-            for (int i = 0; i < 16; ++i) {
-                const float4 f = *place(8 * i + r0, c0);
-                if constexpr (kBf16)
-                    __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.pool) + at + (8 * i + r0) * kD) + c0,
-                           make_uint2(float2_to_bf16x2(f.x, f.y), float2_to_bf16x2(f.z, f.w)));
-                else
-                    __stcs(reinterpret_cast<float4 *>(static_cast<float *>(a.pool) + at + (8 * i + r0) * kD) + c0, f);
+#pragma unroll 1
+            for (int r = r0; r < kD; r += 64) {
+                float4 f[8];
+                float odd = 0.f;   // NaN: an infinity or NaN among the values
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    f[i] = *place(r + 8 * i, c0);
+                    odd = fmaf(f[i].x, 0.f, fmaf(f[i].y, 0.f, fmaf(f[i].z, 0.f, fmaf(f[i].w, 0.f, odd))));
+                }
+                if (odd != 0.f) {
+                    commit_by_one<kBf16>(a, blockIdx.x, r, r + 64);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) store_state<kBf16>(a.pool, at, r + 8 * i, c0, f[i]);
+                }
             }
         }
     }

@@ -378,7 +378,9 @@ int sala_gla_verify_drafts(const void *target_probs, int64_t target_stride, cons
  *                  commit to one slot race; the caller must not do that.
  *   o              bf16 [N, T, H, 128] output
  * A slot >= P, more commits than T_pend or a token count outside [0, T] is recorded as
- * SALA_ERR_BAD_INDEX and its row is treated as padding. q, k, v, pend_k, pend_v, o and the pool
+ * SALA_ERR_BAD_INDEX and its row is treated as padding. Infinities and NaN among the tokens committed and
+ * in the pool give a stored state with the recurrence's infinities and NaN; what they reach of o is infinite
+ * or NaN (either may stand for the other), and the rest of o is as without them. q, k, v, pend_k, pend_v, o and the pool
  * are 16-byte aligned, the other arrays 4-byte aligned. o and the pool overlap nothing else.
  * Errors: SALA_ERR_INVALID_ARG, SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED, SALA_ERR_CUDA.
  */
