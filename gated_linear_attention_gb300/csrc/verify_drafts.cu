@@ -108,8 +108,12 @@ struct PartSum {
         add_units({p.hi[0], p.lo[0]}, kZeroUnits);
         add_units({p.hi[1], p.lo[1]}, kZeroUnits);
     }
-    __device__ __forceinline__ long long units() const { return static_cast<long long>(hi) * (1 << 21) + lo; }
+    __device__ __forceinline__ unsigned long long units() const {
+        return static_cast<unsigned long long>(static_cast<long long>(hi) * (1 << 21) + lo);
+    }
 };
+// Sums over a row are unsigned: 2^20 tokens of probability 1 have 2^63 units.
+using Sum = unsigned long long;
 
 struct VerifyArgs {
     const void *p, *q;                 // target rows [N * (K + 1)], drafter rows [N * K] or null
@@ -169,7 +173,7 @@ struct Weights {
     const T *p, *q;
     int one_at;
 
-    __device__ __forceinline__ long long at(int x) const {
+    __device__ __forceinline__ Sum at(int x) const {
         PartSum s;
         if (q) s.add(prob_load(p + x), prob_load(q + x));
         else if (x != one_at) s.add(prob_load(p + x));
@@ -244,9 +248,9 @@ struct Ring {
 // One lane's share of the sum over tokens [lo, hi), `lo` aligned for 16-byte loads of p and, with
 // kQ (subtract the drafter's row), of q.
 template <typename T, bool kQ>
-__device__ __forceinline__ long long sum_vectors(const Weights<T> &w, int lo, int hi, int lane, Ring &ring) {
+__device__ __forceinline__ Sum sum_vectors(const Weights<T> &w, int lo, int hi, int lane, Ring &ring) {
     constexpr int kN = Vec<T>::kN;
-    long long sum = 0;
+    Sum sum = 0;
     const T *p = w.p + lo + lane * kN, *q = kQ ? w.q + lo + lane * kN : nullptr;
     const int vectors = (hi - lo) / kN - lane;   // of this lane: 0, 32, 64, ..
     uint4 *mine[2] = {&ring.v[0][0][threadIdx.x], &ring.v[1][0][threadIdx.x]};
@@ -289,8 +293,8 @@ __device__ __forceinline__ long long sum_vectors(const Weights<T> &w, int lo, in
 
 // The sum of the weights of tokens [lo, hi) by one warp; every lane returns it.
 template <typename T>
-__device__ __forceinline__ long long sum_part(const Weights<T> &w, int lo, int hi, int lane, Ring &ring) {
-    long long sum = 0;
+__device__ __forceinline__ Sum sum_part(const Weights<T> &w, int lo, int hi, int lane, Ring &ring) {
+    Sum sum = 0;
     const uintptr_t bp = reinterpret_cast<uintptr_t>(w.p), bq = reinterpret_cast<uintptr_t>(w.q);
     if (!w.q || ((bp ^ bq) & 15) == 0) {
         // tokens before the first aligned one (only where the part begins the row)
@@ -330,10 +334,10 @@ __device__ __forceinline__ long long sum_part(const Weights<T> &w, int lo, int h
 }
 
 // Inclusive prefix sum over the lanes of a warp.
-__device__ __forceinline__ long long warp_prefix(long long c, int lane) {
+__device__ __forceinline__ Sum warp_prefix(Sum c, int lane) {
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, c, off);
+        const Sum y = __shfl_up_sync(0xffffffffu, c, off);
         if (lane >= off) c += y;
     }
     return c;
@@ -348,8 +352,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ Ring ring;
     __shared__ int first_s, rejected_s;
-    __shared__ long long all[kMaxCluster * kVerifyWarps];   // sums of the parts, in the first CTA
-    __shared__ long long scan[kVerifyWarps];
+    __shared__ Sum all[kMaxCluster * kVerifyWarps];   // sums of the parts, in the first CTA
+    __shared__ Sum scan[kVerifyWarps];
     cluster.barrier_arrive();   // waited for before the first CTA's memory is written
 
     if (warp == 0) {
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
     // every warp hands its sum to the first CTA, which goes on alone: the others make room
     {
         const int i = rank * kVerifyWarps + warp;
-        const long long sum = sum_part(w, part_begin(i), part_begin(i + 1), lane, ring);
+        const Sum sum = sum_part(w, part_begin(i), part_begin(i + 1), lane, ring);
         cluster.barrier_wait();
         if (lane == 0) *cluster.map_shared_rank(&all[i], 0) = sum;
         cluster.barrier_arrive();
@@ -386,20 +390,20 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
         cluster.barrier_wait();
     }
     auto sum_all = [&] {
-        long long t = 0;
+        Sum t = 0;
         for (int j = lane; j < parts; j += 32) t += all[j];
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
         return t;
     };
-    long long total = sum_all();
+    Sum total = sum_all();
     if (total == 0 && rejected_s) {
         // nothing is left of the target after the drafter's part: draw from the target
         w.q = nullptr;
         w.one_at = -1;
         __syncthreads();
         for (int i = warp; i < parts; i += kVerifyWarps) {
-            const long long sum = sum_part(w, part_begin(i), part_begin(i + 1), lane, ring);
+            const Sum sum = sum_part(w, part_begin(i), part_begin(i + 1), lane, ring);
             if (lane == 0) all[i] = sum;
         }
         __syncthreads();
@@ -410,18 +414,18 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
     for (int i = threadIdx.x; i <= a.K; i += kVerifyThreads)
         if (i != first || total == 0) out[i] = i < first ? __ldg(a.x + n * a.K + i) : -1;
     if (threadIdx.x == 0) a.accepted[n] = first;
-    if (total > 0) {
+    if (total != 0) {
         // the number drawn, in the same units: the whole part of s * total (s is a whole number of
         // 2^-64, or closer to 0 than that)
         float s = __ldg(a.s + n);
         s = s >= 0.f ? fminf(s, 0.99999994f) : 0.f;
-        const long long at = __umul64hi(__float2ull_rz(s * 18446744073709551616.f), total);
+        const Sum at = __umul64hi(__float2ull_rz(s * 18446744073709551616.f), total);
         // the part that holds it: every warp finds the same one
-        long long before = 0;
+        Sum before = 0;
         int part = -1;
         for (int j0 = 0; j0 < parts; j0 += 32) {
-            const long long own = j0 + lane < parts ? all[j0 + lane] : 0;
-            const long long c = before + warp_prefix(own, lane);
+            const Sum own = j0 + lane < parts ? all[j0 + lane] : 0;
+            const Sum c = before + warp_prefix(own, lane);
             const unsigned past = __ballot_sync(0xffffffffu, c > at);
             if (past) {
                 const int l = __ffs(past) - 1;
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
             const int tid = threadIdx.x, x0 = tid == 0 ? lo : min(hi, start + per * tid);
             const int x1 = min(hi, start + per * (tid + 1));
             const bool wide = !w.q || ((reinterpret_cast<uintptr_t>(w.p) ^ reinterpret_cast<uintptr_t>(w.q)) & 15) == 0;
-            long long sum = 0;
+            Sum sum = 0;
             int x = x0;
             if (wide) {
                 for (; x < min(start, x1); ++x) sum += w.at(x);
@@ -459,10 +463,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
             }
 #pragma unroll 8
             for (; x < x1; ++x) sum += w.at(x);
-            const long long c = warp_prefix(sum, lane);
+            const Sum c = warp_prefix(sum, lane);
             if (lane == 31) scan[warp] = c;
             __syncthreads();
-            long long run = before + c - sum;
+            Sum run = before + c - sum;
             for (int i = 0; i < warp; ++i) run += scan[i];
             if (run <= at && at < run + sum) {
                 for (x = x0; x < x1; ++x) {

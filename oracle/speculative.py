@@ -10,10 +10,10 @@ UNIT = 2.0 ** 43   # probabilities count as whole numbers of 2^-43
 
 
 def _units(p):
-    """fp64 array of probabilities -> whole numbers of 2^-43 (Python integers would overflow
-    nothing here: 2^20 values of at most 2^43)."""
+    """fp64 array of probabilities -> whole numbers of 2^-43, at most 2^43 each: 2^20 of them sum to 2^63,
+    which takes unsigned 64-bit sums."""
     p = np.where(p > 0, np.minimum(p, 1.0), 0.0)   # NaN compares false
-    return np.rint(p * UNIT).astype(np.int64)
+    return np.rint(p * UNIT).astype(np.uint64)
 
 
 def _f64(t):
@@ -45,11 +45,11 @@ def verify_drafts(p, q, x, u, s, num_drafts=None):
         w = target
         if rejected:
             if q is None:
-                less = np.zeros(V, np.int64)
+                less = np.zeros(V, np.uint64)
                 less[int(x[n, a])] = int(UNIT)
             else:
                 less = _units(_f64(q[n, a]))
-            w = np.maximum(target - less, 0)
+            w = np.maximum(target, less) - less
             if w.sum() == 0:
                 w = target
         total = int(w.sum())
@@ -59,7 +59,7 @@ def verify_drafts(p, q, x, u, s, num_drafts=None):
             bound = Fraction(at) * total
             cum = np.cumsum(w)
             # the first sum above the bound: sums are whole, so compare with its whole part
-            tokens[n, a] = int(np.searchsorted(cum, bound.numerator // bound.denominator, side="right"))
+            tokens[n, a] = int(np.searchsorted(cum, np.uint64(bound.numerator // bound.denominator), side="right"))
     return tokens, accepted
 
 
