@@ -149,9 +149,9 @@ __device__ int first_rejected(const VerifyArgs &a, int64_t n, bool *rejected) {
         if (x >= 0 && x < a.V) {
             const T *p = static_cast<const T *>(a.p) + (n * (a.K + 1) + i) * a.p_stride;
             const T *q = static_cast<const T *>(a.q) + (n * a.K + i) * a.q_stride;
-            // two 24-bit factors: the product is exact in 64 bits
-            const double qx = a.q ? static_cast<double>(prob_load(q + x)) : 1.0;
-            no = !(static_cast<double>(u) * qx < static_cast<double>(prob_load(p + x)));
+            // taken into [0, 1] as in the sums (NaN as 0); two 24-bit factors: the product is exact in 64 bits
+            const float qx = a.q ? __saturatef(prob_load(q + x)) : 1.f, px = __saturatef(prob_load(p + x));
+            no = !(static_cast<double>(u) * qx < static_cast<double>(px));
             stop = no;
         }
         if (i >= drafts) stop = true, no = false;

@@ -340,9 +340,9 @@ typedef enum { SALA_PROB_F32 = 0, SALA_PROB_BF16 = 1 } sala_prob_dtype;
  *   accepted      int32 [N] output: the number a of accepted tokens
  *   N, K, V       N >= 0 (0 is a no-op), K >= 0 (0: one token is drawn from each target row;
  *                 the drafter's arguments are ignored), 1 <= V <= SALA_VERIFY_MAX_VOCAB
- * Probabilities count as whole numbers of 2^-43 (rounded to nearest; NaN and negative values as
- * 0, values above 1 as 1) and need not sum to 1; the sums are exact, so the result does not
- * depend on how the work is split. Pointers need the alignment of their element type only.
+ * Probabilities below 0 and NaN count as 0, those above 1 as 1; they need not sum to 1. The accept test is
+ * exact. In the sums they are whole numbers of 2^-43 (rounded to nearest), which are exact too, so the result
+ * does not depend on how the work is split. Pointers need the alignment of their element type only.
  * Errors: SALA_ERR_INVALID_ARG, SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED, SALA_ERR_CUDA.
  */
 int sala_gla_verify_drafts(const void *target_probs, int64_t target_stride, const void *draft_probs,

@@ -9,11 +9,15 @@ import torch
 UNIT = 2.0 ** 43   # probabilities count as whole numbers of 2^-43
 
 
+def _probability(p):
+    """p taken into [0, 1]; NaN, which compares false, counts as 0."""
+    return np.where(p > 0, np.minimum(p, 1.0), 0.0)
+
+
 def _units(p):
     """fp64 array of probabilities -> whole numbers of 2^-43, at most 2^43 each: 2^20 of them sum to 2^63,
     which takes unsigned 64-bit sums."""
-    p = np.where(p > 0, np.minimum(p, 1.0), 0.0)   # NaN compares false
-    return np.rint(p * UNIT).astype(np.uint64)
+    return np.rint(_probability(p) * UNIT).astype(np.uint64)
 
 
 def _f64(t):
@@ -34,8 +38,8 @@ def verify_drafts(p, q, x, u, s, num_drafts=None):
             t = int(x[n, a])
             if t < 0 or t >= V:
                 break
-            qx = 1.0 if q is None else float(q[n, a, t])
-            if not float(u[n, a]) * qx < float(p[n, a, t]):
+            qx = 1.0 if q is None else _probability(float(q[n, a, t]))
+            if not float(u[n, a]) * qx < _probability(float(p[n, a, t])):
                 rejected = True
                 break
             tokens[n, a] = t

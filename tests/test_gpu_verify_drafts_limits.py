@@ -1,4 +1,5 @@
-"""The verification of drafted tokens at the ends of its range. What is expected is worked out by hand."""
+"""The verification of drafted tokens at the ends of its range: the largest sum that a row can have, and
+values that are no probabilities in the accept test. What is expected is worked out by hand."""
 import pytest
 import torch
 
@@ -42,3 +43,19 @@ def test_the_largest_sum(sg, dtype):
     # ... without probabilities: one token less
     t, a = _call(sg, p, None, x, [[1.0]] * 5, s)
     assert a == [0] * 5 and t == [[int(x * (V - 1)) + (int(x * (V - 1)) >= 7), -1] for x in s]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_accept_test_takes_values_as_probabilities(sg, dtype):
+    # (p(x), q(x), u) of a drafted token: below 0 and NaN count as 0, above 1 as 1
+    nan, inf = float("nan"), float("inf")
+    rows = [(0.0, -1.0, 0.5, False), (0.5, -1.0, 0.5, True), (0.25, nan, 0.5, True), (0.0, nan, 0.5, False), (nan, 0.5, 0.0, False),
+            (-1.0, 0.5, 0.0, False), (-1.0, -4.0, 0.5, False), (0.75, 2.0, 0.5, True), (0.75, inf, 0.5, True),
+            (2.0, 1.5, 1.0, False), (inf, 1.0, 1.0, False), (inf, inf, 0.5, True), (0.75, 1.0, 0.75, False), (0.5, 0.5, 0.5, True)]
+    N = len(rows)
+    p, q = torch.zeros(N, 2, 40, dtype=dtype), torch.zeros(N, 1, 40, dtype=dtype)
+    p[:, :, 3], q[:, :, 30] = 1.0, 1.0
+    for n, (a, b, _, _) in enumerate(rows):
+        p[n, 0, 9], q[n, 0, 9] = a, b
+    _, accepted = _call(sg, p.cuda(), q.cuda(), [[9]] * N, [[r[2]] for r in rows], [0.0] * N)
+    assert accepted == [int(r[3]) for r in rows]
