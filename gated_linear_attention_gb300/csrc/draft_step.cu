@@ -74,7 +74,7 @@ __device__ __forceinline__ Row read_row(const DraftArgs &a, int n, bool report) 
     r.tokens = a.num_tokens ? __ldg(a.num_tokens + n) : a.T;
     if (r.commits < 0) r.commits = 0;
     const bool bad = r.slot >= a.P || r.commits > a.T_pend || r.tokens < 0 || r.tokens > a.T;
-    if (bad && report) record_status(a.status, SALA_ERR_BAD_INDEX);
+    if (bad && r.slot >= 0 && report) record_status(a.status, SALA_ERR_BAD_INDEX);   // (a padding row's counts are anything)
     if (bad || r.slot < 0) r.commits = r.tokens = 0;
     return r;
 }
