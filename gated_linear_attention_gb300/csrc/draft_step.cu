@@ -141,6 +141,16 @@ struct StepSmem {
     static_assert(kStages > kGroups, "the loads run ahead");
 };
 
+// The rings of the four variants, as the tests model them on the host: stages, groups, full barriers.
+template <typename Sm>
+constexpr bool ring_is(int stages, int groups, int fulls) {
+    return Sm::kStages == stages && Sm::kGroups == groups && Sm::kFulls == fulls;
+}
+static_assert(ring_is<StepSmem<false, 8>>(4, 3, 6));
+static_assert(ring_is<StepSmem<false, 16>>(4, 3, 6));
+static_assert(ring_is<StepSmem<true, 8>>(9, 4, 12));
+static_assert(ring_is<StepSmem<true, 16>>(6, 3, 6));
+
 // pool [P * H, 128, 128]: boxes of one state's 128 rows x 128 bytes; tokens [N, T, H, 2, 64]: boxes of
 // 8 tokens of one head (zeros past T), all columns of keys and queries, half of them of values. (A
 // copy costs its issuing warp about 90 ns whatever its size: boxes of 4 tokens x 64 columns bounded
