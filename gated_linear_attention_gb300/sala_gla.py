@@ -465,7 +465,8 @@ def recurrent_draft_step(q, k, v, g, scale, pool, indices, pending=None, accepte
     new tokens (q, k, v: bf16 [N, T, H, 128], g: fp32 [N, T, H]) from there without storing their
     states. ``accepted``: int32 [N], as from :func:`verify_drafts` (negative: commit nothing);
     ``num_tokens``: int32 [N] or None (T each); pool: fp32 or bf16 [P, H, 128, 128]; indices:
-    int32 [N], negative for padding. q = k = v = g = None only commits. Returns o (bf16
+    int32 [N], negative for padding; a slot that a row commits to may stand in no other row.
+    q = k = v = g = None only commits. Returns o (bf16
     [N, T, H, 128], zeros past a row's tokens), None if there are no new tokens."""
     L, P, H, dt = _pool(pool)
     if pool.dim() != 4:

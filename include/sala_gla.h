@@ -375,8 +375,9 @@ int sala_gla_verify_drafts(const void *target_probs, int64_t target_stride, cons
  *                  arithmetic is fp32; a bf16 state is rounded once, when the commit is stored,
  *                  and o reads the values before that rounding.
  *   state_indices  int32 [N] slots, negative: padding row (o = 0, no state touched, its counts and
- *                  tokens may be anything). Two rows that commit to one slot race; the caller must not
- *                  do that.
+ *                  tokens may be anything). A slot that a row commits to may stand in no other row of
+ *                  the call: two commits race, and a row that only reads sees either state. Rows that
+ *                  commit nothing may share a slot.
  *   o              bf16 [N, T, H, 128] output
  * A slot >= P, more commits than T_pend or a token count outside [0, T] is recorded as
  * SALA_ERR_BAD_INDEX and its row is treated as padding. Infinities and NaN among the tokens committed and
