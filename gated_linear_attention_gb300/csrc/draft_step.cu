@@ -23,7 +23,8 @@
 // state in shared memory, 16 key rows at a time, feeds both. Operands that are fp32 (w_j v_j, the state, the
 // tokens' weights) go in three bf16 parts that sum to them, so every product is exact and the sums are
 // fp32 (with two parts of the state and the weights, 17 of 24 bits, o had three times as many elements on
-// the wrong side of a bf16 rounding; 256 rows of 5, fp32, took as long). An fp32 state is read after the
+// the wrong side of a bf16 rounding; 256 rows of 5, fp32, took 181 us and not 177, 201 ragged bf16 rows 111 and
+// not 113, 256 fp32 rows of 17 328 and not 366). An fp32 state is read after the
 // commit. A bf16 state is read as it was stored, an operand without any
 // arithmetic, and what the commit adds to it enters as the pending tokens' own term (Q K^T w) V.
 // Infinities and NaN: a commit that has them is taken one product at a time (commit_by_one), so that the stored
@@ -33,10 +34,10 @@
 // reaches a result.
 // Longer steps (draft_step_long_kernel) take 16 tokens at a time over a state held in shared memory.
 //
-// Bound by the memory with fp32 states: 256 rows of 5 tokens, 32 heads, 181 us, 6.2 TB/s of what has to
-// move; 16 tokens, 195 us. With bf16 states the same tokens come with half the bytes and the
-// shared-memory accesses and arithmetic of a step show: 5 tokens 112 us (floor 87), 16 tokens 142 us
-// (floor 104).
+// Bound by the memory with fp32 states: 256 rows of 5 tokens, 32 heads, 177 us, 6.4 TB/s of what has to
+// move; 16 tokens, 192 us (floor 184). With bf16 states the same tokens come with half the bytes and the
+// shared-memory accesses and arithmetic of a step show: 5 tokens 112 us (floor 87), 16 tokens 146 us
+// (floor 104), 201 ragged rows of up to 16 116 us (floor 76).
 #include <type_traits>
 
 #include "chunk_tc.cuh"
@@ -122,12 +123,13 @@ struct StepSmem {
     // halves of Q S, [4 warps][kTok / 2][32 lanes] fp32, in the place of the queries once they are read
     static constexpr int kSwap = kQ;
     static_assert(4 * kTok / 2 * 32 * 4 <= kK - kQ, "the halves fit");
-    // Groups: three keep the memory busy with fp32 states; four with bf16 states and 8 tokens (256 rows of
-    // 5 tokens: 109 us, with three 116); with 16 tokens the registers of four do not suffice (201 ragged
-    // rows: 111 us with three, 115 with four). Stages as far as memory goes.
+    // Groups: three keep the memory busy with fp32 states; four with bf16 states and 8 tokens (16 rows of 5
+    // tokens 10.0 us, with three 10.2; 64 rows 31.4 and 31.7; 256 rows, all memory, 111.8 and 110.2); with 16
+    // tokens the registers of four do not suffice (201 ragged rows: 116 us with three, 120 with four). Stages as
+    // far as memory goes.
     static constexpr int kGroups = kBf16 && kTok == 8 ? 4 : 3;
     // (fp32: 4 stages of 33 KB states; with 5 the loads run so far ahead of the stores that the memory
-    // serves both more slowly, 256 rows of 5 tokens in 186 us instead of 178)
+    // serves both more slowly, 256 rows of 5 tokens in 189 us instead of 177)
     static constexpr int kFit = (232448 - 1024 - kGroups * kOwn) / (kStage + kSide);
     static constexpr int kStages = !kBf16 && kFit > 4 ? 4 : kFit;
     // "Full" barriers: a multiple of the groups, so that a barrier's phases are all one group's. Were they
@@ -823,9 +825,9 @@ draft_step_kernel(DraftArgs a, const __grid_constant__ StepMaps maps, unsigned i
 // new tokens; then the state is stored, and each pass adds the block that the one before read for. All
 // copies are asynchronous, a block's at the start of its pass: four CTAs on an SM, which 128 registers a
 // thread allow, hide that from each other (with a second buffer for the blocks, which leaves room for
-// three, 256 fp32 rows of 17 take a fourteenth longer; with plain loads 617 us). Bound by the passes, about
-// 1 us of an SM's time each whatever the block holds: 256 rows of 17, 32 heads, 3 passes, 328 us with fp32
-// states (floor 185), 320 with bf16 (106); 16 rows of 200 bf16 161 us.
+// three, 256 fp32 rows of 17 take a fourteenth longer; with plain loads, nearly twice as long). Bound by the
+// passes, a little over 1 us of an SM's time each whatever the block holds: 256 rows of 17, 32 heads, 3 passes,
+// 359 us with fp32 states (floor 185), 352 with bf16 (106); 16 rows of 200 after 200, bf16, 175 us (floor 24).
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
@@ -976,8 +978,8 @@ cudaError_t launch_draft_step(const void *q, const void *k, const void *v, const
                       static_cast<const uint16_t *>(pend_k), static_cast<const uint16_t *>(pend_v),
                       pend_g, accepted, scale, pool, slots, P, static_cast<uint16_t *>(o), T, T_pend, H,
                       status};
-    // the persistent kernel where a step is one pass: 256 rows of 16, bf16, in 141 us, 197 by the kernel
-    // for longer ones; fp32 195 and 208; one row of 5, 4.3 and 5.4
+    // the persistent kernel where a step is one pass: 256 rows of 16, bf16, in 146 us, 213 by the kernel
+    // for longer ones; fp32 192 and 220; one row of 5, 4.5 and 5.8
     if (T <= 16 && T_pend <= 16) {
         StepMaps maps{};
         cudaError_t e = pool_map(&maps.pool, pool, bf16, P * H);
@@ -987,8 +989,8 @@ cudaError_t launch_draft_step(const void *q, const void *k, const void *v, const
         if (e == cudaSuccess && T) e = token_map(&maps.k, k, N, T, H, false);
         if (e == cudaSuccess && T) e = token_map(&maps.v, v, N, T, H, true);
         if (e != cudaSuccess) return e;
-        // operands of 8 tokens where they suffice: 256 bf16 rows of 5 in 112 us instead of 142, 64 fp32
-        // rows of 5 in 44 us instead of 47 (256 fp32 rows, all memory, 180 us instead of 175)
+        // operands of 8 tokens where they suffice: 256 bf16 rows of 5 in 112 us, with those of 16 in 144; 256
+        // fp32 rows of 5 in 177 and 183, of 8 in 184 and 185, 64 fp32 rows of 5 in 49 and 51, one in 4.5 and 5.1
         const bool few = T <= 8 && T_pend <= 8;
         const unsigned items = static_cast<unsigned>(2 * N * H);
         const unsigned grid = items < static_cast<unsigned>(sm_count) ? items : sm_count;

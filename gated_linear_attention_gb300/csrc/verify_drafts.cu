@@ -20,10 +20,11 @@
 // memory, which finds the part that holds the drawn number and goes through it again (from L2).
 //
 // Bound by the memory for large batches, short of the copy rate by the dependent steps at both ends
-// of a row: 256 rows of 131072 fp32 take 46.4 us where the bytes of p_a and (for the 76 % of rows with a
-// rejection) q_a need 35 us, 1024 rows 145 us (floor 140); one row of 65536 takes 5.7 us, which is latency.
-// With bf16 the arithmetic on twice as many values in the same bytes shows: 512 rows of 131072 take 56 us
-// (floor 35).
+// of a row: 256 rows of 131072 fp32 (5 drafts) take 47 us where the bytes of p_a and (for the 76 % of rows with
+// a rejection) q_a need 35 us, 1024 rows 148 us (floor 140); one row of 65536 takes 5.8 us, which is latency.
+// With bf16 the same bytes take 1.6 times the instructions: 512 rows of 131072 take 56 us (floor 35), with the
+// issue slots a half and the memory two fifths busy. Rows of p and q that are not aligned alike are read one
+// value at a time: 256 fp32 rows of 50257 take 29.0 us, of 50256 25.1; bf16 23.9 and 19.2.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -482,10 +483,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyArg
 }
 
 // CTAs that share a row. Each pays some 5 us of dependent steps (the accept test, the hand-over of its
-// sums), so it gets at least 12 KB of the row's target probabilities (32 rows of 8000 bf16: 8 CTAs 7.3 us,
-// 1 CTA 5.9) and, where the launch fills the SMs anyway, 48 KB (2048 rows of 32000 bf16: 8 CTAs 130 us, 2
-// CTAs 60, 1 CTA 53; 1024 rows of 131072 bf16: 8 CTAs 115, 4 CTAs 96). More CTAs where there is more to
-// read: their ends overlap better (1024 rows of 131072 fp32: 8 CTAs 144 us, 2 CTAs 195).
+// sums), so it gets at least 12 KB of the row's target probabilities (32 rows of 8000 bf16: 8 CTAs 7.5 us,
+// 1 CTA 5.9) and, where the launch fills the SMs anyway, 48 KB (2048 rows of 32000 bf16: 8 CTAs 132 us, 2
+// CTAs 61, 1 CTA 54; 1024 rows of 131072 bf16: 8 CTAs 118, 4 CTAs 98, 2 CTAs 101). More CTAs where there is
+// more to read: their ends overlap better (1024 rows of 131072 fp32: 8 CTAs 148 us, 4 CTAs 154, 2 CTAs 201).
 int cluster_size(int64_t N, int64_t row_bytes, int sm_count) {
     int c = kMaxCluster;
     while (c > 1 && (row_bytes < c * (12 << 10) || (N * c > 8 * sm_count && row_bytes < c * (48 << 10)))) c /= 2;
@@ -499,7 +500,7 @@ static_assert(kSmSmem / kVerifyFits >= kStaticSmem, "a CTA's own memory fits so 
 
 // A cluster's CTAs are packed onto as few SMs as hold them, so a small launch would leave most SMs
 // idle: it asks for the most memory per CTA with which all its clusters still run at once (32 rows of
-// 131072 fp32: 16.5 us packed, 12.4 us spread).
+// 131072 fp32: 14.3 us packed, 12.2 us spread).
 size_t spread(int64_t N, int c, const int *fits) {
     for (int i = 0; c == kMaxCluster && i < kVerifyFits; ++i)
         if (N <= fits[i]) return room_for(i + 1);
