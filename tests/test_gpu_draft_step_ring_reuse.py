@@ -38,7 +38,7 @@ def _tokens(gen, N, T, H, counts):
 
 @pytest.mark.parametrize("storage", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,Tp", [(5, 5), (8, 1), (16, 16), (9, 12)])
-def test_many_rounds_of_the_ring(sg, T, Tp, storage):
+def test_stages_used_many_times(sg, T, Tp, storage):
     N, H, P = 160, 32, 200
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     gen = torch.Generator(device="cuda").manual_seed(T * 100 + Tp)
@@ -59,7 +59,7 @@ def test_many_rounds_of_the_ring(sg, T, Tp, storage):
     pool = before.clone()
     o = call(pool, (0, N))
     assert sg.get_device_status() == 0
-    assert 2 * N * H >= 3 * 9 * sms              # three rounds of the longest ring
+    assert 2 * N * H >= 3 * 9 * sms              # three times through the longest ring
     few = STAGES * sms // (2 * H)                # rows of a call that uses a stage once at most
     pool2, o2 = before.clone(), []
     for r in range(0, N, few):
