@@ -1,5 +1,6 @@
 // C ABI of the sala_gla library: argument validation, per-device set-up, scratch and launch
 // order. Declarations and the contract of every entry point are in include/sala_gla.h.
+#include <algorithm>
 #include <atomic>
 #include <cstdlib>
 #include <mutex>
@@ -63,6 +64,8 @@ DeviceState *device_state(int *err) {
         d.init_error = setup_draft_step_kernel();
         if (d.init_error != cudaSuccess) return;
         d.init_error = setup_verify_drafts_kernel(d.verify_fits);
+        if (d.init_error != cudaSuccess) return;
+        d.init_error = setup_paged_attention_kernel();
     });
     if (d.init_error != cudaSuccess) {
         *err = SALA_ERR_CUDA;
@@ -92,7 +95,10 @@ const char *const kKernelNames[kKernelCount] = {"seg_table", "prefill_fused", "r
                                                 "qk_prologue", "gdn_step", "gdn_fwd",
                                                 "gdn_newv", "prefill_pair",
                                                 "verify_drafts", "draft_step", "pool_plan",
-                                                "pool_copy"};
+                                                "pool_copy", "kv_append", "paged_plan",
+                                                "paged_attention", "paged_combine",
+                                                "paged_weights", "kv_select", "kv_move",
+                                                "token_logprobs"};
 struct TimingRecord {
     int id;
     cudaEvent_t start, stop;
@@ -775,6 +781,203 @@ int sala_gla_state_pool_compact(void *pool, int32_t dtype, int64_t L, int64_t P,
     if (!device_state(&err)) return err;
     if (launch_state_pool_compact(pool, dtype == SALA_STATE_BF16, L, P, H, used, mapping, live,
                                   static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SALA_ERR_CUDA;
+    return SALA_OK;
+}
+
+namespace {
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// What the entry points of a paged cache have in common: its sizes, types and pointers, and the
+// new tokens' offsets. Fills *c but for status.
+int check_kv(const sala_kv_cache *cache, const int64_t *cu, int64_t N, int64_t T, KvArgs *c) {
+    if (!cache || N < 0 || T < 0) return SALA_ERR_INVALID_ARG;
+    const sala_kv_cache &k = *cache;
+    if (k.dtype != SALA_KV_BF16 && k.dtype != SALA_KV_E4M3) return SALA_ERR_INVALID_ARG;
+    if (k.page_size < 16 || k.page_size > 256 || (k.page_size & (k.page_size - 1))) return SALA_ERR_INVALID_ARG;
+    if (k.num_kv_heads < 1 || k.num_kv_heads > 65535 || k.num_pages < 1 || k.table_width < 1) return SALA_ERR_INVALID_ARG;
+    // places and (page, head) rows are counted in 32 bits, bytes in 64
+    if (k.num_pages >= kMaxRows / k.num_kv_heads || k.table_width >= kMaxRows / k.page_size) return SALA_ERR_INVALID_ARG;
+    if (N > (int64_t(1) << 20) / 4 || (N > 0 && T > (kMaxRows - 1) / (cu ? 1 : N)) || k.num_kv_heads > (kMaxRows - 1) / (N + 1))
+        return SALA_ERR_INVALID_ARG;
+    if (!k.k_pages || !k.v_pages || (N > 0 && (!k.block_table || !k.kv_lens))) return SALA_ERR_INVALID_ARG;
+    if (k.dtype == SALA_KV_BF16 && (k.k_scale || k.v_scale)) return SALA_ERR_INVALID_ARG;
+    if (!aligned16(k.k_pages) || !aligned16(k.v_pages) || !aligned4(k.k_scale) || !aligned4(k.v_scale) ||
+        !aligned4(k.weights) || !aligned4(k.block_table) || !aligned4(k.kv_lens) || !aligned8(cu))
+        return SALA_ERR_MISALIGNED;
+    c->k = static_cast<uint8_t *>(k.k_pages);
+    c->v = static_cast<uint8_t *>(k.v_pages);
+    c->k_scale = k.k_scale;
+    c->v_scale = k.v_scale;
+    c->weights = k.weights;
+    c->table = k.block_table;
+    c->lens = k.kv_lens;
+    c->cu = cu;
+    c->P = k.num_pages;
+    c->W = k.table_width;
+    c->N = N;
+    c->T = cu ? T : N * T;
+    c->T_row = T;
+    c->S = k.page_size;
+    c->log_S = 0;
+    while ((1 << c->log_S) < k.page_size) ++c->log_S;
+    c->H = k.num_kv_heads;
+    c->e4m3 = k.dtype == SALA_KV_E4M3;
+    return SALA_OK;
+}
+
+// The cache's arrays as ranges: what may be written first.
+struct KvRanges {
+    Range k, v, weights, reads[5];
+    explicit KvRanges(const KvArgs &c) {
+        const size_t rows = static_cast<size_t>(c.P) * c.H * c.S, n = static_cast<size_t>(c.N);
+        const size_t page_bytes = rows * kD * (c.e4m3 ? 1 : 2), h = static_cast<size_t>(c.H) * 4;
+        k = {c.k, page_bytes};
+        v = {c.v, page_bytes};
+        weights = {c.weights, rows * 4};
+        reads[0] = {c.k_scale, h};
+        reads[1] = {c.v_scale, h};
+        reads[2] = {c.table, n * c.W * 4};
+        reads[3] = {c.lens, n * 4};
+        reads[4] = {c.cu, c.cu ? (n + 1) * 8 : 0};
+    }
+    // `r` overlaps one of the pages or the weights
+    bool stored(const Range &r) const {
+        return overlaps(r.p, r.bytes, k.p, k.bytes) || overlaps(r.p, r.bytes, v.p, v.bytes) ||
+               overlaps(r.p, r.bytes, weights.p, weights.bytes);
+    }
+    // the pages, the weights and the arrays that are only read overlap one another
+    bool mixed() const {
+        if (overlaps(k.p, k.bytes, v.p, v.bytes) || overlaps(k.p, k.bytes, weights.p, weights.bytes) ||
+            overlaps(v.p, v.bytes, weights.p, weights.bytes))
+            return true;
+        for (const Range &r : reads)
+            if (stored(r)) return true;
+        return false;
+    }
+};
+
+// Bytes from the first to the last element of `tokens` rows of `row` elements, `stride` apart.
+size_t strided_bytes(int64_t tokens, int64_t stride, int64_t row) {
+    return tokens > 0 ? (static_cast<size_t>(tokens - 1) * stride + row) * 2 : 0;
+}
+bool good_stride(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0 && stride <= (int64_t(1) << 32); }
+}  // namespace
+
+int sala_gla_kv_append(const sala_kv_cache *cache, const void *k, int64_t k_stride, const void *v,
+                       int64_t v_stride, const int64_t *cu_seqlens, int64_t N, int64_t T, void *stream) {
+    KvArgs c;
+    if (const int e = check_kv(cache, cu_seqlens, N, T, &c)) return e;
+    if (c.T == 0 || N == 0) return SALA_OK;
+    const int64_t row = int64_t(c.H) * kD;
+    if (!k || !v || !good_stride(k_stride, row) || !good_stride(v_stride, row)) return SALA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v)) return SALA_ERR_MISALIGNED;
+    const KvRanges r(c);
+    if (r.mixed() || r.stored(Range{k, strided_bytes(c.T, k_stride, row)}) ||
+        r.stored(Range{v, strided_bytes(c.T, v_stride, row)}))
+        return SALA_ERR_INVALID_ARG;
+    int err = SALA_OK;
+    DeviceState *d = device_state(&err);
+    if (!d) return err;
+    c.status = d->status;
+    return launch_kv_append(c, k, k_stride, v, v_stride, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? SALA_OK : SALA_ERR_CUDA;
+}
+
+int sala_gla_paged_attention(const sala_kv_cache *cache, const void *q, int64_t q_stride, float scale,
+                             const int64_t *cu_seqlens, void *o, float *lse, int32_t accumulate, int64_t N,
+                             int64_t T, int32_t Hq, void *stream) {
+    KvArgs c;
+    if (const int e = check_kv(cache, cu_seqlens, N, T, &c)) return e;
+    if (Hq < 1 || Hq % c.H || Hq / c.H > 128 || !(scale > 0.f) || scale > 3.4e38f) return SALA_ERR_INVALID_ARG;
+    if (accumulate && !c.weights) return SALA_ERR_INVALID_ARG;
+    if (c.T == 0 || N == 0) return SALA_OK;
+    const int64_t row = int64_t(Hq) * kD;
+    if (!q || !o || !good_stride(q_stride, row)) return SALA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) || !aligned4(lse)) return SALA_ERR_MISALIGNED;
+    const KvRanges r(c);
+    const Range qr{q, strided_bytes(c.T, q_stride, row)}, out{o, strided_bytes(c.T, row, row)};
+    const Range lr{lse, static_cast<size_t>(c.T) * Hq * 4};
+    if (r.mixed() || r.stored(qr) || r.stored(out) || r.stored(lr) || overlaps_any(out, r.reads) ||
+        overlaps_any(lr, r.reads) || overlaps(out.p, out.bytes, qr.p, qr.bytes) ||
+        overlaps(lr.p, lr.bytes, qr.p, qr.bytes) || overlaps(lr.p, lr.bytes, out.p, out.bytes))
+        return SALA_ERR_INVALID_ARG;
+    int err = SALA_OK;
+    DeviceState *d = device_state(&err);
+    if (!d) return err;
+    c.status = d->status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void *ws = nullptr;
+    const size_t need = paged_attention_scratch(c, Hq / c.H, accumulate != 0, accumulate && !lse, d->sm_count);
+    if (need && cudaMallocFromPoolAsync(&ws, need, d->pool, st) != cudaSuccess) return SALA_ERR_CUDA;
+    int rc = SALA_OK;
+    if (launch_paged_attention(c, q, q_stride, scale, o, lse, accumulate != 0, Hq / c.H, ws, d->sm_count, st) !=
+        cudaSuccess)
+        rc = SALA_ERR_CUDA;
+    if (ws && cudaFreeAsync(ws, st) != cudaSuccess) rc = SALA_ERR_CUDA;
+    return rc;
+}
+
+int sala_gla_kv_evict(const sala_kv_cache *cache, int64_t budget, int64_t sinks, int64_t recent,
+                      int32_t *new_lens, int32_t *kept, int64_t N, void *stream) {
+    KvArgs c;
+    if (const int e = check_kv(cache, nullptr, N, 0, &c)) return e;
+    if (budget < 1 || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks || budget >= kMaxRows ||
+        !c.weights)
+        return SALA_ERR_INVALID_ARG;
+    if (N == 0) return SALA_OK;
+    if (!aligned4(new_lens) || !aligned4(kept)) return SALA_ERR_MISALIGNED;
+    const size_t kept_bytes = static_cast<size_t>(N) * c.H * budget * 4;
+    const KvRanges r(c);
+    const Range lr{new_lens, static_cast<size_t>(N) * 4}, kr{kept, kept_bytes};
+    if (r.mixed() || r.stored(lr) || r.stored(kr) || overlaps_any(lr, r.reads) || overlaps_any(kr, r.reads) ||
+        overlaps(lr.p, lr.bytes, kr.p, kr.bytes))
+        return SALA_ERR_INVALID_ARG;
+    int err = SALA_OK;
+    DeviceState *d = device_state(&err);
+    if (!d) return err;
+    c.status = d->status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void *ws = nullptr;
+    // no request keeps more places than its table has
+    const int64_t most = std::min(budget, c.W * c.S);
+    if (!kept && cudaMallocFromPoolAsync(&ws, static_cast<size_t>(N) * c.H * most * 4, d->pool, st) != cudaSuccess)
+        return SALA_ERR_CUDA;
+    int rc = SALA_OK;
+    if (launch_kv_evict(c, kept ? budget : most, sinks, recent, new_lens, kept ? kept : static_cast<int32_t *>(ws),
+                        d->sm_count, st) != cudaSuccess)
+        rc = SALA_ERR_CUDA;
+    if (ws && cudaFreeAsync(ws, st) != cudaSuccess) rc = SALA_ERR_CUDA;
+    return rc;
+}
+
+int sala_gla_token_logprobs(const void *logits, int64_t stride, int32_t logit_dtype, const int32_t *tokens,
+                            float *logprobs, float *entropy, int32_t *top_tokens, float *top_logprobs, int64_t N,
+                            int64_t V, int32_t M, int32_t K, void *stream) {
+    if (N < 0 || V < 1 || V > SALA_VERIFY_MAX_VOCAB || M < 0 || K < 0 || K > SALA_LOGPROBS_MAX_TOP)
+        return SALA_ERR_INVALID_ARG;
+    if (logit_dtype != SALA_PROB_F32 && logit_dtype != SALA_PROB_BF16) return SALA_ERR_INVALID_ARG;
+    if (N == 0) return SALA_OK;
+    if (N >= kMaxRows / 8 || M > (1 << 20) || stride < V || stride > (int64_t(1) << 32)) return SALA_ERR_INVALID_ARG;
+    if (!logits || (M > 0 && (!tokens || !logprobs)) || (K > 0 && (!top_tokens || !top_logprobs)))
+        return SALA_ERR_INVALID_ARG;
+    const bool bf16 = logit_dtype == SALA_PROB_BF16;
+    if ((reinterpret_cast<uintptr_t>(logits) & (bf16 ? 1u : 3u)) || !aligned4(tokens) || !aligned4(logprobs) ||
+        !aligned4(entropy) || !aligned4(top_tokens) || !aligned4(top_logprobs))
+        return SALA_ERR_MISALIGNED;
+    const size_t n = static_cast<size_t>(N);
+    const Range all[6] = {{logits, (bf16 ? 2 : 4) * ((n - 1) * stride + V)}, {tokens, M > 0 ? 4 * n * M : 0},
+                          {logprobs, M > 0 ? 4 * n * M : 0}, {entropy, 4 * n},
+                          {top_tokens, K > 0 ? 4 * n * K : 0}, {top_logprobs, K > 0 ? 4 * n * K : 0}};
+    for (int i = 2; i < 6; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlaps(all[i].p, all[i].bytes, all[j].p, all[j].bytes)) return SALA_ERR_INVALID_ARG;
+    if (M == 0 && K == 0 && !entropy) return SALA_OK;
+    int err = SALA_OK;
+    DeviceState *d = device_state(&err);
+    if (!d) return err;
+    if (launch_token_logprobs(logits, stride, bf16, tokens, logprobs, entropy, top_tokens, top_logprobs, N, V, M, K,
+                              d->sm_count, d->status, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SALA_ERR_CUDA;
     return SALA_OK;
 }

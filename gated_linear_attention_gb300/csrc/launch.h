@@ -23,6 +23,14 @@ enum KernelId {
     kKDraftStep,
     kKPoolPlan,
     kKPoolCopy,
+    kKKvAppend,
+    kKPagedPlan,
+    kKPagedAttention,
+    kKPagedCombine,
+    kKPagedWeights,
+    kKKvSelect,
+    kKKvMove,
+    kKTokenLogprobs,
     kKernelCount
 };
 
@@ -161,6 +169,39 @@ cudaError_t launch_state_pool_free(int32_t *used, int64_t P, const int32_t *slot
                                    cudaStream_t st);
 cudaError_t launch_state_pool_compact(void *pool, bool bf16, int64_t L, int64_t P, int H, int32_t *used,
                                       int32_t *mapping, int32_t *live, cudaStream_t st);
+
+// A paged cache and a step's new tokens (see sala_kv_cache); kernels take it by value.
+struct KvArgs {
+    uint8_t *k, *v;                    // [P, H, S, 128] pages, bf16 or e4m3
+    const float *k_scale, *v_scale;    // [H] or null
+    float *weights;                    // [P, H, S] or null
+    const int32_t *table, *lens;       // [N, W], [N]
+    const int64_t *cu;                 // [N + 1] token offsets, or null: T_row tokens each
+    int64_t P, W, N, T, T_row;         // T: tokens in all
+    int S, log_S, H;                   // S = 1 << log_S places to a page, H key/value heads
+    bool e4m3;
+    int *status;
+};
+
+// Keys and values of new tokens (strides in elements between tokens) into the pages.
+cudaError_t launch_kv_append(const KvArgs &c, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                             cudaStream_t st);
+
+// Attention of the new tokens; G query heads on each key/value head. `lse` may be null unless
+// `accumulate`. `ws`: scratch of paged_attention_scratch bytes.
+size_t paged_attention_scratch(const KvArgs &c, int G, bool accumulate, bool own_lse, int sm_count);
+cudaError_t setup_paged_attention_kernel();
+cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_stride, float scale, void *o, float *lse,
+                                   bool accumulate, int G, void *ws, int sm_count, cudaStream_t st);
+
+// Eviction: `kept` [N, H, budget] gets the former places (then -1), the kept tokens move.
+cudaError_t launch_kv_evict(const KvArgs &c, int64_t budget, int64_t sinks, int64_t recent, int32_t *new_lens,
+                            int32_t *kept, int sm_count, cudaStream_t st);
+
+// Log probabilities of tokens [N, M], entropy and the K largest logits of rows of V (fp32, or bf16 if `bf16`).
+cudaError_t launch_token_logprobs(const void *x, int64_t stride, bool bf16, const int32_t *tokens, float *logprobs,
+                                  float *entropy, int32_t *top_tokens, float *top_logprobs, int64_t N, int64_t V,
+                                  int M, int K, int sm_count, int *status, cudaStream_t st);
 
 // Nonzero tag of one prefill call for the hand-off flags (differs from the previous call's).
 uint32_t next_prefill_epoch();

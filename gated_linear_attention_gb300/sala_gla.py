@@ -25,6 +25,8 @@ STATUS_NAMES = {
 }
 SALA_STATE_F32, SALA_STATE_BF16 = 0, 1
 SALA_PROB_F32, SALA_PROB_BF16 = 0, 1
+SALA_KV_BF16, SALA_KV_E4M3 = 0, 1
+LOGPROBS_MAX_TOP = 64
 
 class QkPrologue(ctypes.Structure):
     """``sala_qk_prologue``: RMSNorm weights of q and k (bf16 [128] device pointers), eps,
@@ -33,9 +35,18 @@ class QkPrologue(ctypes.Structure):
                 ("eps", ctypes.c_float), ("rope_theta", ctypes.c_float)]
 
 
+class KvCacheStruct(ctypes.Structure):
+    """``sala_kv_cache``: the pointers and sizes of a paged cache."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scale", "v_scale", "weights",
+                                               "block_table", "kv_lens")] + \
+               [(n, ctypes.c_int64) for n in ("num_pages", "table_width")] + \
+               [(n, ctypes.c_int32) for n in ("page_size", "num_kv_heads", "dtype")]
+
+
 # exported symbols and their ctypes signatures (must match include/sala_gla.h)
 _p, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 _pro = ctypes.POINTER(QkPrologue)
+_kv = ctypes.POINTER(KvCacheStruct)
 SIGNATURES = {
     "sala_gla_chunk_fwd": ([_p, _p, _p, _p, _f32, _p, _p, _p, _p, _i64, _i64, _i32, _i64, _p],
                            ctypes.c_int),
@@ -70,6 +81,12 @@ SIGNATURES = {
     "sala_gla_state_pool_fork": ([_p, _i32, _i64, _i64, _i32, _p, _p, _p, _i64, _p], ctypes.c_int),
     "sala_gla_state_pool_free": ([_p, _i64, _p, _i64, _p], ctypes.c_int),
     "sala_gla_state_pool_compact": ([_p, _i32, _i64, _i64, _i32, _p, _p, _p, _p], ctypes.c_int),
+    "sala_gla_kv_append": ([_kv, _p, _i64, _p, _i64, _p, _i64, _i64, _p], ctypes.c_int),
+    "sala_gla_paged_attention": ([_kv, _p, _i64, _f32, _p, _p, _p, _i32, _i64, _i64, _i32, _p],
+                                 ctypes.c_int),
+    "sala_gla_kv_evict": ([_kv, _i64, _i64, _i64, _p, _p, _i64, _p], ctypes.c_int),
+    "sala_gla_token_logprobs": ([_p, _i64, _i32, _p, _p, _p, _p, _p, _i64, _i64, _i32, _i32, _p],
+                                ctypes.c_int),
 }
 
 
@@ -575,6 +592,186 @@ def state_pool_compact(pool, used, mapping=None, live=None, stream=None):
                                             _ptr(live), _stream(stream))
     _check(rc, "sala_gla_state_pool_compact")
     return mapping, live
+
+
+class KvCache:
+    """The paged key/value cache of one softmax layer, ``sala_kv_cache``. k_pages, v_pages: bf16 or
+    float8_e4m3fn [num_pages, Hkv, page_size, 128], page_size 16 to 256 (a power of two); block_table:
+    int32 [N, width]; kv_lens: int32 [N] tokens of each request, the new ones of the step among
+    them; k_scale, v_scale: fp32 [Hkv] (e4m3 only, None: 1); weights: fp32 [num_pages, Hkv, page_size],
+    the running attention weights that eviction goes by, or None. Holds the tensors, copies nothing;
+    their contents (lengths, tables, pages) may change between calls, ``kv_lens`` and ``block_table``
+    may be replaced by :meth:`with_requests`."""
+    __slots__ = ("k_pages", "v_pages", "block_table", "kv_lens", "k_scale", "v_scale", "weights", "N", "H", "_c")
+
+    def __init__(self, k_pages, v_pages, block_table, kv_lens, k_scale=None, v_scale=None, weights=None):
+        if not isinstance(k_pages, torch.Tensor):
+            raise TypeError("k_pages must be a torch.Tensor")
+        dt = k_pages.dtype
+        if dt not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise TypeError(f"k_pages must be bfloat16 or float8_e4m3fn, got {dt}")
+        if k_pages.dim() != 4 or k_pages.shape[3] != 128 or k_pages.shape[2] not in (16, 32, 64, 128, 256):
+            raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, expected (pages, heads, 16 .. 256, 128)")
+        _need(k_pages, "k_pages", dt)
+        _need(v_pages, "v_pages", dt, k_pages.shape)
+        P, H, S, _ = k_pages.shape
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+            raise ValueError("block_table must be a tensor [N, width]")
+        _need(block_table, "block_table", torch.int32)
+        N, W = block_table.shape
+        _need(kv_lens, "kv_lens", torch.int32, (N,))
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                if dt == torch.bfloat16:
+                    raise ValueError(f"{name} is for float8_e4m3fn pages")
+                _need(t, name, torch.float32, (H,))
+        if weights is not None:
+            _need(weights, "weights", torch.float32, (P, H, S))
+        _one_device(k_pages, v_pages, block_table, kv_lens, k_scale, v_scale, weights)
+        self.k_pages, self.v_pages, self.block_table, self.kv_lens = k_pages, v_pages, block_table, kv_lens
+        self.k_scale, self.v_scale, self.weights, self.N, self.H = k_scale, v_scale, weights, N, H
+        self._c = KvCacheStruct(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(weights),
+                                _ptr(block_table), _ptr(kv_lens), P, W, S, H,
+                                SALA_KV_BF16 if dt == torch.bfloat16 else SALA_KV_E4M3)
+
+    def with_requests(self, block_table, kv_lens):
+        """The same pages with another batch's table and lengths."""
+        return KvCache(self.k_pages, self.v_pages, block_table, kv_lens, self.k_scale, self.v_scale, self.weights)
+
+
+def _one_device(*tensors):
+    """The library launches on the current device; all tensors of a call have to lie there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor lies on {t.device}, the current device is cuda:{dev}")
+
+
+def _new_tokens(x, name, cache, heads, cu_seqlens):
+    """Checks new tokens [N, T, heads, 128], or packed [T, heads, 128] with cu_seqlens, whose tokens
+    may lie apart at equal distances; returns (T, elements between tokens)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.dim() != (4 if cu_seqlens is None else 3) or x.shape[-1] != 128 or \
+            (heads is not None and x.shape[-2] != heads) or (cu_seqlens is None and x.shape[0] != cache.N):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected "
+                         f"{'(%d, T, ' % cache.N if cu_seqlens is None else '(T, '}{heads or 'heads'}, 128)"
+                         f"{'' if cu_seqlens is None else ' with cu_seqlens'}")
+    T, H = x.shape[-3], x.shape[-2]
+    ld = H * 128
+    if not x.is_contiguous():
+        tokens = T if cu_seqlens is not None else T * cache.N
+        if tokens > 1:
+            ld = x.stride(-3) if T > 1 else x.stride(0)
+        if x.stride(-1) != 1 or (H > 1 and x.stride(-2) != 128) or ld < H * 128 or ld % 8 or \
+                (cu_seqlens is None and cache.N > 1 and T > 0 and x.stride(0) != T * ld):
+            raise ValueError(f"{name} must have contiguous tokens at equal distances of a multiple of 8 elements")
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int64, (cache.N + 1,))
+    return T, ld
+
+
+def kv_append(cache, k, v, cu_seqlens=None, stream=None):
+    """Keys and values of new tokens into a :class:`KvCache`, ``sala_gla_kv_append``. k, v: bf16
+    [N, T, Hkv, 128], or packed [T, Hkv, 128] with ``cu_seqlens`` (int64 [N + 1]); tokens may lie
+    apart (slices of a fused projection). ``cache.kv_lens`` counts them already."""
+    T, k_ld = _new_tokens(k, "k", cache, cache.H, cu_seqlens)
+    Tv, v_ld = _new_tokens(v, "v", cache, cache.H, cu_seqlens)
+    if T != Tv:
+        raise ValueError("k and v differ in tokens")
+    _one_device(cache.k_pages, k, v, cu_seqlens)
+    rc = load().sala_gla_kv_append(ctypes.byref(cache._c), _ptr(k), k_ld, _ptr(v), v_ld, _ptr(cu_seqlens), cache.N,
+                                   T, _stream(stream))
+    _check(rc, "sala_gla_kv_append")
+
+
+def paged_attention(q, cache, scale, cu_seqlens=None, accumulate=False, o=None, lse=None, stream=None):
+    """Causal attention of new tokens over a :class:`KvCache` that holds them already,
+    ``sala_gla_paged_attention``. q: bf16 [N, T, Hq, 128], or packed [T, Hq, 128] with ``cu_seqlens``
+    (int64 [N + 1]); tokens may lie apart. ``accumulate`` adds each cached token's attention weight,
+    summed over the new tokens and the heads of its group, to ``cache.weights``. Returns (o bf16, the
+    shape of q; lse fp32 without the last dimension)."""
+    T, ld = _new_tokens(q, "q", cache, None, cu_seqlens)
+    Hq = q.shape[-2]
+    if Hq < 1 or Hq % cache.H or Hq // cache.H > 128:
+        raise ValueError(f"{Hq} query heads do not divide over {cache.H} key/value heads (at most 128 on one)")
+    if accumulate and cache.weights is None:
+        raise ValueError("accumulate needs a cache with weights")
+    _one_device(cache.k_pages, q, cu_seqlens, o, lse)
+    if o is None:
+        o = _empty(q.shape, torch.bfloat16, q, stream)
+    else:
+        _need(o, "o", torch.bfloat16, q.shape)
+    if lse is None:
+        lse = _empty(q.shape[:-1], torch.float32, q, stream)
+    else:
+        _need(lse, "lse", torch.float32, q.shape[:-1])
+    rc = load().sala_gla_paged_attention(ctypes.byref(cache._c), _ptr(q), ld, float(scale), _ptr(cu_seqlens), _ptr(o),
+                                         _ptr(lse), 1 if accumulate else 0, cache.N, T, Hq, _stream(stream))
+    _check(rc, "sala_gla_paged_attention")
+    return o, lse
+
+
+def kv_evict(cache, budget, sinks=0, recent=0, new_lens=None, kept=None, stream=None):
+    """Eviction by accumulated attention weight, in place, ``sala_gla_kv_evict``: each request longer
+    than ``budget`` keeps, per key/value head, its first ``sinks`` tokens, its newest ``recent`` ones and the
+    heaviest others, moved together in order. ``cache.kv_lens`` is not changed (layers share it). Returns
+    (new_lens int32 [N]; kept int32 [N, Hkv, budget]: former places, then -1)."""
+    if cache.weights is None:
+        raise ValueError("eviction needs a cache with weights")
+    _one_device(cache.k_pages, new_lens, kept)
+    shape = (cache.N, cache.H, max(0, int(budget)))
+    if new_lens is None:
+        new_lens = _empty((cache.N,), torch.int32, cache.k_pages, stream)
+    else:
+        _need(new_lens, "new_lens", torch.int32, (cache.N,))
+    if kept is None:
+        kept = _empty(shape, torch.int32, cache.k_pages, stream)
+    else:
+        _need(kept, "kept", torch.int32, shape)
+    rc = load().sala_gla_kv_evict(ctypes.byref(cache._c), int(budget), int(sinks), int(recent), _ptr(new_lens),
+                                  _ptr(kept), cache.N, _stream(stream))
+    _check(rc, "sala_gla_kv_evict")
+    return new_lens, kept
+
+
+def token_logprobs(logits, tokens=None, top=0, entropy=True, stream=None):
+    """Log probabilities of given tokens with entropy and top alternatives, ``sala_gla_token_logprobs``.
+    logits: fp32 or bf16 [N, V], rows may be apart (a padded vocabulary); tokens: int32 [N, M] or
+    [N], or None. Returns (logprobs fp32 like tokens, entropy fp32 [N], top_tokens int32 [N, top],
+    top_logprobs fp32 [N, top]); None in place of what was not asked for."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a tensor [N, V]")
+    if logits.device.type != "cuda":
+        raise ValueError("logits must be a CUDA tensor")
+    dt, (N, V) = logits.dtype, logits.shape
+    if dt not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {dt}")
+    ld = logits.stride(0) if N > 1 else V
+    if (V > 1 and logits.stride(1) != 1) or ld < V:
+        raise ValueError("logits must have contiguous rows")
+    M, logprobs, ent, ids, values = 0, None, None, None, None
+    if tokens is not None:
+        if not isinstance(tokens, torch.Tensor) or tokens.dim() not in (1, 2):
+            raise ValueError("tokens must be a tensor [N] or [N, M]")
+        _need(tokens, "tokens", torch.int32, (N, *tokens.shape[1:]))
+        M = tokens.shape[1] if tokens.dim() == 2 else 1
+        logprobs = _empty(tokens.shape, torch.float32, logits, stream)
+    _one_device(logits, tokens)
+    if entropy:
+        ent = _empty((N,), torch.float32, logits, stream)
+    if top:
+        ids = _empty((N, max(0, int(top))), torch.int32, logits, stream)
+        values = _empty((N, max(0, int(top))), torch.float32, logits, stream)
+    rc = load().sala_gla_token_logprobs(_ptr(logits), ld, SALA_PROB_BF16 if dt == torch.bfloat16 else SALA_PROB_F32,
+                                        _ptr(tokens) if M else None, _ptr(logprobs) if M else None, _ptr(ent), _ptr(ids),
+                                        _ptr(values), N, V, M, int(top), _stream(stream))
+    _check(rc, "sala_gla_token_logprobs")
+    return logprobs, ent, ids, values
 
 
 def get_device_status(stream=None) -> int:

@@ -439,6 +439,132 @@ int sala_gla_state_pool_compact(void *pool, int32_t dtype, int64_t L, int64_t P,
                                 int32_t *mapping, int32_t *live, void *stream);
 
 /*
+ * The paged cache of one softmax layer ("MiniCPM-SALA — Complete Blueprint", "Memory Architecture":
+ * the key/value pool of the minicpm4 layers between the lightning layers, 32 query heads on 2
+ * key/value heads of dimension 128). Pages hold the keys (and, apart, the values) of S consecutive
+ * places of one request, head by head, so that the rows of a (page, head) are contiguous:
+ *
+ *   k_pages, v_pages  [num_pages, num_kv_heads, page_size, 128] of dtype. SALA_KV_BF16: bf16.
+ *                     SALA_KV_E4M3: 8-bit floats (4 exponent, 3 mantissa bits); the value that a
+ *                     byte stands for is the 8-bit float times its head's scale.
+ *   k_scale, v_scale  fp32 [num_kv_heads], positive and finite; with SALA_KV_E4M3 only (NULL: 1)
+ *   weights           fp32 [num_pages, num_kv_heads, page_size] or NULL: the running sum of the attention
+ *                     weight that each cached token received, for sala_gla_kv_evict
+ *   block_table       int32 [N, table_width]: place i of request n lies in page
+ *                     block_table[n, i / page_size] at i % page_size. Only the entries that a call needs are
+ *                     read: the pages of places below kv_lens[n] (those of the new tokens for append).
+ *   kv_lens           int32 [N] tokens of each request in the cache, the new ones of this step among them:
+ *                     its T_n new tokens have the places kv_lens[n] - T_n .. kv_lens[n] - 1. Tokens whose
+ *                     place is negative have none: they are not stored and attend to nothing (a padding
+ *                     row of a batch has kv_lens[n] = 0).
+ *   page_size         16, 32, 64, 128 or 256
+ * A length below 0 or above table_width * page_size is recorded as SALA_ERR_BAD_INDEX and taken as 0; a
+ * page outside [0, num_pages) is recorded as SALA_ERR_BAD_INDEX and the outputs of its request are then
+ * unspecified (no access leaves the tensors). Requests may share pages (a common prefix) in calls
+ * that only read them; append, accumulate and evict write, and there a page that is written belongs
+ * to one request. Pages, k, v, q and o are 16-byte aligned, cu_seqlens 8-byte and the other arrays
+ * 4-byte aligned.
+ */
+typedef enum { SALA_KV_BF16 = 0, SALA_KV_E4M3 = 1 } sala_kv_dtype;
+typedef struct {
+    void *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    float *weights;
+    const int32_t *block_table;
+    const int32_t *kv_lens;
+    int64_t num_pages, table_width;
+    int32_t page_size, num_kv_heads, dtype;
+} sala_kv_cache;
+
+/*
+ * Keys and values of new tokens into the cache.
+ *
+ *   k, v          bf16 [tokens, num_kv_heads, 128], tokens k_stride (v_stride) elements apart: at least
+ *                 num_kv_heads * 128, a multiple of 8 (slices of a fused projection)
+ *   cu_seqlens    int64 [N + 1] DEVICE array of token offsets: request n has the tokens cu[n] .. cu[n + 1] - 1
+ *                 of T in all; NULL: each request has T tokens, request after request. A
+ *                 pair that is not 0 <= cu[n] <= cu[n + 1] <= T is recorded as SALA_ERR_BAD_SEQLENS and its
+ *                 request has no tokens. Tokens behind the last request are not touched.
+ * An e4m3 cache stores v / scale (one correctly rounded fp32 division), rounded to nearest even and
+ * clamped to +-448 (infinities too); NaN stays NaN. With weights, the weights of the places become 0.
+ * No argument may overlap the pages or the weights.
+ * Errors: SALA_ERR_INVALID_ARG, SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED, SALA_ERR_CUDA.
+ */
+int sala_gla_kv_append(const sala_kv_cache *cache, const void *k, int64_t k_stride, const void *v,
+                       int64_t v_stride, const int64_t *cu_seqlens, int64_t N, int64_t T, void *stream);
+
+/*
+ * Causal attention of the new tokens over the cache (which holds them already). For new token t of
+ * request n, at place i = kv_lens[n] - T_n + t, and query head h on key/value head h / (Hq / num_kv_heads):
+ *     p_j = exp(scale q.k_j - lse) for j <= i,   lse = log sum_{j <= i} exp(scale q.k_j),
+ *     o = sum_{j <= i} p_j v_j
+ * One call serves one token per request (decoding), drafted tokens, chunks of prompts and batches
+ * that mix them. A token without a place (see sala_kv_cache) gives o = 0 and lse = -inf. Places past a
+ * token's own, unused rows of pages and table entries past the length do not enter its result, whatever
+ * they hold; an infinity or NaN among what it sees gives an infinite or NaN result where it enters (either
+ * may stand for the other).
+ *
+ *   q           bf16 [tokens, Hq, 128], tokens q_stride elements apart (at least Hq * 128, a multiple of 8)
+ *   cu_seqlens  as for sala_gla_kv_append
+ *   scale       > 0 and finite, typically 128^-0.5
+ *   o           bf16 [tokens, Hq, 128] output. Rows behind the last request are left as they were.
+ *   lse         fp32 [tokens, Hq] output (natural logarithm) or NULL
+ *   accumulate  nonzero: adds p_j, summed over the call's new tokens and the query heads of the group, to
+ *               the weights of place j (the cache needs weights). The order of the sum is fixed.
+ *   Hq          a multiple of num_kv_heads, at most 128 query heads on one
+ * Scores, statistics and sums are fp32; p is rounded to bf16 for the product with v. Scratch comes from
+ * the library's stream-ordered pool (as sala_gla_chunk_fwd). A device-side wait that gives up (2 s)
+ * records SALA_ERR_TIMEOUT in the status word.
+ * Errors: SALA_ERR_INVALID_ARG, SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED, SALA_ERR_CUDA.
+ */
+int sala_gla_paged_attention(const sala_kv_cache *cache, const void *q, int64_t q_stride, float scale,
+                             const int64_t *cu_seqlens, void *o, float *lse, int32_t accumulate, int64_t N,
+                             int64_t T, int32_t Hq, void *stream);
+
+/*
+ * Eviction by accumulated attention weight, in place. A request longer than `budget` keeps, in each
+ * key/value head for itself, its first `sinks` tokens, its newest `recent` ones and of the others the
+ * heaviest, `budget` in all; of equal weights the lower place. (Weights below 0 and NaN count as 0.) The
+ * kept tokens move to the places 0 .. budget - 1 in their order, with their weights; what lies behind
+ * stays as it was, and the pages there are the caller's to reuse. Shorter requests are left alone.
+ *
+ *   new_lens  int32 [N] output, min(kv_lens, budget), or NULL. kv_lens itself is not changed (the layers
+ *             of a model share it).
+ *   kept      int32 [N, num_kv_heads, budget] output, the former places of the tokens now at 0, 1, ..
+ *             (then -1), or NULL
+ *   budget    >= 1;  sinks, recent >= 0 with sinks + recent <= budget
+ * Errors: SALA_ERR_INVALID_ARG (also without weights), SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED,
+ * SALA_ERR_CUDA.
+ */
+int sala_gla_kv_evict(const sala_kv_cache *cache, int64_t budget, int64_t sinks, int64_t recent,
+                      int32_t *new_lens, int32_t *kept, int64_t N, void *stream);
+
+/*
+ * Log probabilities of given tokens under rows of logits, with the entropy and the top alternatives:
+ *     lse = log sum_x exp(l(x)),   logp(x) = l(x) - lse,   entropy = -sum_x exp(logp(x)) logp(x)
+ * in natural logarithms, one read of the logits.
+ *
+ *   logits        [N, V] of logit_dtype (sala_prob_dtype), rows `stride` elements apart (>= V)
+ *   tokens        int32 [N, M] given tokens, or NULL with M = 0. A negative one is padding: its output is 0. One
+ *                 >= V is recorded as SALA_ERR_BAD_INDEX and taken as padding.
+ *   logprobs      fp32 [N, M] output
+ *   entropy       fp32 [N] output or NULL
+ *   top_tokens    int32 [N, K] output, the K largest logits in descending order, of equal ones the lower
+ *                 token first; top_logprobs fp32 [N, K] output, theirs. NULL with K = 0. Past the tokens
+ *                 above -inf: -1 and -inf.
+ *   N, V          N >= 0 (0 is a no-op), 1 <= V <= SALA_VERIFY_MAX_VOCAB
+ *   M, K          M >= 0, 0 <= K <= SALA_LOGPROBS_MAX_TOP
+ * A logit of -inf is a token without probability (logp = -inf, no part of the entropy). NaN counts as -inf and
+ * +inf as the largest finite number. A row without any other value: logp = -inf, entropy 0. Pointers
+ * need the alignment of their element type only. No output overlaps another argument.
+ * Errors: SALA_ERR_INVALID_ARG, SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED, SALA_ERR_CUDA.
+ */
+#define SALA_LOGPROBS_MAX_TOP 64
+int sala_gla_token_logprobs(const void *logits, int64_t stride, int32_t logit_dtype, const int32_t *tokens,
+                            float *logprobs, float *entropy, int32_t *top_tokens, float *top_logprobs, int64_t N,
+                            int64_t V, int32_t M, int32_t K, void *stream);
+
+/*
  * Failure-path test settings of the chunked prefill (process-wide; for tests and diagnosis,
  * not for production use). The prefill hands the state of each (segment, head) unit to the
  * next segment through a flag that the successor waits for, and every such wait is bounded
