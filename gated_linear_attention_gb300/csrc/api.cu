@@ -908,7 +908,7 @@ int sala_gla_paged_attention(const sala_kv_cache *cache, const void *q, int64_t 
     c.status = d->status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     void *ws = nullptr;
-    const size_t need = paged_attention_scratch(c, Hq / c.H, accumulate != 0, accumulate && !lse, d->sm_count);
+    const size_t need = paged_attention_scratch(c, Hq / c.H, accumulate != 0, d->sm_count);
     if (need && cudaMallocFromPoolAsync(&ws, need, d->pool, st) != cudaSuccess) return SALA_ERR_CUDA;
     int rc = SALA_OK;
     if (launch_paged_attention(c, q, q_stride, scale, o, lse, accumulate != 0, Hq / c.H, ws, d->sm_count, st) !=

@@ -187,9 +187,9 @@ struct KvArgs {
 cudaError_t launch_kv_append(const KvArgs &c, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                              cudaStream_t st);
 
-// Attention of the new tokens; G query heads on each key/value head. `lse` may be null unless
-// `accumulate`. `ws`: scratch of paged_attention_scratch bytes.
-size_t paged_attention_scratch(const KvArgs &c, int G, bool accumulate, bool own_lse, int sm_count);
+// Attention of the new tokens; G query heads on each key/value head. `lse` may be null. `ws`: scratch of
+// paged_attention_scratch bytes.
+size_t paged_attention_scratch(const KvArgs &c, int G, bool accumulate, int sm_count);
 cudaError_t setup_paged_attention_kernel();
 cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_stride, float scale, void *o, float *lse,
                                    bool accumulate, int G, void *ws, int sm_count, cudaStream_t st);

@@ -1,0 +1,292 @@
+// What the kernels over a paged cache's tiles share (internal): the split of the work over the CTAs, the shared-
+// memory tiles, and how they are filled.
+#pragma once
+
+#include "chunk_tc.cuh"
+#include "kv_cache.cuh"
+
+namespace sala {
+namespace pt {
+
+constexpr int kTile = 128;                       // rows of a query tile, places of a cache tile
+constexpr uint32_t kHalf = kTile * 128;          // bytes of [128 rows x 64 bf16], 128-byte swizzle
+constexpr uint32_t kTileBytes = 2 * kHalf;
+constexpr uint32_t kRawBytes = kTile * kD;       // bytes of a tile of e4m3 values
+constexpr int kInline = 256;                     // requests whose prefix every CTA takes for itself
+constexpr int kConvertWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// ---- work ----------------------------------------------------------------------------------------
+
+// sum of floor((a i + b) / m) for 0 <= i < n (b >= 0): the remainders' part turns into a sum of the same
+// kind with a and m exchanged, as in the Euclidean algorithm.
+__host__ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    int64_t sum = 0;
+    while (true) {
+        if (a >= m) sum += n * (n - 1) / 2 * (a / m), a %= m;
+        if (b >= m) sum += n * (b / m), b %= m;
+        const int64_t y = a * n + b;
+        if (y < m) return sum;
+        n = y / m;
+        b = y % m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+    }
+}
+
+// Attention: unit u of a request is its tokens [u * block, (u + 1) * block) with the cache tiles up to the last
+// place that they see.
+struct AttendWork {
+    int block;
+    __host__ __device__ int units(int count, int) const { return static_cast<int>((static_cast<int64_t>(count) + block - 1) / block); }
+    __host__ __device__ int64_t tiles(int count, int len, int u) const {
+        const int64_t base = static_cast<int64_t>(len) - count;
+        // more tokens than places: each unit takes all of them, which is more than some see
+        const int64_t to = static_cast<int64_t>(u + 1) * block;
+        const int64_t end = base < 0 ? len : base + (to < count ? to : count);
+        return end > 0 ? (end + kTile - 1) / kTile : 1;
+    }
+    // tiles of the units before u; u is at most the number of units less 1
+    __host__ __device__ int64_t before(int count, int len, int u) const {
+        const int64_t base = static_cast<int64_t>(len) - count;
+        if (base < 0) return u * tiles(count, len, 0);
+        return floor_sum(u, kTile, block, base + block + kTile - 1);
+    }
+};
+
+// Weights: unit u of a request is its cache tile u with the query tiles (of `block` tokens) that see it.
+struct WeightWork {
+    int block;
+    __host__ __device__ int units(int count, int len) const { return count > 0 ? (len + kTile - 1) / kTile : 0; }
+    __host__ __device__ int query_tiles(int count) const { return static_cast<int>((static_cast<int64_t>(count) + block - 1) / block); }
+    __host__ __device__ int first(int count, int len, int u) const {
+        const int64_t from = static_cast<int64_t>(u) * kTile - (static_cast<int64_t>(len) - count);
+        return from > 0 ? static_cast<int>(from / block) : 0;
+    }
+    __host__ __device__ int64_t tiles(int count, int len, int u) const { return query_tiles(count) - first(count, len, u); }
+    __host__ __device__ int64_t before(int count, int len, int u) const {
+        const int64_t base = static_cast<int64_t>(len) - count;
+        const int64_t u0 = base > 0 ? (base + kTile - 1) / kTile : 0;
+        const int64_t all = static_cast<int64_t>(u) * query_tiles(count);
+        return u > u0 ? all - floor_sum(u - u0, block, kTile, u0 * kTile - base) : all;
+    }
+};
+
+template <class Work>
+__host__ __device__ inline int64_t tiles_of(const Work &w, int count, int len) {
+    const int units = w.units(count, len);
+    return units > 0 ? w.before(count, len, units - 1) + w.tiles(count, len, units - 1) : 0;
+}
+
+// The requests' running sums of tiles (of one key/value head), N + 1 of them: in shared memory for up to
+// kInline requests, else in global memory, from the plan kernel.
+struct Starts {
+    const uint32_t *near;
+    const int64_t *far;
+    __device__ __forceinline__ int64_t operator[](int64_t n) const { return near ? near[n] : far[n]; }
+};
+
+// A CTA's range of the flattened tiles (key/value head outermost). With fewer tiles than CTAs the first
+// CTAs get one each, so that no range among those that share a unit is empty.
+__host__ __device__ inline int64_t range_begin(int64_t tiles, int64_t cta, int64_t ctas) {
+    if (tiles <= ctas) return cta < tiles ? cta : tiles;
+    return tiles / ctas * cta + tiles % ctas * cta / ctas;
+}
+// The CTA that has tile `at`.
+__host__ __device__ inline int cta_of(int64_t tiles, int64_t at, int64_t ctas) {
+    if (tiles <= ctas) return static_cast<int>(at);
+    int64_t cta = at / (tiles / ctas + 1);   // at most the one sought
+    while (range_begin(tiles, cta + 1, ctas) <= at) ++cta;
+    return static_cast<int>(cta);
+}
+
+// Threads 0 .. kInline - 1 of a CTA: running sums of the requests' tiles into `start` [N + 1], N <= kInline.
+// `sums` holds kInline / 32 words. Ends with a barrier of the whole CTA.
+template <class Work>
+__device__ __forceinline__ void scan_requests(const KvArgs &c, const Work &work, uint32_t *start, uint32_t *sums) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t x = 0;
+    if (tid < c.N) {
+        const kv::Request r = kv::request(c, tid);
+        x = static_cast<uint32_t>(tiles_of(work, r.count, r.len));
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31 && warp < kInline / 32) sums[warp] = x;
+    __syncthreads();
+    if (tid < kInline) {
+        for (int w = 0; w < warp; ++w) x += sums[w];
+        if (tid < c.N) start[tid + 1] = x;
+        if (tid == 0) start[0] = 0;
+    }
+    __syncthreads();
+}
+
+// Where the flattened tile `at` lies: key/value head, request, unit.
+struct Place {
+    int h, u;
+    int64_t n;
+};
+template <class Work>
+__device__ __forceinline__ Place find(const KvArgs &c, const Work &work, const Starts &start, int64_t per_head, int64_t at) {
+    Place p;
+    p.h = static_cast<int>(at / per_head);
+    at -= per_head * p.h;
+    int64_t lo = 0, hi = c.N;
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) / 2;
+        if (start[mid] <= at) lo = mid;
+        else hi = mid;
+    }
+    p.n = lo;
+    const kv::Request r = kv::request(c, lo);
+    at -= start[lo];
+    int a = 0, b = work.units(r.count, r.len);
+    while (b - a > 1) {
+        const int mid = a + (b - a) / 2;
+        if (work.before(r.count, r.len, mid) <= at) a = mid;
+        else b = mid;
+    }
+    p.u = a;
+    return p;
+}
+
+// Walks the items of a CTA: a range [t0, t1) of the tiles of one unit.
+template <class Work>
+struct Walk {
+    int64_t pos, begin, end, per_head, n;
+    int h, u, units, tiles, t0, t1;
+    int slot;            // where a partial result goes, -1: the item is the whole unit
+    kv::Request r;
+
+    __device__ __forceinline__ void enter(const Work &work, int cta, int64_t unit_begin) {
+        tiles = static_cast<int>(work.tiles(r.count, r.len, u));
+        t0 = static_cast<int>(pos - unit_begin);
+        const int64_t left = end - unit_begin;
+        t1 = left < tiles ? static_cast<int>(left) : tiles;
+        slot = t0 == 0 && t1 == tiles ? -1 : 2 * cta + (t0 == 0 ? 1 : 0);
+    }
+    __device__ __forceinline__ void start_at(const KvArgs &c, const Work &work, const Starts &start, const Place &p, int cta) {
+        h = p.h;
+        n = p.n;
+        u = p.u;
+        r = kv::request(c, n);
+        units = work.units(r.count, r.len);
+        enter(work, cta, per_head * h + start[n] + work.before(r.count, r.len, u));
+    }
+    __device__ __forceinline__ bool next(const KvArgs &c, const Work &work, const Starts &start, int cta) {
+        pos += t1 - t0;
+        if (pos >= end) return false;
+        if (++u == units) {
+            u = 0;
+            do {
+                if (++n == c.N) n = 0, ++h;
+            } while (start[n + 1] == start[n]);
+            r = kv::request(c, n);
+            units = work.units(r.count, r.len);
+        }
+        enter(work, cta, pos);
+        return true;
+    }
+};
+
+// Parts of a unit whose first CTA is `cta`: the slot of part p.
+__device__ __forceinline__ int64_t part_slot(int cta, int p) { return 2 * static_cast<int64_t>(cta + p) + (p == 0 ? 1 : 0); }
+
+// ---- tiles ----------------------------------------------------------------------------------------
+
+// Offset in bytes of the 16-byte piece `piece` (of 16) of a row in a bf16 tile.
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+    return (piece >> 3) * kHalf + tck::sw(row, piece & 7);
+}
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+    return tc::smem_desc_sw128(0, 16, 1024) | ((addr >> 4) & 0x3FFFu);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+    return tc::smem_desc_sw128(0, kHalf, 1024) | ((addr >> 4) & 0x3FFFu);
+}
+
+// A cache tile's boxes, one page (at most 128 places) each, and for bf16 one half of the dimensions: lane l of the
+// loading warp has one. Looks up the page of this lane's box: -2: no box, or all of it at or behind `end`.
+template <bool E4M3>
+__device__ __forceinline__ int box_page(const KvArgs &c, int64_t n, int tile, int end, int lane) {
+    const int box = min(c.S, kTile), bx = E4M3 ? lane : lane >> 1;
+    const int place = tile * kTile + bx * box;
+    return bx < kTile / box && place < end ? kv::page_of(c, n, place) : -2;
+}
+
+// Issues the boxes of a tile into `dst` (the whole warp); `bar` gets their bytes.
+template <bool E4M3>
+__device__ __forceinline__ void load_boxes(const KvArgs &c, const CUtensorMap *map, uint8_t *dst, int tile, int h, int page,
+                                           int lane, uint64_t *bar) {
+    const int box = min(c.S, kTile);
+    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page != -2)) * static_cast<uint32_t>(box) * 128u;
+    if (lane == 0) {
+        if (bytes) tc::mbar_arrive_expect_tx(bar, bytes);
+        else tc::mbar_arrive(bar);
+    }
+    __syncwarp();
+    if (page != -2) {
+        const int y = c.S > kTile ? (tile & 1) * kTile : 0, z = (page < 0 ? 0 : page) * c.H + h;   // an unknown page: any
+        if constexpr (E4M3) tc::tma_load_3d(dst + lane * box * kD, map, 0, y, z, bar);
+        else tc::tma_load_3d(dst + (lane & 1) * kHalf + (lane >> 1) * box * 128, map, (lane & 1) * 64, y, z, bar);
+    }
+    __syncwarp();
+}
+
+// e4m3 values of a tile -> a bf16 tile (exact), by kConvertWarps warps. Eight lanes take two rows, the left half of
+// one and the right half of the other: loads and stores then fall on all banks.
+__device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst, int id) {
+    const int lane8 = id & 7, pair = id >> 3;
+#pragma unroll
+    for (int e = 0; e < 1024 / (32 * kConvertWarps); ++e) {
+        const int group = pair + e * (4 * kConvertWarps);        // 128 groups: two for each pair of rows
+        const int row = (group >> 1) * 2 + (lane8 >> 2), p = (lane8 & 3) + 4 * ((group & 1) ^ (lane8 >> 2));
+        const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * kD + p * 16);
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        uint32_t out[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 lo = kv::e4m3x2_to_float2(in[q] & 0xffffu), hi = kv::e4m3x2_to_float2(in[q] >> 16);
+            out[2 * q] = float2_to_bf16x2(lo.x, lo.y);
+            out[2 * q + 1] = float2_to_bf16x2(hi.x, hi.y);
+        }
+        *reinterpret_cast<uint4 *>(dst + piece_at(row, 2 * p)) = make_uint4(out[0], out[1], out[2], out[3]);
+        *reinterpret_cast<uint4 *>(dst + piece_at(row, 2 * p + 1)) = make_uint4(out[4], out[5], out[6], out[7]);
+    }
+}
+
+// Query rows: `tokens` tokens of the group's G heads from packed token `row` (rows past the end are zeros).
+__device__ __forceinline__ void load_query_tile(uint8_t *dst, const CUtensorMap *map, int h, int G, int64_t row, uint64_t *bar) {
+    for (int half = 0; half < 2; ++half)
+        tc::tma_load_3d(dst + half * kHalf, map, half * 64, h * G, static_cast<int>(row), bar);
+}
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+// ---- kernels' arguments ----------------------------------------------------------------------------
+
+struct AttendArgs {
+    KvArgs c;
+    const int64_t *attend_start, *weight_start;   // [N + 1] running sums of tiles, null: each CTA takes them
+    float *part_o;       // [2 * CTAs, 256, 128] partial O
+    float2 *part_ml;     // [2 * CTAs, 256] its maximum (log2) and sum
+    float2 *stats;       // [T, Hq] each row's maximum (log2) and 1 / sum, or null
+    float *part_w;       // [2 * CTAs, 128] partial sums of weights
+    uint16_t *o;
+    float *lse;
+    float scale;
+    int G, TB;           // query heads on a key/value head, tokens of a query tile
+};
+
+cudaError_t setup_paged_weights_kernel();
+cudaError_t launch_paged_weights(const AttendArgs &a, const Maps &maps, int ctas, cudaStream_t st);
+
+}  // namespace pt
+}  // namespace sala
