@@ -15,10 +15,11 @@
 // unit may be shared by several CTAs, which leave partial results (O, m, sum) that a last kernel joins. This
 // serves one token on a long cache and a full batch alike.
 //
-// Roles: a warpgroup per query tile (a thread holds a row of scores: no shuffles), one warp issues the products,
-// one loads by TMA, a page (and half of the dimensions) a box. While one tile's scores are in its warpgroup, the
-// tensor core works on the other tile. e4m3 tiles land in a ring of their own and four more warps widen them
-// (exactly) to bf16.
+// Roles: two groups of eight warps turn scores into weights, one for each query tile (two lanes share a row), one warp
+// issues the products, one loads by TMA, a page (and half of the dimensions) a box. While one group has its
+// scores, the tensor core works for the other. A unit with one query tile gives its cache tiles to the groups in
+// turn, and the results are joined at its end. e4m3 tiles land in a ring of their own and four more warps
+// widen them (exactly) to bf16.
 //
 // What is masked never enters: scores are replaced, not added to, and V is cleared in the rows behind the unit's
 // last place (0 times a NaN there would be NaN). Rows of V that some tokens of the unit see and others do not are
@@ -33,17 +34,16 @@ using tc::mbar_arrive;
 using tck::wait_or_abort;
 
 constexpr int kRows = 2 * kTile;                 // rows of a unit
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvertWarp = 12;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kConvertWarp = 18;
 constexpr int kQ = 2;                            // query tiles, in front of the cache tiles
-constexpr uint32_t kS0 = 0, kO0 = 256;           // tensor memory columns: S of the two tiles, then O
-constexpr uint32_t kP = 64;                      // P, two values a column, over the right half of S
+constexpr uint32_t kS0 = 0, kO0 = 256;           // tensor memory columns: S (and P over it) of the groups, then O
 constexpr float kRescale = 8.f;                  // growth of the maximum (log2) that rescales O
 constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128, 0, 0), kIdO = tc::idesc_bf16_f32(128, 128, 0, 1);
 
 template <bool E4M3>
 struct Shape {
     static constexpr int kStages = E4M3 ? 3 : 5, kRaw = E4M3 ? 4 : 0;
-    static constexpr int kThreads = E4M3 ? 512 : 320;   // warps 10 and 11 of 16 have no part
+    static constexpr int kThreads = 32 * (E4M3 ? kConvertWarp + kConvertWarps : kConvertWarp);
     static constexpr uint32_t kRawAt = (kQ + kStages) * kTileBytes;
     static constexpr uint32_t kAlloc = kRawAt + kRaw * kRawBytes + 1024;   // aligned to the swizzle's 1024 bytes
 };
@@ -65,7 +65,7 @@ struct Barriers {
     uint64_t raw_full[4], raw_empty[4];         // e4m3 cache tiles
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t q_full, q_free;
-    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+    uint64_t s_full[2], p_full[2], o_full[2], o_free[2], join;
     uint64_t drain;
 };
 
@@ -93,17 +93,30 @@ __device__ __noinline__ void bad_dimensions(const KvArgs &c, int64_t n, int h, i
     }
 }
 
+// The 16-lane forms of tensor memory accesses: lanes l and l + 16 of the warp take the same row, 32 columns apart (or
+// OFF apart, for a store).
+__device__ __forceinline__ void tmem_ld_half_x32(uint32_t taddr, uint32_t (&r)[32]) { tc::tmem_ld_16x32bx2_x32(taddr, r); }
+template <int OFF>
+__device__ __forceinline__ void tmem_st_16x32bx2_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], %17, "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "n"(OFF)
+        : "memory");
+}
+
 template <bool E4M3>
 __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ Maps maps) {
     using Layout = Shape<E4M3>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Barriers bar;
-    __shared__ uint32_t near[kInline + 1], sums[kInline / 32];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, bad_values[2];
     __shared__ Place place;
     __shared__ Item ring[kItems];
+    __shared__ float2 other[kTile];   // maxima and sums of the second group, where both have the same rows
     const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *const smem = smem_raw + (base - tc::smem_u32(smem_raw));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
@@ -131,16 +144,18 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         tc::mbar_init(&bar.q_free, 1);
         for (int t = 0; t < 2; ++t) {
             tc::mbar_init(&bar.s_full[t], 1);
-            tc::mbar_init(&bar.p_full[t], 4);
+            tc::mbar_init(&bar.p_full[t], kMmaWarp / 2);
             tc::mbar_init(&bar.o_full[t], 2);
-            tc::mbar_init(&bar.o_free[t], 4);
+            tc::mbar_init(&bar.o_free[t], kMmaWarp / 2);
         }
+        tc::mbar_init(&bar.join, kMmaWarp / 2);
         tc::mbar_init(&bar.drain, 1);
         tc::fence_barrier_init();
         abort_flag = 0;
     }
     dependent_start();
-    if (!a.attend_start) scan_requests(c, work, near, sums);
+    uint32_t *const near = reinterpret_cast<uint32_t *>(smem);   // where the tiles land later
+    if (!a.attend_start) scan_requests(c, work, near, near + kInline + 1);
     const Starts starts{a.attend_start ? nullptr : near, a.attend_start};
     const int64_t per_head = starts[c.N], all = per_head * c.H;
     const int64_t begin = range_begin(all, cta, gridDim.x), stop = range_begin(all, cta + 1, gridDim.x);
@@ -160,10 +175,8 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         uint32_t it = 0, items = 0, q_issued = 0;   // cache tiles and items so far
         bool ok = true;
         Walk<AttendWork> w;
-        w.per_head = per_head;
-        w.pos = w.begin = begin;
-        w.end = stop;
-        w.start_at(c, work, starts, place, cta);
+        w.start_at(c, work, place, begin, stop, cta);
+        tc::fence_proxy_async_smem();   // the running sums were there before the tiles
         do {
             const int tok = w.u * work.block, slot = items % kItems;
             Item x;
@@ -207,7 +220,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 }
             }
             ++items;
-        } while (ok && w.next(c, work, starts, cta));
+        } while (ok && w.next(c, work, cta));
         if (!ok) {   // copies in flight land before the CTA ends
             if (q_issued) tc::mbar_wait(&bar.q_full, (q_issued - 1) & 1, tck::kWaitNs);
             for (uint32_t j = it > kRing ? it - kRing : 0; j < it; ++j)
@@ -232,11 +245,16 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
     } else if (warp == kMmaWarp && !idle) {
         // ---- products ------------------------------------------------------------------------------
         const bool leader = tc::elect_one();
-        uint32_t it = 0, items = 0, sp[2] = {0, 0}, used[2] = {0, 0};   // tiles loaded, items, score tiles, items of a query tile
-        bool ok = true;
-        auto scores = [&](int t, uint32_t stage) {
+        uint32_t it = 0, items = 0, sp[2] = {0, 0}, used[2] = {0, 0};   // tiles loaded, items, score tiles, items of a group
+        bool ok = true, last = false;
+        auto stage_of = [](uint32_t j) { return j % Layout::kStages; };
+        auto loaded = [&](uint32_t j) {
+            return wait_or_abort(&bar.full[stage_of(j)], (j / Layout::kStages) & 1, aborted, status);
+        };
+        auto scores = [&](int t, int q, uint32_t j) {   // of query tile q, for group t
+            tc::tc_fence_after();
             if (leader) {
-                const uint64_t dq = desc_k(base + t * kTileBytes), dk = desc_k(base + (kQ + stage) * kTileBytes);
+                const uint64_t dq = desc_k(base + q * kTileBytes), dk = desc_k(base + (kQ + stage_of(j)) * kTileBytes);
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
                     const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
@@ -246,84 +264,108 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             }
             __syncwarp();
         };
-        bool last = false;
+        auto release = [&](uint32_t j) {
+            if (leader) tc::umma_commit(&bar.empty[stage_of(j)]);
+            __syncwarp();
+        };
+        // O of group t from its P and the values of tile j; `first` of the item, `final` of the item
+        auto products = [&](int t, uint32_t j, bool first, bool final) {
+            if (!wait_or_abort(&bar.p_full[t], sp[t] & 1, aborted, status)) return false;
+            if (first && used[t] > 0 && !wait_or_abort(&bar.o_free[t], (used[t] - 1) & 1, aborted, status)) return false;
+            ++sp[t];
+            tc::tc_fence_after();
+            if (leader) {
+                const uint64_t dv = desc_mn(base + (kQ + stage_of(j)) * kTileBytes);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    tc::umma_bf16_ta(tmem + kO0 + t * kTile, tmem + kS0 + t * kTile + 8 * ks, dv + ks * (2048 >> 4), kIdO,
+                                     !first || ks > 0);
+                if (final) tc::umma_commit(&bar.o_full[t]);
+            }
+            __syncwarp();
+            return true;
+        };
+        // Clears the rows of V that no token sees, and infinities and NaN in those that not all tokens see: true if any
+        auto clean = [&](const Item &x, int i, uint32_t j) {
+            const int p0 = i * kTile, shared_from = max(0, x.limit + 1), end = x.end();
+            if (p0 + kTile <= shared_from) return false;
+            uint8_t *v = smem + (kQ + stage_of(j)) * kTileBytes;
+            for (int e = lane + max(0, min(kTile, end - p0)) * 16; e < kTile * 16; e += 32)
+                *reinterpret_cast<uint4 *>(v + piece_at(e >> 4, e & 15)) = make_uint4(0, 0, 0, 0);
+            bool found = false;
+            for (int e = lane + max(0, shared_from - p0) * 16; e < min(kTile, end - p0) * 16; e += 32) {
+                uint4 *at = reinterpret_cast<uint4 *>(v + piece_at(e >> 4, e & 15));
+                const uint4 y = *at;
+                bool here = false;
+                const uint4 z = make_uint4(clear_bad(y.x, &here), clear_bad(y.y, &here), clear_bad(y.z, &here),
+                                           clear_bad(y.w, &here));
+                if (here) *at = z, found = true;
+            }
+            tc::fence_proxy_async_smem();
+            return __any_sync(0xffffffffu, found) != 0;
+        };
         do {
             ok = wait_or_abort(&bar.item_full[items % kItems], (items / kItems) & 1, aborted, status);
             if (!ok) break;
             const Item &x = ring[items % kItems];
-            const int nt = x.ntok > a.TB ? 2 : 1, t0 = x.t0, t1 = x.t1;
-            const int end = x.end(), shared_from = max(0, x.limit + 1);
+            const int t0 = x.t0, n = x.t1 - t0;
+            const bool two = x.ntok > a.TB;
             bool bad = false;
-            ok = wait_or_abort(&bar.q_full, items & 1, aborted, status) &&
-                 wait_or_abort(&bar.full[it % Layout::kStages], (it / Layout::kStages) & 1, aborted, status);
+            ok = wait_or_abort(&bar.q_full, items & 1, aborted, status) && loaded(it);
             if (!ok) break;
-            tc::tc_fence_after();
-            for (int t = 0; t < nt; ++t) scores(t, it % Layout::kStages);
-            if (leader) tc::umma_commit(&bar.empty[it % Layout::kStages]);
-            if (t1 - t0 == 1 && leader) tc::umma_commit(&bar.q_free);
-            for (int i = t0; i < t1 && ok; ++i) {
-                const uint32_t vs = (it + 1) % Layout::kStages, ks_next = (it + 2) % Layout::kStages;
-                const bool more = i + 1 < t1;
-                ok = wait_or_abort(&bar.full[vs], ((it + 1) / Layout::kStages) & 1, aborted, status);
-                if (!ok) break;
-                const int p0 = i * kTile;
-                if (p0 + kTile > shared_from) {   // rows of V that not all tokens see, or none
-                    uint8_t *v = smem + (kQ + vs) * kTileBytes;
-                    for (int e = lane + max(0, min(kTile, end - p0)) * 16; e < kTile * 16; e += 32)
-                        *reinterpret_cast<uint4 *>(v + piece_at(e >> 4, e & 15)) = make_uint4(0, 0, 0, 0);
-                    bool found = false;
-                    for (int e = lane + max(0, shared_from - p0) * 16; e < min(kTile, end - p0) * 16; e += 32) {
-                        uint4 *at = reinterpret_cast<uint4 *>(v + piece_at(e >> 4, e & 15));
-                        const uint4 x = *at;
-                        bool here = false;
-                        const uint4 y = make_uint4(clear_bad(x.x, &here), clear_bad(x.y, &here), clear_bad(x.z, &here),
-                                                   clear_bad(x.w, &here));
-                        if (here) *at = y, found = true;
-                    }
-                    bad |= __any_sync(0xffffffffu, found) != 0;
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                for (int t = 0; t < nt && ok; ++t) {
-                    ok = wait_or_abort(&bar.p_full[t], sp[t] & 1, aborted, status);
-                    if (ok && i == t0 && used[t] > 0) ok = wait_or_abort(&bar.o_free[t], (used[t] - 1) & 1, aborted, status);
+            if (two) {   // each cache tile for both query tiles
+                for (int t = 0; t < 2; ++t) scores(t, t, it);
+                release(it);
+                if (n == 1 && leader) tc::umma_commit(&bar.q_free);
+                for (int i = 0; i < n && ok; ++i, it += 2) {
+                    ok = loaded(it + 1);
                     if (!ok) break;
-                    ++sp[t];
-                    tc::tc_fence_after();
-                    if (leader) {
-                        const uint64_t dv = desc_mn(base + (kQ + vs) * kTileBytes);
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc::umma_bf16_ta(tmem + kO0 + t * kTile, tmem + kS0 + t * kTile + kP + 8 * ks, dv + ks * (2048 >> 4), kIdO,
-                                             i > t0 || ks > 0);
-                        if (!more) tc::umma_commit(&bar.o_full[t]);
+                    bad |= clean(x, t0 + i, it + 1);
+                    const bool more = i + 1 < n;
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        ok = products(t, it + 1, i == 0, !more) && (!more || t == 1 || loaded(it + 2));
+                        if (ok && more) scores(t, t, it + 2);
                     }
-                    __syncwarp();
-                    if (more) {
-                        if (t == 0) {
-                            ok = wait_or_abort(&bar.full[ks_next], ((it + 2) / Layout::kStages) & 1, aborted, status);
-                            if (!ok) break;
-                            tc::tc_fence_after();
-                        }
-                        scores(t, ks_next);
+                    if (!ok) break;
+                    release(it + 1);
+                    if (more) release(it + 2);
+                    if (i + 2 == n && leader) tc::umma_commit(&bar.q_free);
+                }
+            } else {     // one query tile: the groups take the cache tiles in turn
+                scores(0, 0, it);
+                release(it);
+                if (n > 1) {
+                    ok = loaded(it + 2);
+                    if (!ok) break;
+                    scores(1, 0, it + 2);
+                    release(it + 2);
+                }
+                if (n <= 2 && leader) tc::umma_commit(&bar.q_free);
+                for (int i = 0; i < n && ok; ++i, it += 2) {
+                    const int t = i & 1;
+                    ok = loaded(it + 1);
+                    if (!ok) break;
+                    bad |= clean(x, t0 + i, it + 1);
+                    ok = products(t, it + 1, i < 2, i + 2 >= n);
+                    if (!ok) break;
+                    release(it + 1);
+                    if (i + 2 < n) {
+                        ok = loaded(it + 4);
+                        if (!ok) break;
+                        scores(t, 0, it + 4);
+                        release(it + 4);
+                        if (i + 3 == n && leader) tc::umma_commit(&bar.q_free);
                     }
                 }
-                if (!ok) break;
-                if (leader) {
-                    tc::umma_commit(&bar.empty[vs]);
-                    if (more) tc::umma_commit(&bar.empty[ks_next]);
-                    if (i + 2 == t1) tc::umma_commit(&bar.q_free);
-                }
-                __syncwarp();
-                it += 2;
             }
             if (!ok) break;
+            const int groups = two || n > 1 ? 2 : 1;
             if (leader)
-                for (int t = 0; t < nt; ++t) {
+                for (int t = 0; t < groups; ++t) {
                     bad_values[t] = bad;
                     mbar_arrive(&bar.o_full[t]);
                 }
-            for (int t = 0; t < nt; ++t) ++used[t];
+            for (int t = 0; t < groups; ++t) ++used[t];
             last = x.last;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
@@ -337,65 +379,53 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             __syncwarp();
         }
     } else if (warp < kMmaWarp && !idle) {
-        // ---- softmax and results: a row of scores a thread -----------------------------------------
-        const int t = warp >> 2, r = threadIdx.x & (kTile - 1);
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + kS0 + t * kTile + lanes, to = tmem + kO0 + t * kTile + lanes;
-        const int my_tok = t * a.TB + r / a.G, g = r % a.G;
-        const bool in_tile = r < a.TB * a.G;
-        const bool warp_in = (warp & 3) * 32 < a.TB * a.G;
-        uint32_t seen = 0, items = 0, mine = 0;   // score tiles, items, items that have this query tile
+        // ---- softmax and results: half a row of scores a thread ----------------------------------------
+        // Lanes l and l + 16 share a row: columns [0, 32) and [64, 96), or [32, 64) and [96, 128).
+        const int t = warp >> 3, half = lane >> 4, r = (warp & 3) * 32 + ((warp >> 2) & 1) * 16 + (lane & 15);
+        const int first_row = r & ~15;
+        const uint32_t lanes = static_cast<uint32_t>(first_row) << 16;
+        const uint32_t ts = tmem + kS0 + t * kTile + lanes, to = tmem + kO0 + lanes;
+        uint32_t seen = 0, items = 0, mine = 0, joined = 0;   // score tiles, items, items of this group, items joined
         bool ok = true, last = false;
         do {
             ok = wait_or_abort(&bar.item_full[items % kItems], (items / kItems) & 1, aborted, status);
             if (!ok) break;
             const Item &x = ring[items % kItems];
             last = x.last;
-            if (t == 1 && x.ntok <= a.TB) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
-                ++items;
-                continue;
-            }
-            const int t0 = x.t0, t1 = x.t1;
-            const bool valid = in_tile && my_tok < x.ntok;
-            const int limit = valid ? x.limit + my_tok : -1;
-            const int first_limit = x.limit + t * a.TB;
+            const bool two = x.ntok > a.TB;
+            const int n = x.t1 - x.t0, step = two ? 1 : 2, my_tile = two ? t : 0;
+            const int my_tok = my_tile * a.TB + r / a.G;
+            const bool valid = r < a.TB * a.G && my_tok < x.ntok;
+            const int limit = valid ? x.limit + my_tok : -1, first_limit = x.limit + my_tile * a.TB;
             // a warp without rows leaves its scores as they are: rows of a product do not mix
-            const bool active = warp_in && t * a.TB + (warp & 3) * 32 / a.G < x.ntok;
+            const bool active = first_row < a.TB * a.G && my_tile * a.TB + first_row / a.G < x.ntok;
             const float scale = a.scale * (c.k_scale ? __ldg(c.k_scale + x.h) : 1.f) * kLog2e;
             float m = -INFINITY, l = 0.f;   // the maximum in units of the scores
-            for (int i = t0; i < t1; ++i) {
+            bool fresh = true;
+            for (int i = x.t0 + (two ? 0 : t), t1 = x.t1; i < t1; i += step) {
                 ok = wait_or_abort(&bar.s_full[t], seen & 1, aborted, status);
                 if (!ok) break;
                 ++seen;
                 tc::tc_fence_after();
                 if (active) {
-                    // The right half stays in registers, the left half is read again: all 128 scores would spill. P
-                    // goes where the right half was.
-                    const int keep = limit - i * kTile;
-                    const bool edge = i * kTile + kTile - 1 > first_limit;
                     uint32_t s[2][32];
-                    auto load = [&](int half) {
-                        tc::tmem_ld_32x32b_x32(ts + 64 * half, s[0]);
-                        tc::tmem_ld_32x32b_x32(ts + 64 * half + 32, s[1]);
-                        tc::tmem_ld_wait();
-                        if (edge)
+                    tmem_ld_half_x32(ts, s[0]);
+                    tmem_ld_half_x32(ts + 64, s[1]);
+                    tc::tmem_ld_wait();
+                    if (i * kTile + kTile - 1 > first_limit) {
+                        const int keep = limit - i * kTile - 32 * half;
 #pragma unroll
-                            for (int j = 0; j < 64; ++j)
-                                if (64 * half + j > keep) s[j >> 5][j & 31] = __float_as_uint(-INFINITY);
-                    };
+                        for (int j = 0; j < 64; ++j)
+                            if ((j >> 5) * 64 + (j & 31) > keep) s[j >> 5][j & 31] = __float_as_uint(-INFINITY);
+                    }
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        load(half);
-#pragma unroll
-                        for (int j = 0; j < 64; j += 2)
-                            top[(j >> 1) & 3] = fmaxf(fmaxf(top[(j >> 1) & 3], __uint_as_float(s[j >> 5][j & 31])),
-                                                      __uint_as_float(s[j >> 5][(j & 31) + 1]));
-                    }
-                    const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    if (i == t0) {
+                    for (int j = 0; j < 64; j += 2)
+                        top[(j >> 1) & 3] = fmaxf(fmaxf(top[(j >> 1) & 3], __uint_as_float(s[j >> 5][j & 31])),
+                                                  __uint_as_float(s[j >> 5][(j & 31) + 1]));
+                    float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    tile_top = fmaxf(tile_top, __shfl_xor_sync(0xffffffffu, tile_top, 16));
+                    if (fresh) {
                         m = tile_top;
                     } else {
                         const bool grow = tile_top > m && !((tile_top - m) * scale <= kRescale);
@@ -405,92 +435,132 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                             l *= f;
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                uint32_t o[32];
-                                tc::tmem_ld_32x32b_x32(to + 32 * q, o);
+                                uint32_t o[16];
+                                const uint32_t at = to + t * kTile + (q >> 1) * 64 + (q & 1) * 16;
+                                tc::tmem_ld_16x32bx2_x16(at, o);
                                 tc::tmem_ld_wait();
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tc::tmem_st_32x32b_x32(to + 32 * q, o);
+                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st_16x32bx2_x16<32>(at, o);
                             }
                         }
                     }
                     const float mc = m == -INFINITY ? 0.f : m * scale;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int half = 1; half >= 0; --half) {
-                        if (half == 0) load(0);
-                        uint32_t pk[32];
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float x = tc::ex2(fmaf(__uint_as_float(s[j >> 4][(2 * j) & 31]), scale, -mc));
-                            const float y = tc::ex2(fmaf(__uint_as_float(s[j >> 4][(2 * j + 1) & 31]), scale, -mc));
-                            sum[j & 3] += x + y;
-                            pk[j] = float2_to_bf16x2(x, y);
+                        for (int j = 0; j < 16; ++j) {
+                            const float e0 = tc::ex2(fmaf(__uint_as_float(s[q][2 * j]), scale, -mc));
+                            const float e1 = tc::ex2(fmaf(__uint_as_float(s[q][2 * j + 1]), scale, -mc));
+                            sum[j & 3] += e0 + e1;
+                            pk[j] = float2_to_bf16x2(e0, e1);
                         }
-                        tc::tmem_st_32x32b_x32(ts + kP + 32 * half, pk);
+                        tmem_st_16x32bx2_x16<16>(ts + 32 * q, pk);   // P over the left half of S, which both lanes have read
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tc::tmem_st_wait();
                 }
+                fresh = false;
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[t]);
             }
             if (!ok) break;
-            ok = wait_or_abort(&bar.o_full[t], mine & 1, aborted, status);
-            if (!ok) break;
-            ++mine;
-            tc::tc_fence_after();
-            if (active) {
-                const bool whole = x.slot < 0, some = limit >= 0;   // some: the row sees a place
+            if (active) l += __shfl_xor_sync(0xffffffffu, l, 16);
+            float mc = m == -INFINITY ? m : m * scale;
+            const bool worked = two || t < n;       // this group has an O
+            if (worked) {
+                ok = wait_or_abort(&bar.o_full[t], mine & 1, aborted, status);
+                if (!ok) break;
+                ++mine;
+                tc::tc_fence_after();
+            }
+            const bool join = !two && n > 1;        // both groups have an O of the same rows
+            float f0 = 1.f, f1 = 0.f;
+            if (join && t == 1) {
+                if (lane < 16) other[r] = make_float2(mc, l);
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.join);
+            } else if (join) {
+                ok = wait_or_abort(&bar.join, joined & 1, aborted, status);
+                if (!ok) break;
+                ++joined;
+                tc::tc_fence_after();
+                const float2 y = other[r];
+                const float top = fmaxf(mc, y.x);
+                f0 = mc == -INFINITY ? 0.f : tc::ex2(mc - top);
+                f1 = y.x == -INFINITY ? 0.f : tc::ex2(y.x - top);
+                l = l * f0 + y.y * f1;
+                mc = top;
+            }
+            if (active && (two || t == 0)) {
+                const int slot = x.slot;
+                const bool whole = slot < 0, some = limit >= 0;   // some: the row sees a place
                 uint32_t dims[4] = {0, 0, 0, 0};
                 if (bad_values[t] && valid) bad_dimensions(c, x.n, x.h, x.limit, limit, dims);
                 const float vs = c.v_scale ? __ldg(c.v_scale + x.h) : 1.f;
                 const float inv = whole ? vs / l : 1.f;
-                const int64_t row = (x.row + my_tok) * (a.G * c.H) + x.h * a.G + g;
-                const int64_t prow = static_cast<int64_t>(x.slot) * kRows + t * kTile + r;
+                const int64_t row = (x.row + my_tok) * (a.G * c.H) + x.h * a.G + r % a.G;
+                const int64_t prow = static_cast<int64_t>(slot) * kRows + my_tile * kTile + r;
+                f0 *= inv;
+                f1 *= inv;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t o[32];
+                    const int col = (q >> 1) * 64 + (q & 1) * 16, mycol = col + 32 * half;
+                    uint32_t o[16];
                     __syncwarp();
-                    tc::tmem_ld_32x32b_x32(to + 32 * q, o);
+                    tc::tmem_ld_16x32bx2_x16(to + (two ? t * kTile : 0) + col, o);
                     tc::tmem_ld_wait();
-                    if (dims[q])
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (dims[q] >> j & 1) o[j] = 0x7fc00000u;
+                    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
+                    if (join) {
+                        uint32_t o1[16];
+                        tc::tmem_ld_16x32bx2_x16(to + kTile + col, o1);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
+                    }
+                    const uint32_t bits = (q >> 1 ? (half ? dims[3] : dims[2]) : half ? dims[1] : dims[0]) >> ((q & 1) * 16);
+                    if (bits & 0xffffu)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (bits >> j & 1) o[j] = 0x7fc00000u;
                     if (valid && whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.o + row * kD + 32 * q);
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.o + row * kD + mycol);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t x[4];
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t y[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float lo = __uint_as_float(o[8 * j + 2 * e]), hi = __uint_as_float(o[8 * j + 2 * e + 1]);
-                                x[e] = some ? float2_to_bf16x2(lo * inv, hi * inv) : 0u;
-                            }
-                            dst[j] = make_uint4(x[0], x[1], x[2], x[3]);
+                            for (int e = 0; e < 4; ++e)
+                                y[e] = some ? float2_to_bf16x2(__uint_as_float(o[8 * j + 2 * e]), __uint_as_float(o[8 * j + 2 * e + 1]))
+                                            : 0u;
+                            dst[j] = make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     } else if (valid) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.part_o + prow * kD + 32 * q);
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.part_o + prow * kD + mycol);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        for (int j = 0; j < 4; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     }
                 }
-                if (valid) {
-                    const float mc = m == -INFINITY ? 0.f : m * scale;
+                if (valid && half == 0) {
+                    const float at = mc == -INFINITY ? 0.f : mc;
                     if (!whole) {
-                        a.part_ml[prow] = make_float2(m == -INFINITY ? m : mc, l);
+                        a.part_ml[prow] = make_float2(mc, l);
                     } else {
-                        if (a.lse) a.lse[row] = some ? (mc + log2f(l)) * kLn2 : -INFINITY;
-                        if (a.stats) a.stats[row] = make_float2(mc, 1.f / l);
+                        if (a.lse) a.lse[row] = some ? (at + log2f(l)) * kLn2 : -INFINITY;
+                        if (a.stats) a.stats[row] = make_float2(at, 1.f / l);
                     }
                 }
             }
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&bar.o_free[t]);
+                if (worked && !(join && t == 1)) mbar_arrive(&bar.o_free[t]);
+                if (join && t == 0) mbar_arrive(&bar.o_free[1]);   // read here
                 mbar_arrive(&bar.item_empty[items % kItems]);
             }
             ++items;
@@ -524,8 +594,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_combine_kernel(const Atten
     __syncthreads();
     const kv::Request r = kv::request(c, place.n);
     const int h = place.h, first_tok = place.u * work.block;
-    const int64_t from = per_head * h + starts[place.n] + work.before(r.count, r.len, place.u);
-    const int64_t to = from + work.tiles(r.count, r.len, place.u);
+    const int64_t from = place.begin, to = from + work.tiles(r.count, r.len, place.u);
     if (from < r0 || to <= r1) return;
     const int parts = cta_of(all, to - 1, ctas) - cta + 1;
     const float vs = c.v_scale ? __ldg(c.v_scale + h) : 1.f;

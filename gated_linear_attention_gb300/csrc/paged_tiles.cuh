@@ -126,10 +126,10 @@ __device__ __forceinline__ void scan_requests(const KvArgs &c, const Work &work,
     __syncthreads();
 }
 
-// Where the flattened tile `at` lies: key/value head, request, unit.
+// Where a flattened tile lies: key/value head, request, unit (with its first tile).
 struct Place {
     int h, u;
-    int64_t n;
+    int64_t n, begin;
 };
 template <class Work>
 __device__ __forceinline__ Place find(const KvArgs &c, const Work &work, const Starts &start, int64_t per_head, int64_t at) {
@@ -152,13 +152,14 @@ __device__ __forceinline__ Place find(const KvArgs &c, const Work &work, const S
         else b = mid;
     }
     p.u = a;
+    p.begin = per_head * p.h + start[lo] + work.before(r.count, r.len, a);
     return p;
 }
 
 // Walks the items of a CTA: a range [t0, t1) of the tiles of one unit.
 template <class Work>
 struct Walk {
-    int64_t pos, begin, end, per_head, n;
+    int64_t pos, end, n;
     int h, u, units, tiles, t0, t1;
     int slot;            // where a partial result goes, -1: the item is the whole unit
     kv::Request r;
@@ -170,24 +171,30 @@ struct Walk {
         t1 = left < tiles ? static_cast<int>(left) : tiles;
         slot = t0 == 0 && t1 == tiles ? -1 : 2 * cta + (t0 == 0 ? 1 : 0);
     }
-    __device__ __forceinline__ void start_at(const KvArgs &c, const Work &work, const Starts &start, const Place &p, int cta) {
+    // the range [from, to), whose first tile lies at p
+    __device__ __forceinline__ void start_at(const KvArgs &c, const Work &work, const Place &p, int64_t from, int64_t to, int cta) {
+        pos = from;
+        end = to;
         h = p.h;
         n = p.n;
         u = p.u;
         r = kv::request(c, n);
         units = work.units(r.count, r.len);
-        enter(work, cta, per_head * h + start[n] + work.before(r.count, r.len, u));
+        enter(work, cta, p.begin);
     }
-    __device__ __forceinline__ bool next(const KvArgs &c, const Work &work, const Starts &start, int cta) {
+    __device__ __forceinline__ bool next(const KvArgs &c, const Work &work, int cta) {
         pos += t1 - t0;
         if (pos >= end) return false;
         if (++u == units) {
             u = 0;
-            do {
-                if (++n == c.N) n = 0, ++h;
-            } while (start[n + 1] == start[n]);
-            r = kv::request(c, n);
-            units = work.units(r.count, r.len);
+            do {   // requests without tiles are passed over; one that has some is ahead, as pos < end
+                if (++n == c.N) {
+                    n = 0;
+                    if (++h == c.H) return false;   // the lengths changed under the call
+                }
+                r = kv::request(c, n);
+                units = work.units(r.count, r.len);
+            } while (units == 0);
         }
         enter(work, cta, pos);
         return true;

@@ -100,20 +100,18 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
     dependent_start();
     if (!a.weight_start) scan_requests(c, work, near, sums);
     const Starts starts{a.weight_start ? nullptr : near, a.weight_start};
-    Walk<WeightWork> w;
-    w.per_head = starts[c.N];
-    const int64_t all = w.per_head * c.H;
-    w.pos = w.begin = range_begin(all, cta, gridDim.x);
-    w.end = range_begin(all, cta + 1, gridDim.x);
-    const bool idle = w.pos >= w.end;
-    if (threadIdx.x == 0 && !idle) place = find(c, work, starts, w.per_head, w.pos);
+    const int64_t per_head = starts[c.N], all = per_head * c.H;
+    const int64_t begin = range_begin(all, cta, gridDim.x), stop = range_begin(all, cta + 1, gridDim.x);
+    const bool idle = begin >= stop;
+    if (threadIdx.x == 0 && !idle) place = find(c, work, starts, per_head, begin);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot;
     volatile int *const aborted = &abort_flag;
     int *const status = c.status;
-    if (!idle) w.start_at(c, work, starts, place, cta);
+    Walk<WeightWork> w;
+    if (!idle) w.start_at(c, work, place, begin, stop, cta);
 
     if (warp == kLoadWarp && !idle) {
         // ---- loads: a cache tile of keys for each unit, query tiles ------------------------------------
@@ -148,7 +146,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 held_n = single ? w.n : -1;
                 held_h = w.h;
             }
-            if (!ok || !w.next(c, work, starts, cta)) break;
+            if (!ok || !w.next(c, work, cta)) break;
             page = box_page<E4M3>(c, w.n, w.u, w.r.len, lane);
         } while (true);
         if (!ok) {   // copies in flight land before the CTA ends
@@ -173,7 +171,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 mbar_arrive(&bar.raw_empty[rw]);
             }
             ++it;
-        } while (w.next(c, work, starts, cta));
+        } while (w.next(c, work, cta));
     } else if (warp == kMmaWarp && !idle) {
         // ---- products ------------------------------------------------------------------------------------
         const bool leader = tc::elect_one();
@@ -218,7 +216,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             if (leader) tc::umma_commit(&bar.k_empty[ks]);
             __syncwarp();
             ++kt;
-        } while (w.next(c, work, starts, cta));
+        } while (w.next(c, work, cta));
         if (!ok) {   // products in flight end before the tensor memory is freed
             if (leader) {
                 tc::umma_commit(&bar.drain);
@@ -321,7 +319,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 }
             }
             tile += m;
-        } while (w.next(c, work, starts, cta));
+        } while (w.next(c, work, cta));
     }
     __syncwarp();
     tc::tc_fence_before();
@@ -346,8 +344,7 @@ __global__ void __launch_bounds__(kInline) paged_weights_join_kernel(const Atten
     if (r == 0) place = find(c, work, starts, per_head, r1 - 1);
     __syncthreads();
     const kv::Request q = kv::request(c, place.n);
-    const int64_t from = per_head * place.h + starts[place.n] + work.before(q.count, q.len, place.u);
-    const int64_t to = from + work.tiles(q.count, q.len, place.u);
+    const int64_t from = place.begin, to = from + work.tiles(q.count, q.len, place.u);
     const int64_t p = static_cast<int64_t>(place.u) * kTile + r;
     if (from < r0 || to <= r1 || r >= kTile || p >= q.len) return;
     const int parts = cta_of(all, to - 1, ctas) - cta + 1;
