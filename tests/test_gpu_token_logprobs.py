@@ -84,6 +84,14 @@ def test_ties_and_values_of_every_kind(dtype, V):
     assert _check(x.to(dtype), tokens, 16) == 0
 
 
+def test_zeros_of_both_signs_are_equal():
+    from gated_linear_attention_gb300 import sala_gla
+    x = torch.full((1, 600), -1.0)
+    x[0, [5, 300]] = -0.0
+    x[0, [9, 401]] = 0.0
+    assert sala_gla.token_logprobs(x.cuda(), top=4)[2].tolist() == [[5, 9, 300, 401]]
+
+
 def test_large_vocabulary_and_overflowing_ties():
     x = torch.zeros(2, 1 << 20)
     x[1, 1 << 19:] = 1.0
