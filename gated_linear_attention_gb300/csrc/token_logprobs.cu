@@ -2,19 +2,19 @@
 //
 // With the row's maximum m:  l = sum exp(x - m),  w = sum exp(x - m) (x - m),  lse = m + log l,
 // logp(x) = (x - m) - log l,  entropy = log l - w / l.
-// Every thread keeps m, l and w of its own elements; a larger maximum m' moves them to it by
-// f = exp(m - m'):  l' = f l,  w' = f (w - (m' - m) l). Pairs join the same way, in a fixed order.
+// A larger maximum m' moves sums to it by f = exp(m - m'):  l' = f l,  w' = f (w - (m' - m) l). Pairs join the same
+// way, in a fixed order.
 //
-// Top alternatives: a thread's m is also the largest of its elements, so the K-th largest of a CTA's 256 maxima
-// is a border that the CTA's K largest elements do not lie below. A search by halves finds a border that K to
-// 2 K + 8 threads reach; their warps go through those threads' elements again (from L2) and list what reaches the border.
-// Ties can make that list long: if it does not fit, the CTA looks for its K largest one by one, each time
-// through all of its elements. Places in the order (value, then the lower token) come from counting.
-//
-// A cluster of up to 8 CTAs shares a row and hands its sums and candidates to the first CTA through distributed
-// shared memory.
+// Two kernels. The first streams: a row is cut into parts, a warp takes a part, and the loads of its next part are
+// in flight while it ends one (a CTA for each row lost a quarter of the time in its first loads and its last sums). It
+// leaves the sums of each part and the maximum of each lane. The second joins the parts of a row and finds the top
+// alternatives: the K-th largest of the lanes' maxima is a border that the row's K largest elements do not lie below. A
+// search by halves finds one that K to 3 K / 2 + 4 of 256 groups of lanes reach, and only the elements of lanes that
+// reach it are read again (from L2). What reaches the border is listed; a place in the order (value, then the lower
+// token) comes from counting. Ties can make the list too long: then the K largest are looked for one by one,
+// each time through the whole row.
+#include <algorithm>
 #include <cfloat>
-#include <cooperative_groups.h>
 
 #include "launch.h"
 #include "tc.cuh"
@@ -22,23 +22,25 @@
 namespace sala {
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
 constexpr int kTop = SALA_LOGPROBS_MAX_TOP;
-constexpr int kList = 512;                // candidates of a CTA
-constexpr int kAhead = 4;                 // 16-byte loads of a thread in flight
+constexpr int kMaxParts = 128;            // parts of a row
+constexpr int kList = 1024;               // candidates of a row
+constexpr int kAhead = 4;                 // 16-byte loads of a lane for its next step
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLow = -1.7e38f;          // what lies below adds nothing to sums whose maximum is above -1e38
+constexpr uint32_t kLowBf16x2 = 0xff00ff00u;   // the same in bf16, -1.7014e38
 
 struct LogprobArgs {
     const void *x;
-    int64_t stride;
+    int64_t stride, N;
     const int32_t *tokens;
     float *logprobs, *entropy;
     int32_t *top_tokens;
     float *top_logprobs;
-    int V, M, K;
+    float *sums;         // [N, parts, 4] m, l, w of the parts
+    float *maxima;       // [N, parts, 32] of their lanes, null with K = 0
+    int V, M, K, parts;
     int *status;
 };
 
@@ -56,6 +58,39 @@ struct Vec {
         else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
 };
+// Larger of each of two bf16 (a NaN loses).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Two floats in one 64-bit register; sums, products and multiply-adds of pairs.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 template <typename T>
 __device__ __forceinline__ float logit(const T *p) {
     if constexpr (sizeof(T) == 4) return clean(__ldg(p));
@@ -67,6 +102,8 @@ __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t u = x == 0.f ? 0u : __float_as_uint(x);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
 struct Sums {
     float m, l, w;
@@ -88,6 +125,8 @@ struct Sums {
         l += o.l;
         w += o.w;
     }
+    // maxima that the packed sums can take: no difference to kLow or above overflows
+    __device__ __forceinline__ bool ordinary() const { return fabsf(m) < 1e38f; }
     __device__ __forceinline__ void add(float x) {   // x <= m, or NaN
         // what lies 200 below the maximum, NaN and -inf among it, adds nothing
         const float d = fmaxf(x - m, -200.f), e = tc::ex2(d * kLog2e);
@@ -99,40 +138,149 @@ __device__ __forceinline__ Sums shuffled(Sums s, int o) {
     return {__shfl_xor_sync(0xffffffffu, s.m, o), __shfl_xor_sync(0xffffffffu, s.l, o), __shfl_xor_sync(0xffffffffu, s.w, o)};
 }
 
-// The elements of a row that a thread has: 16-byte vectors first, first + kThreads, .. below `end` (in vectors from the
-// aligned start of the row), and at most one at the row's ends.
-template <typename T>
-struct Share {
-    const T *row, *body;
-    int begin, end;      // vectors of the CTA
-    int heads, tails, V, bodies;   // elements before the first vector, behind the last; vectors
-    bool ends;           // this CTA has the row's ends
+constexpr uint32_t kNone = 0x007fffffu;   // order_of(-inf)
 
-    __device__ __forceinline__ Share(const T *row_, int V_, int rank, int ctas) : row(row_), V(V_) {
-        constexpr int kN = Vec<T>::kN;
+// A row's elements: up to a vector's worth before the first 16-byte boundary, vectors, and the rest. Part j of `parts` has the
+// vectors [begin(j), begin(j + 1)), lane l of its warp those at l, l + 32, .. from the first; part 0 also has the
+// elements at the row's ends, one to a lane.
+template <typename T>
+struct Row {
+    static constexpr int kN = Vec<T>::kN;
+    const T *row, *body;
+    int heads, tails, V, vectors, parts;
+    __device__ __forceinline__ Row(const LogprobArgs &a, int64_t n)
+        : row(static_cast<const T *>(a.x) + n * a.stride), V(a.V), parts(a.parts) {
         heads = min(V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / static_cast<int>(sizeof(T)));
         body = row + heads;
-        bodies = (V - heads) / kN;
-        tails = V - heads - bodies * kN;
-        begin = static_cast<int>(static_cast<int64_t>(bodies) * rank / ctas);
-        end = static_cast<int>(static_cast<int64_t>(bodies) * (rank + 1) / ctas);
-        ends = rank == 0;
+        vectors = (V - heads) / kN;
+        tails = V - heads - vectors * kN;
     }
-    // the element at the row's ends that thread tid has, or -1
-    __device__ __forceinline__ int extra(int tid) const {
-        return !ends || tid >= heads + tails ? -1 : tid < heads ? tid : V - tails + (tid - heads);
+    __device__ __forceinline__ int begin(int part) const { return static_cast<int>(static_cast<int64_t>(vectors) * part / parts); }
+    __device__ __forceinline__ int end_element(int lane) const {   // -1: none
+        return lane >= heads + tails ? -1 : lane < heads ? lane : V - tails + (lane - heads);
     }
+    __device__ __forceinline__ int token(int vector, int e) const { return heads + vector * kN + e; }
 };
 
+// The sums of a lane's next vectors.
+template <typename T>
+__device__ __forceinline__ void add_vectors(Sums &s, const Vec<T> (&x)[kAhead]) {
+    constexpr int kN = Vec<T>::kN;
+    float top = -INFINITY;
+    if constexpr (kN == 8) {
+        uint32_t t2 = 0xff80ff80u;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            t2 = max_bf16x2(max_bf16x2(max_bf16x2(t2, x[u].r.x), max_bf16x2(x[u].r.y, x[u].r.z)), x[u].r.w);
+        top = fmaxf(__uint_as_float(t2 << 16), __uint_as_float(t2 & 0xffff0000u));
+    } else {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int e = 0; e < kN; ++e) top = fmaxf(top, x[u].at(e));   // NaN is passed over
+    }
+    if (top > s.m) s.move_to(fminf(top, FLT_MAX));   // +inf counts as the largest finite number
+    if (s.m == -INFINITY) return;
+    if (!s.ordinary()) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int e = 0; e < kN; ++e) s.add(clean(x[u].at(e)));
+        return;
+    }
+    const uint64_t minus_m = pair(-s.m, -s.m), log2e = pair(kLog2e, kLog2e);
+    uint64_t l = pair(s.l, 0.f), w = pair(s.w, 0.f);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+        const uint32_t r[4] = {x[u].r.x, x[u].r.y, x[u].r.z, x[u].r.w};
+#pragma unroll
+        for (int e = 0; e < kN; e += 2) {
+            uint64_t y;
+            if constexpr (kN == 8) {
+                const float2 f = bf16x2_to_float2(max_bf16x2(r[e / 2], kLowBf16x2));
+                y = pair(f.x, f.y);
+            } else {
+                y = pair(fmaxf(__uint_as_float(r[e]), kLow), fmaxf(__uint_as_float(r[e + 1]), kLow));
+            }
+            const uint64_t d = add2(y, minus_m);
+            const float2 p = unpair(mul2(d, log2e));
+            const uint64_t ex = pair(tc::ex2(p.x), tc::ex2(p.y));
+            l = add2(l, ex);
+            w = fma2(ex, d, w);
+        }
+    }
+    s.l = unpair(l).x + unpair(l).y;
+    s.w = unpair(w).x + unpair(w).y;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) logprob_parts_kernel(const LogprobArgs a) {
+    constexpr int kN = Vec<T>::kN;
+    dependent_start();
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps, tasks = a.N * a.parts;
+    int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (task >= tasks) return;
+    Vec<T> x[kAhead], next[kAhead];
+    const T *body = nullptr;     // of the task whose vectors are loaded next
+    int at = 0, end = 0;
+    float at_end = 0.f;          // the lane's element at the row's ends
+    int has_end = 0;
+    auto enter = [&](int64_t t) {
+        const int64_t n = t / a.parts;
+        const int part = static_cast<int>(t - n * a.parts);
+        const Row<T> r(a, n);
+        body = r.body;
+        at = r.begin(part);
+        end = r.begin(part + 1);
+        const int e = part == 0 ? r.end_element(lane) : -1;
+        has_end = e >= 0;
+        if (has_end) at_end = logit(r.row + e);
+    };
+    auto load = [&]() {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int v = at + u * 32 + lane;
+            if (v < end) next[u].load(body + static_cast<int64_t>(v) * kN);
+            else next[u].r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);   // NaN in fp32, -inf in bf16
+        }
+        at += kAhead * 32;
+    };
+    enter(task);
+    load();
+    Sums s{-INFINITY, 0.f, 0.f};
+    while (true) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) x[u] = next[u];
+        const bool last = at >= end;
+        const float mine = at_end;
+        const int has = has_end;
+        if (last && task + warps < tasks) enter(task + warps);
+        if (!last || task + warps < tasks) load();
+        add_vectors(s, x);
+        if (!last) continue;
+        if (has) {
+            if (mine > s.m) s.move_to(mine);
+            if (s.m > -INFINITY) s.add(mine);
+        }
+        if (a.maxima) a.maxima[task * 32 + lane] = s.m;
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) s.join(shuffled(s, o));
+        if (lane == 0) *reinterpret_cast<float4 *>(a.sums + task * 4) = make_float4(s.m, s.l, s.w, 0.f);
+        task += warps;
+        if (task >= tasks) return;
+        s = {-INFINITY, 0.f, 0.f};
+    }
+}
+
 struct Shared {
-    Sums sums[kWarps];
     uint32_t keys[kList];
     int index[kList];
-    int count;
-    // the first CTA's, filled by its cluster
-    Sums all[kMaxCluster];
-    uint32_t top_keys[kMaxCluster * kTop];
-    int top_index[kMaxCluster * kTop];
+    int count, lanes;
+    uint2 ends[kWarps];
+    uint16_t who[kMaxParts * 32];
+    uint32_t out_keys[kTop];
+    int out_index[kTop];
 };
 
 // Writes the K largest of n candidates in order, of equal keys the lower index first, then 0 and -1 (a key of 0 is
@@ -150,195 +298,228 @@ __device__ __forceinline__ void ranked(const uint32_t *keys, const int *index, i
     }
 }
 
-// The K largest elements of the CTA's share into out (order_of, token), given each thread's maximum.
-template <typename T>
-__device__ __forceinline__ void cta_top(Shared &sh, const Share<T> &share, float mine, int K, uint32_t *out_keys, int *out_index) {
-    constexpr int kN = Vec<T>::kN;
-    constexpr uint32_t kNone = 0x007fffffu;   // order_of(-inf)
-    const int tid = threadIdx.x, lane = tid & 31;
-    const uint32_t key = order_of(mine);
-    if (tid == 0) sh.count = 0;
-    // a border that at least K threads reach (above -inf: all of them where there are fewer), by halves
-    uint32_t lo = kNone + 1, hi = 0xff800000u;   // count(lo) >= K or lo is the least; count(hi) < K
-    int reach = __syncthreads_count(key >= lo);
-    while (reach > 2 * K + 8 && hi - lo > 1) {
+// A border that at least K of the CTA's threads reach with their keys (the least above -inf where there are fewer) and
+// not many more, by halves between the least and the largest key.
+__device__ __forceinline__ uint32_t border_of(Shared &sh, uint32_t key, int K) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t most = __reduce_max_sync(0xffffffffu, key), least = __reduce_min_sync(0xffffffffu, key);
+    __syncthreads();
+    if (lane == 0) sh.ends[warp] = make_uint2(least, most);
+    __syncthreads();
+    uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) lo = min(lo, sh.ends[w].x), hi = max(hi, sh.ends[w].y);
+    ++hi;                          // count(hi) = 0
+    lo = max(lo, kNone + 1);       // count(lo) >= K, or lo is the least above -inf
+    int reach = kThreads;
+    while (reach > K + K / 2 + 4 && hi - lo > 1 && hi > lo) {
         const uint32_t mid = lo + (hi - lo) / 2;
         const int n = __syncthreads_count(key >= mid);
         if (n >= K) lo = mid, reach = n;
         else hi = mid;
     }
-    // every element that reaches the border, a thread's at a time by its whole warp
-    unsigned left = __ballot_sync(0xffffffffu, key >= lo);
-    while (left) {
-        const int who = (tid & ~31) + __ffs(left) - 1;
-        left &= left - 1;
-        for (int v = share.begin + who + lane * kThreads; v < share.end; v += 32 * kThreads) {
-            Vec<T> x;
-            x.load(share.body + static_cast<int64_t>(v) * kN);
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
-                const uint32_t k = order_of(clean(x.at(e)));
-                if (k < lo) continue;
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kList) sh.keys[at] = k, sh.index[at] = share.heads + v * kN + e;
-            }
-        }
-        const int extra = share.extra(who);
-        if (lane == 0 && extra >= 0) {
-            const uint32_t k = order_of(logit(share.row + extra));
-            if (k >= lo) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kList) sh.keys[at] = k, sh.index[at] = extra;
-            }
-        }
-    }
-    __syncthreads();
-    const int n = sh.count;
-    if (n <= kList) {
-        ranked(sh.keys, sh.index, n, K, out_keys, out_index);
-        return;
-    }
-    // too many ties: one after the other
-    uint32_t last = 0xffffffffu;
-    int at = -1;
-    for (int r = 0; r < K; ++r) {
-        uint32_t best = 0;
-        int bi = INT32_MAX;
-        auto see = [&](uint32_t k, int i) {
-            if (k > kNone && (k < last || (k == last && i > at)) && (k > best || (k == best && i < bi))) best = k, bi = i;
-        };
-        for (int v = share.begin + tid; v < share.end; v += kThreads) {
-            Vec<T> x;
-            x.load(share.body + static_cast<int64_t>(v) * kN);
-#pragma unroll
-            for (int e = 0; e < kN; ++e) see(order_of(clean(x.at(e))), share.heads + v * kN + e);
-        }
-        const int extra = share.extra(tid);
-        if (extra >= 0) see(order_of(logit(share.row + extra)), extra);
-        for (int o = 16; o > 0; o /= 2) {
-            const uint32_t k = __shfl_xor_sync(0xffffffffu, best, o);
-            const int i = __shfl_xor_sync(0xffffffffu, bi, o);
-            if (k > best || (k == best && i < bi)) best = k, bi = i;
-        }
-        __syncthreads();
-        if (lane == 0) sh.keys[tid >> 5] = best, sh.index[tid >> 5] = bi;
-        __syncthreads();
-        best = 0;
-        bi = INT32_MAX;
-        for (int w = 0; w < kWarps; ++w)
-            if (sh.keys[w] > best || (sh.keys[w] == best && sh.index[w] < bi)) best = sh.keys[w], bi = sh.index[w];
-        last = best;
-        at = bi;
-        if (tid == 0) out_keys[r] = best, out_index[r] = best ? bi : -1;
-    }
+    return lo;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobArgs a) {
-    constexpr int kN = Vec<T>::kN;
-    __shared__ Shared sh;
-    dependent_start();
-    const cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-    if (ctas > 1) cluster.barrier_arrive();   // waited for before the first access to another CTA's memory
-    const int64_t n = blockIdx.x / ctas;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const T *row = static_cast<const T *>(a.x) + n * a.stride;
-    const Share<T> share(row, a.V, rank, ctas);
+// The K largest of the n listed candidates, in order.
+__device__ __forceinline__ void listed_top(Shared &sh, int n, int K, uint32_t *out_keys, int *out_index) {
+    const int tid = threadIdx.x;
+    if (n > kThreads / 2) {   // fewer first: counting goes by the square
+        uint32_t k[kList / kThreads];
+        int x[kList / kThreads];
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kList / kThreads; ++i) {
+            const int at = tid + i * kThreads;
+            k[i] = at < n ? sh.keys[at] : 0u;
+            x[i] = at < n ? sh.index[at] : -1;
+            best = max(best, k[i]);
+        }
+        const uint32_t lo = border_of(sh, best, K);   // a border of each thread's largest: K candidates reach it
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kList / kThreads; ++i)
+            if (k[i] >= lo && k[i]) {
+                const int at = atomicAdd(&sh.count, 1);
+                sh.keys[at] = k[i];
+                sh.index[at] = x[i];
+            }
+        __syncthreads();
+        n = sh.count;
+    }
+    ranked(sh.keys, sh.index, n, K, out_keys, out_index);
+}
 
+// The sums of a row, by one warp.
+__device__ __forceinline__ Sums row_sums(const LogprobArgs &a, int64_t n, int lane) {
     Sums s{-INFINITY, 0.f, 0.f};
-    for (int v = share.begin + tid; v < share.end; v += kAhead * kThreads) {
-        Vec<T> x[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (v + u * kThreads < share.end) x[u].load(share.body + static_cast<int64_t>(v + u * kThreads) * kN);
-            else x[u].r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);   // NaN in fp32, -inf in bf16
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-            for (int e = 0; e < kN; ++e) top = fmaxf(top, x[u].at(e));   // NaN is passed over
-        if (top == INFINITY) {   // counts as the largest finite number
-            if (s.m < FLT_MAX) s.move_to(FLT_MAX);
-            for (int u = 0; u < kAhead; ++u)
-                for (int e = 0; e < kN; ++e) s.add(clean(x[u].at(e)));
-            continue;
-        }
-        if (top > s.m) s.move_to(top);
-        if (s.m == -INFINITY) continue;
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-            for (int e = 0; e < kN; ++e) s.add(x[u].at(e));
+    for (int p = lane; p < a.parts; p += 32) {
+        const float4 y = *reinterpret_cast<const float4 *>(a.sums + (n * a.parts + p) * 4);
+        s.join({y.x, y.y, y.z});
     }
-    if (const int extra = share.extra(tid); extra >= 0) {
-        const float x = logit(row + extra);
-        if (x > s.m) s.move_to(x);
-        if (s.m > -INFINITY) s.add(x);
-    }
-    const float mine = s.m;
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) s.join(shuffled(s, o));
-    if (lane == 0) sh.sums[warp] = s;
+    return s;
+}
 
-    if (ctas > 1) cluster.barrier_wait();
-    Shared *first = ctas > 1 ? cluster.map_shared_rank(&sh, 0) : &sh;
-    if (a.K > 0) cta_top(sh, share, mine, a.K, first->top_keys + rank * a.K, first->top_index + rank * a.K);
-    __syncthreads();
-    if (tid == 0) {
-        s = sh.sums[0];
-        for (int w = 1; w < kWarps; ++w) s.join(sh.sums[w]);
-        first->all[rank] = s;
-    }
-    if (ctas > 1) cluster.sync();
-    else __syncthreads();
-    if (rank != 0) return;
-
-    s = sh.all[0];
-    for (int c = 1; c < ctas; ++c) s.join(sh.all[c]);
+// The entropy and the given tokens' log probabilities of a row, by `threads` threads from 0.
+template <typename T>
+__device__ __forceinline__ void row_results(const LogprobArgs &a, int64_t n, const Sums &s, int id, int threads) {
     const bool none = s.m == -INFINITY;
     const float logl = logf(s.l);
-    if (tid == 0 && a.entropy) a.entropy[n] = none ? 0.f : fmaxf(0.f, logl - s.w / s.l);
-    for (int j = tid; j < a.M; j += kThreads) {
+    if (id == 0 && a.entropy) a.entropy[n] = none ? 0.f : fmaxf(0.f, logl - s.w / s.l);
+    const T *row = static_cast<const T *>(a.x) + n * a.stride;
+    for (int j = id; j < a.M; j += threads) {
         const int t = __ldg(a.tokens + n * a.M + j);
         if (t >= a.V) record_status(a.status, SALA_ERR_BAD_INDEX);
         a.logprobs[n * a.M + j] = t < 0 || t >= a.V ? 0.f : none ? -INFINITY : (logit(row + t) - s.m) - logl;
     }
-    if (a.K == 0) return;
-    uint32_t *keys = sh.top_keys;
-    int *index = sh.top_index;
-    if (ctas > 1) {
-        ranked(sh.top_keys, sh.top_index, ctas * a.K, a.K, sh.keys, sh.index);   // the empty places come last
-        __syncthreads();
-        keys = sh.keys;
-        index = sh.index;
+}
+
+// Without alternatives: a warp a row.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) logprob_join_kernel(const LogprobArgs a) {
+    dependent_start();
+    const int lane = threadIdx.x & 31;
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (n < a.N) row_results<T>(a, n, row_sums(a, n, lane), lane, 32);
+}
+
+// With alternatives: a CTA a row.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) logprob_top_kernel(const LogprobArgs a) {
+    constexpr int kN = Vec<T>::kN;
+    __shared__ Shared sh;
+    __shared__ Sums sums;
+    dependent_start();
+    const int64_t n = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.K, lanes = a.parts * 32;
+    const Row<T> row(a, n);
+    const float *maxima = a.maxima + n * lanes;
+    uint32_t key = kNone;
+    for (int i = tid; i < lanes; i += kThreads) key = max(key, order_of(maxima[i]));
+    if (warp == kWarps - 1) {
+        const Sums s = row_sums(a, n, lane);
+        if (lane == 0) sums = s;
     }
-    for (int r = tid; r < a.K; r += kThreads) {
-        const uint32_t k = keys[r];
-        const float x = __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-        a.top_tokens[n * a.K + r] = k ? index[r] : -1;
-        a.top_logprobs[n * a.K + r] = k ? (x - s.m) - logl : -INFINITY;
+    if (tid == 0) sh.count = sh.lanes = 0;
+    const uint32_t lo = border_of(sh, key, K);
+    const Sums s = sums;
+    row_results<T>(a, n, s, tid, kThreads);
+    for (int i = tid; i < lanes; i += kThreads)
+        if (order_of(maxima[i]) >= lo) sh.who[atomicAdd(&sh.lanes, 1)] = static_cast<uint16_t>(i);
+    __syncthreads();
+    // every element that reaches the border
+    auto list = [&](float y, int i) {
+        const uint32_t k = order_of(y);
+        if (k < lo) return;
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kList) sh.keys[at] = k, sh.index[at] = i;
+    };
+    const int per = (row.vectors / a.parts + 1 + 31) / 32, items = sh.lanes * per;
+#pragma unroll 4
+    for (int j = tid; j < items; j += kThreads) {
+        const int p = j / per, who = sh.who[p], part = who >> 5, v = row.begin(part) + (who & 31) + (j - p * per) * 32;
+        if (v < row.begin(part + 1)) {
+            Vec<T> x;
+            x.load(row.body + static_cast<int64_t>(v) * kN);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) list(clean(x.at(e)), row.token(v, e));
+        }
+    }
+    if (tid < 32 && row.end_element(tid) >= 0) list(logit(row.row + row.end_element(tid)), row.end_element(tid));
+    __syncthreads();
+    const int listed = sh.count;
+    if (listed <= kList) {
+        listed_top(sh, listed, K, sh.out_keys, sh.out_index);
+        __syncthreads();
+    } else {   // too many ties: one after the other
+        uint32_t last = 0xffffffffu;
+        int at = -1;
+        for (int r = 0; r < K; ++r) {
+            uint32_t best = 0;
+            int bi = INT32_MAX;
+            auto see = [&](float y, int i) {
+                const uint32_t k = order_of(y);
+                if (k > kNone && (k < last || (k == last && i > at)) && (k > best || (k == best && i < bi))) best = k, bi = i;
+            };
+            for (int v = tid; v < row.vectors; v += kThreads) {
+                Vec<T> x;
+                x.load(row.body + static_cast<int64_t>(v) * kN);
+#pragma unroll
+                for (int e = 0; e < kN; ++e) see(clean(x.at(e)), row.token(v, e));
+            }
+            if (tid < 32 && row.end_element(tid) >= 0) see(logit(row.row + row.end_element(tid)), row.end_element(tid));
+            for (int o = 16; o > 0; o /= 2) {
+                const uint32_t k = __shfl_xor_sync(0xffffffffu, best, o);
+                const int i = __shfl_xor_sync(0xffffffffu, bi, o);
+                if (k > best || (k == best && i < bi)) best = k, bi = i;
+            }
+            __syncthreads();
+            if (lane == 0) sh.keys[warp] = best, sh.index[warp] = bi;
+            __syncthreads();
+            best = 0;
+            bi = INT32_MAX;
+            for (int w = 0; w < kWarps; ++w)
+                if (sh.keys[w] > best || (sh.keys[w] == best && sh.index[w] < bi)) best = sh.keys[w], bi = sh.index[w];
+            last = best;
+            at = bi;
+            if (tid == 0) sh.out_keys[r] = best, sh.out_index[r] = bi;
+        }
+        __syncthreads();
+    }
+    const float logl = logf(s.l);
+    for (int r = tid; r < K; r += kThreads) {
+        const uint32_t k = sh.out_keys[r];
+        a.top_tokens[n * K + r] = k ? sh.out_index[r] : -1;
+        a.top_logprobs[n * K + r] = k ? (value_of(k) - s.m) - logl : -INFINITY;
     }
 }
 
-// CTAs that share a row.
-int cluster_size(int64_t N, int64_t row_bytes, int sm_count) {
-    int c = kMaxCluster;
-    while (c > 1 && (row_bytes < c * (8 << 10) || (N * c > 8 * sm_count && row_bytes < c * (48 << 10)))) c /= 2;
-    return c;
+// Parts of a row: at least 2 KB each, and as many as give every warp the same number of them (as near as it goes) or
+// there are warps for. `warps` at once.
+int parts_of(int64_t N, int64_t row_bytes, int K, int64_t warps) {
+    const int64_t most = std::max<int64_t>(K > 0 && row_bytes > 4096 ? 4 : 1, std::min<int64_t>(kMaxParts, row_bytes / 2048));
+    int best = 1;
+    double score = -1.0;
+    for (int64_t p = K > 0 && row_bytes > 4096 ? 4 : 1; p <= most; ++p) {
+        const int64_t rounds = (N * p + warps - 1) / warps;
+        // the share of the warps at work, less what starting a part costs beside its bytes
+        const double busy = static_cast<double>(N * p) / static_cast<double>(rounds * warps);
+        const double s = busy * static_cast<double>(row_bytes / p) / static_cast<double>(row_bytes / p + 1024);
+        if (s > score) score = s, best = static_cast<int>(p);
+    }
+    return best;
 }
+
+constexpr int kWarpsPerSm = 32;
 
 }  // namespace
 
+size_t token_logprobs_scratch(int64_t N, int64_t V, bool bf16, int K, int sm_count) {
+    const int parts = parts_of(N, V * (bf16 ? 2 : 4), K, static_cast<int64_t>(sm_count) * kWarpsPerSm);
+    return static_cast<size_t>(N) * parts * (16 + (K > 0 ? 128 : 0));
+}
+
 cudaError_t launch_token_logprobs(const void *x, int64_t stride, bool bf16, const int32_t *tokens, float *logprobs,
                                   float *entropy, int32_t *top_tokens, float *top_logprobs, int64_t N, int64_t V,
-                                  int M, int K, int sm_count, int *status, cudaStream_t st) {
+                                  int M, int K, void *ws, int sm_count, int *status, cudaStream_t st) {
     LaunchTimer timer(kKTokenLogprobs, st);
-    const LogprobArgs a{x, stride, tokens, logprobs, entropy, top_tokens, top_logprobs, static_cast<int>(V), M, K, status};
-    const int c = cluster_size(N, V * (bf16 ? 2 : 4), sm_count);
-    return launch_dependent_cluster(bf16 ? token_logprobs_kernel<uint16_t> : token_logprobs_kernel<float>,
-                                    static_cast<unsigned>(N * c), c, kThreads, 0, st, a);
+    const int64_t warps = static_cast<int64_t>(sm_count) * kWarpsPerSm;
+    const int parts = parts_of(N, V * (bf16 ? 2 : 4), K, warps);
+    float *sums = static_cast<float *>(ws);
+    const LogprobArgs a{x, stride, N, tokens, logprobs, entropy, top_tokens, top_logprobs, sums,
+                        K > 0 ? sums + N * parts * 4 : nullptr, static_cast<int>(V), M, K, parts, status};
+    const int64_t blocks = std::min((N * parts + kWarps - 1) / kWarps, warps / kWarps);
+    cudaError_t e = launch_dependent(bf16 ? logprob_parts_kernel<uint16_t> : logprob_parts_kernel<float>,
+                                     dim3(static_cast<unsigned>(blocks)), kThreads, st, a);
+    if (e != cudaSuccess) return e;
+    if (K > 0)
+        return launch_dependent(bf16 ? logprob_top_kernel<uint16_t> : logprob_top_kernel<float>,
+                                dim3(static_cast<unsigned>(N)), kThreads, st, a);
+    return launch_dependent(bf16 ? logprob_join_kernel<uint16_t> : logprob_join_kernel<float>,
+                            dim3(static_cast<unsigned>((N + kWarps - 1) / kWarps)), kThreads, st, a);
 }
 
 }  // namespace sala
