@@ -889,7 +889,7 @@ int sala_gla_paged_attention(const sala_kv_cache *cache, const void *q, int64_t 
                              int64_t T, int32_t Hq, void *stream) {
     KvArgs c;
     if (const int e = check_kv(cache, cu_seqlens, N, T, &c)) return e;
-    if (Hq < 1 || Hq % c.H || Hq / c.H > 128 || !(scale > 0.f) || scale > 3.4e38f) return SALA_ERR_INVALID_ARG;
+    if (Hq < 1 || Hq % c.H || Hq / c.H > 128 || !(scale >= 1e-18f && scale <= 1e18f)) return SALA_ERR_INVALID_ARG;
     if (accumulate && !c.weights) return SALA_ERR_INVALID_ARG;
     if (c.T == 0 || N == 0) return SALA_OK;
     const int64_t row = int64_t(Hq) * kD;

@@ -60,6 +60,12 @@ struct alignas(16) Item {
 };
 constexpr int kItems = 4;
 
+// A unit that this CTA began and others finished: `parts` partial results, from this CTA on (0: none).
+struct alignas(16) JoinUnit {
+    int64_t row;
+    int h, ntok, limit, parts;
+};
+
 struct Barriers {
     uint64_t full[5], empty[5];                 // cache tiles
     uint64_t raw_full[4], raw_empty[4];         // e4m3 cache tiles
@@ -164,6 +170,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
+    if (idle && threadIdx.x == 0) static_cast<JoinUnit *>(a.joins)[cta].parts = 0;
     const uint32_t tmem = tmem_slot;
     volatile int *const aborted = &abort_flag;
     int *const status = c.status;
@@ -174,6 +181,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         uint64_t *const full = E4M3 ? bar.raw_full : bar.full, *const empty = E4M3 ? bar.raw_empty : bar.empty;
         uint32_t it = 0, items = 0, q_issued = 0;   // cache tiles and items so far
         bool ok = true;
+        JoinUnit join = {0, 0, 0, 0, 0};
         Walk<AttendWork> w;
         w.start_at(c, work, place, begin, stop, cta);
         tc::fence_proxy_async_smem();   // the running sums were there before the tiles
@@ -220,7 +228,10 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 }
             }
             ++items;
+            if (ok && x.last && lane == 0 && x.slot >= 0 && x.t0 == 0)
+                join = {x.row, x.h, x.ntok, x.limit, cta_of(all, w.pos + w.tiles - 1, gridDim.x) - cta + 1};
         } while (ok && w.next(c, work, cta));
+        if (lane == 0) static_cast<JoinUnit *>(a.joins)[cta] = join;
         if (!ok) {   // copies in flight land before the CTA ends
             if (q_issued) tc::mbar_wait(&bar.q_full, (q_issued - 1) & 1, tck::kWaitNs);
             for (uint32_t j = it > kRing ? it - kRing : 0; j < it; ++j)
@@ -446,20 +457,23 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                         }
                     }
                     const float mc = m == -INFINITY ? 0.f : m * scale;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t scale2 = tc::pair(scale, scale), minus = tc::pair(-mc, -mc);
+                    uint64_t sum2[2] = {0, 0};   // pairs of zeros
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const float e0 = tc::ex2(fmaf(__uint_as_float(s[q][2 * j]), scale, -mc));
-                            const float e1 = tc::ex2(fmaf(__uint_as_float(s[q][2 * j + 1]), scale, -mc));
-                            sum[j & 3] += e0 + e1;
+                            const float2 y = tc::unpair(tc::fma2(
+                                tc::pair(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), scale2, minus));
+                            const float e0 = tc::ex2(y.x), e1 = tc::ex2(y.y);
+                            sum2[j & 1] = tc::add2(sum2[j & 1], tc::pair(e0, e1));
                             pk[j] = float2_to_bf16x2(e0, e1);
                         }
                         tmem_st_16x32bx2_x16<16>(ts + 32 * q, pk);   // P over the left half of S, which both lanes have read
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 even = tc::unpair(sum2[0]), odd = tc::unpair(sum2[1]);
+                    l += (even.x + even.y) + (odd.x + odd.y);
                     tc::tmem_st_wait();
                 }
                 fresh = false;
@@ -552,7 +566,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                         a.part_ml[prow] = make_float2(mc, l);
                     } else {
                         if (a.lse) a.lse[row] = some ? (at + log2f(l)) * kLn2 : -INFINITY;
-                        if (a.stats) a.stats[row] = make_float2(at, 1.f / l);
+                        if (a.stats) a.stats[row] = at + log2f(l);
                     }
                 }
             }
@@ -575,33 +589,18 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
 
 // ---- joins the partial results of units that several CTAs share -----------------------------------
 
-constexpr int kJoinThreads = 256, kJoinRows = 32;
+constexpr int kJoinThreads = 256, kJoinRows = 8;   // a warp a row
 
-__global__ void __launch_bounds__(kJoinThreads) paged_combine_kernel(const AttendArgs a, int ctas) {
-    __shared__ uint32_t near[kInline + 1], sums[kInline / 32];
-    __shared__ Place place;
+__global__ void __launch_bounds__(kJoinThreads) paged_combine_kernel(const AttendArgs a) {
     dependent_start();
     const KvArgs &c = a.c;
-    const AttendWork work{2 * a.TB};
-    if (!a.attend_start) scan_requests(c, work, near, sums);
-    const Starts starts{a.attend_start ? nullptr : near, a.attend_start};
-    const int64_t per_head = starts[c.N], all = per_head * c.H;
-    // this CTA's last unit, if it begins here and ends in a later one
     const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r0 = range_begin(all, cta, ctas), r1 = range_begin(all, cta + 1, ctas);
-    if (r0 >= r1 || r1 >= all) return;
-    if (threadIdx.x == 0) place = find(c, work, starts, per_head, r1 - 1);
-    __syncthreads();
-    const kv::Request r = kv::request(c, place.n);
-    const int h = place.h, first_tok = place.u * work.block;
-    const int64_t from = place.begin, to = from + work.tiles(r.count, r.len, place.u);
-    if (from < r0 || to <= r1) return;
-    const int parts = cta_of(all, to - 1, ctas) - cta + 1;
-    const float vs = c.v_scale ? __ldg(c.v_scale + h) : 1.f;
-    for (int k = warp; k < kJoinRows; k += kJoinThreads / 32) {
-        const int row = blockIdx.y * kJoinRows + k, t = row / kTile, rr = row - t * kTile;
-        const int tok = first_tok + t * a.TB + rr / a.G;
-        if (rr >= a.TB * a.G || t * a.TB + rr / a.G >= work.block || tok >= r.count) continue;
+    const JoinUnit x = static_cast<const JoinUnit *>(a.joins)[cta];
+    const int parts = x.parts, row = blockIdx.y * kJoinRows + warp, t = row / kTile, rr = row - t * kTile;
+    const int tok = t * a.TB + rr / a.G;
+    if (parts == 0 || rr >= a.TB * a.G || tok >= x.ntok) return;
+    const float vs = c.v_scale ? __ldg(c.v_scale + x.h) : 1.f;
+    {
         float top = -INFINITY;
         for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_ml[part_slot(cta, p) * kRows + row].x);
         for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -618,7 +617,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_combine_kernel(const Atten
             for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
             total += l;
             const int here = min(32, parts - p0);
-#pragma unroll 4
+#pragma unroll 8
             for (int p = 0; p < here; ++p) {
                 const float w = __shfl_sync(0xffffffffu, f, p);
                 const float4 v = *reinterpret_cast<const float4 *>(a.part_o + (part_slot(cta, p0 + p) * kRows + row) * kD + lane * 4);
@@ -628,15 +627,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_combine_kernel(const Atten
                 acc.w += w * v.w;
             }
         }
-        const bool some = r.len - r.count + tok >= 0;
+        const bool some = x.limit + tok >= 0;
         const float inv = vs / total;
-        const int64_t out = (r.first + tok) * (a.G * c.H) + h * a.G + rr % a.G;
+        const int64_t out = (x.row + tok) * (a.G * c.H) + x.h * a.G + rr % a.G;
         *reinterpret_cast<uint2 *>(a.o + out * kD + lane * 4) =
             some ? make_uint2(float2_to_bf16x2(acc.x * inv, acc.y * inv), float2_to_bf16x2(acc.z * inv, acc.w * inv))
                  : make_uint2(0, 0);
         if (lane == 0) {
             if (a.lse) a.lse[out] = some ? (at + log2f(total)) * kLn2 : -INFINITY;
-            if (a.stats) a.stats[out] = make_float2(at, 1.f / total);
+            if (a.stats) a.stats[out] = at + log2f(total);
         }
     }
 }
@@ -714,9 +713,10 @@ size_t lay_out(const KvArgs &c, int G, bool accumulate, int ctas, char *ws, Atte
     const size_t n = (static_cast<size_t>(c.N) + 1) * 8, slots = static_cast<size_t>(ctas) * 2;
     a->attend_start = near ? nullptr : reinterpret_cast<int64_t *>(take(n));
     a->weight_start = near || !accumulate ? nullptr : reinterpret_cast<int64_t *>(take(n));
+    a->joins = take(static_cast<size_t>(ctas) * sizeof(JoinUnit));
     a->part_o = reinterpret_cast<float *>(take(slots * kRows * kD * 4));
     a->part_ml = reinterpret_cast<float2 *>(take(slots * kRows * 8));
-    a->stats = accumulate ? reinterpret_cast<float2 *>(take(static_cast<size_t>(c.T) * G * c.H * 8)) : nullptr;
+    a->stats = accumulate ? reinterpret_cast<float *>(take(static_cast<size_t>(c.T) * G * c.H * 4)) : nullptr;
     a->part_w = accumulate ? reinterpret_cast<float *>(take(slots * kTile * 4)) : nullptr;
     return at;
 }
@@ -780,7 +780,10 @@ cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_str
     }
     {
         LaunchTimer timer(kKPagedCombine, st);
-        e = launch_dependent(paged_combine_kernel, dim3(sm_count, kRows / kJoinRows), kJoinThreads, st, a, sm_count);
+        // rows that a unit can have
+        const int64_t tokens = c.cu ? c.T : c.T_row;
+        const int rows = tokens <= a.TB ? static_cast<int>(tokens) * G : kRows;
+        e = launch_dependent(paged_combine_kernel, dim3(sm_count, (rows + kJoinRows - 1) / kJoinRows), kJoinThreads, st, a);
         if (e != cudaSuccess || !accumulate) return e;
     }
     return launch_paged_weights(a, maps, sm_count, st);

@@ -89,16 +89,18 @@ struct Starts {
 
 // A CTA's range of the flattened tiles (key/value head outermost). With fewer tiles than CTAs the first
 // CTAs get one each, so that no range among those that share a unit is empty.
-__host__ __device__ inline int64_t range_begin(int64_t tiles, int64_t cta, int64_t ctas) {
+__host__ __device__ inline int64_t range_begin(int64_t tiles, int cta, int ctas) {
     if (tiles <= ctas) return cta < tiles ? cta : tiles;
-    return tiles / ctas * cta + tiles % ctas * cta / ctas;
+    if (tiles >> 32) return tiles / ctas * cta + tiles % ctas * cta / ctas;
+    const uint32_t q = static_cast<uint32_t>(tiles) / ctas, rest = static_cast<uint32_t>(tiles) - q * ctas;   // 64-bit divisions are slow
+    return static_cast<int64_t>(q) * cta + rest * cta / ctas;
 }
 // The CTA that has tile `at`.
-__host__ __device__ inline int cta_of(int64_t tiles, int64_t at, int64_t ctas) {
+__host__ __device__ inline int cta_of(int64_t tiles, int64_t at, int ctas) {
     if (tiles <= ctas) return static_cast<int>(at);
-    int64_t cta = at / (tiles / ctas + 1);   // at most the one sought
+    int cta = static_cast<int>(at / (tiles / ctas + 1));   // at most the one sought
     while (range_begin(tiles, cta + 1, ctas) <= at) ++cta;
-    return static_cast<int>(cta);
+    return cta;
 }
 
 // Threads 0 .. kInline - 1 of a CTA: running sums of the requests' tiles into `start` [N + 1], N <= kInline.
@@ -282,9 +284,10 @@ struct Maps {
 struct AttendArgs {
     KvArgs c;
     const int64_t *attend_start, *weight_start;   // [N + 1] running sums of tiles, null: each CTA takes them
+    void *joins;         // [CTAs] units that several CTAs share
     float *part_o;       // [2 * CTAs, 256, 128] partial O
     float2 *part_ml;     // [2 * CTAs, 256] its maximum (log2) and sum
-    float2 *stats;       // [T, Hq] each row's maximum (log2) and 1 / sum, or null
+    float *stats;        // [T, Hq] log2 of each row's sum of exponentials, or null
     float *part_w;       // [2 * CTAs, 128] partial sums of weights
     uint16_t *o;
     float *lse;

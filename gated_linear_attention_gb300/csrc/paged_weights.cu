@@ -1,15 +1,16 @@
 // The attention weight that each cached token received, added to its running sum.
 //
-// Runs after the attention, when every row's maximum m and sum l are known:
-//     weights[j] += sum over the rows r that see j of  2^(c k_j.q_r - m_r) / l_r
+// Runs after the attention, when every row's y = log2 sum 2^(c s) is known (c = scale * k_scale * log2 e):
+//     weights[j] += sum over the rows r that see j of  2^(c k_j.q_r - y_r)
 // The scores are made again, transposed: S^T = K Q^T (tcgen05, 128 places x 128 rows). A place is then a lane of
-// tensor memory and its sum over the rows a thread's own, without shuffles or atomics, in a fixed order; m and 1 / l
-// are the same for all lanes and come from shared memory. Each element costs one multiply-add into exp2 and
-// one into the sum.
+// tensor memory and its sum over the rows a thread's own, without shuffles or atomics, in a fixed order. y is the same
+// for all lanes: it enters as one more step of the product, columns of ones beside K and -y / c as three bf16 terms (24
+// bits) beside Q, so that an element costs a multiplication, an exp2 and an addition. (Read from shared memory
+// instead, it competed with the operands of the products: 7 query tiles on 6007 places 295 us.)
 //
 // A unit is a cache tile with the query tiles that see it; CTAs take equal shares of all of them, and units that
-// several CTAs share leave partial sums for a last kernel. Two warpgroups take the query tiles in turn, from four
-// score buffers in tensor memory. With one query tile for a request (decoding) it stays in shared memory while the
+// several CTAs share leave partial sums for a last kernel. Four groups of four warps take the score tiles in turn, from
+// four buffers in tensor memory. With one query tile for a request (decoding) it stays in shared memory while the
 // request's cache tiles pass: the kernel then reads the keys once, which bounds it.
 #include "paged_tiles.cuh"
 
@@ -20,35 +21,49 @@ using namespace pt;
 using tc::mbar_arrive;
 using tck::wait_or_abort;
 
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvertWarp = 12;
-constexpr int kBuffers = 4;                      // score tiles in tensor memory
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kStatsWarp = 18, kConvertWarp = 19;
+constexpr int kGroups = 4;                       // of four warps; score tiles in tensor memory
+constexpr uint32_t kAuxBytes = kTile * 32;       // [128 rows x 16 bf16], 32-byte swizzle
 
 template <bool E4M3>
 struct Shape {
     static constexpr int kKeys = E4M3 ? 2 : 3, kQueries = E4M3 ? 2 : 3, kRaw = E4M3 ? 5 : 0;   // tiles in shared memory
-    static constexpr int kThreads = E4M3 ? 512 : 320;
+    static constexpr int kThreads = 32 * (E4M3 ? kConvertWarp + kConvertWarps : kConvertWarp);
     static constexpr uint32_t kQueriesAt = kKeys * kTileBytes, kRawAt = kQueriesAt + kQueries * kTileBytes;
-    static constexpr uint32_t kAlloc = kRawAt + kRaw * kRawBytes + 1024;
+    static constexpr uint32_t kOnesAt = kRawAt + kRaw * kRawBytes, kAuxAt = kOnesAt + kAuxBytes;
+    static constexpr uint32_t kAlloc = kAuxAt + kQueries * kAuxBytes + 1024;
 };
+
+// What the roles of a CTA do next, from the loading warp: cache tiles [u0, u0 + nu) of request n with nq query tiles
+// from the one whose first token is packed token `row` at place `limit`, `ntok` tokens in all. nu > 1 only with nq = 1.
+struct alignas(16) Item {
+    int64_t row;
+    int n, h, len, u0, nu, nq, ntok, limit;
+    int slot;            // where a partial result goes, -1: the item is the whole unit
+    int last;
+};
+constexpr int kItems = 4;
 
 struct Barriers {
     uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], raw_full[5], raw_empty[5];
-    uint64_t s_full[kBuffers], s_free[kBuffers];
-    uint64_t part_full[2], part_free[2];
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t s_full[kGroups], s_free[kGroups];
+    uint64_t part_full[kGroups], part_free[kGroups];
     uint64_t drain;
 };
 
-// Rows of one query tile of a request: `rows` of them, the first token at place `limit`.
-struct Queries {
-    int64_t row;         // packed token
-    int rows, limit;
-    __device__ __forceinline__ Queries(const kv::Request &r, int tile, int TB, int G) {
-        const int tok = tile * TB;
-        row = r.first + tok;
-        rows = min(TB, r.count - tok) * G;
-        limit = r.len - r.count + tok;
-    }
-};
+// Byte offset of 16-byte piece `piece` (of 2) of a row in a tile of 16 columns.
+__device__ __forceinline__ uint32_t aux_at(int row, int piece) { return row * 32 + ((piece ^ ((row >> 2) & 1)) << 4); }
+
+// Descriptor of such a tile: 32-byte swizzle (layout 6), 256 bytes from 8 rows to the next.
+__device__ __forceinline__ uint64_t desc_aux(uint32_t addr) {
+    uint64_t d = (addr >> 4) & 0x3FFFu;
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>(256 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(6) << 61;
+    return d;
+}
 
 template <bool E4M3>
 __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
@@ -56,9 +71,8 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
     using Layout = Shape<E4M3>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Barriers bar;
-    __shared__ __align__(16) float2 stats[8][kTile];   // a warp's own copy of the rows' maxima and 1 / sums
-    __shared__ float parts[2][kTile];
-    __shared__ uint32_t near[kInline + 1], sums[kInline / 32];
+    __shared__ float parts[kGroups][kTile];
+    __shared__ Item ring[kItems];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ Place place;
@@ -78,27 +92,35 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             tc::mbar_init(&bar.k_empty[i], 1);
         }
         for (int i = 0; i < Layout::kQueries; ++i) {
-            tc::mbar_init(&bar.q_full[i], 1);
+            tc::mbar_init(&bar.q_full[i], 2);
             tc::mbar_init(&bar.q_empty[i], 1);
         }
         for (int i = 0; i < Layout::kRaw; ++i) {
             tc::mbar_init(&bar.raw_full[i], 1);
             tc::mbar_init(&bar.raw_empty[i], kConvertWarps);
         }
-        for (int i = 0; i < kBuffers; ++i) {
+        for (int i = 0; i < kItems; ++i) {
+            tc::mbar_init(&bar.item_full[i], 1);
+            tc::mbar_init(&bar.item_empty[i], 18 + (E4M3 ? kConvertWarps : 0));
+        }
+        for (int i = 0; i < kGroups; ++i) {
             tc::mbar_init(&bar.s_full[i], 1);
             tc::mbar_init(&bar.s_free[i], 4);
-        }
-        for (int t = 0; t < 2; ++t) {
-            tc::mbar_init(&bar.part_full[t], 4);
-            tc::mbar_init(&bar.part_free[t], 4);
+            tc::mbar_init(&bar.part_full[i], 4);
+            tc::mbar_init(&bar.part_free[i], 4);
         }
         tc::mbar_init(&bar.drain, 1);
         tc::fence_barrier_init();
         abort_flag = 0;
     }
+    if (threadIdx.x < kTile) {   // the columns beside K: three ones, then zeros
+        *reinterpret_cast<uint4 *>(smem + Layout::kOnesAt + aux_at(threadIdx.x, 0)) = make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
+        *reinterpret_cast<uint4 *>(smem + Layout::kOnesAt + aux_at(threadIdx.x, 1)) = make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async_smem();
+    }
     dependent_start();
-    if (!a.weight_start) scan_requests(c, work, near, sums);
+    uint32_t *const near = reinterpret_cast<uint32_t *>(smem);   // where the tiles land later
+    if (!a.weight_start) scan_requests(c, work, near, near + kInline + 1);
     const Starts starts{a.weight_start ? nullptr : near, a.weight_start};
     const int64_t per_head = starts[c.N], all = per_head * c.H;
     const int64_t begin = range_begin(all, cta, gridDim.x), stop = range_begin(all, cta + 1, gridDim.x);
@@ -110,113 +132,182 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
     const uint32_t tmem = tmem_slot;
     volatile int *const aborted = &abort_flag;
     int *const status = c.status;
-    Walk<WeightWork> w;
-    if (!idle) w.start_at(c, work, place, begin, stop, cta);
+    // the items from the ring, for every role but the loading warp
+    uint32_t items = 0;
+    auto take = [&](Item &x) {
+        if (!wait_or_abort(&bar.item_full[items % kItems], (items / kItems) & 1, aborted, status)) return false;
+        x = ring[items % kItems];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
+        ++items;
+        return true;
+    };
 
     if (warp == kLoadWarp && !idle) {
-        // ---- loads: a cache tile of keys for each unit, query tiles ------------------------------------
+        // ---- loads: a cache tile of keys after another, query tiles ------------------------------------
         constexpr int kRing = E4M3 ? Layout::kRaw : Layout::kKeys;
         uint64_t *const full = E4M3 ? bar.raw_full : bar.k_full, *const empty = E4M3 ? bar.raw_empty : bar.k_empty;
         uint32_t kt = 0, qt = 0;
-        int64_t held_n = -1;   // the request (and head) whose only query tile is in shared memory
-        int held_h = -1;
-        int page = box_page<E4M3>(c, w.n, w.u, w.r.len, lane);
         bool ok = true;
+        Walk<WeightWork> w;
+        w.start_at(c, work, place, begin, stop, cta);
+        tc::fence_proxy_async_smem();   // the running sums were there before the tiles
         do {
-            const int st = kt % kRing;
-            ok = kt < kRing || wait_or_abort(&empty[st], (kt / kRing - 1) & 1, aborted, status);
-            if (!ok) break;
-            load_boxes<E4M3>(c, &maps.k, smem + (E4M3 ? Layout::kRawAt + st * kRawBytes : st * kTileBytes), w.u, w.h, page, lane,
-                             &full[st]);
-            ++kt;
             const bool single = work.query_tiles(w.r.count) == 1;
-            if (!(single && held_n == w.n && held_h == w.h)) {
-                const int q0 = work.first(w.r.count, w.r.len, w.u);
-                for (int i = w.t0; i < w.t1; ++i, ++qt) {
+            const int q0 = work.first(w.r.count, w.r.len, w.u) + w.t0, slot = items % kItems;
+            Item x;
+            x.row = w.r.first + q0 * a.TB;
+            x.n = static_cast<int>(w.n);
+            x.h = w.h;
+            x.len = w.r.len;
+            x.u0 = w.u;
+            x.nu = single ? static_cast<int>(min(static_cast<int64_t>(w.units - w.u), stop - w.pos)) : 1;
+            x.nq = w.t1 - w.t0;
+            x.ntok = w.r.count - q0 * a.TB;
+            x.limit = w.r.len - w.r.count + q0 * a.TB;
+            x.slot = w.slot;
+            w.u += x.nu - 1;
+            w.pos += x.nu - 1;
+            x.last = w.pos + (w.t1 - w.t0) >= stop;
+            ok = items < kItems || wait_or_abort(&bar.item_empty[slot], (items / kItems - 1) & 1, aborted, status);
+            if (!ok) break;
+            if (lane == 0) {
+                ring[slot] = x;
+                mbar_arrive(&bar.item_full[slot]);
+            }
+            __syncwarp();
+            ++items;
+            int page = box_page<E4M3>(c, x.n, x.u0, x.len, lane);   // of the next tile: looked up ahead
+            for (int i = 0; i < x.nu && ok; ++i, ++kt) {
+                const int here = page, st = kt % kRing;
+                page = i + 1 < x.nu ? box_page<E4M3>(c, x.n, x.u0 + i + 1, x.len, lane) : -2;
+                ok = kt < kRing || wait_or_abort(&empty[st], (kt / kRing - 1) & 1, aborted, status);
+                if (!ok) break;
+                load_boxes<E4M3>(c, &maps.k, smem + (E4M3 ? Layout::kRawAt + st * kRawBytes : st * kTileBytes), x.u0 + i, x.h, here,
+                                 lane, &full[st]);
+                for (int q = 0; i == 0 && q < x.nq; ++q, ++qt) {
                     const int s = qt % Layout::kQueries;
                     ok = qt < Layout::kQueries || wait_or_abort(&bar.q_empty[s], (qt / Layout::kQueries - 1) & 1, aborted, status);
                     if (!ok) break;
                     if (lane == 0) {
-                        const Queries x(w.r, q0 + i, a.TB, a.G);
                         tc::mbar_arrive_expect_tx(&bar.q_full[s], 2 * static_cast<uint32_t>(a.TB * a.G) * 128u);
-                        load_query_tile(smem + Layout::kQueriesAt + s * kTileBytes, &maps.q, w.h, a.G, x.row, &bar.q_full[s]);
+                        load_query_tile(smem + Layout::kQueriesAt + s * kTileBytes, &maps.q, x.h, a.G, x.row + q * a.TB, &bar.q_full[s]);
                     }
                     __syncwarp();
                 }
-                held_n = single ? w.n : -1;
-                held_h = w.h;
             }
-            if (!ok || !w.next(c, work, cta)) break;
-            page = box_page<E4M3>(c, w.n, w.u, w.r.len, lane);
-        } while (true);
+        } while (ok && w.next(c, work, cta));
         if (!ok) {   // copies in flight land before the CTA ends
             for (uint32_t j = kt > kRing ? kt - kRing : 0; j < kt; ++j)
                 tc::mbar_wait(&full[j % kRing], (j / kRing) & 1, tck::kWaitNs);
             for (uint32_t j = qt > Layout::kQueries ? qt - Layout::kQueries : 0; j < qt; ++j)
                 tc::mbar_wait(&bar.q_full[j % Layout::kQueries], (j / Layout::kQueries) & 1, tck::kWaitNs);
         }
+    } else if (warp == kStatsWarp && !idle) {
+        // ---- the columns beside Q: -y / c of each row ------------------------------------------------------
+        uint32_t qt = 0;
+        const int Hq = a.G * c.H;
+        Item x;
+        bool ok = true;
+        do {
+            ok = take(x);
+            if (!ok) break;
+            const float inv = -1.f / (a.scale * (c.k_scale ? __ldg(c.k_scale + x.h) : 1.f) * kLog2e);
+            float next[4];
+            auto fetch = [&](int q) {   // rows 32 e + lane of query tile q
+                const int rows = min(a.TB, x.ntok - q * a.TB) * a.G;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 32 * e + lane, tok = row / a.G;
+                    next[e] = row < rows ? a.stats[(x.row + q * a.TB + tok) * Hq + x.h * a.G + row - tok * a.G] : 0.f;
+                }
+            };
+            fetch(0);
+            for (int q = 0; q < x.nq; ++q, ++qt) {
+                const int s = qt % Layout::kQueries;
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = next[e];
+                if (q + 1 < x.nq) fetch(q + 1);
+                ok = qt < Layout::kQueries || wait_or_abort(&bar.q_empty[s], (qt / Layout::kQueries - 1) & 1, aborted, status);
+                if (!ok) break;
+                uint8_t *aux = smem + Layout::kAuxAt + s * kAuxBytes;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = y[e] * inv;
+                    const float hi = __bfloat162float(__float2bfloat16_rn(v));
+                    const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
+                    *reinterpret_cast<uint4 *>(aux + aux_at(32 * e + lane, 0)) =
+                        make_uint4(float2_to_bf16x2(hi, mid), float2_to_bf16x2((v - hi) - mid, 0.f), 0, 0);
+                    *reinterpret_cast<uint4 *>(aux + aux_at(32 * e + lane, 1)) = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.q_full[s]);
+            }
+        } while (ok && !x.last);
     } else if (E4M3 && warp >= kConvertWarp && !idle) {
         // ---- e4m3 keys to bf16 ---------------------------------------------------------------------------
         constexpr int kRaw = E4M3 ? Layout::kRaw : 1;
         uint32_t it = 0;
+        Item x;
+        bool ok = true;
         do {
-            const int st = it % Layout::kKeys, rw = it % kRaw;
-            if (!wait_or_abort(&bar.raw_full[rw], (it / kRaw) & 1, aborted, status)) break;
-            if (it >= Layout::kKeys && !wait_or_abort(&bar.k_empty[st], (it / Layout::kKeys - 1) & 1, aborted, status)) break;
-            convert_tile(smem + Layout::kRawAt + rw * kRawBytes, smem + st * kTileBytes, threadIdx.x - 32 * kConvertWarp);
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar.k_full[st]);
-                mbar_arrive(&bar.raw_empty[rw]);
+            ok = take(x);
+            for (int i = 0; ok && i < x.nu; ++i, ++it) {
+                const int st = it % Layout::kKeys, rw = it % kRaw;
+                ok = wait_or_abort(&bar.raw_full[rw], (it / kRaw) & 1, aborted, status) &&
+                     (it < Layout::kKeys || wait_or_abort(&bar.k_empty[st], (it / Layout::kKeys - 1) & 1, aborted, status));
+                if (!ok) break;
+                convert_tile(smem + Layout::kRawAt + rw * kRawBytes, smem + st * kTileBytes, threadIdx.x - 32 * kConvertWarp);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar.k_full[st]);
+                    mbar_arrive(&bar.raw_empty[rw]);
+                }
             }
-            ++it;
-        } while (w.next(c, work, cta));
+        } while (ok && !x.last);
     } else if (warp == kMmaWarp && !idle) {
         // ---- products ------------------------------------------------------------------------------------
         const bool leader = tc::elect_one();
         uint32_t kt = 0, qt = 0, tile = 0;
-        int64_t held_n = -1;
-        int held_h = -1, held_slot = 0;
         bool ok = true;
+        Item x;
         do {
-            const int ks = kt % Layout::kKeys;
-            const bool single = work.query_tiles(w.r.count) == 1;
-            const bool fresh = !(single && held_n == w.n && held_h == w.h);
-            if (fresh && held_n >= 0 && leader) tc::umma_commit(&bar.q_empty[held_slot]);
-            ok = wait_or_abort(&bar.k_full[ks], (kt / Layout::kKeys) & 1, aborted, status);
-            const int q0 = work.first(w.r.count, w.r.len, w.u);
-            for (int i = w.t0; i < w.t1 && ok; ++i, ++tile) {
-                const Queries x(w.r, q0 + i, a.TB, a.G);
-                const int slot = fresh ? qt % Layout::kQueries : held_slot, b = tile % kBuffers;
-                if (fresh) {
-                    ok = wait_or_abort(&bar.q_full[slot], (qt / Layout::kQueries) & 1, aborted, status);
-                    ++qt;
-                }
-                ok = ok && (tile < kBuffers || wait_or_abort(&bar.s_free[b], (tile / kBuffers - 1) & 1, aborted, status));
-                if (!ok) break;
-                tc::tc_fence_after();
-                if (leader) {
-                    const uint32_t id = tc::idesc_bf16_f32(128, (x.rows + 15) & ~15, 0, 0);
-                    const uint64_t dk = desc_k(base + ks * kTileBytes), dq = desc_k(base + Layout::kQueriesAt + slot * kTileBytes);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
-                        tc::umma_bf16(tmem + b * kTile, dk + off, dq + off, id, s > 0);
-                    }
-                    tc::umma_commit(&bar.s_full[b]);
-                    if (!single) tc::umma_commit(&bar.q_empty[slot]);
-                }
-                __syncwarp();
-                held_slot = slot;
-            }
+            ok = take(x);
             if (!ok) break;
-            held_n = single ? w.n : -1;
-            held_h = w.h;
-            if (leader) tc::umma_commit(&bar.k_empty[ks]);
-            __syncwarp();
-            ++kt;
-        } while (w.next(c, work, cta));
+            for (int i = 0; i < x.nu && ok; ++i, ++kt) {
+                const int ks = kt % Layout::kKeys;
+                ok = wait_or_abort(&bar.k_full[ks], (kt / Layout::kKeys) & 1, aborted, status);
+                for (int q = 0; q < x.nq && ok; ++q, ++tile) {
+                    const uint32_t j = qt + q;
+                    const int s = j % Layout::kQueries, b = tile % kGroups, rows = min(a.TB, x.ntok - q * a.TB) * a.G;
+                    if (i == 0) ok = wait_or_abort(&bar.q_full[s], (j / Layout::kQueries) & 1, aborted, status);
+                    ok = ok && (tile < kGroups || wait_or_abort(&bar.s_free[b], (tile / kGroups - 1) & 1, aborted, status));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    if (leader) {
+                        const uint32_t id = tc::idesc_bf16_f32(128, (rows + 15) & ~15, 0, 0);
+                        const uint64_t dk = desc_k(base + ks * kTileBytes), dq = desc_k(base + Layout::kQueriesAt + s * kTileBytes);
+                        tc::umma_bf16(tmem + b * kTile, desc_aux(base + Layout::kOnesAt), desc_aux(base + Layout::kAuxAt + s * kAuxBytes),
+                                      id, 0u);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                            tc::umma_bf16(tmem + b * kTile, dk + off, dq + off, id, 1u);
+                        }
+                        tc::umma_commit(&bar.s_full[b]);
+                        if (i + 1 == x.nu) tc::umma_commit(&bar.q_empty[s]);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (leader) tc::umma_commit(&bar.k_empty[ks]);
+                __syncwarp();
+            }
+            qt += x.nq;
+        } while (ok && !x.last);
         if (!ok) {   // products in flight end before the tensor memory is freed
             if (leader) {
                 tc::umma_commit(&bar.drain);
@@ -226,100 +317,97 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         }
     } else if (warp < kMmaWarp && !idle) {
         // ---- sums: a place a thread ------------------------------------------------------------------------
-        const int g = warp >> 2, r = threadIdx.x & (kTile - 1), Hq = a.G * c.H;
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        float2 *const mine = stats[warp];
-        uint32_t tile = 0, sent = 0, got = 0;
+        const int g = warp >> 2, r = threadIdx.x & (kTile - 1);
+        const uint32_t ts = tmem + g * kTile + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        uint32_t tile = 0, done = 0;             // score tiles of the CTA, of this group
+        uint32_t sent = 0, flips = 0;             // partial sums handed over; parity of every group's, a bit each
         bool ok = true;
+        Item x;
         do {
-            const int m = w.t1 - w.t0, q0 = work.first(w.r.count, w.r.len, w.u) + w.t0, p = w.u * kTile + r;
-            const int owner = tile & 1;
-            const float scale = a.scale * (c.k_scale ? __ldg(c.k_scale + w.h) : 1.f) * kLog2e;
-            float2 next[4];
-            auto fetch = [&](int i) {   // the statistics of the rows 32 e + lane of query tile i of the item
-                const Queries x(w.r, q0 + i, a.TB, a.G);
+            ok = take(x);
+            if (!ok) break;
+            const float scale = a.scale * (c.k_scale ? __ldg(c.k_scale + x.h) : 1.f) * kLog2e;
+            const uint64_t scale2 = tc::pair(scale, scale);
+            const int m = x.nq;
+            for (int i = 0; i < x.nu && ok; ++i, tile += m) {
+                const int p = (x.u0 + i) * kTile + r, owner = tile % kGroups;
+                const int mine = (g - owner) & (kGroups - 1);   // this group's first query tile of the unit
+                const uint32_t before = flips;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 32 * e + lane, tok = row / a.G;
-                    next[e] = row < x.rows ? a.stats[(x.row + tok) * Hq + w.h * a.G + row - tok * a.G] : make_float2(0.f, 0.f);
-                }
-            };
-            float total = 0.f;
-            int i = (tile & 1) == g ? 0 : 1;
-            if (i < m) fetch(i);
-            for (; i < m; i += 2) {
-                const uint32_t k = tile + i, b = k % kBuffers;
-                const Queries x(w.r, q0 + i, a.TB, a.G);
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mine[32 * e + lane] = next[e];
-                __syncwarp();
-                if (i + 2 < m) fetch(i + 2);
-                ok = wait_or_abort(&bar.s_full[b], (k / kBuffers) & 1, aborted, status);
-                if (!ok) break;
-                tc::tc_fence_after();
-                const bool full = x.rows == kTile && x.limit >= w.u * kTile + kTile - 1;
-                const int ahead = p - x.limit, from = ahead <= 0 ? 0 : ahead >= a.TB ? kTile : ahead * a.G;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (32 * q >= x.rows) break;
-                    uint32_t s[32];
-                    tc::tmem_ld_32x32b_x32(tmem + b * kTile + 32 * q + lanes, s);
-                    tc::tmem_ld_wait();
-                    const float4 *st = reinterpret_cast<const float4 *>(mine + 32 * q);
-                    if (full) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float4 y = st[j];
-                            const float e0 = tc::ex2(fmaf(__uint_as_float(s[2 * j]), scale, -y.x));
-                            const float e1 = tc::ex2(fmaf(__uint_as_float(s[2 * j + 1]), scale, -y.z));
-                            sum[(2 * j) & 3] = fmaf(e0, y.y, sum[(2 * j) & 3]);
-                            sum[(2 * j + 1) & 3] = fmaf(e1, y.w, sum[(2 * j + 1) & 3]);
-                        }
-                    } else {   // rows that see the place: not before `from`, not behind the last
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float4 y = st[j];
-                            const int n = 32 * q + 2 * j;
-                            const float e0 = tc::ex2(fmaf(__uint_as_float(s[2 * j]), scale, -y.x)) * y.y;
-                            const float e1 = tc::ex2(fmaf(__uint_as_float(s[2 * j + 1]), scale, -y.z)) * y.w;
-                            sum[(2 * j) & 3] += n >= from && n < x.rows ? e0 : 0.f;
-                            sum[(2 * j + 1) & 3] += n + 1 >= from && n + 1 < x.rows ? e1 : 0.f;
-                        }
+                for (int o = 1; o < kGroups; ++o)
+                    if (o < m) flips ^= 1u << ((owner + o) & (kGroups - 1));
+                if (mine >= m) continue;
+                float *weight = nullptr;
+                float old = 0.f;
+                if (mine == 0 && x.slot < 0 && p < x.len) {     // looked up while the scores are made
+                    const int page = kv::page_of(c, x.n, p);
+                    if (page >= 0) {
+                        weight = c.weights + kv::row_of(c, page, x.h, p);
+                        old = *weight;
                     }
                 }
-                total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.s_free[b]);
-            }
-            if (!ok) break;
-            if (m > 1 && g != owner) {   // to the warpgroup that has the unit's first query tile
-                ok = sent == 0 || wait_or_abort(&bar.part_free[g], (sent - 1) & 1, aborted, status);
-                if (!ok) break;
-                parts[g][r] = total;
-                ++sent;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.part_full[g]);
-            } else if (m > 1) {
-                ok = wait_or_abort(&bar.part_full[1 - g], got & 1, aborted, status);
-                if (!ok) break;
-                total += parts[1 - g][r];
-                ++got;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.part_free[1 - g]);
-            }
-            if (g == owner) {
-                if (w.slot >= 0) {
-                    a.part_w[static_cast<int64_t>(w.slot) * kTile + r] = total;
-                } else if (p < w.r.len) {
-                    const int page = kv::page_of(c, w.n, p);
-                    if (page >= 0) c.weights[kv::row_of(c, page, w.h, p)] += total;
+                float total = 0.f;
+                for (int q = mine; q < m; q += kGroups, ++done) {
+                    ok = wait_or_abort(&bar.s_full[g], done & 1, aborted, status);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const int rows = min(a.TB, x.ntok - q * a.TB) * a.G;
+                    // rows that see the place: from `from` on
+                    const int ahead = p - x.limit - q * a.TB, from = ahead <= 0 ? 0 : ahead >= a.TB ? kTile : ahead * a.G;
+                    const bool seen = x.limit + q * a.TB >= (x.u0 + i) * kTile + kTile - 1;   // by all rows, every place
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint64_t sum2[2] = {0, 0};   // pairs of zeros
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (32 * e >= rows) break;
+                        uint32_t s[32];
+                        tc::tmem_ld_32x32b_x32(ts + 32 * e, s);
+                        tc::tmem_ld_wait();
+                        if (seen && 32 * e + 32 <= rows) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                const float2 y = tc::unpair(tc::mul2(tc::pair(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), scale2));
+                                sum2[(j >> 1) & 1] = tc::add2(sum2[(j >> 1) & 1], tc::pair(tc::ex2(y.x), tc::ex2(y.y)));
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float y = tc::ex2(__uint_as_float(s[j]) * scale);
+                                sum[j & 3] += 32 * e + j >= from && 32 * e + j < rows ? y : 0.f;
+                            }
+                        }
+                    }
+                    const float2 even = tc::unpair(sum2[0]), odd = tc::unpair(sum2[1]);
+                    total += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((even.x + even.y) + (odd.x + odd.y));
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.s_free[g]);
                 }
+                if (!ok) break;
+                if (mine > 0) {   // to the group that has the unit's first query tile
+                    ok = sent == 0 || wait_or_abort(&bar.part_free[g], (sent - 1) & 1, aborted, status);
+                    if (!ok) break;
+                    parts[g][r] = total;
+                    ++sent;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.part_full[g]);
+                    continue;
+                }
+#pragma unroll
+                for (int o = 1; o < kGroups; ++o) {
+                    if (o >= m) break;
+                    const int from = (g + o) & (kGroups - 1);
+                    ok = wait_or_abort(&bar.part_full[from], (before >> from) & 1, aborted, status);
+                    if (!ok) break;
+                    total += parts[from][r];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.part_free[from]);
+                }
+                if (!ok) break;
+                if (x.slot >= 0) a.part_w[static_cast<int64_t>(x.slot) * kTile + r] = total;
+                else if (weight) *weight = old + total;
             }
-            tile += m;
-        } while (w.next(c, work, cta));
+        } while (ok && !x.last);
     }
     __syncwarp();
     tc::tc_fence_before();

@@ -64,33 +64,6 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Two floats in one 64-bit register; sums, products and multiply-adds of pairs.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t p) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 template <typename T>
 __device__ __forceinline__ float logit(const T *p) {
     if constexpr (sizeof(T) == 4) return clean(__ldg(p));
@@ -188,8 +161,8 @@ __device__ __forceinline__ void add_vectors(Sums &s, const Vec<T> (&x)[kAhead]) 
             for (int e = 0; e < kN; ++e) s.add(clean(x[u].at(e)));
         return;
     }
-    const uint64_t minus_m = pair(-s.m, -s.m), log2e = pair(kLog2e, kLog2e);
-    uint64_t l = pair(s.l, 0.f), w = pair(s.w, 0.f);
+    const uint64_t minus_m = tc::pair(-s.m, -s.m), log2e = tc::pair(kLog2e, kLog2e);
+    uint64_t l = tc::pair(s.l, 0.f), w = tc::pair(s.w, 0.f);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
         const uint32_t r[4] = {x[u].r.x, x[u].r.y, x[u].r.z, x[u].r.w};
@@ -198,19 +171,19 @@ __device__ __forceinline__ void add_vectors(Sums &s, const Vec<T> (&x)[kAhead]) 
             uint64_t y;
             if constexpr (kN == 8) {
                 const float2 f = bf16x2_to_float2(max_bf16x2(r[e / 2], kLowBf16x2));
-                y = pair(f.x, f.y);
+                y = tc::pair(f.x, f.y);
             } else {
-                y = pair(fmaxf(__uint_as_float(r[e]), kLow), fmaxf(__uint_as_float(r[e + 1]), kLow));
+                y = tc::pair(fmaxf(__uint_as_float(r[e]), kLow), fmaxf(__uint_as_float(r[e + 1]), kLow));
             }
-            const uint64_t d = add2(y, minus_m);
-            const float2 p = unpair(mul2(d, log2e));
-            const uint64_t ex = pair(tc::ex2(p.x), tc::ex2(p.y));
-            l = add2(l, ex);
-            w = fma2(ex, d, w);
+            const uint64_t d = tc::add2(y, minus_m);
+            const float2 p = tc::unpair(tc::mul2(d, log2e));
+            const uint64_t ex = tc::pair(tc::ex2(p.x), tc::ex2(p.y));
+            l = tc::add2(l, ex);
+            w = tc::fma2(ex, d, w);
         }
     }
-    s.l = unpair(l).x + unpair(l).y;
-    s.w = unpair(w).x + unpair(w).y;
+    s.l = tc::unpair(l).x + tc::unpair(l).y;
+    s.w = tc::unpair(w).x + tc::unpair(w).y;
 }
 
 template <typename T>

@@ -447,7 +447,7 @@ int sala_gla_state_pool_compact(void *pool, int32_t dtype, int64_t L, int64_t P,
  *   k_pages, v_pages  [num_pages, num_kv_heads, page_size, 128] of dtype. SALA_KV_BF16: bf16.
  *                     SALA_KV_E4M3: 8-bit floats (4 exponent, 3 mantissa bits); the value that a
  *                     byte stands for is the 8-bit float times its head's scale.
- *   k_scale, v_scale  fp32 [num_kv_heads], positive and finite; with SALA_KV_E4M3 only (NULL: 1)
+ *   k_scale, v_scale  fp32 [num_kv_heads], from 1e-12 to 1e12; with SALA_KV_E4M3 only (NULL: 1)
  *   weights           fp32 [num_pages, num_kv_heads, page_size] or NULL: the running sum of the attention
  *                     weight that each cached token received, for sala_gla_kv_evict
  *   block_table       int32 [N, table_width]: place i of request n lies in page
@@ -506,7 +506,7 @@ int sala_gla_kv_append(const sala_kv_cache *cache, const void *k, int64_t k_stri
  *
  *   q           bf16 [tokens, Hq, 128], tokens q_stride elements apart (at least Hq * 128, a multiple of 8)
  *   cu_seqlens  as for sala_gla_kv_append
- *   scale       > 0 and finite, typically 128^-0.5
+ *   scale       from 1e-18 to 1e18, typically 128^-0.5
  *   o           bf16 [tokens, Hq, 128] output. Rows behind the last request are left as they were.
  *   lse         fp32 [tokens, Hq] output (natural logarithm) or NULL
  *   accumulate  nonzero: adds p_j, summed over the call's new tokens and the query heads of the group, to
