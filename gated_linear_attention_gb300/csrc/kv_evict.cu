@@ -7,9 +7,9 @@
 // the places that stay, ascending, to `kept`.
 //
 // The second moves rows: place kept[i] -> i. kept[i] >= i and ascending, so a CTA that walks the places in
-// blocks may write block b once every thread has read it: the sources of later blocks lie at or
-// behind their own destinations, past everything written so far. Blocks depend on each other only within a
-// (request, head, array, slice of the row), so keys, values, weights and slices of a row are CTAs of their own.
+// blocks may write block b once every thread has read it: the sources of later blocks lie at or behind their own
+// destinations, past everything written so far. Blocks depend on each other only within a (request, head, array,
+// slice of the row), so keys, values, weights and slices of a row are CTAs of their own.
 #include "kv_cache.cuh"
 
 namespace sala {
@@ -125,54 +125,73 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const KvArgs c, 
     }
 }
 
-constexpr int kMoveThreads = 256, kUnroll = 4;
+constexpr int kMoveThreads = 256, kEach = 4;
 
-// One array of one (request, head), cut into `slices` parts of its rows: VEC bytes a thread.
-template <typename V>
+// Rows kept[i] -> i of one array of one (request, head), `bytes` of a row from `offset` on: 16 bytes a thread and row.
 __device__ __forceinline__ void move_rows(const KvArgs &c, int64_t n, int h, const int32_t *kept, int first, int count,
-                                          uint8_t *base, int row_bytes, int slice, int slices) {
-    const int per_row = row_bytes / slices / static_cast<int>(sizeof(V));   // vectors of a row here
-    const int tokens = kMoveThreads * kUnroll / per_row;
-    const int sub = threadIdx.x % per_row, row0 = threadIdx.x / per_row, rows = kMoveThreads / per_row;
-    const int offset = slice * (row_bytes / slices) + sub * static_cast<int>(sizeof(V));
-    V held[kUnroll], next[kUnroll];
-    auto load = [&](int b, V (&x)[kUnroll]) {
+                                          uint8_t *base, int row_bytes, int offset, int bytes) {
+    const int per_row = bytes / 16, rows = kMoveThreads / per_row;   // threads of a row, rows at once
+    const int row0 = threadIdx.x / per_row;
+    base += offset + threadIdx.x % per_row * 16;
+    for (int b = first; b < count; b += rows * kEach) {
+        uint4 x[kEach];
+        uint8_t *to[kEach];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int i = b + row0 + u * rows;
-            const int src = i < count ? __ldg(kept + i) : -1;
-            const int page = src >= 0 && src != i ? kv::page_of(c, n, src) : -1;
-            if (page >= 0) x[u] = *reinterpret_cast<const V *>(base + kv::row_of(c, page, h, src) * row_bytes + offset);
+        for (int e = 0; e < kEach; ++e) {
+            const int i = b + row0 + e * rows, src = i < count ? __ldg(kept + i) : -1;
+            to[e] = nullptr;
+            if (src >= 0 && src != i) {
+                const int p = kv::page_of(c, n, src), q = kv::page_of(c, n, i);
+                if (p >= 0 && q >= 0) {
+                    x[e] = *reinterpret_cast<const uint4 *>(base + kv::row_of(c, p, h, src) * row_bytes);
+                    to[e] = base + kv::row_of(c, q, h, i) * row_bytes;
+                }
+            }
         }
-    };
-    load(first, held);
-    for (int b = first; b < count; b += tokens) {
-        if (b + tokens < count) load(b + tokens, next);
         __syncthreads();   // every source of this block is read
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int i = b + row0 + u * rows;
-            const int src = i < count ? __ldg(kept + i) : -1;
-            const int page = src >= 0 && src != i ? kv::page_of(c, n, i) : -1;
-            if (page >= 0 && kv::page_of(c, n, src) >= 0)
-                *reinterpret_cast<V *>(base + kv::row_of(c, page, h, i) * row_bytes + offset) = held[u];
-            held[u] = next[u];
-        }
+        for (int e = 0; e < kEach; ++e)
+            if (to[e]) *reinterpret_cast<uint4 *>(to[e]) = x[e];
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const KvArgs c, const EvictArgs a, int slices) {
+// The weights of one (request, head), a thread a place.
+__device__ __forceinline__ void move_weights(const KvArgs &c, int64_t n, int h, const int32_t *kept, int first, int count) {
+    for (int b = first; b < count; b += kMoveThreads * kEach) {
+        float x[kEach];
+        float *to[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int i = b + e * kMoveThreads + static_cast<int>(threadIdx.x), src = i < count ? __ldg(kept + i) : -1;
+            to[e] = nullptr;
+            if (src >= 0 && src != i) {
+                const int p = kv::page_of(c, n, src), q = kv::page_of(c, n, i);
+                if (p >= 0 && q >= 0) {
+                    x[e] = c.weights[kv::row_of(c, p, h, src)];
+                    to[e] = c.weights + kv::row_of(c, q, h, i);
+                }
+            }
+        }
+        __syncthreads();   // every source of this block is read
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            if (to[e]) *to[e] = x[e];
+    }
+}
+
+__global__ void __launch_bounds__(kMoveThreads, 6) kv_move_kernel(const KvArgs c, const EvictArgs a, int slices) {
     dependent_start();
     const int64_t n = blockIdx.x / c.H;
     const int h = static_cast<int>(blockIdx.x - n * c.H), part = blockIdx.y;
     const int len = kv::request_len(c, n);
     if (len <= a.budget) return;
     const int32_t *kept = a.kept + static_cast<int64_t>(blockIdx.x) * a.budget;
-    if (part == 2 * slices)
-        move_rows<float>(c, n, h, kept, a.sinks, a.budget, reinterpret_cast<uint8_t *>(c.weights), 4, 0, 1);
-    else
-        move_rows<uint4>(c, n, h, kept, a.sinks, a.budget, part < slices ? c.k : c.v, c.e4m3 ? kD : 2 * kD,
-                         part % slices, slices);
+    if (part == 2 * slices) {
+        move_weights(c, n, h, kept, a.sinks, a.budget);
+        return;
+    }
+    const int row = c.e4m3 ? kD : 2 * kD, bytes = row / slices;
+    move_rows(c, n, h, kept, a.sinks, a.budget, part < slices ? c.k : c.v, row, part % slices * bytes, bytes);
 }
 
 }  // namespace
