@@ -52,6 +52,15 @@ __device__ __forceinline__ void dependent_start() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// The two halves by themselves. A kernel whose first kernel-wide wait is over before it lets its dependents start gives them
+// all of what lay before it on the stream; they wait only for what the kernel itself writes.
+__device__ __forceinline__ void let_dependents_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Launch as a programmatic dependent of the work before it on the stream: only the launch
 // latency overlaps the previous grid's last wave (the kernel begins with dependent_start).
 // `cluster`: CTAs per cluster along x (0: no clusters); `smem`: dynamic shared memory.

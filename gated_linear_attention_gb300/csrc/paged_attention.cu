@@ -33,18 +33,18 @@ using namespace pt;
 using tc::mbar_arrive;
 using tck::wait_or_abort;
 
-constexpr int kRows = 2 * kTile;                 // rows of a unit
+constexpr int kRows = 2 * kTile;                 // rows of a unit, at most
 constexpr int kMmaWarp = 16, kLoadWarp = 17, kConvertWarp = 18;
-constexpr int kQ = 2;                            // query tiles, in front of the cache tiles
 constexpr uint32_t kS0 = 0, kO0 = 256;           // tensor memory columns: S (and P over it) of the groups, then O
 constexpr float kRescale = 8.f;                  // growth of the maximum (log2) that rescales O
 constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128, 0, 0), kIdO = tc::idesc_bf16_f32(128, 128, 0, 1);
 
-template <bool E4M3>
+// Shared memory of units with Q query tiles: the queries, the ring of cache tiles, the ring of e4m3 tiles.
+template <bool E4M3, int Q>
 struct Shape {
-    static constexpr int kStages = E4M3 ? 3 : 5, kRaw = E4M3 ? 4 : 0;
+    static constexpr int kStages = E4M3 ? 3 : 7 - Q, kRaw = E4M3 ? 8 - 2 * Q : 0;
     static constexpr int kThreads = 32 * (E4M3 ? kConvertWarp + kConvertWarps : kConvertWarp);
-    static constexpr uint32_t kRawAt = (kQ + kStages) * kTileBytes;
+    static constexpr uint32_t kRawAt = (Q + kStages) * kTileBytes;
     static constexpr uint32_t kAlloc = kRawAt + kRaw * kRawBytes + 1024;   // aligned to the swizzle's 1024 bytes
 };
 
@@ -67,8 +67,8 @@ struct alignas(16) JoinUnit {
 };
 
 struct Barriers {
-    uint64_t full[5], empty[5];                 // cache tiles
-    uint64_t raw_full[4], raw_empty[4];         // e4m3 cache tiles
+    uint64_t full[6], empty[6];                 // cache tiles
+    uint64_t raw_full[6], raw_empty[6];         // e4m3 cache tiles
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t q_full, q_free;
     uint64_t s_full[2], p_full[2], o_full[2], o_free[2], join;
@@ -112,10 +112,10 @@ __device__ __forceinline__ void tmem_st_16x32bx2_x16(uint32_t taddr, const uint3
         : "memory");
 }
 
-template <bool E4M3>
-__global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
+template <bool E4M3, int kQ>
+__global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ Maps maps) {
-    using Layout = Shape<E4M3>;
+    using Layout = Shape<E4M3, kQ>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Barriers bar;
     __shared__ uint32_t tmem_slot;
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
     uint8_t *const smem = smem_raw + (base - tc::smem_u32(smem_raw));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
     const KvArgs &c = a.c;
-    const AttendWork work{2 * a.TB};
+    const AttendWork work{kQ * a.TB};
 
     if (warp == kMmaWarp) {
         tc::tmem_alloc(&tmem_slot, 512);
@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         tc::fence_barrier_init();
         abort_flag = 0;
     }
-    dependent_start();
+    wait_for_previous();
+    let_dependents_start();   // which so have the lengths, offsets and pages as this kernel has them
     uint32_t *const near = reinterpret_cast<uint32_t *>(smem);   // where the tiles land later
     if (!a.attend_start) scan_requests(c, work, near, near + kInline + 1);
     const Starts starts{a.attend_start ? nullptr : near, a.attend_start};
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 mbar_arrive(&bar.item_full[slot]);
             }
             __syncwarp();
-            const int end = x.end(), nt = x.ntok > a.TB ? 2 : 1;
+            const int end = x.end(), nt = kQ == 2 && x.ntok > a.TB ? 2 : 1;
             int page = box_page<E4M3>(c, w.n, w.t0, end, lane);   // of the next tile: looked up ahead
             for (int i = w.t0; i < w.t1 && ok; ++i) {
                 const int here = page;
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             if (!ok) break;
             const Item &x = ring[items % kItems];
             const int t0 = x.t0, n = x.t1 - t0;
-            const bool two = x.ntok > a.TB;
+            const bool two = kQ == 2 && x.ntok > a.TB;
             bool bad = false;
             ok = wait_or_abort(&bar.q_full, items & 1, aborted, status) && loaded(it);
             if (!ok) break;
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             if (!ok) break;
             const Item &x = ring[items % kItems];
             last = x.last;
-            const bool two = x.ntok > a.TB;
+            const bool two = kQ == 2 && x.ntok > a.TB;
             const int n = x.t1 - x.t0, step = two ? 1 : 2, my_tile = two ? t : 0;
             const int my_tok = my_tile * a.TB + r / a.G;
             const bool valid = r < a.TB * a.G && my_tok < x.ntok;
@@ -665,10 +666,10 @@ __device__ __forceinline__ int64_t block_inclusive(int64_t x, int64_t *warp_sums
 }
 
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const KvArgs c, int64_t *attend_start, int64_t *weight_start,
-                                                                  int TB) {
+                                                                  int block, int TB) {
     __shared__ int64_t warp_sums[kPlanThreads / 32];
     dependent_start();
-    const AttendWork aw{2 * TB};
+    const AttendWork aw{block};
     const WeightWork ww{TB};
     int64_t a_sum = 0, w_sum = 0;
     for (int64_t b = 0; b < c.N; b += kPlanThreads) {
@@ -714,6 +715,7 @@ size_t lay_out(const KvArgs &c, int G, bool accumulate, int ctas, char *ws, Atte
     a->attend_start = near ? nullptr : reinterpret_cast<int64_t *>(take(n));
     a->weight_start = near || !accumulate ? nullptr : reinterpret_cast<int64_t *>(take(n));
     a->joins = take(static_cast<size_t>(ctas) * sizeof(JoinUnit));
+    a->weight_joins = accumulate ? take(static_cast<size_t>(ctas) * 16) : nullptr;
     a->part_o = reinterpret_cast<float *>(take(slots * kRows * kD * 4));
     a->part_ml = reinterpret_cast<float2 *>(take(slots * kRows * 8));
     a->stats = accumulate ? reinterpret_cast<float *>(take(static_cast<size_t>(c.T) * G * c.H * 4)) : nullptr;
@@ -728,10 +730,15 @@ size_t paged_attention_scratch(const KvArgs &c, int G, bool accumulate, int sm_c
 }
 
 cudaError_t setup_paged_attention_kernel() {
-    cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Shape<false>::kAlloc);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(paged_attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<true>::kAlloc);
+    cudaError_t e = cudaSuccess;
+    auto allow = [&](const void *kernel, size_t bytes) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    };
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<false, 1>), Shape<false, 1>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<false, 2>), Shape<false, 2>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<true, 1>), Shape<true, 1>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<true, 2>), Shape<true, 2>::kAlloc);
     return e == cudaSuccess ? setup_paged_weights_kernel() : e;
 }
 
@@ -745,6 +752,9 @@ cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_str
     a.scale = scale;
     a.G = G;
     a.TB = kTile / G;
+    // Units of two query tiles read the cache half as often; units of one leave their room to cache tiles in flight. With
+    // more than one tile of tokens a request on average the former count.
+    const int Q = c.T > c.N * a.TB ? 2 : 1;
     Maps maps;
     cudaError_t e;
     {
@@ -767,22 +777,26 @@ cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_str
     if (a.attend_start) {
         LaunchTimer timer(kKPagedPlan, st);
         e = launch_dependent(paged_plan_kernel, dim3(1), kPlanThreads, st, c, const_cast<int64_t *>(a.attend_start),
-                             const_cast<int64_t *>(a.weight_start), a.TB);
+                             const_cast<int64_t *>(a.weight_start), Q * a.TB, a.TB);
         if (e != cudaSuccess) return e;
     }
     {
         LaunchTimer timer(kKPagedAttention, st);
-        e = c.e4m3 ? launch_dependent_cluster(paged_attention_kernel<true>, dim3(sm_count), 0, Shape<true>::kThreads,
-                                              Shape<true>::kAlloc, st, a, maps)
-                   : launch_dependent_cluster(paged_attention_kernel<false>, dim3(sm_count), 0, Shape<false>::kThreads,
-                                              Shape<false>::kAlloc, st, a, maps);
+        auto launch = [&](auto kernel, auto shape) {
+            using S = decltype(shape);
+            return launch_dependent_cluster(kernel, dim3(sm_count), 0, S::kThreads, S::kAlloc, st, a, maps);
+        };
+        e = c.e4m3 ? (Q == 2 ? launch(paged_attention_kernel<true, 2>, Shape<true, 2>{})
+                             : launch(paged_attention_kernel<true, 1>, Shape<true, 1>{}))
+                   : (Q == 2 ? launch(paged_attention_kernel<false, 2>, Shape<false, 2>{})
+                             : launch(paged_attention_kernel<false, 1>, Shape<false, 1>{}));
         if (e != cudaSuccess) return e;
     }
     {
         LaunchTimer timer(kKPagedCombine, st);
         // rows that a unit can have
         const int64_t tokens = c.cu ? c.T : c.T_row;
-        const int rows = tokens <= a.TB ? static_cast<int>(tokens) * G : kRows;
+        const int rows = tokens <= a.TB ? static_cast<int>(tokens) * G : Q * kTile;
         e = launch_dependent(paged_combine_kernel, dim3(sm_count, (rows + kJoinRows - 1) / kJoinRows), kJoinThreads, st, a);
         if (e != cudaSuccess || !accumulate) return e;
     }

@@ -284,7 +284,7 @@ struct Maps {
 struct AttendArgs {
     KvArgs c;
     const int64_t *attend_start, *weight_start;   // [N + 1] running sums of tiles, null: each CTA takes them
-    void *joins;         // [CTAs] units that several CTAs share
+    void *joins, *weight_joins;   // [CTAs] units that several CTAs share
     float *part_o;       // [2 * CTAs, 256, 128] partial O
     float2 *part_ml;     // [2 * CTAs, 256] its maximum (log2) and sum
     float *stats;        // [T, Hq] log2 of each row's sum of exponentials, or null

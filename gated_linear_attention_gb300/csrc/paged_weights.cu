@@ -44,6 +44,11 @@ struct alignas(16) Item {
 };
 constexpr int kItems = 4;
 
+// A cache tile that this CTA began and others finished: `parts` partial sums, from this CTA on (0: none).
+struct JoinUnit {
+    int n, h, u, parts;
+};
+
 struct Barriers {
     uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], raw_full[5], raw_empty[5];
     uint64_t item_full[kItems], item_empty[kItems];
@@ -118,7 +123,9 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         *reinterpret_cast<uint4 *>(smem + Layout::kOnesAt + aux_at(threadIdx.x, 1)) = make_uint4(0, 0, 0, 0);
         tc::fence_proxy_async_smem();
     }
-    dependent_start();
+    // The attention waited for what lay before it and then let the joining of its results, and this kernel, start: the
+    // lengths and offsets are there, and only what follows the split of the work waits for the rows' statistics.
+    let_dependents_start();
     uint32_t *const near = reinterpret_cast<uint32_t *>(smem);   // where the tiles land later
     if (!a.weight_start) scan_requests(c, work, near, near + kInline + 1);
     const Starts starts{a.weight_start ? nullptr : near, a.weight_start};
@@ -126,9 +133,11 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
     const int64_t begin = range_begin(all, cta, gridDim.x), stop = range_begin(all, cta + 1, gridDim.x);
     const bool idle = begin >= stop;
     if (threadIdx.x == 0 && !idle) place = find(c, work, starts, per_head, begin);
+    wait_for_previous();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
+    if (idle && threadIdx.x == 0) static_cast<JoinUnit *>(a.weight_joins)[cta].parts = 0;
     const uint32_t tmem = tmem_slot;
     volatile int *const aborted = &abort_flag;
     int *const status = c.status;
@@ -149,6 +158,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         uint64_t *const full = E4M3 ? bar.raw_full : bar.k_full, *const empty = E4M3 ? bar.raw_empty : bar.k_empty;
         uint32_t kt = 0, qt = 0;
         bool ok = true;
+        JoinUnit join = {0, 0, 0, 0};
         Walk<WeightWork> w;
         w.start_at(c, work, place, begin, stop, cta);
         tc::fence_proxy_async_smem();   // the running sums were there before the tiles
@@ -196,7 +206,10 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                     __syncwarp();
                 }
             }
+            if (x.last && x.slot >= 0 && w.t0 == 0)
+                join = {x.n, x.h, x.u0, cta_of(all, w.pos + w.tiles - 1, gridDim.x) - cta + 1};
         } while (ok && w.next(c, work, cta));
+        if (lane == 0) static_cast<JoinUnit *>(a.weight_joins)[cta] = join;
         if (!ok) {   // copies in flight land before the CTA ends
             for (uint32_t j = kt > kRing ? kt - kRing : 0; j < kt; ++j)
                 tc::mbar_wait(&full[j % kRing], (j / kRing) & 1, tck::kWaitNs);
@@ -416,30 +429,18 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
 }
 
-// Adds the partial sums of units that several CTAs share, in the order of the CTAs.
-__global__ void __launch_bounds__(kInline) paged_weights_join_kernel(const AttendArgs a, int ctas) {
-    __shared__ uint32_t near[kInline + 1], sums[kInline / 32];
-    __shared__ Place place;
+// Adds the partial sums of cache tiles that several CTAs share, in the order of the CTAs.
+__global__ void __launch_bounds__(kTile) paged_weights_join_kernel(const AttendArgs a) {
     dependent_start();
     const KvArgs &c = a.c;
-    const WeightWork work{a.TB};
-    if (!a.weight_start) scan_requests(c, work, near, sums);
-    const Starts starts{a.weight_start ? nullptr : near, a.weight_start};
-    const int64_t per_head = starts[c.N], all = per_head * c.H;
     const int cta = blockIdx.x, r = threadIdx.x;
-    const int64_t r0 = range_begin(all, cta, ctas), r1 = range_begin(all, cta + 1, ctas);
-    if (r0 >= r1 || r1 >= all) return;
-    if (r == 0) place = find(c, work, starts, per_head, r1 - 1);
-    __syncthreads();
-    const kv::Request q = kv::request(c, place.n);
-    const int64_t from = place.begin, to = from + work.tiles(q.count, q.len, place.u);
-    const int64_t p = static_cast<int64_t>(place.u) * kTile + r;
-    if (from < r0 || to <= r1 || r >= kTile || p >= q.len) return;
-    const int parts = cta_of(all, to - 1, ctas) - cta + 1;
+    const JoinUnit x = static_cast<const JoinUnit *>(a.weight_joins)[cta];
+    const int64_t p = static_cast<int64_t>(x.u) * kTile + r;
+    if (x.parts == 0 || p >= kv::request_len(c, x.n)) return;
     float sum = 0.f;
-    for (int i = 0; i < parts; ++i) sum += a.part_w[part_slot(cta, i) * kTile + r];
-    const int page = kv::page_of(c, place.n, static_cast<int>(p));
-    if (page >= 0) c.weights[kv::row_of(c, page, place.h, static_cast<int>(p))] += sum;
+    for (int i = 0; i < x.parts; ++i) sum += a.part_w[part_slot(cta, i) * kTile + r];
+    const int page = kv::page_of(c, x.n, static_cast<int>(p));
+    if (page >= 0) c.weights[kv::row_of(c, page, x.h, static_cast<int>(p))] += sum;
 }
 
 }  // namespace
@@ -464,7 +465,7 @@ cudaError_t launch_paged_weights(const AttendArgs &a, const Maps &maps, int ctas
         if (e != cudaSuccess) return e;
     }
     LaunchTimer timer(kKPagedCombine, st);
-    return launch_dependent(paged_weights_join_kernel, dim3(ctas), kInline, st, a, ctas);
+    return launch_dependent(paged_weights_join_kernel, dim3(ctas), kTile, st, a);
 }
 
 }  // namespace pt
