@@ -42,7 +42,7 @@ constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128, 0, 0), kIdO = tc::idesc_b
 // Shared memory of units with Q query tiles: the queries, the ring of cache tiles, the ring of e4m3 tiles.
 template <bool E4M3, int Q>
 struct Shape {
-    static constexpr int kStages = E4M3 ? 3 : 7 - Q, kRaw = E4M3 ? 8 - 2 * Q : 0;
+    static constexpr int kStages = E4M3 ? 4 : 7 - Q, kRaw = E4M3 ? 6 - 2 * Q : 0;
     static constexpr int kThreads = 32 * (E4M3 ? kConvertWarp + kConvertWarps : kConvertWarp);
     static constexpr uint32_t kRawAt = (Q + kStages) * kTileBytes;
     static constexpr uint32_t kAlloc = kRawAt + kRaw * kRawBytes + 1024;   // aligned to the swizzle's 1024 bytes
@@ -241,17 +241,26 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
     } else if (E4M3 && warp >= kConvertWarp && !idle) {
         // ---- e4m3 tiles to bf16 --------------------------------------------------------------------
         constexpr int kRaw = E4M3 ? Layout::kRaw : 1;
+        const int id = threadIdx.x - 32 * kConvertWarp;
         const int64_t tiles = 2 * (stop - begin);
-        for (int64_t it = 0; it < tiles; ++it) {
-            const int st = it % Layout::kStages, rw = it % kRaw;
-            if (!wait_or_abort(&bar.raw_full[rw], (it / kRaw) & 1, aborted, status)) break;
-            if (it >= Layout::kStages && !wait_or_abort(&bar.empty[st], (it / Layout::kStages - 1) & 1, aborted, status)) break;
-            convert_tile(smem + Layout::kRawAt + rw * kRawBytes, smem + (kQ + st) * kTileBytes, threadIdx.x - 32 * kConvertWarp);
+        uint4 held[kPieces];   // of the next tile: read while the stores of this one drain
+        bool ok = wait_or_abort(&bar.raw_full[0], 0, aborted, status);
+        if (ok) read_pieces(held, smem + Layout::kRawAt, id);
+        for (int64_t it = 0; it < tiles && ok; ++it) {
+            const int st = it % Layout::kStages, rw = it % kRaw, next = (it + 1) % kRaw;
+            ok = it < Layout::kStages || wait_or_abort(&bar.empty[st], (it / Layout::kStages - 1) & 1, aborted, status);
+            if (!ok) break;
+            store_pieces(held, smem + (kQ + st) * kTileBytes, id);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.raw_empty[rw]);
+            const bool there = it + 1 < tiles && tc::mbar_test_wait(&bar.raw_full[next], ((it + 1) / kRaw) & 1);
+            if (there) read_pieces(held, smem + Layout::kRawAt + next * kRawBytes, id);
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar.full[st]);
-                mbar_arrive(&bar.raw_empty[rw]);
+            if (lane == 0) mbar_arrive(&bar.full[st]);
+            if (it + 1 < tiles && !there) {
+                ok = wait_or_abort(&bar.raw_full[next], ((it + 1) / kRaw) & 1, aborted, status);
+                if (ok) read_pieces(held, smem + Layout::kRawAt + next * kRawBytes, id);
             }
         }
     } else if (warp == kMmaWarp && !idle) {
@@ -420,21 +429,27 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                 ++seen;
                 tc::tc_fence_after();
                 if (active) {
-                    uint32_t s[2][32];
-                    tmem_ld_half_x32(ts, s[0]);
-                    tmem_ld_half_x32(ts + 64, s[1]);
-                    tc::tmem_ld_wait();
-                    if (i * kTile + kTile - 1 > first_limit) {
-                        const int keep = limit - i * kTile - 32 * half;
+                    // bf16: all 64 scores in registers; e4m3, with fewer registers a thread: 32 at a time, twice
+                    uint32_t s[E4M3 ? 1 : 2][32];
+                    const int keep = limit - i * kTile - 32 * half;
+                    const bool edge = i * kTile + kTile - 1 > first_limit;
+                    auto load = [&](int q, uint32_t (&x)[32]) {
+                        tmem_ld_half_x32(ts + 64 * q, x);
+                        tc::tmem_ld_wait();
+                        if (edge)
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if ((j >> 5) * 64 + (j & 31) > keep) s[j >> 5][j & 31] = __float_as_uint(-INFINITY);
-                    }
+                            for (int j = 0; j < 32; ++j)
+                                if (64 * q + j > keep) x[j] = __float_as_uint(-INFINITY);
+                    };
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int j = 0; j < 64; j += 2)
-                        top[(j >> 1) & 3] = fmaxf(fmaxf(top[(j >> 1) & 3], __uint_as_float(s[j >> 5][j & 31])),
-                                                  __uint_as_float(s[j >> 5][(j & 31) + 1]));
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t (&y)[32] = s[E4M3 ? 0 : q];
+                        load(q, y);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2)
+                            top[(j >> 1) & 3] = fmaxf(fmaxf(top[(j >> 1) & 3], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
+                    }
                     float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     tile_top = fmaxf(tile_top, __shfl_xor_sync(0xffffffffu, tile_top, 16));
                     if (fresh) {
@@ -462,11 +477,13 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                     uint64_t sum2[2] = {0, 0};   // pairs of zeros
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
+                        uint32_t (&z)[32] = s[E4M3 ? 0 : q];
+                        if (E4M3) load(q, z);
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const float2 y = tc::unpair(tc::fma2(
-                                tc::pair(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), scale2, minus));
+                                tc::pair(__uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1])), scale2, minus));
                             const float e0 = tc::ex2(y.x), e1 = tc::ex2(y.y);
                             sum2[j & 1] = tc::add2(sum2[j & 1], tc::pair(e0, e1));
                             pk[j] = float2_to_bf16x2(e0, e1);

@@ -13,7 +13,8 @@ constexpr uint32_t kHalf = kTile * 128;          // bytes of [128 rows x 64 bf16
 constexpr uint32_t kTileBytes = 2 * kHalf;
 constexpr uint32_t kRawBytes = kTile * kD;       // bytes of a tile of e4m3 values
 constexpr int kInline = 256;                     // requests whose prefix every CTA takes for itself
-constexpr int kConvertWarps = 4;
+constexpr int kConvertWarps = 8;                 // that widen e4m3 tiles
+constexpr int kPieces = 1024 / (32 * kConvertWarps);   // 16-byte pieces of a tile a thread
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---- work ----------------------------------------------------------------------------------------
@@ -247,22 +248,26 @@ __device__ __forceinline__ void load_boxes(const KvArgs &c, const CUtensorMap *m
     __syncwarp();
 }
 
-// e4m3 values of a tile -> a bf16 tile (exact), by kConvertWarps warps. Eight lanes take two rows, the left half of
-// one and the right half of the other: loads and stores then fall on all banks.
-__device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst, int id) {
-    const int lane8 = id & 7, pair = id >> 3;
+// Thread id's pieces of an e4m3 tile: eight lanes take two rows, the left half of one and the right half of the other, so
+// that loads and stores fall on all banks.
+__device__ __forceinline__ int piece_row(int id, int e) { return 2 * (((id >> 3) + e * 4 * kConvertWarps) >> 1) + (id >> 2 & 1); }
+__device__ __forceinline__ int piece_of_row(int id) { return (id & 3) + 4 * ((id >> 3 & 1) ^ (id >> 2 & 1)); }
+__device__ __forceinline__ void read_pieces(uint4 (&x)[kPieces], const uint8_t *raw, int id) {
 #pragma unroll
-    for (int e = 0; e < 1024 / (32 * kConvertWarps); ++e) {
-        const int group = pair + e * (4 * kConvertWarps);        // 128 groups: two for each pair of rows
-        const int row = (group >> 1) * 2 + (lane8 >> 2), p = (lane8 & 3) + 4 * ((group & 1) ^ (lane8 >> 2));
-        const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * kD + p * 16);
-        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+    for (int e = 0; e < kPieces; ++e)
+        x[e] = *reinterpret_cast<const uint4 *>(raw + piece_row(id, e) * kD + piece_of_row(id) * 16);
+}
+// Stores them as bf16 (exact).
+__device__ __forceinline__ void store_pieces(const uint4 (&x)[kPieces], uint8_t *dst, int id) {
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) {
+        const int row = piece_row(id, e), p = piece_of_row(id);
+        const uint32_t in[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
         uint32_t out[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float2 lo = kv::e4m3x2_to_float2(in[q] & 0xffffu), hi = kv::e4m3x2_to_float2(in[q] >> 16);
-            out[2 * q] = float2_to_bf16x2(lo.x, lo.y);
-            out[2 * q + 1] = float2_to_bf16x2(hi.x, hi.y);
+        for (int q = 0; q < 8; ++q) {
+            const float2 f = kv::e4m3x2_to_float2(q & 1 ? in[q >> 1] >> 16 : in[q >> 1] & 0xffffu);
+            out[q] = float2_to_bf16x2(f.x, f.y);
         }
         *reinterpret_cast<uint4 *>(dst + piece_at(row, 2 * p)) = make_uint4(out[0], out[1], out[2], out[3]);
         *reinterpret_cast<uint4 *>(dst + piece_at(row, 2 * p + 1)) = make_uint4(out[4], out[5], out[6], out[7]);

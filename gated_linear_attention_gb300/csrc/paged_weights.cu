@@ -272,7 +272,9 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 ok = wait_or_abort(&bar.raw_full[rw], (it / kRaw) & 1, aborted, status) &&
                      (it < Layout::kKeys || wait_or_abort(&bar.k_empty[st], (it / Layout::kKeys - 1) & 1, aborted, status));
                 if (!ok) break;
-                convert_tile(smem + Layout::kRawAt + rw * kRawBytes, smem + st * kTileBytes, threadIdx.x - 32 * kConvertWarp);
+                uint4 held[kPieces];
+                read_pieces(held, smem + Layout::kRawAt + rw * kRawBytes, threadIdx.x - 32 * kConvertWarp);
+                store_pieces(held, smem + st * kTileBytes, threadIdx.x - 32 * kConvertWarp);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
