@@ -265,52 +265,57 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
         }
     } else if (warp == kMmaWarp && !idle) {
         // ---- products ------------------------------------------------------------------------------
-        const bool leader = tc::elect_one();
-        uint32_t it = 0, items = 0, sp[2] = {0, 0}, used[2] = {0, 0};   // tiles loaded, items, score tiles, items of a group
+        constexpr int S = Layout::kStages;
+        const uint32_t full = tc::smem_u32(bar.full), empty = tc::smem_u32(bar.empty), s_full = tc::smem_u32(bar.s_full);
+        const uint32_t p_full = tc::smem_u32(bar.p_full), o_full = tc::smem_u32(bar.o_full), o_free = tc::smem_u32(bar.o_free);
+        const uint32_t q_free = tc::smem_u32(&bar.q_free), q_full = tc::smem_u32(&bar.q_full);
+        const uint64_t first_k = desc_k(base), first_mn = desc_mn(base + kQ * kTileBytes);   // of the first tile, the first stage
+        uint32_t items = 0, p_parity = 0, o_used = 0, o_parity = 3;   // a bit for each group
         bool ok = true, last = false;
-        auto stage_of = [](uint32_t j) { return j % Layout::kStages; };
-        auto loaded = [&](uint32_t j) {
-            return wait_or_abort(&bar.full[stage_of(j)], (j / Layout::kStages) & 1, aborted, status);
+        auto passed = [&](uint32_t b, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_at(b, parity, aborted, status)) != 0;
         };
-        auto scores = [&](int t, int q, uint32_t j) {   // of query tile q, for group t
-            tc::tc_fence_after();
-            if (leader) {
-                const uint64_t dq = desc_k(base + q * kTileBytes), dk = desc_k(base + (kQ + stage_of(j)) * kTileBytes);
+        auto scores = [&](int t, int q, uint32_t stage) {   // of query tile q, for group t
+            if (tc::elect_one()) {
+                const uint64_t dq = first_k + q * (kTileBytes >> 4), dk = first_k + (kQ + stage) * (kTileBytes >> 4);
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
                     const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
                     tc::umma_bf16(tmem + kS0 + t * kTile, dq + off, dk + off, kIdS, ks > 0);
                 }
-                tc::umma_commit(&bar.s_full[t]);
+                commit_at(s_full + 8 * t);
             }
             __syncwarp();
         };
-        auto release = [&](uint32_t j) {
-            if (leader) tc::umma_commit(&bar.empty[stage_of(j)]);
+        auto commit = [&](uint32_t b) {
+            if (tc::elect_one()) commit_at(b);
             __syncwarp();
         };
-        // O of group t from its P and the values of tile j; `first` of the item, `final` of the item
-        auto products = [&](int t, uint32_t j, bool first, bool final) {
-            if (!wait_or_abort(&bar.p_full[t], sp[t] & 1, aborted, status)) return false;
-            if (first && used[t] > 0 && !wait_or_abort(&bar.o_free[t], (used[t] - 1) & 1, aborted, status)) return false;
-            ++sp[t];
+        // O of group t from its P and the values of a stage; `first` of the item, `final` of the item
+        auto products = [&](int t, uint32_t stage, bool first, bool final) {
+            if (!passed(p_full + 8 * t, p_parity >> t & 1)) return false;
+            if (first) {   // the results of the item before are read
+                if ((o_used >> t & 1) && !passed(o_free + 8 * t, o_parity >> t & 1)) return false;
+                o_used |= 1u << t;
+                o_parity ^= 1u << t;
+            }
+            p_parity ^= 1u << t;
             tc::tc_fence_after();
-            if (leader) {
-                const uint64_t dv = desc_mn(base + (kQ + stage_of(j)) * kTileBytes);
+            if (tc::elect_one()) {
+                const uint64_t dv = first_mn + stage * (kTileBytes >> 4);
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
                     tc::umma_bf16_ta(tmem + kO0 + t * kTile, tmem + kS0 + t * kTile + 8 * ks, dv + ks * (2048 >> 4), kIdO,
                                      !first || ks > 0);
-                if (final) tc::umma_commit(&bar.o_full[t]);
+                if (final) commit_at(o_full + 8 * t);
             }
             __syncwarp();
             return true;
         };
         // Clears the rows of V that no token sees, and infinities and NaN in those that not all tokens see: true if any
-        auto clean = [&](const Item &x, int i, uint32_t j) {
-            const int p0 = i * kTile, shared_from = max(0, x.limit + 1), end = x.end();
-            if (p0 + kTile <= shared_from) return false;
-            uint8_t *v = smem + (kQ + stage_of(j)) * kTileBytes;
+        auto clean = [&](int shared_from, int end, int i, uint32_t stage) {
+            const int p0 = i * kTile;
+            uint8_t *v = smem + (kQ + stage) * kTileBytes;
             for (int e = lane + max(0, min(kTile, end - p0)) * 16; e < kTile * 16; e += 32)
                 *reinterpret_cast<uint4 *>(v + piece_at(e >> 4, e & 15)) = make_uint4(0, 0, 0, 0);
             bool found = false;
@@ -325,75 +330,94 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
             tc::fence_proxy_async_smem();
             return __any_sync(0xffffffffu, found) != 0;
         };
+        Ring<S> k, v;   // the stages of the next keys and values
+        v.advance(1);
         do {
-            ok = wait_or_abort(&bar.item_full[items % kItems], (items / kItems) & 1, aborted, status);
+            ok = passed(tc::smem_u32(&bar.item_full[items % kItems]), items / kItems & 1);
             if (!ok) break;
             const Item &x = ring[items % kItems];
-            const int t0 = x.t0, n = x.t1 - t0;
-            const bool two = kQ == 2 && x.ntok > a.TB;
+            auto uniform = [](int y) { return __shfl_sync(0xffffffffu, y, 0); };
+            const int t0 = uniform(x.t0), n = uniform(x.t1) - t0, end = uniform(x.end()), shared_from = max(0, uniform(x.limit) + 1);
+            const int whole = shared_from / kTile - t0;      // tiles before this one have no row to clear
+            const bool two = kQ == 2 && uniform(x.ntok) > a.TB;
             bool bad = false;
-            ok = wait_or_abort(&bar.q_full, items & 1, aborted, status) && loaded(it);
+            ok = passed(q_full, items & 1) && passed(full + 8 * k.at, k.parity);
             if (!ok) break;
+            tc::tc_fence_after();
             if (two) {   // each cache tile for both query tiles
-                for (int t = 0; t < 2; ++t) scores(t, t, it);
-                release(it);
-                if (n == 1 && leader) tc::umma_commit(&bar.q_free);
-                for (int i = 0; i < n && ok; ++i, it += 2) {
-                    ok = loaded(it + 1);
-                    if (!ok) break;
-                    bad |= clean(x, t0 + i, it + 1);
+                scores(0, 0, k.at);
+                scores(1, 1, k.at);
+                commit(empty + 8 * k.at);
+                k.advance(2);
+                if (n == 1) commit(q_free);
+                for (int i = 0; i < n; ++i) {
                     const bool more = i + 1 < n;
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        ok = products(t, it + 1, i == 0, !more) && (!more || t == 1 || loaded(it + 2));
-                        if (ok && more) scores(t, t, it + 2);
-                    }
+                    ok = passed(full + 8 * v.at, v.parity);
                     if (!ok) break;
-                    release(it + 1);
-                    if (more) release(it + 2);
-                    if (i + 2 == n && leader) tc::umma_commit(&bar.q_free);
+                    if (i >= whole) bad |= clean(shared_from, end, t0 + i, v.at);
+                    ok = products(0, v.at, i == 0, !more) && (!more || passed(full + 8 * k.at, k.parity));
+                    if (!ok) break;
+                    if (more) scores(0, 0, k.at);
+                    ok = products(1, v.at, i == 0, !more);
+                    if (!ok) break;
+                    if (more) scores(1, 1, k.at);
+                    if (tc::elect_one()) {
+                        commit_at(empty + 8 * v.at);
+                        if (more) commit_at(empty + 8 * k.at);
+                        if (i + 2 == n) commit_at(q_free);
+                    }
+                    __syncwarp();
+                    v.advance(2);
+                    if (more) k.advance(2);
                 }
             } else {     // one query tile: the groups take the cache tiles in turn
-                scores(0, 0, it);
-                release(it);
+                scores(0, 0, k.at);
+                commit(empty + 8 * k.at);
+                k.advance(2);
                 if (n > 1) {
-                    ok = loaded(it + 2);
+                    ok = passed(full + 8 * k.at, k.parity);
                     if (!ok) break;
-                    scores(1, 0, it + 2);
-                    release(it + 2);
+                    scores(1, 0, k.at);
+                    commit(empty + 8 * k.at);
+                    k.advance(2);
                 }
-                if (n <= 2 && leader) tc::umma_commit(&bar.q_free);
-                for (int i = 0; i < n && ok; ++i, it += 2) {
+                if (n <= 2) commit(q_free);
+                for (int i = 0; i < n; ++i) {
                     const int t = i & 1;
-                    ok = loaded(it + 1);
+                    ok = passed(full + 8 * v.at, v.parity);
                     if (!ok) break;
-                    bad |= clean(x, t0 + i, it + 1);
-                    ok = products(t, it + 1, i < 2, i + 2 >= n);
+                    if (i >= whole) bad |= clean(shared_from, end, t0 + i, v.at);
+                    ok = products(t, v.at, i < 2, i + 2 >= n);
                     if (!ok) break;
-                    release(it + 1);
+                    commit(empty + 8 * v.at);
+                    v.advance(2);
                     if (i + 2 < n) {
-                        ok = loaded(it + 4);
+                        ok = passed(full + 8 * k.at, k.parity);
                         if (!ok) break;
-                        scores(t, 0, it + 4);
-                        release(it + 4);
-                        if (i + 3 == n && leader) tc::umma_commit(&bar.q_free);
+                        scores(t, 0, k.at);
+                        if (tc::elect_one()) {
+                            commit_at(empty + 8 * k.at);
+                            if (i + 3 == n) commit_at(q_free);
+                        }
+                        __syncwarp();
+                        k.advance(2);
                     }
                 }
             }
             if (!ok) break;
             const int groups = two || n > 1 ? 2 : 1;
-            if (leader)
+            if (tc::elect_one())
                 for (int t = 0; t < groups; ++t) {
                     bad_values[t] = bad;
                     mbar_arrive(&bar.o_full[t]);
                 }
-            for (int t = 0; t < groups; ++t) ++used[t];
-            last = x.last;
+            last = uniform(x.last) != 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
             ++items;
         } while (!last);
         if (!ok) {   // products in flight end before the tensor memory is freed
-            if (leader) {
+            if (tc::elect_one()) {
                 tc::umma_commit(&bar.drain);
                 tc::mbar_wait(&bar.drain, 0, tck::kWaitNs);
             }

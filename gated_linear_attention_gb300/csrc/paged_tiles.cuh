@@ -36,11 +36,16 @@ __host__ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
     }
 }
 
+// x / y for 0 <= x < 2^32 and y > 0: 64-bit divisions are slow.
+__host__ __device__ inline int divide(int64_t x, int y) {
+    return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+}
+
 // Attention: unit u of a request is its tokens [u * block, (u + 1) * block) with the cache tiles up to the last
 // place that they see.
 struct AttendWork {
     int block;
-    __host__ __device__ int units(int count, int) const { return static_cast<int>((static_cast<int64_t>(count) + block - 1) / block); }
+    __host__ __device__ int units(int count, int) const { return divide(static_cast<int64_t>(count) + block - 1, block); }
     __host__ __device__ int64_t tiles(int count, int len, int u) const {
         const int64_t base = static_cast<int64_t>(len) - count;
         // more tokens than places: each unit takes all of them, which is more than some see
@@ -51,7 +56,7 @@ struct AttendWork {
     // tiles of the units before u; u is at most the number of units less 1
     __host__ __device__ int64_t before(int count, int len, int u) const {
         const int64_t base = static_cast<int64_t>(len) - count;
-        if (base < 0) return u * tiles(count, len, 0);
+        if (base < 0 || u == 0) return u * tiles(count, len, 0);
         return floor_sum(u, kTile, block, base + block + kTile - 1);
     }
 };
@@ -60,17 +65,17 @@ struct AttendWork {
 struct WeightWork {
     int block;
     __host__ __device__ int units(int count, int len) const { return count > 0 ? (len + kTile - 1) / kTile : 0; }
-    __host__ __device__ int query_tiles(int count) const { return static_cast<int>((static_cast<int64_t>(count) + block - 1) / block); }
+    __host__ __device__ int query_tiles(int count) const { return divide(static_cast<int64_t>(count) + block - 1, block); }
     __host__ __device__ int first(int count, int len, int u) const {
         const int64_t from = static_cast<int64_t>(u) * kTile - (static_cast<int64_t>(len) - count);
-        return from > 0 ? static_cast<int>(from / block) : 0;
+        return from > 0 ? divide(from, block) : 0;   // below count
     }
     __host__ __device__ int64_t tiles(int count, int len, int u) const { return query_tiles(count) - first(count, len, u); }
     __host__ __device__ int64_t before(int count, int len, int u) const {
         const int64_t base = static_cast<int64_t>(len) - count;
         const int64_t u0 = base > 0 ? (base + kTile - 1) / kTile : 0;
         const int64_t all = static_cast<int64_t>(u) * query_tiles(count);
-        return u > u0 ? all - floor_sum(u - u0, block, kTile, u0 * kTile - base) : all;
+        return u > u0 && query_tiles(count) > 1 ? all - floor_sum(u - u0, block, kTile, u0 * kTile - base) : all;
     }
 };
 
@@ -137,7 +142,7 @@ struct Place {
 template <class Work>
 __device__ __forceinline__ Place find(const KvArgs &c, const Work &work, const Starts &start, int64_t per_head, int64_t at) {
     Place p;
-    p.h = static_cast<int>(at / per_head);
+    p.h = at >> 32 || per_head >> 32 ? static_cast<int>(at / per_head) : divide(at, static_cast<int>(per_head));
     at -= per_head * p.h;
     int64_t lo = 0, hi = c.N;
     while (hi - lo > 1) {
@@ -273,6 +278,45 @@ __device__ __forceinline__ void store_pieces(const uint4 (&x)[kPieces], uint8_t 
         *reinterpret_cast<uint4 *>(dst + piece_at(row, 2 * p + 1)) = make_uint4(out[4], out[5], out[6], out[7]);
     }
 }
+
+// ---- barriers by their shared-memory address --------------------------------------------------------
+// The warp that issues the products pays for every scalar instruction between two of them (its queue is short), so it
+// keeps addresses, stages and parities in registers.
+
+static __device__ __noinline__ bool wait_at_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status) {
+    const uint64_t t0 = tc::global_timer_ns();
+    while (true) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        if (tc::global_timer_ns() - t0 > tck::kWaitNs) {
+            *abort_flag = 1;
+            record_status(status, SALA_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok || wait_at_slow(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ void commit_at(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A place in a ring of N stages and the parity of its phase.
+template <int N>
+struct Ring {
+    uint32_t at = 0, parity = 0;
+    __device__ __forceinline__ void advance(uint32_t n) {   // n <= N
+        at += n;
+        if (at >= N) at -= N, parity ^= 1u;
+    }
+};
 
 // Query rows: `tokens` tokens of the group's G heads from packed token `row` (rows past the end are zeros).
 __device__ __forceinline__ void load_query_tile(uint8_t *dst, const CUtensorMap *map, int h, int G, int64_t row, uint64_t *bar) {

@@ -285,24 +285,29 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         } while (ok && !x.last);
     } else if (warp == kMmaWarp && !idle) {
         // ---- products ------------------------------------------------------------------------------------
-        const bool leader = tc::elect_one();
+        // uniform over the warp, as in the attention
+        auto passed = [&](uint64_t *b, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_abort(b, parity & 1, aborted, status)) != 0;
+        };
         uint32_t kt = 0, qt = 0, tile = 0;
         bool ok = true;
         Item x;
         do {
-            ok = take(x);
+            ok = __all_sync(0xffffffffu, take(x)) != 0;
             if (!ok) break;
-            for (int i = 0; i < x.nu && ok; ++i, ++kt) {
+            const int nu = __shfl_sync(0xffffffffu, x.nu, 0), nq = __shfl_sync(0xffffffffu, x.nq, 0);
+            const int ntok = __shfl_sync(0xffffffffu, x.ntok, 0);
+            for (int i = 0; i < nu && ok; ++i, ++kt) {
                 const int ks = kt % Layout::kKeys;
-                ok = wait_or_abort(&bar.k_full[ks], (kt / Layout::kKeys) & 1, aborted, status);
-                for (int q = 0; q < x.nq && ok; ++q, ++tile) {
+                ok = passed(&bar.k_full[ks], kt / Layout::kKeys);
+                for (int q = 0; q < nq && ok; ++q, ++tile) {
                     const uint32_t j = qt + q;
-                    const int s = j % Layout::kQueries, b = tile % kGroups, rows = min(a.TB, x.ntok - q * a.TB) * a.G;
-                    if (i == 0) ok = wait_or_abort(&bar.q_full[s], (j / Layout::kQueries) & 1, aborted, status);
-                    ok = ok && (tile < kGroups || wait_or_abort(&bar.s_free[b], (tile / kGroups - 1) & 1, aborted, status));
+                    const int s = j % Layout::kQueries, b = tile % kGroups, rows = min(a.TB, ntok - q * a.TB) * a.G;
+                    if (i == 0) ok = passed(&bar.q_full[s], j / Layout::kQueries);
+                    ok = ok && (tile < kGroups || passed(&bar.s_free[b], tile / kGroups - 1));
                     if (!ok) break;
                     tc::tc_fence_after();
-                    if (leader) {
+                    if (tc::elect_one()) {
                         const uint32_t id = tc::idesc_bf16_f32(128, (rows + 15) & ~15, 0, 0);
                         const uint64_t dk = desc_k(base + ks * kTileBytes), dq = desc_k(base + Layout::kQueriesAt + s * kTileBytes);
                         tc::umma_bf16(tmem + b * kTile, desc_aux(base + Layout::kOnesAt), desc_aux(base + Layout::kAuxAt + s * kAuxBytes),
@@ -313,18 +318,18 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                             tc::umma_bf16(tmem + b * kTile, dk + off, dq + off, id, 1u);
                         }
                         tc::umma_commit(&bar.s_full[b]);
-                        if (i + 1 == x.nu) tc::umma_commit(&bar.q_empty[s]);
+                        if (i + 1 == nu) tc::umma_commit(&bar.q_empty[s]);
                     }
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (leader) tc::umma_commit(&bar.k_empty[ks]);
+                if (tc::elect_one()) tc::umma_commit(&bar.k_empty[ks]);
                 __syncwarp();
             }
-            qt += x.nq;
-        } while (ok && !x.last);
+            qt += nq;
+        } while (ok && !__shfl_sync(0xffffffffu, x.last, 0));
         if (!ok) {   // products in flight end before the tensor memory is freed
-            if (leader) {
+            if (tc::elect_one()) {
                 tc::umma_commit(&bar.drain);
                 tc::mbar_wait(&bar.drain, 0, tck::kWaitNs);
             }

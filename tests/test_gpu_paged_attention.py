@@ -101,6 +101,24 @@ def test_long_cache_split_over_many_blocks(kind):
     _run(c, q, cu, accumulate=True)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,Hq", [(1, 16), (3, 16), (1, 64), (40, 16)])
+def test_more_tiles_than_blocks(kind, T, Hq):
+    """Blocks that go through several units of one to seven tiles each, whole and shared."""
+    lens = [T + (137 * n) % 830 for n in range(61)]
+    c = make_cache(lens, 32, 8, kind, seed=T, weights=True)
+    q, _ = new_tokens([T * len(lens)], Hq, size=2.0)
+    _run(c, q.reshape(len(lens), T, Hq, 128), accumulate=True)
+
+
+def test_more_requests_than_a_block_scans():
+    lens = [1 + (53 * n) % 300 for n in range(300)]
+    c = make_cache(lens, 16, 2, seed=1, weights=True)
+    counts = [n % 3 for n in range(300)]
+    q, cu = new_tokens(counts, 8, size=2.0)
+    _run(c, q, cu, accumulate=True)
+
+
 def test_peaked_and_growing_scores():
     """Scores that rise along the cache (the maximum moves in every tile), and far apart ones."""
     c = make_cache([700], 16, 1, seed=3)
