@@ -27,7 +27,7 @@ constexpr uint32_t kAuxBytes = kTile * 32;       // [128 rows x 16 bf16], 32-byt
 
 template <bool E4M3>
 struct Shape {
-    static constexpr int kKeys = E4M3 ? 2 : 3, kQueries = E4M3 ? 2 : 3, kRaw = E4M3 ? 5 : 0;   // tiles in shared memory
+    static constexpr int kKeys = 3, kQueries = E4M3 ? 2 : 3, kRaw = E4M3 ? 3 : 0;   // tiles in shared memory
     static constexpr int kThreads = 32 * (E4M3 ? kConvertWarp + kConvertWarps : kConvertWarp);
     static constexpr uint32_t kQueriesAt = kKeys * kTileBytes, kRawAt = kQueriesAt + kQueries * kTileBytes;
     static constexpr uint32_t kOnesAt = kRawAt + kRaw * kRawBytes, kAuxAt = kOnesAt + kAuxBytes;
@@ -285,48 +285,60 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         } while (ok && !x.last);
     } else if (warp == kMmaWarp && !idle) {
         // ---- products ------------------------------------------------------------------------------------
-        // uniform over the warp, as in the attention
-        auto passed = [&](uint64_t *b, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_abort(b, parity & 1, aborted, status)) != 0;
-        };
-        uint32_t kt = 0, qt = 0, tile = 0;
+        const uint32_t k_full = tc::smem_u32(bar.k_full), k_empty = tc::smem_u32(bar.k_empty), q_full = tc::smem_u32(bar.q_full);
+        const uint32_t q_empty = tc::smem_u32(bar.q_empty), s_full = tc::smem_u32(bar.s_full), s_free = tc::smem_u32(bar.s_free);
+        const uint64_t first_k = desc_k(base), first_q = desc_k(base + Layout::kQueriesAt);
+        const uint64_t ones = desc_aux(base + Layout::kOnesAt), first_aux = desc_aux(base + Layout::kAuxAt);
+        Ring<Layout::kKeys> k;
+        Ring<Layout::kQueries> q;
+        Ring<kGroups> b;
         bool ok = true;
         Item x;
+        auto passed = [&](uint32_t at, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_at(at, parity, aborted, status)) != 0;
+        };
+        // The scores of a query tile with `rows` rows, into the next buffer; the tile's room is free after the `last` of them
+        auto scores = [&](int rows, bool last, bool keys_last) {
+            if (!passed(s_free + 8 * b.at, b.parity ^ 1u)) return false;   // passes at once the first time
+            tc::tc_fence_after();
+            if (tc::elect_one()) {
+                const uint32_t id = tc::idesc_bf16_f32(128, (rows + 15) & ~15, 0, 0), d = tmem + b.at * kTile;
+                const uint64_t dk = first_k + k.at * (kTileBytes >> 4), dq = first_q + q.at * (kTileBytes >> 4);
+                tc::umma_bf16(d, ones, first_aux + q.at * (kAuxBytes >> 4), id, 0u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
+                    tc::umma_bf16(d, dk + off, dq + off, id, 1u);
+                }
+                commit_at(s_full + 8 * b.at);
+                if (last) commit_at(q_empty + 8 * q.at);
+                if (keys_last) commit_at(k_empty + 8 * k.at);
+            }
+            __syncwarp();
+            b.advance(1);
+            return true;
+        };
         do {
             ok = __all_sync(0xffffffffu, take(x)) != 0;
             if (!ok) break;
             const int nu = __shfl_sync(0xffffffffu, x.nu, 0), nq = __shfl_sync(0xffffffffu, x.nq, 0);
-            const int ntok = __shfl_sync(0xffffffffu, x.ntok, 0);
-            for (int i = 0; i < nu && ok; ++i, ++kt) {
-                const int ks = kt % Layout::kKeys;
-                ok = passed(&bar.k_full[ks], kt / Layout::kKeys);
-                for (int q = 0; q < nq && ok; ++q, ++tile) {
-                    const uint32_t j = qt + q;
-                    const int s = j % Layout::kQueries, b = tile % kGroups, rows = min(a.TB, ntok - q * a.TB) * a.G;
-                    if (i == 0) ok = passed(&bar.q_full[s], j / Layout::kQueries);
-                    ok = ok && (tile < kGroups || passed(&bar.s_free[b], tile / kGroups - 1));
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    if (tc::elect_one()) {
-                        const uint32_t id = tc::idesc_bf16_f32(128, (rows + 15) & ~15, 0, 0);
-                        const uint64_t dk = desc_k(base + ks * kTileBytes), dq = desc_k(base + Layout::kQueriesAt + s * kTileBytes);
-                        tc::umma_bf16(tmem + b * kTile, desc_aux(base + Layout::kOnesAt), desc_aux(base + Layout::kAuxAt + s * kAuxBytes),
-                                      id, 0u);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-                            tc::umma_bf16(tmem + b * kTile, dk + off, dq + off, id, 1u);
-                        }
-                        tc::umma_commit(&bar.s_full[b]);
-                        if (i + 1 == nu) tc::umma_commit(&bar.q_empty[s]);
-                    }
-                    __syncwarp();
+            int left = __shfl_sync(0xffffffffu, x.ntok, 0);
+            if (nq == 1) {   // a query tile for a run of cache tiles
+                const int rows = min(a.TB, left) * a.G;
+                ok = passed(q_full + 8 * q.at, q.parity);
+                for (int i = 0; i < nu && ok; ++i) {
+                    ok = passed(k_full + 8 * k.at, k.parity) && scores(rows, i + 1 == nu, true);
+                    k.advance(1);
                 }
-                if (!ok) break;
-                if (tc::elect_one()) tc::umma_commit(&bar.k_empty[ks]);
-                __syncwarp();
+                q.advance(1);
+            } else {         // a cache tile for a run of query tiles
+                ok = passed(k_full + 8 * k.at, k.parity);
+                for (int i = 0; i < nq && ok; ++i, left -= a.TB) {
+                    ok = passed(q_full + 8 * q.at, q.parity) && scores(min(a.TB, left) * a.G, true, i + 1 == nq);
+                    q.advance(1);
+                }
+                k.advance(1);
             }
-            qt += nq;
         } while (ok && !__shfl_sync(0xffffffffu, x.last, 0));
         if (!ok) {   // products in flight end before the tensor memory is freed
             if (tc::elect_one()) {
