@@ -354,91 +354,119 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         uint32_t tile = 0, done = 0;             // score tiles of the CTA, of this group
         uint32_t sent = 0, flips = 0;             // partial sums handed over; parity of every group's, a bit each
         bool ok = true;
-        Item x;
+        Item x{};
+        float scale = 0.f;
+        // The sum over the rows of query tile q that see place p of the item's cache tile i
+        auto sum_tile = [&](int i, int p, int q) {
+            ok = wait_or_abort(&bar.s_full[g], done & 1, aborted, status);
+            if (!ok) return 0.f;
+            ++done;
+            tc::tc_fence_after();
+            const int rows = min(a.TB, x.ntok - q * a.TB) * a.G;
+            const bool seen = x.limit + q * a.TB >= (x.u0 + i) * kTile + kTile - 1;   // by all rows, every place
+            const int ahead = p - x.limit - q * a.TB;
+            const int from = ahead <= 0 ? 0 : ahead >= a.TB ? kTile : ahead * a.G;   // rows before it do not see the place
+            const uint64_t scale2 = tc::pair(scale, scale);
+            uint64_t sum2[2] = {0, 0};   // pairs of zeros
+            float rest = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (32 * e >= rows) break;
+                uint32_t s[32];
+                tc::tmem_ld_32x32b_x32(ts + 32 * e, s);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int n0 = 32 * e + 16 * half;
+                    if (seen && n0 + 16 <= rows) {
+#pragma unroll
+                        for (int j = 16 * half; j < 16 * half + 16; j += 2) {
+                            const float2 y = tc::unpair(tc::mul2(tc::pair(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), scale2));
+                            sum2[(j >> 1) & 1] = tc::add2(sum2[(j >> 1) & 1], tc::pair(tc::ex2(y.x), tc::ex2(y.y)));
+                        }
+                    } else if (n0 < rows) {
+#pragma unroll
+                        for (int j = 16 * half; j < 16 * half + 16; ++j) {
+                            const float y = tc::ex2(__uint_as_float(s[j]) * scale);
+                            rest += 32 * e + j >= from && 32 * e + j < rows ? y : 0.f;
+                        }
+                    }
+                }
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.s_free[g]);
+            const float2 even = tc::unpair(sum2[0]), odd = tc::unpair(sum2[1]);
+            return rest + ((even.x + even.y) + (odd.x + odd.y));
+        };
+        // Where place p's weight lies (null: nowhere, or the item's result is partial), and its value so far
+        struct Weight {
+            float *at = nullptr, old = 0.f;
+        };
+        auto look = [&](int p) {
+            Weight w;
+            if (x.slot < 0 && p < x.len) {
+                const int page = kv::page_of(c, x.n, p);
+                if (page >= 0) {
+                    w.at = c.weights + kv::row_of(c, page, x.h, p);
+                    w.old = *w.at;
+                }
+            }
+            return w;
+        };
+        auto finish = [&](const Weight &w, float total) {
+            if (x.slot >= 0) a.part_w[static_cast<int64_t>(x.slot) * kTile + r] = total;
+            else if (w.at) *w.at = w.old + total;
+        };
         do {
             ok = take(x);
             if (!ok) break;
-            const float scale = a.scale * (c.k_scale ? __ldg(c.k_scale + x.h) : 1.f) * kLog2e;
-            const uint64_t scale2 = tc::pair(scale, scale);
-            const int m = x.nq;
-            for (int i = 0; i < x.nu && ok; ++i, tile += m) {
-                const int p = (x.u0 + i) * kTile + r, owner = tile % kGroups;
-                const int mine = (g - owner) & (kGroups - 1);   // this group's first query tile of the unit
-                const uint32_t before = flips;
-#pragma unroll
-                for (int o = 1; o < kGroups; ++o)
-                    if (o < m) flips ^= 1u << ((owner + o) & (kGroups - 1));
-                if (mine >= m) continue;
-                float *weight = nullptr;
-                float old = 0.f;
-                if (mine == 0 && x.slot < 0 && p < x.len) {     // looked up while the scores are made
-                    const int page = kv::page_of(c, x.n, p);
-                    if (page >= 0) {
-                        weight = c.weights + kv::row_of(c, page, x.h, p);
-                        old = *weight;
-                    }
+            scale = a.scale * (c.k_scale ? __ldg(c.k_scale + x.h) : 1.f) * kLog2e;
+            const int m = x.nq, p = x.u0 * kTile + r, owner = tile % kGroups;
+            const int mine = (g - owner) & (kGroups - 1);   // this group's first tile of the item
+            if (m == 1) {        // every fourth cache tile; its weights are looked up a turn ahead
+                Weight next;
+                if (mine < x.nu) next = look(p + mine * kTile);
+                for (int i = mine; i < x.nu && ok; i += kGroups) {
+                    const Weight w = next;
+                    if (i + kGroups < x.nu) next = look(p + (i + kGroups) * kTile);
+                    const float total = sum_tile(i, p + i * kTile, 0);
+                    if (ok) finish(w, total);
                 }
-                float total = 0.f;
-                for (int q = mine; q < m; q += kGroups, ++done) {
-                    ok = wait_or_abort(&bar.s_full[g], done & 1, aborted, status);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    const int rows = min(a.TB, x.ntok - q * a.TB) * a.G;
-                    // rows that see the place: from `from` on
-                    const int ahead = p - x.limit - q * a.TB, from = ahead <= 0 ? 0 : ahead >= a.TB ? kTile : ahead * a.G;
-                    const bool seen = x.limit + q * a.TB >= (x.u0 + i) * kTile + kTile - 1;   // by all rows, every place
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint64_t sum2[2] = {0, 0};   // pairs of zeros
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (32 * e >= rows) break;
-                        uint32_t s[32];
-                        tc::tmem_ld_32x32b_x32(ts + 32 * e, s);
-                        tc::tmem_ld_wait();
-                        if (seen && 32 * e + 32 <= rows) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                const float2 y = tc::unpair(tc::mul2(tc::pair(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), scale2));
-                                sum2[(j >> 1) & 1] = tc::add2(sum2[(j >> 1) & 1], tc::pair(tc::ex2(y.x), tc::ex2(y.y)));
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float y = tc::ex2(__uint_as_float(s[j]) * scale);
-                                sum[j & 3] += 32 * e + j >= from && 32 * e + j < rows ? y : 0.f;
-                            }
-                        }
-                    }
-                    const float2 even = tc::unpair(sum2[0]), odd = tc::unpair(sum2[1]);
-                    total += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((even.x + even.y) + (odd.x + odd.y));
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.s_free[g]);
-                }
-                if (!ok) break;
-                if (mine > 0) {   // to the group that has the unit's first query tile
-                    ok = sent == 0 || wait_or_abort(&bar.part_free[g], (sent - 1) & 1, aborted, status);
-                    if (!ok) break;
-                    parts[g][r] = total;
-                    ++sent;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.part_full[g]);
-                    continue;
-                }
-#pragma unroll
-                for (int o = 1; o < kGroups; ++o) {
-                    if (o >= m) break;
-                    const int from = (g + o) & (kGroups - 1);
-                    ok = wait_or_abort(&bar.part_full[from], (before >> from) & 1, aborted, status);
-                    if (!ok) break;
-                    total += parts[from][r];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.part_free[from]);
-                }
-                if (!ok) break;
-                if (x.slot >= 0) a.part_w[static_cast<int64_t>(x.slot) * kTile + r] = total;
-                else if (weight) *weight = old + total;
+                tile += x.nu;
+                continue;
             }
+            tile += m;
+            const uint32_t before = flips;
+#pragma unroll
+            for (int o = 1; o < kGroups; ++o)
+                if (o < m) flips ^= 1u << ((owner + o) & (kGroups - 1));
+            if (mine >= m) continue;
+            Weight w;
+            if (mine == 0) w = look(p);
+            float total = 0.f;
+            for (int q = mine; q < m && ok; q += kGroups) total += sum_tile(0, p, q);
+            if (!ok) break;
+            if (mine > 0) {   // to the group that has the unit's first query tile
+                ok = sent == 0 || wait_or_abort(&bar.part_free[g], (sent - 1) & 1, aborted, status);
+                if (!ok) break;
+                parts[g][r] = total;
+                ++sent;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.part_full[g]);
+                continue;
+            }
+#pragma unroll
+            for (int o = 1; o < kGroups; ++o) {
+                if (o >= m) break;
+                const int from = (g + o) & (kGroups - 1);
+                ok = wait_or_abort(&bar.part_full[from], (before >> from) & 1, aborted, status);
+                if (!ok) break;
+                total += parts[from][r];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.part_free[from]);
+            }
+            if (ok) finish(w, total);
         } while (ok && !x.last);
     }
     __syncwarp();
