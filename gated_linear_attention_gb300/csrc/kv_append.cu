@@ -11,6 +11,13 @@ namespace {
 
 constexpr int kThreads = 256, kTokens = 8;
 
+// x / s, correctly rounded where an e4m3 value comes of it (Markstein: with r the correctly rounded 1 / s, one correction
+// q + (x - q s) r of q = x r rounds correctly). What lies past 2^10 is clamped anyway; infinities and NaN stay.
+__device__ __forceinline__ float divided(float x, float s, float r) {
+    const float q = x * r;
+    return fabsf(q) <= 1024.f ? fmaf(fmaf(-q, s, x), r, q) : q;
+}
+
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvArgs c, const uint16_t *__restrict__ k,
                                                              int64_t k_stride, const uint16_t *__restrict__ v,
@@ -43,6 +50,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvArgs c, con
     }
     const float *scales = value ? c.v_scale : c.k_scale;
     const float s = E4M3 && scales ? __ldg(scales + h) : 1.f;
+    const float inverse = __frcp_rn(s);
     uint8_t *dst = value ? c.v : c.k;
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
@@ -54,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvArgs c, con
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 f = bf16x2_to_float2(w[j]);
-                b[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s)), __NV_SATFINITE, __NV_E4M3);
+                b[j] = __nv_cvt_float2_to_fp8x2(make_float2(divided(f.x, s, inverse), divided(f.y, s, inverse)), __NV_SATFINITE, __NV_E4M3);
             }
             *reinterpret_cast<uint2 *>(dst + to * kD + part * 8) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
         } else {

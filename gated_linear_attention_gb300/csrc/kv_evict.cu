@@ -67,7 +67,29 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const KvArgs c, 
         const int page = kv::page_of(c, n, i);
         return page < 0 ? 0u : key_of(c.weights[kv::row_of(c, page, h, i)]);
     };
-    for (int i = s + tid; i < min(e, s + kCached); i += kSelThreads) keys[i - s] = load(i);
+    constexpr int kAtOnce = 8;   // lookups in flight: pages first, then weights
+    for (int b = s; b < min(e, s + kCached); b += kAtOnce * kSelThreads) {
+        int page[kAtOnce];
+        float w[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = b + u * kSelThreads + tid;
+            page[u] = i < min(e, s + kCached) ? __ldg(c.table + n * c.W + (i >> c.log_S)) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = b + u * kSelThreads + tid;
+            if (i >= min(e, s + kCached)) break;
+            const bool known = page[u] >= 0 && page[u] < c.P;
+            if (!known) record_status(c.status, SALA_ERR_BAD_INDEX);
+            w[u] = known ? c.weights[kv::row_of(c, page[u], h, i)] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int i = b + u * kSelThreads + tid;
+            if (i < min(e, s + kCached)) keys[i - s] = key_of(w[u]);
+        }
+    }
     __syncthreads();
     auto key = [&](int i) -> uint32_t { return i - s < kCached ? keys[i - s] : load(i); };
 

@@ -631,54 +631,77 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
 
 // ---- joins the partial results of units that several CTAs share -----------------------------------
 
-constexpr int kJoinThreads = 256, kJoinRows = 8;   // a warp a row
+// A warp a row, or (few rows, as with one token on a long cache that all CTAs share) four warps with a quarter of the
+// parts each, whose loads would follow one another in one: 16 rows of 32 parts 13 us and 9; units of 256 rows 20 us
+// and 98 the other way round.
+constexpr int kJoinRows = 8;
 
-__global__ void __launch_bounds__(kJoinThreads) paged_combine_kernel(const AttendArgs a) {
+template <int kJoinSplit>
+__global__ void __launch_bounds__(32 * kJoinRows * kJoinSplit) paged_combine_kernel(const AttendArgs a) {
+    __shared__ float4 sums[kJoinRows][kJoinSplit][32];
+    __shared__ float totals[kJoinRows][kJoinSplit];
     dependent_start();
     const KvArgs &c = a.c;
-    const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = warp / kJoinSplit, s = warp % kJoinSplit;
     const JoinUnit x = static_cast<const JoinUnit *>(a.joins)[cta];
-    const int parts = x.parts, row = blockIdx.y * kJoinRows + warp, t = row / kTile, rr = row - t * kTile;
+    const int parts = x.parts, row = blockIdx.y * kJoinRows + k, t = row / kTile, rr = row - t * kTile;
+    if (parts == 0) return;
     const int tok = t * a.TB + rr / a.G;
-    if (parts == 0 || rr >= a.TB * a.G || tok >= x.ntok) return;
-    const float vs = c.v_scale ? __ldg(c.v_scale + x.h) : 1.f;
-    {
+    const bool valid = rr < a.TB * a.G && tok < x.ntok;
+    float at = 0.f;
+    if (valid) {
         float top = -INFINITY;
         for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_ml[part_slot(cta, p) * kRows + row].x);
         for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float at = top == -INFINITY ? 0.f : top;
+        at = top == -INFINITY ? 0.f : top;
         float total = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = 0; p0 < parts; p0 += 32) {
+        for (int p0 = s; p0 < parts; p0 += 32 * kJoinSplit) {   // parts s, s + 4, ..: lane l has the l-th of these
             float f = 0.f, l = 0.f;
-            if (p0 + lane < parts) {
-                const float2 ml = a.part_ml[part_slot(cta, p0 + lane) * kRows + row];
+            const int mine = p0 + lane * kJoinSplit;
+            if (mine < parts) {
+                const float2 ml = a.part_ml[part_slot(cta, mine) * kRows + row];
                 f = ml.x == -INFINITY ? 0.f : tc::ex2(ml.x - at);
                 l = ml.y * f;
             }
             for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
             total += l;
-            const int here = min(32, parts - p0);
+            const int here = min(32, (parts - p0 + kJoinSplit - 1) / kJoinSplit);
 #pragma unroll 8
-            for (int p = 0; p < here; ++p) {
-                const float w = __shfl_sync(0xffffffffu, f, p);
-                const float4 v = *reinterpret_cast<const float4 *>(a.part_o + (part_slot(cta, p0 + p) * kRows + row) * kD + lane * 4);
+            for (int i = 0; i < here; ++i) {
+                const float w = __shfl_sync(0xffffffffu, f, i);
+                const float4 v = *reinterpret_cast<const float4 *>(
+                    a.part_o + (part_slot(cta, p0 + i * kJoinSplit) * kRows + row) * kD + lane * 4);
                 acc.x += w * v.x;
                 acc.y += w * v.y;
                 acc.z += w * v.z;
                 acc.w += w * v.w;
             }
         }
-        const bool some = x.limit + tok >= 0;
-        const float inv = vs / total;
-        const int64_t out = (x.row + tok) * (a.G * c.H) + x.h * a.G + rr % a.G;
-        *reinterpret_cast<uint2 *>(a.o + out * kD + lane * 4) =
-            some ? make_uint2(float2_to_bf16x2(acc.x * inv, acc.y * inv), float2_to_bf16x2(acc.z * inv, acc.w * inv))
-                 : make_uint2(0, 0);
-        if (lane == 0) {
-            if (a.lse) a.lse[out] = some ? (at + log2f(total)) * kLn2 : -INFINITY;
-            if (a.stats) a.stats[out] = at + log2f(total);
-        }
+        sums[k][s][lane] = acc;
+        if (lane == 0) totals[k][s] = total;
+    }
+    __syncthreads();
+    if (!valid || s != 0) return;
+    float total = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kJoinSplit; ++i) {
+        const float4 v = sums[k][i][lane];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        total += totals[k][i];
+    }
+    const bool some = x.limit + tok >= 0;
+    const float vs = c.v_scale ? __ldg(c.v_scale + x.h) : 1.f, inv = vs / total;
+    const int64_t out = (x.row + tok) * (a.G * c.H) + x.h * a.G + rr % a.G;
+    *reinterpret_cast<uint2 *>(a.o + out * kD + lane * 4) =
+        some ? make_uint2(float2_to_bf16x2(acc.x * inv, acc.y * inv), float2_to_bf16x2(acc.z * inv, acc.w * inv)) : make_uint2(0, 0);
+    if (lane == 0) {
+        if (a.lse) a.lse[out] = some ? (at + log2f(total)) * kLn2 : -INFINITY;
+        if (a.stats) a.stats[out] = at + log2f(total);
     }
 }
 
@@ -838,7 +861,9 @@ cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_str
         // rows that a unit can have
         const int64_t tokens = c.cu ? c.T : c.T_row;
         const int rows = tokens <= a.TB ? static_cast<int>(tokens) * G : Q * kTile;
-        e = launch_dependent(paged_combine_kernel, dim3(sm_count, (rows + kJoinRows - 1) / kJoinRows), kJoinThreads, st, a);
+        const dim3 grid(sm_count, (rows + kJoinRows - 1) / kJoinRows);
+        e = rows <= 32 ? launch_dependent(paged_combine_kernel<4>, grid, 32 * kJoinRows * 4, st, a)
+                       : launch_dependent(paged_combine_kernel<1>, grid, 32 * kJoinRows, st, a);
         if (e != cudaSuccess || !accumulate) return e;
     }
     return launch_paged_weights(a, maps, sm_count, st);

@@ -336,17 +336,29 @@ __device__ __forceinline__ Sums row_sums(const LogprobArgs &a, int64_t n, int la
     return s;
 }
 
+// A thread's first given token of a row and its logit, loaded before the row's sums are there.
+struct Asked {
+    int token;
+    float logit;
+};
+template <typename T>
+__device__ __forceinline__ Asked ask(const LogprobArgs &a, int64_t n, int j) {
+    Asked y{-1, 0.f};
+    if (j < a.M) y.token = __ldg(a.tokens + n * a.M + j);
+    if (y.token >= 0 && y.token < a.V) y.logit = logit(static_cast<const T *>(a.x) + n * a.stride + y.token);
+    return y;
+}
+
 // The entropy and the given tokens' log probabilities of a row, by `threads` threads from 0.
 template <typename T>
-__device__ __forceinline__ void row_results(const LogprobArgs &a, int64_t n, const Sums &s, int id, int threads) {
+__device__ __forceinline__ void row_results(const LogprobArgs &a, int64_t n, const Sums &s, Asked y, int id, int threads) {
     const bool none = s.m == -INFINITY;
     const float logl = logf(s.l);
     if (id == 0 && a.entropy) a.entropy[n] = none ? 0.f : fmaxf(0.f, logl - s.w / s.l);
-    const T *row = static_cast<const T *>(a.x) + n * a.stride;
     for (int j = id; j < a.M; j += threads) {
-        const int t = __ldg(a.tokens + n * a.M + j);
-        if (t >= a.V) record_status(a.status, SALA_ERR_BAD_INDEX);
-        a.logprobs[n * a.M + j] = t < 0 || t >= a.V ? 0.f : none ? -INFINITY : (logit(row + t) - s.m) - logl;
+        if (j != id) y = ask<T>(a, n, j);
+        if (y.token >= a.V) record_status(a.status, SALA_ERR_BAD_INDEX);
+        a.logprobs[n * a.M + j] = y.token < 0 || y.token >= a.V ? 0.f : none ? -INFINITY : (y.logit - s.m) - logl;
     }
 }
 
@@ -356,7 +368,9 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(const LogprobArg
     dependent_start();
     const int lane = threadIdx.x & 31;
     const int64_t n = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (n < a.N) row_results<T>(a, n, row_sums(a, n, lane), lane, 32);
+    if (n >= a.N) return;
+    const Asked y = ask<T>(a, n, lane);
+    row_results<T>(a, n, row_sums(a, n, lane), y, lane, 32);
 }
 
 // With alternatives: a CTA a row.
@@ -370,8 +384,13 @@ __global__ void __launch_bounds__(kThreads) logprob_top_kernel(const LogprobArgs
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.K, lanes = a.parts * 32;
     const Row<T> row(a, n);
     const float *maxima = a.maxima + n * lanes;
-    uint32_t key = kNone;
-    for (int i = tid; i < lanes; i += kThreads) key = max(key, order_of(maxima[i]));
+    const Asked asked = ask<T>(a, n, tid);
+    constexpr int kMine = kMaxParts * 32 / kThreads;   // lanes of a thread, at most
+    uint32_t held[kMine], key = kNone;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) held[i] = tid + i * kThreads < lanes ? order_of(maxima[tid + i * kThreads]) : 0u;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) key = max(key, held[i]);
     if (warp == kWarps - 1) {
         const Sums s = row_sums(a, n, lane);
         if (lane == 0) sums = s;
@@ -379,9 +398,9 @@ __global__ void __launch_bounds__(kThreads) logprob_top_kernel(const LogprobArgs
     if (tid == 0) sh.count = sh.lanes = 0;
     const uint32_t lo = border_of(sh, key, K);
     const Sums s = sums;
-    row_results<T>(a, n, s, tid, kThreads);
-    for (int i = tid; i < lanes; i += kThreads)
-        if (order_of(maxima[i]) >= lo) sh.who[atomicAdd(&sh.lanes, 1)] = static_cast<uint16_t>(i);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        if (held[i] >= lo) sh.who[atomicAdd(&sh.lanes, 1)] = static_cast<uint16_t>(tid + i * kThreads);
     __syncthreads();
     // every element that reaches the border
     auto list = [&](float y, int i) {
@@ -391,17 +410,29 @@ __global__ void __launch_bounds__(kThreads) logprob_top_kernel(const LogprobArgs
         if (at < kList) sh.keys[at] = k, sh.index[at] = i;
     };
     const int per = (row.vectors / a.parts + 1 + 31) / 32, items = sh.lanes * per;
-#pragma unroll 4
-    for (int j = tid; j < items; j += kThreads) {
-        const int p = j / per, who = sh.who[p], part = who >> 5, v = row.begin(part) + (who & 31) + (j - p * per) * 32;
-        if (v < row.begin(part + 1)) {
-            Vec<T> x;
-            x.load(row.body + static_cast<int64_t>(v) * kN);
+    constexpr int kAtOnce = 8;   // loads in flight
+    for (int j0 = 0; j0 < items; j0 += kAtOnce * kThreads) {
+        Vec<T> x[kAtOnce];
+        int at[kAtOnce];
 #pragma unroll
-            for (int e = 0; e < kN; ++e) list(clean(x.at(e)), row.token(v, e));
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int j = j0 + u * kThreads + tid;
+            at[u] = -1;
+            if (j < items) {
+                const int p = j / per, who = sh.who[p], part = who >> 5, v = row.begin(part) + (who & 31) + (j - p * per) * 32;
+                if (v < row.begin(part + 1)) at[u] = v;
+            }
+            if (at[u] >= 0) x[u].load(row.body + static_cast<int64_t>(at[u]) * kN);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            if (at[u] < 0) continue;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) list(clean(x[u].at(e)), row.token(at[u], e));
         }
     }
     if (tid < 32 && row.end_element(tid) >= 0) list(logit(row.row + row.end_element(tid)), row.end_element(tid));
+    row_results<T>(a, n, s, asked, tid, kThreads);
     __syncthreads();
     const int listed = sh.count;
     if (listed <= kList) {
