@@ -304,12 +304,13 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             if (tc::elect_one()) {
                 const uint32_t id = tc::idesc_bf16_f32(128, (rows + 15) & ~15, 0, 0), d = tmem + b.at * kTile;
                 const uint64_t dk = first_k + k.at * (kTileBytes >> 4), dq = first_q + q.at * (kTileBytes >> 4);
-                tc::umma_bf16(d, ones, first_aux + q.at * (kAuxBytes >> 4), id, 0u);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
-                    tc::umma_bf16(d, dk + off, dq + off, id, 1u);
+                    tc::umma_bf16(d, dk + off, dq + off, id, i > 0);
                 }
+                // last: what it leaves is small, and the score before it has the attention's own roundings
+                tc::umma_bf16(d, ones, first_aux + q.at * (kAuxBytes >> 4), id, 1u);
                 commit_at(s_full + 8 * b.at);
                 if (last) commit_at(q_empty + 8 * q.at);
                 if (keys_last) commit_at(k_empty + 8 * k.at);
