@@ -602,37 +602,40 @@ class KvCache:
     the running attention weights that eviction goes by, or None. Holds the tensors, copies nothing;
     their contents (lengths, tables, pages) may change between calls, ``kv_lens`` and ``block_table``
     may be replaced by :meth:`with_requests`."""
-    __slots__ = ("k_pages", "v_pages", "block_table", "kv_lens", "k_scale", "v_scale", "weights", "N", "H", "_c")
+    __slots__ = ("k_pages", "v_pages", "block_table", "kv_lens", "k_scale", "v_scale", "weights", "N", "H", "_c", "_ref")
 
     def __init__(self, k_pages, v_pages, block_table, kv_lens, k_scale=None, v_scale=None, weights=None):
         if not isinstance(k_pages, torch.Tensor):
             raise TypeError("k_pages must be a torch.Tensor")
-        dt = k_pages.dtype
+        dt, shape = k_pages.dtype, k_pages.shape
         if dt not in (torch.bfloat16, torch.float8_e4m3fn):
             raise TypeError(f"k_pages must be bfloat16 or float8_e4m3fn, got {dt}")
-        if k_pages.dim() != 4 or k_pages.shape[3] != 128 or k_pages.shape[2] not in (16, 32, 64, 128, 256):
-            raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, expected (pages, heads, 16 .. 256, 128)")
+        if len(shape) != 4 or shape[3] != 128 or shape[2] not in (16, 32, 64, 128, 256):
+            raise ValueError(f"k_pages has shape {tuple(shape)}, expected (pages, heads, 16 .. 256, 128)")
         _need(k_pages, "k_pages", dt)
-        _need(v_pages, "v_pages", dt, k_pages.shape)
-        P, H, S, _ = k_pages.shape
+        _need(v_pages, "v_pages", dt, shape)
+        P, H, S, _ = shape
         if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
             raise ValueError("block_table must be a tensor [N, width]")
         _need(block_table, "block_table", torch.int32)
         N, W = block_table.shape
         _need(kv_lens, "kv_lens", torch.int32, (N,))
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t is not None:
-                if dt == torch.bfloat16:
-                    raise ValueError(f"{name} is for float8_e4m3fn pages")
-                _need(t, name, torch.float32, (H,))
+        bf16 = dt == torch.bfloat16
+        if k_scale is not None or v_scale is not None:
+            if bf16:
+                raise ValueError("k_scale and v_scale are for float8_e4m3fn pages")
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if t is not None:
+                    _need(t, name, torch.float32, (H,))
         if weights is not None:
             _need(weights, "weights", torch.float32, (P, H, S))
         _one_device(k_pages, v_pages, block_table, kv_lens, k_scale, v_scale, weights)
         self.k_pages, self.v_pages, self.block_table, self.kv_lens = k_pages, v_pages, block_table, kv_lens
         self.k_scale, self.v_scale, self.weights, self.N, self.H = k_scale, v_scale, weights, N, H
-        self._c = KvCacheStruct(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(weights),
-                                _ptr(block_table), _ptr(kv_lens), P, W, S, H,
-                                SALA_KV_BF16 if dt == torch.bfloat16 else SALA_KV_E4M3)
+        self._c = KvCacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scale), _ptr(v_scale), _ptr(weights),
+                                block_table.data_ptr(), kv_lens.data_ptr(), P, W, S, H,
+                                SALA_KV_BF16 if bf16 else SALA_KV_E4M3)
+        self._ref = ctypes.byref(self._c)
 
     def with_requests(self, block_table, kv_lens):
         """The same pages with another batch's table and lengths."""
@@ -640,28 +643,38 @@ class KvCache:
 
 
 def _one_device(*tensors):
-    """The library launches on the current device; all tensors of a call have to lie there."""
-    dev = torch.cuda.current_device()
+    """The library launches on the current device; all tensors of a call have to lie there. Returns it."""
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor lies on {t.device}, the current device is cuda:{dev}")
+    return dev
+
+
+def _stream_on(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _new_tokens(x, name, cache, heads, cu_seqlens):
     """Checks new tokens [N, T, heads, 128], or packed [T, heads, 128] with cu_seqlens, whose tokens
-    may lie apart at equal distances; returns (T, elements between tokens)."""
+    may lie apart at equal distances; returns (T, heads, elements between tokens)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if x.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
-    if x.dim() != (4 if cu_seqlens is None else 3) or x.shape[-1] != 128 or \
-            (heads is not None and x.shape[-2] != heads) or (cu_seqlens is None and x.shape[0] != cache.N):
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected "
+    shape = x.shape
+    if cu_seqlens is None:
+        ok = len(shape) == 4 and shape[0] == cache.N
+    else:
+        ok = len(shape) == 3
+        _need(cu_seqlens, "cu_seqlens", torch.int64, (cache.N + 1,))
+    if not ok or shape[-1] != 128 or (heads is not None and shape[-2] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected "
                          f"{'(%d, T, ' % cache.N if cu_seqlens is None else '(T, '}{heads or 'heads'}, 128)"
                          f"{'' if cu_seqlens is None else ' with cu_seqlens'}")
-    T, H = x.shape[-3], x.shape[-2]
+    T, H = shape[-3], shape[-2]
     ld = H * 128
     if not x.is_contiguous():
         tokens = T if cu_seqlens is not None else T * cache.N
@@ -670,22 +683,20 @@ def _new_tokens(x, name, cache, heads, cu_seqlens):
         if x.stride(-1) != 1 or (H > 1 and x.stride(-2) != 128) or ld < H * 128 or ld % 8 or \
                 (cu_seqlens is None and cache.N > 1 and T > 0 and x.stride(0) != T * ld):
             raise ValueError(f"{name} must have contiguous tokens at equal distances of a multiple of 8 elements")
-    if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", torch.int64, (cache.N + 1,))
-    return T, ld
+    return T, H, ld
 
 
 def kv_append(cache, k, v, cu_seqlens=None, stream=None):
     """Keys and values of new tokens into a :class:`KvCache`, ``sala_gla_kv_append``. k, v: bf16
     [N, T, Hkv, 128], or packed [T, Hkv, 128] with ``cu_seqlens`` (int64 [N + 1]); tokens may lie
     apart (slices of a fused projection). ``cache.kv_lens`` counts them already."""
-    T, k_ld = _new_tokens(k, "k", cache, cache.H, cu_seqlens)
-    Tv, v_ld = _new_tokens(v, "v", cache, cache.H, cu_seqlens)
+    T, _, k_ld = _new_tokens(k, "k", cache, cache.H, cu_seqlens)
+    Tv, _, v_ld = _new_tokens(v, "v", cache, cache.H, cu_seqlens)
     if T != Tv:
         raise ValueError("k and v differ in tokens")
-    _one_device(cache.k_pages, k, v, cu_seqlens)
-    rc = load().sala_gla_kv_append(ctypes.byref(cache._c), _ptr(k), k_ld, _ptr(v), v_ld, _ptr(cu_seqlens), cache.N,
-                                   T, _stream(stream))
+    dev = _one_device(cache.k_pages, k, v, cu_seqlens)
+    rc = load().sala_gla_kv_append(cache._ref, k.data_ptr(), k_ld, v.data_ptr(), v_ld, _ptr(cu_seqlens), cache.N, T,
+                                   _stream_on(stream, dev))
     _check(rc, "sala_gla_kv_append")
 
 
@@ -695,13 +706,12 @@ def paged_attention(q, cache, scale, cu_seqlens=None, accumulate=False, o=None, 
     (int64 [N + 1]); tokens may lie apart. ``accumulate`` adds each cached token's attention weight,
     summed over the new tokens and the heads of its group, to ``cache.weights``. Returns (o bf16, the
     shape of q; lse fp32 without the last dimension)."""
-    T, ld = _new_tokens(q, "q", cache, None, cu_seqlens)
-    Hq = q.shape[-2]
+    T, Hq, ld = _new_tokens(q, "q", cache, None, cu_seqlens)
     if Hq < 1 or Hq % cache.H or Hq // cache.H > 128:
         raise ValueError(f"{Hq} query heads do not divide over {cache.H} key/value heads (at most 128 on one)")
     if accumulate and cache.weights is None:
         raise ValueError("accumulate needs a cache with weights")
-    _one_device(cache.k_pages, q, cu_seqlens, o, lse)
+    dev = _one_device(cache.k_pages, q, cu_seqlens, o, lse)
     if o is None:
         o = _empty(q.shape, torch.bfloat16, q, stream)
     else:
@@ -710,8 +720,8 @@ def paged_attention(q, cache, scale, cu_seqlens=None, accumulate=False, o=None, 
         lse = _empty(q.shape[:-1], torch.float32, q, stream)
     else:
         _need(lse, "lse", torch.float32, q.shape[:-1])
-    rc = load().sala_gla_paged_attention(ctypes.byref(cache._c), _ptr(q), ld, float(scale), _ptr(cu_seqlens), _ptr(o),
-                                         _ptr(lse), 1 if accumulate else 0, cache.N, T, Hq, _stream(stream))
+    rc = load().sala_gla_paged_attention(cache._ref, q.data_ptr(), ld, scale, _ptr(cu_seqlens), o.data_ptr(),
+                                         lse.data_ptr(), 1 if accumulate else 0, cache.N, T, Hq, _stream_on(stream, dev))
     _check(rc, "sala_gla_paged_attention")
     return o, lse
 
@@ -723,7 +733,7 @@ def kv_evict(cache, budget, sinks=0, recent=0, new_lens=None, kept=None, stream=
     (new_lens int32 [N]; kept int32 [N, Hkv, budget]: former places, then -1)."""
     if cache.weights is None:
         raise ValueError("eviction needs a cache with weights")
-    _one_device(cache.k_pages, new_lens, kept)
+    dev = _one_device(cache.k_pages, new_lens, kept)
     shape = (cache.N, cache.H, max(0, int(budget)))
     if new_lens is None:
         new_lens = _empty((cache.N,), torch.int32, cache.k_pages, stream)
@@ -733,8 +743,8 @@ def kv_evict(cache, budget, sinks=0, recent=0, new_lens=None, kept=None, stream=
         kept = _empty(shape, torch.int32, cache.k_pages, stream)
     else:
         _need(kept, "kept", torch.int32, shape)
-    rc = load().sala_gla_kv_evict(ctypes.byref(cache._c), int(budget), int(sinks), int(recent), _ptr(new_lens),
-                                  _ptr(kept), cache.N, _stream(stream))
+    rc = load().sala_gla_kv_evict(cache._ref, int(budget), int(sinks), int(recent), new_lens.data_ptr(),
+                                  kept.data_ptr(), cache.N, _stream_on(stream, dev))
     _check(rc, "sala_gla_kv_evict")
     return new_lens, kept
 
@@ -761,7 +771,7 @@ def token_logprobs(logits, tokens=None, top=0, entropy=True, stream=None):
         _need(tokens, "tokens", torch.int32, (N, *tokens.shape[1:]))
         M = tokens.shape[1] if tokens.dim() == 2 else 1
         logprobs = _empty(tokens.shape, torch.float32, logits, stream)
-    _one_device(logits, tokens)
+    dev = _one_device(logits, tokens)
     if entropy:
         ent = _empty((N,), torch.float32, logits, stream)
     if top:
@@ -769,7 +779,7 @@ def token_logprobs(logits, tokens=None, top=0, entropy=True, stream=None):
         values = _empty((N, max(0, int(top))), torch.float32, logits, stream)
     rc = load().sala_gla_token_logprobs(_ptr(logits), ld, SALA_PROB_BF16 if dt == torch.bfloat16 else SALA_PROB_F32,
                                         _ptr(tokens) if M else None, _ptr(logprobs) if M else None, _ptr(ent), _ptr(ids),
-                                        _ptr(values), N, V, M, int(top), _stream(stream))
+                                        _ptr(values), N, V, M, int(top), _stream_on(stream, dev))
     _check(rc, "sala_gla_token_logprobs")
     return logprobs, ent, ids, values
 
