@@ -71,7 +71,7 @@ struct Barriers {
     uint64_t raw_full[6], raw_empty[6];         // e4m3 cache tiles
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t q_full, q_free;
-    uint64_t s_full[2], p_full[2], o_full[2], o_free[2], join;
+    uint64_t s_full[2], p_full[2], p_rest[2], o_full[2], o_free[2], join;   // P: its first 64 places, the others
     uint64_t drain;
 };
 
@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
         for (int t = 0; t < 2; ++t) {
             tc::mbar_init(&bar.s_full[t], 1);
             tc::mbar_init(&bar.p_full[t], kMmaWarp / 2);
+            tc::mbar_init(&bar.p_rest[t], kMmaWarp / 2);
             tc::mbar_init(&bar.o_full[t], 2);
             tc::mbar_init(&bar.o_free[t], kMmaWarp / 2);
         }
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
         // ---- products ------------------------------------------------------------------------------
         constexpr int S = Layout::kStages;
         const uint32_t full = tc::smem_u32(bar.full), empty = tc::smem_u32(bar.empty), s_full = tc::smem_u32(bar.s_full);
-        const uint32_t p_full = tc::smem_u32(bar.p_full), o_full = tc::smem_u32(bar.o_full), o_free = tc::smem_u32(bar.o_free);
+        const uint32_t p_full = tc::smem_u32(bar.p_full), p_rest = tc::smem_u32(bar.p_rest), o_full = tc::smem_u32(bar.o_full), o_free = tc::smem_u32(bar.o_free);
         const uint32_t q_free = tc::smem_u32(&bar.q_free), q_full = tc::smem_u32(&bar.q_full);
         const uint64_t first_k = desc_k(base), first_mn = desc_mn(base + kQ * kTileBytes);   // of the first tile, the first stage
         uint32_t items = 0, p_parity = 0, o_used = 0, o_parity = 3;   // a bit for each group
@@ -299,17 +300,22 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                 o_used |= 1u << t;
                 o_parity ^= 1u << t;
             }
-            p_parity ^= 1u << t;
-            tc::tc_fence_after();
-            if (tc::elect_one()) {
-                const uint64_t dv = first_mn + stage * (kTileBytes >> 4);
+            // the first 64 places' products go while the others' weights are made
+            const uint64_t dv = first_mn + stage * (kTileBytes >> 4);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    tc::umma_bf16_ta(tmem + kO0 + t * kTile, tmem + kS0 + t * kTile + 8 * ks, dv + ks * (2048 >> 4), kIdO,
-                                     !first || ks > 0);
-                if (final) commit_at(o_full + 8 * t);
+            for (int part = 0; part < 2; ++part) {
+                if (part == 1 && !passed(p_rest + 8 * t, p_parity >> t & 1)) return false;
+                tc::tc_fence_after();
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
+                        tc::umma_bf16_ta(tmem + kO0 + t * kTile, tmem + kS0 + t * kTile + 8 * ks, dv + ks * (2048 >> 4), kIdO,
+                                         !first || ks > 0);
+                    if (part == 1 && final) commit_at(o_full + 8 * t);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            p_parity ^= 1u << t;
             return true;
         };
         // Clears the rows of V that no token sees, and infinities and NaN in those that not all tokens see: true if any
@@ -513,6 +519,12 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                             pk[j] = float2_to_bf16x2(e0, e1);
                         }
                         tmem_st_16x32bx2_x16<16>(ts + 32 * q, pk);   // P over the left half of S, which both lanes have read
+                        if (q == 0) {
+                            tc::tmem_st_wait();
+                            tc::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar.p_full[t]);
+                        }
                     }
                     const float2 even = tc::unpair(sum2[0]), odd = tc::unpair(sum2[1]);
                     l += (even.x + even.y) + (odd.x + odd.y);
@@ -521,7 +533,10 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                 fresh = false;
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_full[t]);
+                if (lane == 0) {
+                    if (!active) mbar_arrive(&bar.p_full[t]);
+                    mbar_arrive(&bar.p_rest[t]);
+                }
             }
             if (!ok) break;
             if (active) l += __shfl_xor_sync(0xffffffffu, l, 16);
