@@ -356,25 +356,53 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                 commit(empty + 8 * k.at);
                 k.advance(2);
                 if (n == 1) commit(q_free);
-                for (int i = 0; i < n; ++i) {
+                for (int i = 0; i < n && ok; ++i) {
                     const bool more = i + 1 < n;
-                    ok = passed(full + 8 * v.at, v.parity);
-                    if (!ok) break;
+                    // The keys are waited for before the products: nothing but issues lies between those and the next
+                    // scores. A wait that gave up is noted, and voted on once a tile.
+                    bool fine = wait_at(full + 8 * v.at, v.parity, aborted, status);
                     if (i >= whole) bad |= clean(shared_from, end, t0 + i, v.at);
-                    ok = products(0, v.at, i == 0, !more) && (!more || passed(full + 8 * k.at, k.parity));
-                    if (!ok) break;
-                    if (more) scores(0, 0, k.at);
-                    ok = products(1, v.at, i == 0, !more);
-                    if (!ok) break;
-                    if (more) scores(1, 1, k.at);
-                    if (tc::elect_one()) {
-                        commit_at(empty + 8 * v.at);
-                        if (more) commit_at(empty + 8 * k.at);
-                        if (i + 2 == n) commit_at(q_free);
+                    if (more) fine &= wait_at(full + 8 * k.at, k.parity, aborted, status);
+                    const uint64_t dv = first_mn + v.at * (kTileBytes >> 4), dk = first_k + (kQ + k.at) * (kTileBytes >> 4);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t d = tmem + kO0 + t * kTile, ps = tmem + kS0 + t * kTile, pp = p_parity >> t & 1;
+                        if (i == 0 && (o_used >> t & 1)) fine &= wait_at(o_free + 8 * t, o_parity >> t & 1, aborted, status);
+                        fine &= wait_at(p_full + 8 * t, pp, aborted, status);
+                        tc::tc_fence_after();
+                        if (tc::elect_one()) {
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                tc::umma_bf16_ta(d, ps + 8 * ks, dv + ks * (2048 >> 4), kIdO, i > 0 || ks > 0);
+                        }
+                        fine &= wait_at(p_rest + 8 * t, pp, aborted, status);
+                        tc::tc_fence_after();
+                        if (tc::elect_one()) {
+#pragma unroll
+                            for (int ks = 4; ks < 8; ++ks) tc::umma_bf16_ta(d, ps + 8 * ks, dv + ks * (2048 >> 4), kIdO, 1u);
+                            if (more) {
+                                const uint64_t dq = first_k + t * (kTileBytes >> 4);
+#pragma unroll
+                                for (int ks = 0; ks < 8; ++ks) {
+                                    const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                                    tc::umma_bf16(ps, dq + off, dk + off, kIdS, ks > 0);
+                                }
+                                commit_at(s_full + 8 * t);
+                            } else {
+                                commit_at(o_full + 8 * t);
+                            }
+                            if (t == 1) {
+                                commit_at(empty + 8 * v.at);
+                                if (more) commit_at(empty + 8 * k.at);
+                                if (i + 2 == n) commit_at(q_free);
+                            }
+                        }
                     }
-                    __syncwarp();
+                    if (i == 0) o_used = 3, o_parity ^= 3u;
+                    p_parity ^= 3u;
                     v.advance(2);
                     if (more) k.advance(2);
+                    ok = __all_sync(0xffffffffu, fine) != 0;
                 }
             } else {     // one query tile: the groups take the cache tiles in turn
                 scores(0, 0, k.at);
