@@ -19,8 +19,8 @@ __device__ __forceinline__ float divided(float x, float s, float r) {
 }
 
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvArgs c, const uint16_t *__restrict__ k,
-                                                             int64_t k_stride, const uint16_t *__restrict__ v,
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvArgs c, const uint16_t *k,
+                                                             int64_t k_stride, const uint16_t *v,
                                                              int64_t v_stride) {
     dependent_start();
     if (blockIdx.x == 0 && c.cu)   // every pair of offsets is looked at, those without tokens too
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvArgs c, con
     uint4 x[kTokens];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i)
-        x[i] = t0 + i < c.T ? __ldg(reinterpret_cast<const uint4 *>(src + i * stride)) : make_uint4(0, 0, 0, 0);
+        x[i] = t0 + i < c.T ? *reinterpret_cast<const uint4 *>(src + i * stride) : make_uint4(0, 0, 0, 0);
     int64_t row = -1;   // of the token t0 + lane; -1: it has none
     if (lane < kTokens && t0 + lane < c.T) {
         const int64_t n = kv::request_of(c, t0 + lane);
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvArgs c, con
         if (c.weights && row >= 0) c.weights[row] = 0.f;
     }
     const float *scales = value ? c.v_scale : c.k_scale;
-    const float s = E4M3 && scales ? __ldg(scales + h) : 1.f;
+    const float s = E4M3 && scales ? kv::load(scales + h) : 1.f;
     const float inverse = __frcp_rn(s);
     uint8_t *dst = value ? c.v : c.k;
 #pragma unroll

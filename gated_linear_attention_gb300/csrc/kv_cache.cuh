@@ -9,6 +9,25 @@
 namespace sala {
 namespace kv {
 
+// A word of an input. A kernel that starts as a programmatic dependent is resident while the work before it may still write
+// its inputs, so they are read by plain loads (the read-only path asks for data that stays as it is for the kernel's
+// life), which keep their order to the kernel-wide wait and may pass the stores and records of the kernel itself.
+__device__ __forceinline__ int32_t load(const int32_t *p) {
+    int32_t r;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ int64_t load(const int64_t *p) {
+    int64_t r;
+    asm volatile("ld.global.s64 %0, [%1];" : "=l"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ float load(const float *p) {
+    float r;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(r) : "l"(p));
+    return r;
+}
+
 // One request of a call: its new tokens [first, first + count) and its places [0, len). A malformed
 // pair of offsets or length is recorded, and the request then has no tokens or no places.
 struct Request {
@@ -17,7 +36,7 @@ struct Request {
 };
 
 __device__ __forceinline__ int request_len(const KvArgs &c, int64_t n) {
-    const int len = __ldg(c.lens + n);
+    const int len = load(c.lens + n);
     if (len >= 0 && len <= c.W * c.S) return len;
     record_status(c.status, SALA_ERR_BAD_INDEX);
     return 0;
@@ -28,7 +47,7 @@ __device__ __forceinline__ Request request(const KvArgs &c, int64_t n) {
     r.first = n * c.T_row;
     r.count = static_cast<int>(c.T_row);
     if (c.cu) {
-        const int64_t a = __ldg(c.cu + n), b = __ldg(c.cu + n + 1);
+        const int64_t a = load(c.cu + n), b = load(c.cu + n + 1);
         const bool ok = a >= 0 && b >= a && b <= c.T;
         if (!ok) record_status(c.status, SALA_ERR_BAD_SEQLENS);
         r.first = ok ? a : 0;
@@ -44,7 +63,7 @@ __device__ __forceinline__ int64_t request_of(const KvArgs &c, int64_t t) {
     int64_t lo = 0, hi = c.N;   // cu[lo] <= t < cu[hi] where the offsets are well formed
     while (hi - lo > 1) {
         const int64_t mid = (lo + hi) / 2;
-        if (__ldg(c.cu + mid) <= t) lo = mid;
+        if (load(c.cu + mid) <= t) lo = mid;
         else hi = mid;
     }
     return lo;
@@ -52,7 +71,7 @@ __device__ __forceinline__ int64_t request_of(const KvArgs &c, int64_t t) {
 
 // The page of place i of request n (its length covers i), or -1 where the table holds none.
 __device__ __forceinline__ int page_of(const KvArgs &c, int64_t n, int i) {
-    const int p = __ldg(c.table + n * c.W + (i >> c.log_S));
+    const int p = load(c.table + n * c.W + (i >> c.log_S));
     if (p >= 0 && p < c.P) return p;
     record_status(c.status, SALA_ERR_BAD_INDEX);
     return -1;

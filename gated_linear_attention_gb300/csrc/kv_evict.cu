@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const KvArgs c, 
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
             const int i = b + u * kSelThreads + tid;
-            page[u] = i < min(e, s + kCached) ? __ldg(c.table + n * c.W + (i >> c.log_S)) : -1;
+            page[u] = i < min(e, s + kCached) ? kv::load(c.table + n * c.W + (i >> c.log_S)) : -1;
         }
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
@@ -157,23 +157,24 @@ __device__ __forceinline__ void move_rows(const KvArgs &c, int64_t n, int h, con
     base += offset + threadIdx.x % per_row * 16;
     for (int b = first; b < count; b += rows * kEach) {
         uint4 x[kEach];
-        uint8_t *to[kEach];
+        int src[kEach], to[kEach];   // pages of row i; -1: it stays as it is
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-            const int i = b + row0 + e * rows, src = i < count ? __ldg(kept + i) : -1;
-            to[e] = nullptr;
-            if (src >= 0 && src != i) {
-                const int p = kv::page_of(c, n, src), q = kv::page_of(c, n, i);
-                if (p >= 0 && q >= 0) {
-                    x[e] = *reinterpret_cast<const uint4 *>(base + kv::row_of(c, p, h, src) * row_bytes);
-                    to[e] = base + kv::row_of(c, q, h, i) * row_bytes;
-                }
-            }
+            const int i = b + row0 + e * rows;
+            src[e] = i < count ? kv::load(kept + i) : -1;
+        }
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int i = b + row0 + e * rows;
+            const bool moves = src[e] >= 0 && src[e] != i;
+            const int p = moves ? kv::page_of(c, n, src[e]) : -1;
+            to[e] = p >= 0 ? kv::page_of(c, n, i) : -1;
+            if (to[e] >= 0) x[e] = *reinterpret_cast<const uint4 *>(base + kv::row_of(c, p, h, src[e]) * row_bytes);
         }
         __syncthreads();   // every source of this block is read
 #pragma unroll
         for (int e = 0; e < kEach; ++e)
-            if (to[e]) *reinterpret_cast<uint4 *>(to[e]) = x[e];
+            if (to[e] >= 0) *reinterpret_cast<uint4 *>(base + kv::row_of(c, to[e], h, b + row0 + e * rows) * row_bytes) = x[e];
     }
 }
 
@@ -184,7 +185,7 @@ __device__ __forceinline__ void move_weights(const KvArgs &c, int64_t n, int h, 
         float *to[kEach];
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-            const int i = b + e * kMoveThreads + static_cast<int>(threadIdx.x), src = i < count ? __ldg(kept + i) : -1;
+            const int i = b + e * kMoveThreads + static_cast<int>(threadIdx.x), src = i < count ? kv::load(kept + i) : -1;
             to[e] = nullptr;
             if (src >= 0 && src != i) {
                 const int p = kv::page_of(c, n, src), q = kv::page_of(c, n, i);

@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
             const int limit = valid ? x.limit + my_tok : -1, first_limit = x.limit + my_tile * a.TB;
             // a warp without rows leaves its scores as they are: rows of a product do not mix
             const bool active = first_row < a.TB * a.G && my_tile * a.TB + first_row / a.G < x.ntok;
-            const float scale = a.scale * (c.k_scale ? __ldg(c.k_scale + x.h) : 1.f) * kLog2e;
+            const float scale = a.scale * (c.k_scale ? kv::load(c.k_scale + x.h) : 1.f) * kLog2e;
             float m = -INFINITY, l = 0.f;   // the maximum in units of the scores
             bool fresh = true;
             for (int i = x.t0 + (two ? 0 : t), t1 = x.t1; i < t1; i += step) {
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                 const bool whole = slot < 0, some = limit >= 0;   // some: the row sees a place
                 uint32_t dims[4] = {0, 0, 0, 0};
                 if (bad_values[t] && valid) bad_dimensions(c, x.n, x.h, x.limit, limit, dims);
-                const float vs = c.v_scale ? __ldg(c.v_scale + x.h) : 1.f;
+                const float vs = c.v_scale ? kv::load(c.v_scale + x.h) : 1.f;
                 const float inv = whole ? vs / l : 1.f;
                 const int64_t row = (x.row + my_tok) * (a.G * c.H) + x.h * a.G + r % a.G;
                 const int64_t prow = static_cast<int64_t>(slot) * kRows + my_tile * kTile + r;
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(32 * kJoinRows * kJoinSplit) paged_combine_ker
         total += totals[k][i];
     }
     const bool some = x.limit + tok >= 0;
-    const float vs = c.v_scale ? __ldg(c.v_scale + x.h) : 1.f, inv = vs / total;
+    const float vs = c.v_scale ? kv::load(c.v_scale + x.h) : 1.f, inv = vs / total;
     const int64_t out = (x.row + tok) * (a.G * c.H) + x.h * a.G + rr % a.G;
     *reinterpret_cast<uint2 *>(a.o + out * kD + lane * 4) =
         some ? make_uint2(float2_to_bf16x2(acc.x * inv, acc.y * inv), float2_to_bf16x2(acc.z * inv, acc.w * inv)) : make_uint2(0, 0);

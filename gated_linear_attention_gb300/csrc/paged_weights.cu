@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         do {
             ok = take(x);
             if (!ok) break;
-            const float inv = -1.f / (a.scale * (c.k_scale ? __ldg(c.k_scale + x.h) : 1.f) * kLog2e);
+            const float inv = -1.f / (a.scale * (c.k_scale ? kv::load(c.k_scale + x.h) : 1.f) * kLog2e);
             float next[4];
             auto fetch = [&](int q) {   // rows 32 e + lane of query tile q
                 const int rows = min(a.TB, x.ntok - q * a.TB) * a.G;
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         do {
             ok = take(x);
             if (!ok) break;
-            scale = a.scale * (c.k_scale ? __ldg(c.k_scale + x.h) : 1.f) * kLog2e;
+            scale = a.scale * (c.k_scale ? kv::load(c.k_scale + x.h) : 1.f) * kLog2e;
             const int m = x.nq, p = x.u0 * kTile + r, owner = tile % kGroups;
             const int mine = (g - owner) & (kGroups - 1);   // this group's first tile of the item
             if (m == 1) {        // every fourth cache tile; its weights are looked up a turn ahead

@@ -51,7 +51,7 @@ template <typename T>
 struct Vec {
     static constexpr int kN = 16 / sizeof(T);
     uint4 r;
-    __device__ __forceinline__ void load(const T *p) { r = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void load(const T *p) { r = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ float at(int i) const {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
@@ -66,8 +66,8 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 }
 template <typename T>
 __device__ __forceinline__ float logit(const T *p) {
-    if constexpr (sizeof(T) == 4) return clean(__ldg(p));
-    else return clean(bf16_bits_to_float(__ldg(p)));
+    if constexpr (sizeof(T) == 4) return clean(*p);
+    else return clean(bf16_bits_to_float(*p));
 }
 
 // Order-preserving whole numbers of floats without NaN; -0 is 0.
@@ -344,7 +344,7 @@ struct Asked {
 template <typename T>
 __device__ __forceinline__ Asked ask(const LogprobArgs &a, int64_t n, int j) {
     Asked y{-1, 0.f};
-    if (j < a.M) y.token = __ldg(a.tokens + n * a.M + j);
+    if (j < a.M) y.token = a.tokens[n * a.M + j];
     if (y.token >= 0 && y.token < a.V) y.logit = logit(static_cast<const T *>(a.x) + n * a.stride + y.token);
     return y;
 }

@@ -462,8 +462,8 @@ int sala_gla_state_pool_compact(void *pool, int32_t dtype, int64_t L, int64_t P,
  * page outside [0, num_pages) is recorded as SALA_ERR_BAD_INDEX and the outputs of its request are then
  * unspecified (no access leaves the tensors). Requests may share pages (a common prefix) in calls
  * that only read them; append, accumulate and evict write, and there a page that is written belongs
- * to one request. Pages, k, v, q and o are 16-byte aligned, cu_seqlens 8-byte and the other arrays
- * 4-byte aligned.
+ * to one request and to one entry of its row (else its contents are unspecified). Pages, k, v, q and
+ * o are 16-byte aligned, cu_seqlens 8-byte and the other arrays 4-byte aligned.
  */
 typedef enum { SALA_KV_BF16 = 0, SALA_KV_E4M3 = 1 } sala_kv_dtype;
 typedef struct {

@@ -8,7 +8,7 @@ import math
 import pytest
 import torch
 
-from paged_inputs import on_cpu, on_gpu
+from paged_inputs import bits, on_cpu, on_gpu
 
 pytestmark = pytest.mark.gpu
 SCALE = 128 ** -0.5
@@ -123,3 +123,40 @@ def test_a_captured_step_serves_growing_requests():
         g.kv_lens.copy_(ng)
         e.kv_lens.copy_(ne)
     assert torch.equal(g.kv_lens.cpu(), torch.tensor([12, 12, 12, 12], dtype=torch.int32)) and lib.get_device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_calls_in_a_row_read_what_the_call_before_wrote(kind):
+    """Calls that start while the one before them ends: evictions that write the lengths which the next calls go by, from
+    one buffer into the other, give the same bits as the same calls with the device idle between them."""
+    from gated_linear_attention_gb300 import sala_gla as lib
+    c = _cache(kind)
+    gen = torch.Generator().manual_seed(8)
+    for name in ("k_pages", "v_pages"):
+        c[name] = torch.randn(c[name].shape, generator=gen).to(c[name].dtype)
+    c["weights"] = torch.rand(c["weights"].shape, generator=gen)
+    c["lens"] = torch.tensor([190, 130, 70, 192], dtype=torch.int32)
+    q, k, v = (torch.randn(N, 3, h, 128, generator=gen).to(torch.bfloat16).cuda() for h in (HQ, H, H))
+
+    def chain(wait):
+        a = on_gpu(c)
+        b = a.with_requests(a.block_table, torch.zeros_like(a.kv_lens))
+        kept = torch.zeros(N, H, 176, dtype=torch.int32, device="cuda")
+        out = []
+        for i, budget in enumerate(range(176, 16, -16)):
+            now, after = (a, b) if i % 2 == 0 else (b, a)
+            for call in (lambda: lib.kv_append(now, k, v), lambda: lib.paged_attention(q, now, SCALE, accumulate=True),
+                         lambda: lib.kv_evict(now, budget, sinks=2, recent=5, new_lens=after.kv_lens,
+                                              kept=kept.view(-1)[:N * H * budget].view(N, H, budget))):
+                out.append(call())
+                if wait:
+                    torch.cuda.synchronize()
+            out.append(now.kv_lens)
+        torch.cuda.synchronize()
+        return [t for r in out if r is not None for t in (r if isinstance(r, tuple) else (r,)) if t.dtype != torch.int32] + \
+               [a.kv_lens, b.kv_lens, kept, bits(a.k_pages), bits(a.v_pages), a.weights]
+
+    want = chain(True)
+    for _ in range(10):
+        assert all(torch.equal(x, y) for x, y in zip(chain(False), want))
+    assert lib.get_device_status() == 0
