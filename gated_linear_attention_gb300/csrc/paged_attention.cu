@@ -18,8 +18,15 @@
 // Roles: two groups of eight warps turn scores into weights, one for each query tile (two lanes share a row), one warp
 // issues the products, one loads by TMA, a page (and half of the dimensions) a box. While one group has its
 // scores, the tensor core works for the other. A unit with one query tile gives its cache tiles to the groups in
-// turn, and the results are joined at its end. e4m3 tiles land in a ring of their own and four more warps
+// turn, and the results are joined at its end. e4m3 tiles land in a ring of their own and eight more warps
 // widen them (exactly) to bf16.
+//
+// Bounds, at 32 query heads on 2 key/value heads. 256 requests of one token on up to 12288 bf16 places: the cache's 2.15 GB,
+// 335 us = 6.4 TB/s. A chunk of 4096 tokens on 32768 places: 2.06 TFLOP in 1355 us = 1520 TFLOP/s, the products, which wait in
+// part for the exponentials (128 x 128 of them to 8.4 MFLOP) and run at the clock that the power limit leaves. 61 requests with 5
+// tokens on 8192 e4m3 places: 85 us against 40 for its bytes; the tiles pass shared memory three times more (read and
+// stored by the widening, read by the product). fp16 tiles, cheaper to widen, took longer (the queries then need a scale
+// for each row to stay in range). One token on 4001 places: 15 us of launch, split, one tile a CTA and join.
 //
 // What is masked never enters: scores are replaced, not added to, and V is cleared in the rows behind the unit's
 // last place (0 times a NaN there would be NaN). Rows of V that some tokens of the unit see and others do not are
@@ -674,77 +681,141 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
 
 // ---- joins the partial results of units that several CTAs share -----------------------------------
 
-// A warp a row, or (few rows, as with one token on a long cache that all CTAs share) four warps with a quarter of the
-// parts each, whose loads would follow one another in one: 16 rows of 32 parts 13 us and 9; units of 256 rows 20 us
-// and 98 the other way round.
-constexpr int kJoinRows = 8;
+// Few rows (one token on a long cache that all CTAs share, in many parts): a block has 8 rows, and four warps a quarter of
+// a row's parts each, whose loads would follow one another in one. Otherwise a warp has two rows, mostly in two to four
+// parts, whose statistics and values it loads at once. 16 rows of 32 parts take 13 us the second way and 9 the first, units
+// of 256 rows the other way round 98 us and 20. Of these the 40 MB of a chunk of 4096 tokens on 32768 places take 16 us
+// (26 with a row a warp and one load after the other, 19 with four rows).
+constexpr int kJoinWarps = 8, kJoinEach = 2;   // of a block, rows of a warp
 
 template <int kJoinSplit>
-__global__ void __launch_bounds__(32 * kJoinRows * kJoinSplit) paged_combine_kernel(const AttendArgs a) {
-    __shared__ float4 sums[kJoinRows][kJoinSplit][32];
-    __shared__ float totals[kJoinRows][kJoinSplit];
-    dependent_start();
-    const KvArgs &c = a.c;
-    const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = warp / kJoinSplit, s = warp % kJoinSplit;
-    const JoinUnit x = static_cast<const JoinUnit *>(a.joins)[cta];
-    const int parts = x.parts, row = blockIdx.y * kJoinRows + k, t = row / kTile, rr = row - t * kTile;
-    if (parts == 0) return;
-    const int tok = t * a.TB + rr / a.G;
-    const bool valid = rr < a.TB * a.G && tok < x.ntok;
-    float at = 0.f;
-    if (valid) {
-        float top = -INFINITY;
-        for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_ml[part_slot(cta, p) * kRows + row].x);
-        for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        at = top == -INFINITY ? 0.f : top;
-        float total = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = s; p0 < parts; p0 += 32 * kJoinSplit) {   // parts s, s + 4, ..: lane l has the l-th of these
-            float f = 0.f, l = 0.f;
-            const int mine = p0 + lane * kJoinSplit;
-            if (mine < parts) {
-                const float2 ml = a.part_ml[part_slot(cta, mine) * kRows + row];
-                f = ml.x == -INFINITY ? 0.f : tc::ex2(ml.x - at);
-                l = ml.y * f;
-            }
-            for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
-            total += l;
-            const int here = min(32, (parts - p0 + kJoinSplit - 1) / kJoinSplit);
-#pragma unroll 8
-            for (int i = 0; i < here; ++i) {
-                const float w = __shfl_sync(0xffffffffu, f, i);
-                const float4 v = *reinterpret_cast<const float4 *>(
-                    a.part_o + (part_slot(cta, p0 + i * kJoinSplit) * kRows + row) * kD + lane * 4);
-                acc.x += w * v.x;
-                acc.y += w * v.y;
-                acc.z += w * v.z;
-                acc.w += w * v.w;
-            }
-        }
-        sums[k][s][lane] = acc;
-        if (lane == 0) totals[k][s] = total;
-    }
-    __syncthreads();
-    if (!valid || s != 0) return;
-    float total = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kJoinSplit; ++i) {
-        const float4 v = sums[k][i][lane];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-        total += totals[k][i];
-    }
+__host__ __device__ constexpr int join_rows() { return kJoinSplit > 1 ? kJoinWarps : kJoinEach * kJoinWarps; }   // of a block
+
+// The results of row rr of query tile t: acc / total, its maximum.
+__device__ __forceinline__ void joined_row(const AttendArgs &a, const JoinUnit &x, int tok, int rr, int lane, float4 acc, float total,
+                                           float at) {
     const bool some = x.limit + tok >= 0;
-    const float vs = c.v_scale ? kv::load(c.v_scale + x.h) : 1.f, inv = vs / total;
-    const int64_t out = (x.row + tok) * (a.G * c.H) + x.h * a.G + rr % a.G;
+    const float vs = a.c.v_scale ? kv::load(a.c.v_scale + x.h) : 1.f, inv = vs / total;
+    const int64_t out = (x.row + tok) * (a.G * a.c.H) + x.h * a.G + rr % a.G;
     *reinterpret_cast<uint2 *>(a.o + out * kD + lane * 4) =
         some ? make_uint2(float2_to_bf16x2(acc.x * inv, acc.y * inv), float2_to_bf16x2(acc.z * inv, acc.w * inv)) : make_uint2(0, 0);
     if (lane == 0) {
         if (a.lse) a.lse[out] = some ? (at + log2f(total)) * kLn2 : -INFINITY;
         if (a.stats) a.stats[out] = at + log2f(total);
+    }
+}
+
+__device__ __forceinline__ void add_part(float4 &acc, float w, const float4 &v) {
+    acc.x += w * v.x;
+    acc.y += w * v.y;
+    acc.z += w * v.z;
+    acc.w += w * v.w;
+}
+
+// The sum over parts s, s + split, .. of a row, by a warp; `at`: the maximum over all parts.
+__device__ __forceinline__ void join_parts(const AttendArgs &a, int cta, int parts, int row, int s, int split, int lane, float4 *acc,
+                                           float *total, float *at) {
+    float top = -INFINITY;
+    for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_ml[part_slot(cta, p) * kRows + row].x);
+    for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    *at = top == -INFINITY ? 0.f : top;
+    *total = 0.f;
+    *acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = s; p0 < parts; p0 += 32 * split) {   // lane l has the statistics of the l-th of these
+        float f = 0.f, l = 0.f;
+        const int mine = p0 + lane * split;
+        if (mine < parts) {
+            const float2 ml = a.part_ml[part_slot(cta, mine) * kRows + row];
+            f = ml.x == -INFINITY ? 0.f : tc::ex2(ml.x - *at);
+            l = ml.y * f;
+        }
+        for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+        *total += l;
+        const int here = min(32, (parts - p0 + split - 1) / split);
+#pragma unroll 8
+        for (int i = 0; i < here; ++i)
+            add_part(*acc, __shfl_sync(0xffffffffu, f, i),
+                     *reinterpret_cast<const float4 *>(a.part_o + (part_slot(cta, p0 + i * split) * kRows + row) * kD + lane * 4));
+    }
+}
+
+// The token of a unit's row, -1: it has none.
+__device__ __forceinline__ int token_of(const AttendArgs &a, const JoinUnit &x, int row) {
+    const int rr = row % kTile, tok = row / kTile * a.TB + rr / a.G;
+    return rr < a.TB * a.G && tok < x.ntok ? tok : -1;
+}
+
+// Rows [row0, row0 + kJoinEach) of a unit in kParts parts, by a warp that has all of their loads in flight.
+template <int kParts>
+__device__ __forceinline__ void join_rows_at_once(const AttendArgs &a, const JoinUnit &x, int cta, int row0, int lane) {
+    float2 ml[kJoinEach][kParts];
+    float4 v[kJoinEach][kParts];
+#pragma unroll
+    for (int e = 0; e < kJoinEach; ++e)
+        if (token_of(a, x, row0 + e) >= 0)
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                const int64_t at = part_slot(cta, p) * kRows + row0 + e;
+                ml[e][p] = a.part_ml[at];
+                v[e][p] = *reinterpret_cast<const float4 *>(a.part_o + at * kD + lane * 4);
+            }
+#pragma unroll
+    for (int e = 0; e < kJoinEach; ++e) {
+        const int tok = token_of(a, x, row0 + e);
+        if (tok < 0) continue;
+        float top = -INFINITY, total = 0.f;
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) top = fmaxf(top, ml[e][p].x);
+        const float at = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+            const float f = ml[e][p].x == -INFINITY ? 0.f : tc::ex2(ml[e][p].x - at);
+            total += ml[e][p].y * f;
+            add_part(acc, f, v[e][p]);
+        }
+        joined_row(a, x, tok, (row0 + e) % kTile, lane, acc, total, at);
+    }
+}
+
+template <int kJoinSplit>
+__global__ void __launch_bounds__(32 * kJoinWarps * kJoinSplit) paged_combine_kernel(const AttendArgs a) {
+    dependent_start();
+    const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const JoinUnit x = static_cast<const JoinUnit *>(a.joins)[cta];
+    if (x.parts == 0) return;
+    if constexpr (kJoinSplit > 1) {
+        __shared__ float4 sums[kJoinWarps][kJoinSplit][32];
+        __shared__ float totals[kJoinWarps][kJoinSplit];
+        const int k = warp / kJoinSplit, s = warp % kJoinSplit, row = blockIdx.y * join_rows<kJoinSplit>() + k, tok = token_of(a, x, row);
+        float at = 0.f;
+        if (tok >= 0) {
+            float4 acc;
+            float total;
+            join_parts(a, cta, x.parts, row, s, kJoinSplit, lane, &acc, &total, &at);
+            sums[k][s][lane] = acc;
+            if (lane == 0) totals[k][s] = total;
+        }
+        __syncthreads();
+        if (tok < 0 || s != 0) return;
+        float total = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kJoinSplit; ++i) add_part(acc, 1.f, sums[k][i][lane]), total += totals[k][i];
+        joined_row(a, x, tok, row % kTile, lane, acc, total, at);
+    } else {
+        const int row0 = blockIdx.y * join_rows<1>() + warp * kJoinEach;
+        if (x.parts == 2) return join_rows_at_once<2>(a, x, cta, row0, lane);
+        if (x.parts == 3) return join_rows_at_once<3>(a, x, cta, row0, lane);
+        if (x.parts == 4) return join_rows_at_once<4>(a, x, cta, row0, lane);
+        for (int row = row0; row < row0 + kJoinEach; ++row) {
+            const int tok = token_of(a, x, row);
+            if (tok < 0) continue;
+            float4 acc;
+            float total, at;
+            join_parts(a, cta, x.parts, row, 0, 1, lane, &acc, &total, &at);
+            joined_row(a, x, tok, row % kTile, lane, acc, total, at);
+        }
     }
 }
 
@@ -860,7 +931,9 @@ cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_str
     a.G = G;
     a.TB = kTile / G;
     // Units of two query tiles read the cache half as often; units of one leave their room to cache tiles in flight. With
-    // more than one tile of tokens a request on average the former count.
+    // more than one tile of tokens a request on average the former count: a chunk of 4096 tokens has each cache tile read
+    // by half as many units, where 256 requests of one token, which fill half a unit of one tile, went from 350 to 340 us
+    // with the stages that the second query tile's room gives.
     const int Q = c.T > c.N * a.TB ? 2 : 1;
     Maps maps;
     cudaError_t e;
@@ -904,9 +977,11 @@ cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_str
         // rows that a unit can have
         const int64_t tokens = c.cu ? c.T : c.T_row;
         const int rows = tokens <= a.TB ? static_cast<int>(tokens) * G : Q * kTile;
-        const dim3 grid(sm_count, (rows + kJoinRows - 1) / kJoinRows);
-        e = rows <= 32 ? launch_dependent(paged_combine_kernel<4>, grid, 32 * kJoinRows * 4, st, a)
-                       : launch_dependent(paged_combine_kernel<1>, grid, 32 * kJoinRows, st, a);
+        auto launch = [&](auto kernel, int block_rows, int threads) {
+            return launch_dependent(kernel, dim3(sm_count, (rows + block_rows - 1) / block_rows), threads, st, a);
+        };
+        e = rows <= 32 ? launch(paged_combine_kernel<4>, join_rows<4>(), 32 * kJoinWarps * 4)
+                       : launch(paged_combine_kernel<1>, join_rows<1>(), 32 * kJoinWarps);
         if (e != cudaSuccess || !accumulate) return e;
     }
     return launch_paged_weights(a, maps, sm_count, st);
