@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
             const int t0 = uniform(x.t0), n = uniform(x.t1) - t0, end = uniform(x.end()), shared_from = max(0, uniform(x.limit) + 1);
             const int whole = shared_from / kTile - t0;      // tiles before this one have no row to clear
             const bool two = kQ == 2 && uniform(x.ntok) > a.TB;
+            const int lead = two ? 0 : items & 1;   // the group of the first cache tile, which ends the item
             bool bad = false;
             ok = passed(q_full, items & 1) && passed(full + 8 * k.at, k.parity);
             if (!ok) break;
@@ -412,19 +413,19 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                     ok = __all_sync(0xffffffffu, fine) != 0;
                 }
             } else {     // one query tile: the groups take the cache tiles in turn
-                scores(0, 0, k.at);
+                scores(lead, 0, k.at);
                 commit(empty + 8 * k.at);
                 k.advance(2);
                 if (n > 1) {
                     ok = passed(full + 8 * k.at, k.parity);
                     if (!ok) break;
-                    scores(1, 0, k.at);
+                    scores(lead ^ 1, 0, k.at);
                     commit(empty + 8 * k.at);
                     k.advance(2);
                 }
                 if (n <= 2) commit(q_free);
                 for (int i = 0; i < n; ++i) {
-                    const int t = i & 1;
+                    const int t = (i & 1) ^ lead;
                     ok = passed(full + 8 * v.at, v.parity);
                     if (!ok) break;
                     if (i >= whole) bad |= clean(shared_from, end, t0 + i, v.at);
@@ -446,12 +447,12 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                 }
             }
             if (!ok) break;
-            const int groups = two || n > 1 ? 2 : 1;
             if (tc::elect_one())
-                for (int t = 0; t < groups; ++t) {
-                    bad_values[t] = bad;
-                    mbar_arrive(&bar.o_full[t]);
-                }
+                for (int t = 0; t < 2; ++t)
+                    if (two || n > 1 || t == lead) {
+                        bad_values[t] = bad;
+                        mbar_arrive(&bar.o_full[t]);
+                    }
             last = uniform(x.last) != 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
@@ -471,33 +472,47 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
         const int first_row = r & ~15;
         const uint32_t lanes = static_cast<uint32_t>(first_row) << 16;
         const uint32_t ts = tmem + kS0 + t * kTile + lanes, to = tmem + kO0 + lanes;
-        uint32_t seen = 0, items = 0, mine = 0, joined = 0;   // score tiles, items, items of this group, items joined
+        // In one register: the parities of score tiles, of items with an O of this group and of joined items, and the items. What
+        // an item's rows are is read again after its tiles: registers are short in between.
+        uint32_t count = 0;
+        constexpr uint32_t kSeen = 1, kMine = 2, kJoined = 4, kItem = 8;
         bool ok = true, last = false;
         do {
-            ok = wait_or_abort(&bar.item_full[items % kItems], (items / kItems) & 1, aborted, status);
+            ok = wait_or_abort(&bar.item_full[count / kItem % kItems], (count / (kItem * kItems)) & 1, aborted, status);
             if (!ok) break;
-            const Item &x = ring[items % kItems];
+            const Item &x = ring[count / kItem % kItems];
             last = x.last;
-            const bool two = kQ == 2 && x.ntok > a.TB;
-            const int n = x.t1 - x.t0, step = two ? 1 : 2, my_tile = two ? t : 0;
-            const int my_tok = my_tile * a.TB + r / a.G;
-            const bool valid = r < a.TB * a.G && my_tok < x.ntok;
-            const int limit = valid ? x.limit + my_tok : -1, first_limit = x.limit + my_tile * a.TB;
-            // a warp without rows leaves its scores as they are: rows of a product do not mix
-            const bool active = first_row < a.TB * a.G && my_tile * a.TB + first_row / a.G < x.ntok;
+            struct Rows {
+                bool two, valid, active;   // active: a warp without rows leaves its scores as they are: rows of a product do not mix
+                int tile, turn, tok, limit;
+            };
+            auto rows = [&]() {
+                Rows y;
+                y.two = kQ == 2 && x.ntok > a.TB;
+                y.tile = y.two ? t : 0;
+                y.turn = y.two ? 0 : t ^ (count / kItem & 1);   // of the cache tiles: 0, 2, .. (and ends the item) or 1, 3, ..
+                y.tok = y.tile * a.TB + r / a.G;
+                y.valid = r < a.TB * a.G && y.tok < x.ntok;
+                y.active = first_row < a.TB * a.G && y.tile * a.TB + first_row / a.G < x.ntok;
+                y.limit = y.valid ? x.limit + y.tok : -1;
+                return y;
+            };
+            const Rows in = rows();
+            const bool active = in.active;
+            const int step = in.two ? 1 : 2, edge_from = max(0, x.limit + in.tile * a.TB + 1) / kTile, keep0 = in.limit - 32 * half;
             const float scale = a.scale * (c.k_scale ? kv::load(c.k_scale + x.h) : 1.f) * kLog2e;
             float m = -INFINITY, l = 0.f;   // the maximum in units of the scores
             bool fresh = true;
-            for (int i = x.t0 + (two ? 0 : t), t1 = x.t1; i < t1; i += step) {
-                ok = wait_or_abort(&bar.s_full[t], seen & 1, aborted, status);
+            for (int i = x.t0 + in.turn, t1 = x.t1; i < t1; i += step) {
+                ok = wait_or_abort(&bar.s_full[t], count & kSeen ? 1 : 0, aborted, status);
                 if (!ok) break;
-                ++seen;
+                count ^= kSeen;
                 tc::tc_fence_after();
                 if (active) {
                     // bf16: all 64 scores in registers; e4m3, with fewer registers a thread: 32 at a time, twice
                     uint32_t s[E4M3 ? 1 : 2][32];
-                    const int keep = limit - i * kTile - 32 * half;
-                    const bool edge = i * kTile + kTile - 1 > first_limit;
+                    const int keep = keep0 - i * kTile;
+                    const bool edge = i >= edge_from;
                     auto load = [&](int q, uint32_t (&x)[32]) {
                         tmem_ld_half_x32(ts + 64 * q, x);
                         tc::tmem_ld_wait();
@@ -574,26 +589,27 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                 }
             }
             if (!ok) break;
-            if (active) l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const auto [two, valid, busy, my_tile, turn, my_tok, limit] = rows();
+            const int n = x.t1 - x.t0;
+            if (busy) l += __shfl_xor_sync(0xffffffffu, l, 16);
             float mc = m == -INFINITY ? m : m * scale;
-            const bool worked = two || t < n;       // this group has an O
+            const bool worked = turn < n;           // this group has an O
             if (worked) {
-                ok = wait_or_abort(&bar.o_full[t], mine & 1, aborted, status);
+                ok = wait_or_abort(&bar.o_full[t], count & kMine ? 1 : 0, aborted, status);
                 if (!ok) break;
-                ++mine;
+                count ^= kMine;
                 tc::tc_fence_after();
             }
             const bool join = !two && n > 1;        // both groups have an O of the same rows
             float f0 = 1.f, f1 = 0.f;
-            if (join && t == 1) {
+            if (join && turn == 1) {
                 if (lane < 16) other[r] = make_float2(mc, l);
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.join);
             } else if (join) {
-                ok = wait_or_abort(&bar.join, joined & 1, aborted, status);
+                ok = wait_or_abort(&bar.join, count & kJoined ? 1 : 0, aborted, status);
                 if (!ok) break;
-                ++joined;
                 tc::tc_fence_after();
                 const float2 y = other[r];
                 const float top = fmaxf(mc, y.x);
@@ -602,7 +618,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                 l = l * f0 + y.y * f1;
                 mc = top;
             }
-            if (active && (two || t == 0)) {
+            if (busy && turn == 0) {
                 const int slot = x.slot;
                 const bool whole = slot < 0, some = limit >= 0;   // some: the row sees a place
                 uint32_t dims[4] = {0, 0, 0, 0};
@@ -618,13 +634,13 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                     const int col = (q >> 1) * 64 + (q & 1) * 16, mycol = col + 32 * half;
                     uint32_t o[16];
                     __syncwarp();
-                    tc::tmem_ld_16x32bx2_x16(to + (two ? t * kTile : 0) + col, o);
+                    tc::tmem_ld_16x32bx2_x16(to + t * kTile + col, o);
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
                     if (join) {
                         uint32_t o1[16];
-                        tc::tmem_ld_16x32bx2_x16(to + kTile + col, o1);
+                        tc::tmem_ld_16x32bx2_x16(to + (t ^ 1) * kTile + col, o1);
                         tc::tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
@@ -665,11 +681,12 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (worked && !(join && t == 1)) mbar_arrive(&bar.o_free[t]);
-                if (join && t == 0) mbar_arrive(&bar.o_free[1]);   // read here
-                mbar_arrive(&bar.item_empty[items % kItems]);
+                if (worked && !(join && turn == 1)) mbar_arrive(&bar.o_free[t]);
+                if (join && turn == 0) mbar_arrive(&bar.o_free[t ^ 1]);   // read here
+                mbar_arrive(&bar.item_empty[count / kItem % kItems]);
             }
-            ++items;
+            if (join) count ^= kJoined;
+            count += kItem;
         } while (!last);
     }
     __syncwarp();
