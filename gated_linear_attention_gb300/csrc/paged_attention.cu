@@ -118,6 +118,16 @@ __device__ __forceinline__ void tmem_st_16x32bx2_x16(uint32_t taddr, const uint3
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "n"(OFF)
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld_half_x8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], 32;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_half_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], 32, {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 
 template <bool E4M3, int kQ>
 __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
@@ -471,11 +481,12 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
         const int t = warp >> 3, half = lane >> 4, r = (warp & 3) * 32 + ((warp >> 2) & 1) * 16 + (lane & 15);
         const int first_row = r & ~15;
         const uint32_t lanes = static_cast<uint32_t>(first_row) << 16;
-        const uint32_t ts = tmem + kS0 + t * kTile + lanes, to = tmem + kO0 + lanes;
-        // In one register: the parities of score tiles, of items with an O of this group and of joined items, and the items. What
-        // an item's rows are is read again after its tiles: registers are short in between.
+        const uint32_t ts = tmem + kS0 + t * kTile + lanes;
+        constexpr uint32_t kO = kO0 - kS0;   // from a group's S to its O
+        // In one register: the parities of score tiles, of items with an O of this group and of joined items, whether an item has
+        // a maximum, and the items. What an item's rows are is read again after its tiles: registers are short in between.
         uint32_t count = 0;
-        constexpr uint32_t kSeen = 1, kMine = 2, kJoined = 4, kItem = 8;
+        constexpr uint32_t kSeen = 1, kMine = 2, kJoined = 4, kBegun = 8, kItem = 16;
         bool ok = true, last = false;
         do {
             ok = wait_or_abort(&bar.item_full[count / kItem % kItems], (count / (kItem * kItems)) & 1, aborted, status);
@@ -499,11 +510,13 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
             };
             const Rows in = rows();
             const bool active = in.active;
-            const int step = in.two ? 1 : 2, edge_from = max(0, x.limit + in.tile * a.TB + 1) / kTile, keep0 = in.limit - 32 * half;
+            const int step = in.two ? 1 : 2, first = x.t0 + in.turn;
+            // the last place seen, from the first score of this thread (a row without a token: as the first token's)
+            int keep = (in.valid ? in.limit : x.limit + in.tile * a.TB) - 32 * half - first * kTile;
             const float scale = a.scale * (c.k_scale ? kv::load(c.k_scale + x.h) : 1.f) * kLog2e;
             float m = -INFINITY, l = 0.f;   // the maximum in units of the scores
-            bool fresh = true;
-            for (int i = x.t0 + in.turn, t1 = x.t1; i < t1; i += step) {
+            count &= ~kBegun;
+            for (int left = (x.t1 - first + step - 1) / step; left > 0; --left, keep -= step * kTile) {
                 ok = wait_or_abort(&bar.s_full[t], count & kSeen ? 1 : 0, aborted, status);
                 if (!ok) break;
                 count ^= kSeen;
@@ -511,12 +524,10 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                 if (active) {
                     // bf16: all 64 scores in registers; e4m3, with fewer registers a thread: 32 at a time, twice
                     uint32_t s[E4M3 ? 1 : 2][32];
-                    const int keep = keep0 - i * kTile;
-                    const bool edge = i >= edge_from;
                     auto load = [&](int q, uint32_t (&x)[32]) {
                         tmem_ld_half_x32(ts + 64 * q, x);
                         tc::tmem_ld_wait();
-                        if (edge)
+                        if (keep < 64 + 31)
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
                                 if (64 * q + j > keep) x[j] = __float_as_uint(-INFINITY);
@@ -532,7 +543,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                     }
                     float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     tile_top = fmaxf(tile_top, __shfl_xor_sync(0xffffffffu, tile_top, 16));
-                    if (fresh) {
+                    if (!(count & kBegun)) {
                         m = tile_top;
                     } else {
                         const bool grow = tile_top > m && !((tile_top - m) * scale <= kRescale);
@@ -540,15 +551,15 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                             const float f = !grow ? 1.f : m == -INFINITY ? 0.f : tc::ex2((m - tile_top) * scale);
                             if (grow) m = tile_top;
                             l *= f;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint32_t o[16];
-                                const uint32_t at = to + t * kTile + (q >> 1) * 64 + (q & 1) * 16;
-                                tc::tmem_ld_16x32bx2_x16(at, o);
+#pragma unroll 1
+                            for (int q = 0; q < 8; ++q) {   // few at a time: the scores fill the registers
+                                uint32_t o[8];
+                                const uint32_t at = ts + kO + (q >> 2) * 64 + (q & 3) * 8;
+                                tmem_ld_half_x8(at, o);
                                 tc::tmem_ld_wait();
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st_16x32bx2_x16<32>(at, o);
+                                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st_half_x8(at, o);
                             }
                         }
                     }
@@ -580,7 +591,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                     l += (even.x + even.y) + (odd.x + odd.y);
                     tc::tmem_st_wait();
                 }
-                fresh = false;
+                count |= kBegun;
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -634,13 +645,13 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                     const int col = (q >> 1) * 64 + (q & 1) * 16, mycol = col + 32 * half;
                     uint32_t o[16];
                     __syncwarp();
-                    tc::tmem_ld_16x32bx2_x16(to + t * kTile + col, o);
+                    tc::tmem_ld_16x32bx2_x16(ts + kO + col, o);
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
                     if (join) {
                         uint32_t o1[16];
-                        tc::tmem_ld_16x32bx2_x16(to + (t ^ 1) * kTile + col, o1);
+                        tc::tmem_ld_16x32bx2_x16(ts + kO + (t ? -kTile : kTile) + col, o1);
                         tc::tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
