@@ -300,9 +300,10 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         auto passed = [&](uint32_t at, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_at(at, parity, aborted, status)) != 0;
         };
-        // The scores of a query tile with `rows` rows, into the next buffer; the tile's room is free after the `last` of them
-        auto scores = [&](int rows, bool last, bool keys_last) {
-            if (!passed(s_free + 8 * b.at, b.parity ^ 1u)) return false;   // passes at once the first time
+        // The scores of the next query tile, with `rows` rows, for the next keys, into the next buffer; the tiles' rooms are free
+        // after the last of them. As in the attention, a wait that gave up is noted in `fine` and voted on once a tile.
+        auto scores = [&](bool fine, int rows, bool query_last, bool keys_last) {
+            fine &= wait_at(s_free + 8 * b.at, b.parity ^ 1u, aborted, status);   // passes at once the first time
             tc::tc_fence_after();
             if (tc::elect_one()) {
                 const uint32_t id = tc::idesc_bf16_f32(128, (rows + 15) & ~15, 0, 0), d = tmem + b.at * kTile;
@@ -315,12 +316,11 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 // last: what it leaves is small, and the score before it has the attention's own roundings
                 tc::umma_bf16(d, ones, first_aux + q.at * (kAuxBytes >> 4), id, 1u);
                 commit_at(s_full + 8 * b.at);
-                if (last) commit_at(q_empty + 8 * q.at);
+                if (query_last) commit_at(q_empty + 8 * q.at);
                 if (keys_last) commit_at(k_empty + 8 * k.at);
             }
-            __syncwarp();
             b.advance(1);
-            return true;
+            return __all_sync(0xffffffffu, fine) != 0;
         };
         do {
             ok = __all_sync(0xffffffffu, take(x)) != 0;
@@ -331,14 +331,14 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 const int rows = min(a.TB, left) * a.G;
                 ok = passed(q_full + 8 * q.at, q.parity);
                 for (int i = 0; i < nu && ok; ++i) {
-                    ok = passed(k_full + 8 * k.at, k.parity) && scores(rows, i + 1 == nu, true);
+                    ok = scores(wait_at(k_full + 8 * k.at, k.parity, aborted, status), rows, i + 1 == nu, true);
                     k.advance(1);
                 }
                 q.advance(1);
             } else {         // a cache tile for a run of query tiles
                 ok = passed(k_full + 8 * k.at, k.parity);
                 for (int i = 0; i < nq && ok; ++i, left -= a.TB) {
-                    ok = passed(q_full + 8 * q.at, q.parity) && scores(min(a.TB, left) * a.G, true, i + 1 == nq);
+                    ok = scores(wait_at(q_full + 8 * q.at, q.parity, aborted, status), min(a.TB, left) * a.G, true, i + 1 == nq);
                     q.advance(1);
                 }
                 k.advance(1);
