@@ -18,15 +18,17 @@
 // Roles: two groups of eight warps turn scores into weights, one for each query tile (two lanes share a row), one warp
 // issues the products, one loads by TMA, a page (and half of the dimensions) a box. While one group has its
 // scores, the tensor core works for the other. A unit with one query tile gives its cache tiles to the groups in
-// turn, and the results are joined at its end. e4m3 tiles land in a ring of their own and eight more warps
+// turn, and the results are joined at its end, by the group that had the first (also in turn: the other one has the next
+// unit's scores meanwhile). e4m3 tiles land in a ring of their own and eight more warps
 // widen them (exactly) to bf16.
 //
 // Bounds, at 32 query heads on 2 key/value heads. 256 requests of one token on up to 12288 bf16 places: the cache's 2.15 GB,
-// 335 us = 6.4 TB/s. A chunk of 4096 tokens on 32768 places: 2.06 TFLOP in 1355 us = 1520 TFLOP/s, the products, which wait in
-// part for the exponentials (128 x 128 of them to 8.4 MFLOP) and run at the clock that the power limit leaves. 61 requests with 5
-// tokens on 8192 e4m3 places: 85 us against 40 for its bytes; the tiles pass shared memory three times more (read and
+// 318 us = 6.8 TB/s, a copy's rate. A chunk of 4096 tokens on 32768 places: 2.06 TFLOP in 1240 us = 1660 TFLOP/s, the products at
+// the clock that the power limit leaves (a library product 1695). A softmax thread has 96 registers and 64 scores: what is not
+// needed between a tile's scores and its weights stays out of registers there, which took 120 us off the chunk. 61 requests with
+// 5 tokens on 8192 e4m3 places: 84 us against 40 for its bytes; the tiles pass shared memory three times more (read and
 // stored by the widening, read by the product). fp16 tiles, cheaper to widen, took longer (the queries then need a scale
-// for each row to stay in range). One token on 4001 places: 15 us of launch, split, one tile a CTA and join.
+// for each row to stay in range). One token on 4001 places: 14 us of launch, split, one tile a CTA and join.
 //
 // What is masked never enters: scores are replaced, not added to, and V is cleared in the rows behind the unit's
 // last place (0 times a NaN there would be NaN). Rows of V that some tokens of the unit see and others do not are
@@ -960,8 +962,8 @@ cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_str
     a.TB = kTile / G;
     // Units of two query tiles read the cache half as often; units of one leave their room to cache tiles in flight. With
     // more than one tile of tokens a request on average the former count: a chunk of 4096 tokens has each cache tile read
-    // by half as many units, where 256 requests of one token, which fill half a unit of one tile, went from 350 to 340 us
-    // with the stages that the second query tile's room gives.
+    // by half as many units, where 256 requests of one token, which fill a part of one tile, went from 350 to 340 us when
+    // the second query tile's room became a stage.
     const int Q = c.T > c.N * a.TB ? 2 : 1;
     Maps maps;
     cudaError_t e;

@@ -13,8 +13,9 @@
 // four buffers in tensor memory. With one query tile for a request (decoding) it stays in shared memory while the
 // request's cache tiles pass: the kernel then reads the keys once, which bounds it: 61 requests with 5 tokens on 8192
 // e4m3 places, 128 MB of keys, in 48 us (2.7 TB/s; the keys are widened as in the attention). With many tiles the exp2 of
-// every score bounds it: 7 prompts of up to 2011 tokens at the end of 6007 places, 204 us for 243 GFLOP. Units of two cache
-// tiles, which halve the reads of the queries, took 194 there but 51 for the drafts.
+// every score bounds it: 7 prompts of up to 2011 tokens at the end of 6007 places, 201 us for 243 GFLOP. Units of two cache
+// tiles, which halve the reads of the queries, took 194 there but 51 for the drafts; reading a score tile's next columns while
+// the last are summed changed nothing.
 #include "paged_tiles.cuh"
 
 namespace sala {
