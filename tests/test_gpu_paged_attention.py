@@ -111,6 +111,16 @@ def test_more_tiles_than_blocks(kind, T, Hq):
     _run(c, q.reshape(len(lens), T, Hq, 128), accumulate=True)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [1, 9])
+def test_short_units_one_after_another(kind, T):
+    """Blocks that go through a dozen units of mostly one tile, some of two or three: the softmax groups lead them in turn."""
+    lens = [T + (29 * n) % 118 + (130 if n % 5 == 3 else 0) + (100 if n % 7 == 6 else 0) for n in range(230)]
+    c = make_cache(lens, 32, 8, kind, seed=T, weights=True)
+    q, _ = new_tokens([T * len(lens)], 16, size=3.0)
+    _run(c, q.reshape(len(lens), T, 16, 128), accumulate=True)
+
+
 def test_more_requests_than_a_block_scans():
     lens = [1 + (53 * n) % 300 for n in range(300)]
     c = make_cache(lens, 16, 2, seed=1, weights=True)
@@ -132,6 +142,22 @@ def test_peaked_and_growing_scores():
     q[2] *= 8
     q[3] *= -8
     _run(c, q.reshape(1, 6, 4, 128))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_growing_scores_of_two_query_tiles(kind):
+    """The same for units of two query tiles, and tokens whose maximum stays beside some whose maximum moves."""
+    c = make_cache([900], 32, 1, kind, seed=5, weights=True)
+    unit = 1.0 if kind == "bf16" else float(c["k_scale"][0])
+    for i in range(900):
+        p, s = int(c["table"][0, i // 32]), i % 32
+        c["k_pages"][p, 0, s] = (torch.full((128,), 0.01 * i) / unit).clamp(max=448 if kind == "e4m3" else 1e9).to(
+            c["k_pages"].dtype)   # a cast to e4m3 alone makes NaN of what is above
+    q, _ = new_tokens([24 * 16], 1, size=0.05)
+    q = q.reshape(1, 24, 16, 128)
+    q[0, ::3] += 1
+    q[0, 1::3, ::2] -= 1
+    _run(c, q, accumulate=True)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
