@@ -16,7 +16,7 @@
 // serves one token on a long cache and a full batch alike.
 //
 // Roles: two groups of eight warps turn scores into weights, one for each query tile (two lanes share a row), one warp
-// issues the products, one loads by TMA, a page (and half of the dimensions) a box. While one group has its
+// issues the products, one (two for small pages) loads by TMA, a page (and half of the dimensions) a box. While one group has its
 // scores, the tensor core works for the other. A unit with one query tile gives its cache tiles to the groups in
 // turn, and the results are joined at its end, by the group that had the first (also in turn: the other one has the next
 // unit's scores meanwhile). e4m3 tiles land in a ring of their own and eight more warps
@@ -33,6 +33,8 @@
 // What is masked never enters: scores are replaced, not added to, and V is cleared in the rows behind the unit's
 // last place (0 times a NaN there would be NaN). Rows of V that some tokens of the unit see and others do not are
 // searched for infinities and NaN, which are cleared and put into the results that see them at the end.
+#include <type_traits>
+
 #include "paged_tiles.cuh"
 
 namespace sala {
@@ -43,14 +45,16 @@ using tc::mbar_arrive;
 using tck::wait_or_abort;
 
 constexpr int kRows = 2 * kTile;                 // rows of a unit, at most
-constexpr int kMmaWarp = 16, kLoadWarp = 17, kConvertWarp = 18;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kValueWarp = 18;
 constexpr uint32_t kS0 = 0, kO0 = 256;           // tensor memory columns: S (and P over it) of the groups, then O
 constexpr float kRescale = 8.f;                  // growth of the maximum (log2) that rescales O
 constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128, 0, 0), kIdO = tc::idesc_bf16_f32(128, 128, 0, 1);
 
-// Shared memory of units with Q query tiles: the queries, the ring of cache tiles, the ring of e4m3 tiles.
-template <bool E4M3, int Q>
+// Shared memory of units with Q query tiles: the queries, the ring of cache tiles, the ring of e4m3 tiles. Split: the values
+// have a loading warp of their own.
+template <bool E4M3, int Q, bool Split>
 struct Shape {
+    static constexpr int kConvertWarp = Split ? kValueWarp + 1 : kValueWarp;
     static constexpr int kStages = E4M3 ? 4 : 7 - Q, kRaw = E4M3 ? 6 - 2 * Q : 0;
     static constexpr int kThreads = 32 * (E4M3 ? kConvertWarp + kConvertWarps : kConvertWarp);
     static constexpr uint32_t kRawAt = (Q + kStages) * kTileBytes;
@@ -131,10 +135,11 @@ __device__ __forceinline__ void tmem_st_half_x8(uint32_t taddr, const uint32_t (
                  : "memory");
 }
 
-template <bool E4M3, int kQ>
-__global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
+template <bool E4M3, int kQ, bool kSplit>
+__global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ Maps maps) {
-    using Layout = Shape<E4M3, kQ>;
+    using Layout = Shape<E4M3, kQ, kSplit>;
+    constexpr int kConvertWarp = Layout::kConvertWarp;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Barriers bar;
     __shared__ uint32_t tmem_slot;
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             tc::mbar_init(&bar.item_full[i], 1);
-            tc::mbar_init(&bar.item_empty[i], kMmaWarp + 1);
+            tc::mbar_init(&bar.item_empty[i], kMmaWarp + 1 + kSplit);
         }
         tc::mbar_init(&bar.q_full, 1);
         tc::mbar_init(&bar.q_free, 1);
@@ -196,10 +201,17 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
     volatile int *const aborted = &abort_flag;
     int *const status = c.status;
 
+    // the ring of tiles as they land: keys and values in turn
+    constexpr uint32_t kRing = E4M3 ? Layout::kRaw : Layout::kStages;
+    uint64_t *const full = E4M3 ? bar.raw_full : bar.full, *const empty = E4M3 ? bar.raw_empty : bar.empty;
+    auto tile_at = [](uint32_t st) { return E4M3 ? Layout::kRawAt + st * kRawBytes : (kQ + st) * kTileBytes; };
+    // Copies in flight of a loading warp that gives up before tile `it` land before the CTA ends; `odd`: of the values alone.
+    auto drain_tiles = [&](uint32_t it, uint32_t odd) {
+        for (uint32_t j = it > kRing ? it - kRing : 0; j < it; ++j)
+            if (!kSplit || (j & 1) == odd) tc::mbar_wait(&full[j % kRing], (j / kRing) & 1, tck::kWaitNs);
+    };
     if (warp == kLoadWarp && !idle) {
         // ---- loads: Q of each item, then K and V of each cache tile -----------------------------
-        constexpr int kRing = E4M3 ? Layout::kRaw : Layout::kStages;
-        uint64_t *const full = E4M3 ? bar.raw_full : bar.full, *const empty = E4M3 ? bar.raw_empty : bar.empty;
         uint32_t it = 0, items = 0, q_issued = 0;   // cache tiles and items so far
         bool ok = true;
         JoinUnit join = {0, 0, 0, 0, 0};
@@ -231,11 +243,11 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
                 const int here = page;
                 page = i + 1 < w.t1 ? box_page<E4M3>(c, w.n, i + 1, end, lane) : -2;
                 for (int kv = 0; kv < 2; ++kv, ++it) {
+                    if (kv == 1 && kSplit) continue;
                     const int st = it % kRing;
                     ok = it < kRing || wait_or_abort(&empty[st], (it / kRing - 1) & 1, aborted, status);
                     if (!ok) break;
-                    uint8_t *dst = smem + (E4M3 ? Layout::kRawAt + st * kRawBytes : (kQ + st) * kTileBytes);
-                    load_boxes<E4M3>(c, kv ? &maps.v : &maps.k, dst, i, w.h, here, lane, &full[st]);
+                    load_boxes<E4M3>(c, kv ? &maps.v : &maps.k, smem + tile_at(st), i, w.h, here, lane, &full[st]);
                     if (i == w.t0 && kv == 0) {   // behind the first K: its buffer may still be in use
                         ok = items == 0 || wait_or_abort(&bar.q_free, (items - 1) & 1, aborted, status);
                         if (ok && lane == 0) {
@@ -255,9 +267,31 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ>::kThreads, 1)
         if (lane == 0) static_cast<JoinUnit *>(a.joins)[cta] = join;
         if (!ok) {   // copies in flight land before the CTA ends
             if (q_issued) tc::mbar_wait(&bar.q_full, (q_issued - 1) & 1, tck::kWaitNs);
-            for (uint32_t j = it > kRing ? it - kRing : 0; j < it; ++j)
-                tc::mbar_wait(&full[j % kRing], (j / kRing) & 1, tck::kWaitNs);
+            drain_tiles(it, 0);
         }
+    } else if (kSplit && warp == kValueWarp && !idle) {
+        // ---- loads of the values where one warp does not keep up ------------------------------------
+        uint32_t it = 1, items = 0;
+        bool ok = true, last = false;
+        do {
+            ok = wait_or_abort(&bar.item_full[items % kItems], (items / kItems) & 1, aborted, status);
+            if (!ok) break;
+            const Item &x = ring[items % kItems];
+            const int n = x.n, h = x.h, end = x.end(), t1 = x.t1;
+            last = x.last;
+            int page = box_page<E4M3>(c, n, x.t0, end, lane);
+            for (int i = x.t0; i < t1; ++i, it += 2) {
+                const int here = page, st = it % kRing;
+                page = i + 1 < t1 ? box_page<E4M3>(c, n, i + 1, end, lane) : -2;
+                ok = it < kRing || wait_or_abort(&empty[st], (it / kRing - 1) & 1, aborted, status);
+                if (!ok) break;
+                load_boxes<E4M3>(c, &maps.v, smem + tile_at(st), i, h, here, lane, &full[st]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
+            ++items;
+        } while (ok && !last);
+        if (!ok) drain_tiles(it, 1);
     } else if (E4M3 && warp >= kConvertWarp && !idle) {
         // ---- e4m3 tiles to bf16 --------------------------------------------------------------------
         constexpr int kRaw = E4M3 ? Layout::kRaw : 1;
@@ -943,10 +977,14 @@ cudaError_t setup_paged_attention_kernel() {
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     };
-    allow(reinterpret_cast<const void *>(paged_attention_kernel<false, 1>), Shape<false, 1>::kAlloc);
-    allow(reinterpret_cast<const void *>(paged_attention_kernel<false, 2>), Shape<false, 2>::kAlloc);
-    allow(reinterpret_cast<const void *>(paged_attention_kernel<true, 1>), Shape<true, 1>::kAlloc);
-    allow(reinterpret_cast<const void *>(paged_attention_kernel<true, 2>), Shape<true, 2>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<false, 1, false>), Shape<false, 1, false>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<false, 1, true>), Shape<false, 1, true>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<false, 2, false>), Shape<false, 2, false>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<false, 2, true>), Shape<false, 2, true>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<true, 1, false>), Shape<true, 1, false>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<true, 1, true>), Shape<true, 1, true>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<true, 2, false>), Shape<true, 2, false>::kAlloc);
+    allow(reinterpret_cast<const void *>(paged_attention_kernel<true, 2, true>), Shape<true, 2, true>::kAlloc);
     return e == cudaSuccess ? setup_paged_weights_kernel() : e;
 }
 
@@ -965,6 +1003,12 @@ cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_str
     // by half as many units, where 256 requests of one token, which fill a part of one tile, went from 350 to 340 us when
     // the second query tile's room became a stage.
     const int Q = c.T > c.N * a.TB ? 2 : 1;
+    // A warp issues its lanes' boxes one after another, and the 16 of a bf16 tile in pages of 16 places (8 of an e4m3 tile) bound the
+    // kernel: a second warp then loads the values. Pages of 16 and the two warps: a chunk of 2048 tokens on 16384 places
+    // 424 -> 350 us, 128 requests of one token on up to 12288 places 196 -> 171 (e4m3 180 -> 147), but 256 on up to 120 places
+    // and 8 key/value heads 53.6 -> 57.7, as the values wait for the item. In pages of 32 the same chunk 348 -> 358 and the
+    // requests 167 -> 171 (e4m3 150 -> 147): one warp.
+    const bool split = c.S < 32;
     Maps maps;
     cudaError_t e;
     {
@@ -996,10 +1040,17 @@ cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_str
             using S = decltype(shape);
             return launch_dependent_cluster(kernel, dim3(sm_count), 0, S::kThreads, S::kAlloc, st, a, maps);
         };
-        e = c.e4m3 ? (Q == 2 ? launch(paged_attention_kernel<true, 2>, Shape<true, 2>{})
-                             : launch(paged_attention_kernel<true, 1>, Shape<true, 1>{}))
-                   : (Q == 2 ? launch(paged_attention_kernel<false, 2>, Shape<false, 2>{})
-                             : launch(paged_attention_kernel<false, 1>, Shape<false, 1>{}));
+        auto launch_split = [&](auto e4m3, auto q) {
+            constexpr bool kE = decltype(e4m3)::value;
+            constexpr int kQ = decltype(q)::value;
+            return split ? launch(paged_attention_kernel<kE, kQ, true>, Shape<kE, kQ, true>{})
+                         : launch(paged_attention_kernel<kE, kQ, false>, Shape<kE, kQ, false>{});
+        };
+        using std::integral_constant;
+        const integral_constant<int, 1> one;
+        const integral_constant<int, 2> two;
+        e = c.e4m3 ? (Q == 2 ? launch_split(std::true_type{}, two) : launch_split(std::true_type{}, one))
+                   : (Q == 2 ? launch_split(std::false_type{}, two) : launch_split(std::false_type{}, one));
         if (e != cudaSuccess) return e;
     }
     {
