@@ -978,11 +978,12 @@ int sala_gla_token_logprobs(const void *logits, int64_t stride, int32_t logit_dt
     if (!d) return err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     void *ws = nullptr;
-    if (cudaMallocFromPoolAsync(&ws, token_logprobs_scratch(N, V, bf16, K, d->sm_count), d->pool, st) != cudaSuccess)
+    const int parts = token_logprobs_parts(N, V, bf16, K, d->sm_count);
+    if (cudaMallocFromPoolAsync(&ws, token_logprobs_scratch(N, parts, K), d->pool, st) != cudaSuccess)
         return SALA_ERR_CUDA;
     int rc = SALA_OK;
     if (launch_token_logprobs(logits, stride, bf16, tokens, logprobs, entropy, top_tokens, top_logprobs, N, V, M, K, ws,
-                              d->sm_count, d->status, st) != cudaSuccess)
+                              parts, d->sm_count, d->status, st) != cudaSuccess)
         rc = SALA_ERR_CUDA;
     if (cudaFreeAsync(ws, st) != cudaSuccess) rc = SALA_ERR_CUDA;
     return rc;

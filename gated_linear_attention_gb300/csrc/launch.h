@@ -199,11 +199,12 @@ cudaError_t launch_kv_evict(const KvArgs &c, int64_t budget, int64_t sinks, int6
                             int32_t *kept, int sm_count, cudaStream_t st);
 
 // Log probabilities of tokens [N, M], entropy and the K largest logits of rows of V (fp32, or bf16 if `bf16`).
-// `ws`: scratch of token_logprobs_scratch bytes.
-size_t token_logprobs_scratch(int64_t N, int64_t V, bool bf16, int K, int sm_count);
+// `ws`: scratch of token_logprobs_scratch bytes, for rows cut into token_logprobs_parts.
+int token_logprobs_parts(int64_t N, int64_t V, bool bf16, int K, int sm_count);
+size_t token_logprobs_scratch(int64_t N, int parts, int K);
 cudaError_t launch_token_logprobs(const void *x, int64_t stride, bool bf16, const int32_t *tokens, float *logprobs,
                                   float *entropy, int32_t *top_tokens, float *top_logprobs, int64_t N, int64_t V,
-                                  int M, int K, void *ws, int sm_count, int *status, cudaStream_t st);
+                                  int M, int K, void *ws, int parts, int sm_count, int *status, cudaStream_t st);
 
 // Nonzero tag of one prefill call for the hand-off flags (differs from the previous call's).
 uint32_t next_prefill_epoch();

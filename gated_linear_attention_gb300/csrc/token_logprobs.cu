@@ -489,13 +489,16 @@ __global__ void __launch_bounds__(kThreads) logprob_top_kernel(const LogprobArgs
 // there are warps for. `warps` at once.
 int parts_of(int64_t N, int64_t row_bytes, int K, int64_t warps) {
     const int64_t most = std::max<int64_t>(K > 0 && row_bytes > 4096 ? 4 : 1, std::min<int64_t>(kMaxParts, row_bytes / 2048));
+    if (N * most <= warps) return static_cast<int>(most);   // one round: the score below grows with p
     int best = 1;
     double score = -1.0;
     for (int64_t p = K > 0 && row_bytes > 4096 ? 4 : 1; p <= most; ++p) {
+        const double full = static_cast<double>(row_bytes / p) / static_cast<double>(row_bytes / p + 1024);
+        if (full <= score) break;   // no later one is better, whatever its rounds
         const int64_t rounds = (N * p + warps - 1) / warps;
         // the share of the warps at work, less what starting a part costs beside its bytes
         const double busy = static_cast<double>(N * p) / static_cast<double>(rounds * warps);
-        const double s = busy * static_cast<double>(row_bytes / p) / static_cast<double>(row_bytes / p + 1024);
+        const double s = busy * full;
         if (s > score) score = s, best = static_cast<int>(p);
     }
     return best;
@@ -505,17 +508,18 @@ constexpr int kWarpsPerSm = 32;
 
 }  // namespace
 
-size_t token_logprobs_scratch(int64_t N, int64_t V, bool bf16, int K, int sm_count) {
-    const int parts = parts_of(N, V * (bf16 ? 2 : 4), K, static_cast<int64_t>(sm_count) * kWarpsPerSm);
+int token_logprobs_parts(int64_t N, int64_t V, bool bf16, int K, int sm_count) {
+    return parts_of(N, V * (bf16 ? 2 : 4), K, static_cast<int64_t>(sm_count) * kWarpsPerSm);
+}
+size_t token_logprobs_scratch(int64_t N, int parts, int K) {
     return static_cast<size_t>(N) * parts * (16 + (K > 0 ? 128 : 0));
 }
 
 cudaError_t launch_token_logprobs(const void *x, int64_t stride, bool bf16, const int32_t *tokens, float *logprobs,
                                   float *entropy, int32_t *top_tokens, float *top_logprobs, int64_t N, int64_t V,
-                                  int M, int K, void *ws, int sm_count, int *status, cudaStream_t st) {
+                                  int M, int K, void *ws, int parts, int sm_count, int *status, cudaStream_t st) {
     LaunchTimer timer(kKTokenLogprobs, st);
     const int64_t warps = static_cast<int64_t>(sm_count) * kWarpsPerSm;
-    const int parts = parts_of(N, V * (bf16 ? 2 : 4), K, warps);
     float *sums = static_cast<float *>(ws);
     const LogprobArgs a{x, stride, N, tokens, logprobs, entropy, top_tokens, top_logprobs, sums,
                         K > 0 ? sums + N * parts * 4 : nullptr, static_cast<int>(V), M, K, parts, status};
