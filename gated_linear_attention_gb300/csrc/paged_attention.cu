@@ -42,7 +42,6 @@ namespace {
 
 using namespace pt;
 using tc::mbar_arrive;
-using tck::wait_or_abort;
 
 constexpr int kRows = 2 * kTile;                 // rows of a unit, at most
 constexpr int kMmaWarp = 16, kLoadWarp = 17, kValueWarp = 18;
@@ -230,7 +229,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
             x.t1 = w.t1;
             x.slot = w.slot;
             x.last = w.pos + (w.t1 - w.t0) >= stop;
-            ok = items < kItems || wait_or_abort(&bar.item_empty[slot], (items / kItems - 1) & 1, aborted, status);
+            ok = items < kItems || wait_warp(&bar.item_empty[slot], (items / kItems - 1) & 1, aborted, status);
             if (!ok) break;
             if (lane == 0) {
                 ring[slot] = x;
@@ -245,11 +244,11 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
                 for (int kv = 0; kv < 2; ++kv, ++it) {
                     if (kv == 1 && kSplit) continue;
                     const int st = it % kRing;
-                    ok = it < kRing || wait_or_abort(&empty[st], (it / kRing - 1) & 1, aborted, status);
+                    ok = it < kRing || wait_warp(&empty[st], (it / kRing - 1) & 1, aborted, status);
                     if (!ok) break;
                     load_boxes<E4M3>(c, kv ? &maps.v : &maps.k, smem + tile_at(st), i, w.h, here, lane, &full[st]);
                     if (i == w.t0 && kv == 0) {   // behind the first K: its buffer may still be in use
-                        ok = items == 0 || wait_or_abort(&bar.q_free, (items - 1) & 1, aborted, status);
+                        ok = items == 0 || wait_warp(&bar.q_free, (items - 1) & 1, aborted, status);
                         if (ok && lane == 0) {
                             tc::mbar_arrive_expect_tx(&bar.q_full, nt * 2 * static_cast<uint32_t>(a.TB * a.G) * 128u);
                             for (int t = 0; t < nt; ++t)
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
         uint32_t it = 1, items = 0;
         bool ok = true, last = false;
         do {
-            ok = wait_or_abort(&bar.item_full[items % kItems], (items / kItems) & 1, aborted, status);
+            ok = wait_warp(&bar.item_full[items % kItems], (items / kItems) & 1, aborted, status);
             if (!ok) break;
             const Item &x = ring[items % kItems];
             const int n = x.n, h = x.h, end = x.end(), t1 = x.t1;
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
             for (int i = x.t0; i < t1; ++i, it += 2) {
                 const int here = page, st = it % kRing;
                 page = i + 1 < t1 ? box_page<E4M3>(c, n, i + 1, end, lane) : -2;
-                ok = it < kRing || wait_or_abort(&empty[st], (it / kRing - 1) & 1, aborted, status);
+                ok = it < kRing || wait_warp(&empty[st], (it / kRing - 1) & 1, aborted, status);
                 if (!ok) break;
                 load_boxes<E4M3>(c, &maps.v, smem + tile_at(st), i, h, here, lane, &full[st]);
             }
@@ -298,22 +297,22 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
         const int id = threadIdx.x - 32 * kConvertWarp;
         const int64_t tiles = 2 * (stop - begin);
         uint4 held[kPieces];   // of the next tile: read while the stores of this one drain
-        bool ok = wait_or_abort(&bar.raw_full[0], 0, aborted, status);
+        bool ok = wait_warp(&bar.raw_full[0], 0, aborted, status);
         if (ok) read_pieces(held, smem + Layout::kRawAt, id);
         for (int64_t it = 0; it < tiles && ok; ++it) {
             const int st = it % Layout::kStages, rw = it % kRaw, next = (it + 1) % kRaw;
-            ok = it < Layout::kStages || wait_or_abort(&bar.empty[st], (it / Layout::kStages - 1) & 1, aborted, status);
+            ok = it < Layout::kStages || wait_warp(&bar.empty[st], (it / Layout::kStages - 1) & 1, aborted, status);
             if (!ok) break;
             store_pieces(held, smem + (kQ + st) * kTileBytes, id);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.raw_empty[rw]);
-            const bool there = it + 1 < tiles && tc::mbar_test_wait(&bar.raw_full[next], ((it + 1) / kRaw) & 1);
+            const bool there = it + 1 < tiles && __all_sync(0xffffffffu, tc::mbar_test_wait(&bar.raw_full[next], ((it + 1) / kRaw) & 1));
             if (there) read_pieces(held, smem + Layout::kRawAt + next * kRawBytes, id);
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.full[st]);
             if (it + 1 < tiles && !there) {
-                ok = wait_or_abort(&bar.raw_full[next], ((it + 1) / kRaw) & 1, aborted, status);
+                ok = wait_warp(&bar.raw_full[next], ((it + 1) / kRaw) & 1, aborted, status);
                 if (ok) read_pieces(held, smem + Layout::kRawAt + next * kRawBytes, id);
             }
         }
@@ -525,7 +524,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
         constexpr uint32_t kSeen = 1, kMine = 2, kJoined = 4, kBegun = 8, kItem = 16;
         bool ok = true, last = false;
         do {
-            ok = wait_or_abort(&bar.item_full[count / kItem % kItems], (count / (kItem * kItems)) & 1, aborted, status);
+            ok = wait_warp(&bar.item_full[count / kItem % kItems], (count / (kItem * kItems)) & 1, aborted, status);
             if (!ok) break;
             const Item &x = ring[count / kItem % kItems];
             last = x.last;
@@ -553,7 +552,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
             float m = -INFINITY, l = 0.f;   // the maximum in units of the scores
             count &= ~kBegun;
             for (int left = (x.t1 - first + step - 1) / step; left > 0; --left, keep -= step * kTile) {
-                ok = wait_or_abort(&bar.s_full[t], count & kSeen ? 1 : 0, aborted, status);
+                ok = wait_warp(&bar.s_full[t], count & kSeen ? 1 : 0, aborted, status);
                 if (!ok) break;
                 count ^= kSeen;
                 tc::tc_fence_after();
@@ -642,7 +641,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
             float mc = m == -INFINITY ? m : m * scale;
             const bool worked = turn < n;           // this group has an O
             if (worked) {
-                ok = wait_or_abort(&bar.o_full[t], count & kMine ? 1 : 0, aborted, status);
+                ok = wait_warp(&bar.o_full[t], count & kMine ? 1 : 0, aborted, status);
                 if (!ok) break;
                 count ^= kMine;
                 tc::tc_fence_after();
@@ -655,7 +654,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.join);
             } else if (join) {
-                ok = wait_or_abort(&bar.join, count & kJoined ? 1 : 0, aborted, status);
+                ok = wait_warp(&bar.join, count & kJoined ? 1 : 0, aborted, status);
                 if (!ok) break;
                 tc::tc_fence_after();
                 const float2 y = other[r];

@@ -279,6 +279,14 @@ __device__ __forceinline__ void store_pieces(const uint4 (&x)[kPieces], uint8_t 
     }
 }
 
+// ---- waits ----------------------------------------------------------------------------------------
+// A wait of a whole warp. By itself a lane may run out of time, or see that another role gave up, where its neighbour sees
+// the phase complete; what follows may need the whole warp (tensor memory, shuffles, votes), so that the lanes go by a vote.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status) {
+    if (__all_sync(0xffffffffu, tc::mbar_test_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, tck::wait_or_abort_slow(bar, parity, abort_flag, status)) != 0;
+}
+
 // ---- barriers by their shared-memory address --------------------------------------------------------
 // The warp that issues the products pays for every scalar instruction between two of them (its queue is short), so it
 // keeps addresses, stages and parities in registers.

@@ -23,7 +23,6 @@ namespace {
 
 using namespace pt;
 using tc::mbar_arrive;
-using tck::wait_or_abort;
 
 constexpr int kMmaWarp = 16, kLoadWarp = 17, kStatsWarp = 18, kConvertWarp = 19;
 constexpr int kGroups = 4;                       // of four warps; score tiles in tensor memory
@@ -148,7 +147,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
     // the items from the ring, for every role but the loading warp
     uint32_t items = 0;
     auto take = [&](Item &x) {
-        if (!wait_or_abort(&bar.item_full[items % kItems], (items / kItems) & 1, aborted, status)) return false;
+        if (!wait_warp(&bar.item_full[items % kItems], (items / kItems) & 1, aborted, status)) return false;
         x = ring[items % kItems];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
@@ -183,7 +182,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             w.u += x.nu - 1;
             w.pos += x.nu - 1;
             x.last = w.pos + (w.t1 - w.t0) >= stop;
-            ok = items < kItems || wait_or_abort(&bar.item_empty[slot], (items / kItems - 1) & 1, aborted, status);
+            ok = items < kItems || wait_warp(&bar.item_empty[slot], (items / kItems - 1) & 1, aborted, status);
             if (!ok) break;
             if (lane == 0) {
                 ring[slot] = x;
@@ -195,13 +194,13 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             for (int i = 0; i < x.nu && ok; ++i, ++kt) {
                 const int here = page, st = kt % kRing;
                 page = i + 1 < x.nu ? box_page<E4M3>(c, x.n, x.u0 + i + 1, x.len, lane) : -2;
-                ok = kt < kRing || wait_or_abort(&empty[st], (kt / kRing - 1) & 1, aborted, status);
+                ok = kt < kRing || wait_warp(&empty[st], (kt / kRing - 1) & 1, aborted, status);
                 if (!ok) break;
                 load_boxes<E4M3>(c, &maps.k, smem + (E4M3 ? Layout::kRawAt + st * kRawBytes : st * kTileBytes), x.u0 + i, x.h, here,
                                  lane, &full[st]);
                 for (int q = 0; i == 0 && q < x.nq; ++q, ++qt) {
                     const int s = qt % Layout::kQueries;
-                    ok = qt < Layout::kQueries || wait_or_abort(&bar.q_empty[s], (qt / Layout::kQueries - 1) & 1, aborted, status);
+                    ok = qt < Layout::kQueries || wait_warp(&bar.q_empty[s], (qt / Layout::kQueries - 1) & 1, aborted, status);
                     if (!ok) break;
                     if (lane == 0) {
                         tc::mbar_arrive_expect_tx(&bar.q_full[s], 2 * static_cast<uint32_t>(a.TB * a.G) * 128u);
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = next[e];
                 if (q + 1 < x.nq) fetch(q + 1);
-                ok = qt < Layout::kQueries || wait_or_abort(&bar.q_empty[s], (qt / Layout::kQueries - 1) & 1, aborted, status);
+                ok = qt < Layout::kQueries || wait_warp(&bar.q_empty[s], (qt / Layout::kQueries - 1) & 1, aborted, status);
                 if (!ok) break;
                 uint8_t *aux = smem + Layout::kAuxAt + s * kAuxBytes;
 #pragma unroll
@@ -273,8 +272,8 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             ok = take(x);
             for (int i = 0; ok && i < x.nu; ++i, ++it) {
                 const int st = it % Layout::kKeys, rw = it % kRaw;
-                ok = wait_or_abort(&bar.raw_full[rw], (it / kRaw) & 1, aborted, status) &&
-                     (it < Layout::kKeys || wait_or_abort(&bar.k_empty[st], (it / Layout::kKeys - 1) & 1, aborted, status));
+                ok = wait_warp(&bar.raw_full[rw], (it / kRaw) & 1, aborted, status) &&
+                     (it < Layout::kKeys || wait_warp(&bar.k_empty[st], (it / Layout::kKeys - 1) & 1, aborted, status));
                 if (!ok) break;
                 uint4 held[kPieces];
                 read_pieces(held, smem + Layout::kRawAt + rw * kRawBytes, threadIdx.x - 32 * kConvertWarp);
@@ -363,7 +362,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         float scale = 0.f;
         // The sum over the rows of query tile q that see place p of the item's cache tile i
         auto sum_tile = [&](int i, int p, int q) {
-            ok = wait_or_abort(&bar.s_full[g], done & 1, aborted, status);
+            ok = wait_warp(&bar.s_full[g], done & 1, aborted, status);
             if (!ok) return 0.f;
             ++done;
             tc::tc_fence_after();
@@ -453,7 +452,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             for (int q = mine; q < m && ok; q += kGroups) total += sum_tile(0, p, q);
             if (!ok) break;
             if (mine > 0) {   // to the group that has the unit's first query tile
-                ok = sent == 0 || wait_or_abort(&bar.part_free[g], (sent - 1) & 1, aborted, status);
+                ok = sent == 0 || wait_warp(&bar.part_free[g], (sent - 1) & 1, aborted, status);
                 if (!ok) break;
                 parts[g][r] = total;
                 ++sent;
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
             for (int o = 1; o < kGroups; ++o) {
                 if (o >= m) break;
                 const int from = (g + o) & (kGroups - 1);
-                ok = wait_or_abort(&bar.part_full[from], (before >> from) & 1, aborted, status);
+                ok = wait_warp(&bar.part_full[from], (before >> from) & 1, aborted, status);
                 if (!ok) break;
                 total += parts[from][r];
                 __syncwarp();

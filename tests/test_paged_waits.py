@@ -1,0 +1,35 @@
+"""Waits of the attention's and the weights' persistent kernels (csrc/paged_attention.cu, csrc/paged_weights.cu) that can give
+up, read from the source. One lane may run out of time, or see that another role gave up, where its neighbour sees the phase
+complete, and what follows a wait takes the whole warp (tensor memory accesses, shuffles, votes): every such wait is
+voted on, so that no lane leaves alone. The path itself is not run: nothing may hang a GPU."""
+import os
+import re
+
+import pytest
+
+from gated_linear_attention_gb300 import build
+
+FILES = ("paged_attention.cu", "paged_weights.cu")
+
+
+def _code(name):
+    with open(os.path.join(build.CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_waits_are_voted_on(name):
+    code = _code(name)
+    assert code.count("wait_warp(") > 5
+    for at in re.finditer(r"(tck::|tc::)?\b(wait_or_abort\w*|mbar_test_wait|mbar_try_wait)\(", code):
+        assert code[:at.start()].endswith("__all_sync(0xffffffffu, "), code[at.start() - 60:at.end() + 40]
+    # the product role notes its waits' results, and votes on them once a tile
+    for line in code.splitlines():
+        if "wait_at(" in line:
+            assert "__all_sync(0xffffffffu, wait_at(" in line or "fine" in line or "scores(wait_at(" in line, line
+    assert "__all_sync(0xffffffffu, fine)" in code
+
+
+def test_the_wait_of_a_warp_votes():
+    body = _code("paged_tiles.cuh").split("bool wait_warp(")[1].split("\n}\n")[0]
+    assert body.count("__all_sync(0xffffffffu, ") == body.count("return") == 2
