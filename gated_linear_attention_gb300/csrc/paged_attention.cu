@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
             for (int i = w.t0; i < w.t1 && ok; ++i) {
                 const int here = page;
                 page = i + 1 < w.t1 ? box_page<E4M3>(c, w.n, i + 1, end, lane) : -2;
-                for (int kv = 0; kv < 2; ++kv, ++it) {
+                for (int kv = 0; kv < 2 && ok; ++kv, ++it) {   // a wait for room for the queries that gave up stands
                     if (kv == 1 && kSplit) continue;
                     const int st = it % kRing;
                     ok = it < kRing || wait_warp(&empty[st], (it / kRing - 1) & 1, aborted, status);

@@ -33,3 +33,31 @@ def test_waits_are_voted_on(name):
 def test_the_wait_of_a_warp_votes():
     body = _code("paged_tiles.cuh").split("bool wait_warp(")[1].split("\n}\n")[0]
     assert body.count("__all_sync(0xffffffffu, ") == body.count("return") == 2
+
+
+def _loops(code):
+    """(header, body) of each loop with a braced body."""
+    for at in re.finditer(r"\bfor \(", code):
+        depth, i = 1, at.end()
+        while depth:
+            depth += {"(": 1, ")": -1}.get(code[i], 0)
+            i += 1
+        if code[i:i + 2] != " {":
+            continue
+        end, depth = i + 2, 1
+        while depth:
+            depth += {"{": 1, "}": -1}.get(code[end], 0)
+            end += 1
+        yield code[at.end():i], code[i:end]
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_a_loop_ends_with_a_wait_that_gave_up(name):
+    """Either its header looks at the result, or each wait in it is followed by the way out."""
+    seen = 0
+    for header, body in _loops(_code(name)):
+        for at in re.finditer(r"\bok = [^;]*(wait_warp|passed)\([^;]*;", body):
+            seen += 1
+            assert "&& ok" in header or body[at.end():].split()[:3] == ["if", "(!ok)", "break;"] or \
+                body[at.end():].split()[:4] == ["if", "(!ok)", "return", "0.f;"], (header, at.group(0))
+    assert seen > 3
