@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
     constexpr uint32_t kRing = E4M3 ? Layout::kRaw : Layout::kStages;
     uint64_t *const full = E4M3 ? bar.raw_full : bar.full, *const empty = E4M3 ? bar.raw_empty : bar.empty;
     auto tile_at = [](uint32_t st) { return E4M3 ? Layout::kRawAt + st * kRawBytes : (kQ + st) * kTileBytes; };
-    // Copies in flight of a loading warp that gives up before tile `it` land before the CTA ends; `odd`: of the values alone.
+    // The last copies of a loading warp, those before tile `it`, land before the CTA ends, whoever gave up; `odd`: of the values alone.
     auto drain_tiles = [&](uint32_t it, uint32_t odd) {
         for (uint32_t j = it > kRing ? it - kRing : 0; j < it; ++j)
             if (!kSplit || (j & 1) == odd) tc::mbar_wait(&full[j % kRing], (j / kRing) & 1, tck::kWaitNs);
@@ -264,10 +264,8 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
                 join = {x.row, x.h, x.ntok, x.limit, cta_of(all, w.pos + w.tiles - 1, gridDim.x) - cta + 1};
         } while (ok && w.next(c, work, cta));
         if (lane == 0) static_cast<JoinUnit *>(a.joins)[cta] = join;
-        if (!ok) {   // copies in flight land before the CTA ends
-            if (q_issued) tc::mbar_wait(&bar.q_full, (q_issued - 1) & 1, tck::kWaitNs);
-            drain_tiles(it, 0);
-        }
+        if (q_issued) tc::mbar_wait(&bar.q_full, (q_issued - 1) & 1, tck::kWaitNs);
+        drain_tiles(it, 0);
     } else if (kSplit && warp == kValueWarp && !idle) {
         // ---- loads of the values where one warp does not keep up ------------------------------------
         uint32_t it = 1, items = 0;
@@ -290,7 +288,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
             if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
             ++items;
         } while (ok && !last);
-        if (!ok) drain_tiles(it, 1);
+        drain_tiles(it, 1);
     } else if (E4M3 && warp >= kConvertWarp && !idle) {
         // ---- e4m3 tiles to bf16 --------------------------------------------------------------------
         constexpr int kRaw = E4M3 ? Layout::kRaw : 1;
@@ -503,13 +501,11 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
             if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
             ++items;
         } while (!last);
-        if (!ok) {   // products in flight end before the tensor memory is freed
-            if (tc::elect_one()) {
-                tc::umma_commit(&bar.drain);
-                tc::mbar_wait(&bar.drain, 0, tck::kWaitNs);
-            }
-            __syncwarp();
+        if (tc::elect_one()) {   // products in flight end before the tensor memory is freed, whoever gave up
+            tc::umma_commit(&bar.drain);
+            tc::mbar_wait(&bar.drain, 0, tck::kWaitNs);
         }
+        __syncwarp();
     } else if (warp < kMmaWarp && !idle) {
         // ---- softmax and results: half a row of scores a thread ----------------------------------------
         // Lanes l and l + 16 share a row: columns [0, 32) and [64, 96), or [32, 64) and [96, 128).

@@ -213,12 +213,11 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 join = {x.n, x.h, x.u0, cta_of(all, w.pos + w.tiles - 1, gridDim.x) - cta + 1};
         } while (ok && w.next(c, work, cta));
         if (lane == 0) static_cast<JoinUnit *>(a.weight_joins)[cta] = join;
-        if (!ok) {   // copies in flight land before the CTA ends
-            for (uint32_t j = kt > kRing ? kt - kRing : 0; j < kt; ++j)
-                tc::mbar_wait(&full[j % kRing], (j / kRing) & 1, tck::kWaitNs);
-            for (uint32_t j = qt > Layout::kQueries ? qt - Layout::kQueries : 0; j < qt; ++j)
-                tc::mbar_wait(&bar.q_full[j % Layout::kQueries], (j / Layout::kQueries) & 1, tck::kWaitNs);
-        }
+        // the last copies land before the CTA ends, whoever gave up
+        for (uint32_t j = kt > kRing ? kt - kRing : 0; j < kt; ++j)
+            tc::mbar_wait(&full[j % kRing], (j / kRing) & 1, tck::kWaitNs);
+        for (uint32_t j = qt > Layout::kQueries ? qt - Layout::kQueries : 0; j < qt; ++j)
+            tc::mbar_wait(&bar.q_full[j % Layout::kQueries], (j / Layout::kQueries) & 1, tck::kWaitNs);
     } else if (warp == kStatsWarp && !idle) {
         // ---- the columns beside Q: -y / c of each row ------------------------------------------------------
         uint32_t qt = 0;
@@ -344,13 +343,11 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 k.advance(1);
             }
         } while (ok && !__shfl_sync(0xffffffffu, x.last, 0));
-        if (!ok) {   // products in flight end before the tensor memory is freed
-            if (tc::elect_one()) {
-                tc::umma_commit(&bar.drain);
-                tc::mbar_wait(&bar.drain, 0, tck::kWaitNs);
-            }
-            __syncwarp();
+        if (tc::elect_one()) {   // products in flight end before the tensor memory is freed, whoever gave up
+            tc::umma_commit(&bar.drain);
+            tc::mbar_wait(&bar.drain, 0, tck::kWaitNs);
         }
+        __syncwarp();
     } else if (warp < kMmaWarp && !idle) {
         // ---- sums: a place a thread ------------------------------------------------------------------------
         const int g = warp >> 2, r = threadIdx.x & (kTile - 1);

@@ -61,3 +61,11 @@ def test_a_loop_ends_with_a_wait_that_gave_up(name):
             assert "&& ok" in header or body[at.end():].split()[:3] == ["if", "(!ok)", "break;"] or \
                 body[at.end():].split()[:4] == ["if", "(!ok)", "return", "0.f;"], (header, at.group(0))
     assert seen > 3
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_copies_and_products_in_flight_are_waited_for_whoever_gave_up(name):
+    """A role that ends well may have copies or products in flight when another one gives up."""
+    code = _code(name)
+    assert "mbar_wait(&bar.drain" in code and "mbar_wait(&bar.q_full" in code
+    assert not re.search(r"if \(!ok\)( \{)?\s*(drain|for|if \(q_issued\)|if \(tc::elect_one)", code)
