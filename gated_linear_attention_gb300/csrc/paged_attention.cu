@@ -47,6 +47,11 @@ constexpr int kRows = 2 * kTile;                 // rows of a unit, at most
 constexpr int kMmaWarp = 16, kLoadWarp = 17, kValueWarp = 18;
 constexpr uint32_t kS0 = 0, kO0 = 256;           // tensor memory columns: S (and P over it) of the groups, then O
 constexpr float kRescale = 8.f;                  // growth of the maximum (log2) that rescales O
+// c m beyond which the scores' differences are taken before the factor c. Below it the rounding of c m is 2^-14 at most, no more than
+// those of such scores themselves. (Taken in the
+// usual way's registers they made a chunk of 1320 us 30 to 70 us longer; as a way of their own 12, and 256 requests on up to 1000
+// places with 8 key/value heads 127 -> 134 us.)
+constexpr float kFar = 1024.f;
 constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128, 0, 0), kIdO = tc::idesc_bf16_f32(128, 128, 0, 1);
 
 // Shared memory of units with Q query tiles: the queries, the ring of cache tiles, the ring of e4m3 tiles. Split: the values
@@ -110,6 +115,22 @@ __device__ __noinline__ void bad_dimensions(const KvArgs &c, int64_t n, int h, i
             if (!isfinite(value_at(c, row, d))) dims[d >> 5] |= 1u << (d & 31);
     }
 }
+
+// Factor c of a head's scores: the exponents are c s.
+__device__ __forceinline__ float exponent_scale(const AttendArgs &a, int h) {
+    return a.scale * (a.c.k_scale ? kv::load(a.c.k_scale + h) : 1.f) * kLog2e;
+}
+
+// 2^(c (m - top)): what moves a part of a row with the maximum m to the maximum of all parts. The part's P and sum are
+// 2^(c s - [c m]) with the rounded product [c m], so that the difference of the rounded products joins them exactly; where c m
+// is far from 0 they are 2^(c (s - m)), and the products' roundings would be more than the difference.
+__device__ __forceinline__ float part_factor(float m, float top, float scale) {
+    if (m == -INFINITY) return 0.f;
+    const float at = __fmul_rn(top, scale);
+    return tc::ex2(fabsf(at) > kFar ? (m - top) * scale : __fsub_rn(__fmul_rn(m, scale), at));
+}
+// c m of a row's maximum, 0 where it has none
+__device__ __forceinline__ float exponent_of(float m, float scale) { return m == -INFINITY ? 0.f : m * scale; }
 
 // The 16-lane forms of tensor memory accesses: lanes l and l + 16 of the warp take the same row, 32 columns apart (or
 // OFF apart, for a store).
@@ -515,9 +536,9 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
         const uint32_t ts = tmem + kS0 + t * kTile + lanes;
         constexpr uint32_t kO = kO0 - kS0;   // from a group's S to its O
         // In one register: the parities of score tiles, of items with an O of this group and of joined items, whether an item has
-        // a maximum, and the items. What an item's rows are is read again after its tiles: registers are short in between.
+        // a maximum, whether one of the warp's rows has one far from 0, and the items. What an item's rows are is read again after its tiles: registers are short in between.
         uint32_t count = 0;
-        constexpr uint32_t kSeen = 1, kMine = 2, kJoined = 4, kBegun = 8, kItem = 16;
+        constexpr uint32_t kSeen = 1, kMine = 2, kJoined = 4, kBegun = 8, kFarRows = 16, kItem = 32;
         bool ok = true, last = false;
         do {
             ok = wait_warp(&bar.item_full[count / kItem % kItems], (count / (kItem * kItems)) & 1, aborted, status);
@@ -544,9 +565,9 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
             const int step = in.two ? 1 : 2, first = x.t0 + in.turn;
             // the last place seen, from the first score of this thread (a row without a token: as the first token's)
             int keep = (in.valid ? in.limit : x.limit + in.tile * a.TB) - 32 * half - first * kTile;
-            const float scale = a.scale * (c.k_scale ? kv::load(c.k_scale + x.h) : 1.f) * kLog2e;
+            const float scale = exponent_scale(a, x.h);
             float m = -INFINITY, l = 0.f;   // the maximum in units of the scores
-            count &= ~kBegun;
+            count &= ~(kBegun | kFarRows);
             for (int left = (x.t1 - first + step - 1) / step; left > 0; --left, keep -= step * kTile) {
                 ok = wait_warp(&bar.s_full[t], count & kSeen ? 1 : 0, aborted, status);
                 if (!ok) break;
@@ -576,11 +597,13 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
                     tile_top = fmaxf(tile_top, __shfl_xor_sync(0xffffffffu, tile_top, 16));
                     if (!(count & kBegun)) {
                         m = tile_top;
+                        if (__any_sync(0xffffffffu, fabsf(exponent_of(m, scale)) > kFar)) count |= kFarRows;
                     } else {
                         const bool grow = tile_top > m && !((tile_top - m) * scale <= kRescale);
                         if (__any_sync(0xffffffffu, grow)) {
                             const float f = !grow ? 1.f : m == -INFINITY ? 0.f : tc::ex2((m - tile_top) * scale);
                             if (grow) m = tile_top;
+                            if (__any_sync(0xffffffffu, fabsf(exponent_of(m, scale)) > kFar)) count |= kFarRows;
                             l *= f;
 #pragma unroll 1
                             for (int q = 0; q < 8; ++q) {   // few at a time: the scores fill the registers
@@ -594,13 +617,12 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
                             }
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.f : m * scale;
-                    const uint64_t scale2 = tc::pair(scale, scale), minus = tc::pair(-mc, -mc);
+                    // P = 2^(c s - c m) by multiply-adds, whose exponents all have the one rounding of c m. It cancels in P over its sum,
+                    // but not where c m is so large that it is a factor out of range: s - m then comes first (exact near the maximum).
+                    const float mc = exponent_of(m, scale);
                     uint64_t sum2[2] = {0, 0};   // pairs of zeros
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t (&z)[32] = s[E4M3 ? 0 : q];
-                        if (E4M3) load(q, z);
+                    const uint64_t scale2 = tc::pair(scale, scale);
+                    auto weights = [&](int q, const uint32_t (&z)[32], uint64_t minus) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -616,6 +638,24 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
                             tc::tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&bar.p_full[t]);
+                        }
+                    };
+                    if (count & kFarRows) {
+                        const bool far = fabsf(mc) > kFar;
+                        const float low = far ? 0.f : -mc, shift = far ? m : 0.f;
+#pragma unroll 1
+                        for (int q = 0; q < 2; ++q) {   // the scores once more: held on from above they would cost the usual way registers
+                            uint32_t z[32];
+                            load(q, z);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) z[j] = __float_as_uint(__uint_as_float(z[j]) - shift);
+                            weights(q, z, tc::pair(low, low));
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            if (E4M3) load(q, s[0]);
+                            weights(q, s[E4M3 ? 0 : q], tc::pair(-mc, -mc));
                         }
                     }
                     const float2 even = tc::unpair(sum2[0]), odd = tc::unpair(sum2[1]);
@@ -634,7 +674,6 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
             const auto [two, valid, busy, my_tile, turn, my_tok, limit] = rows();
             const int n = x.t1 - x.t0;
             if (busy) l += __shfl_xor_sync(0xffffffffu, l, 16);
-            float mc = m == -INFINITY ? m : m * scale;
             const bool worked = turn < n;           // this group has an O
             if (worked) {
                 ok = wait_warp(&bar.o_full[t], count & kMine ? 1 : 0, aborted, status);
@@ -645,7 +684,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
             const bool join = !two && n > 1;        // both groups have an O of the same rows
             float f0 = 1.f, f1 = 0.f;
             if (join && turn == 1) {
-                if (lane < 16) other[r] = make_float2(mc, l);
+                if (lane < 16) other[r] = make_float2(m, l);
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.join);
@@ -654,11 +693,11 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
                 if (!ok) break;
                 tc::tc_fence_after();
                 const float2 y = other[r];
-                const float top = fmaxf(mc, y.x);
-                f0 = mc == -INFINITY ? 0.f : tc::ex2(mc - top);
-                f1 = y.x == -INFINITY ? 0.f : tc::ex2(y.x - top);
+                const float top = fmaxf(m, y.x);
+                f0 = part_factor(m, top, scale);
+                f1 = part_factor(y.x, top, scale);
                 l = l * f0 + y.y * f1;
-                mc = top;
+                m = top;
             }
             if (busy && turn == 0) {
                 const int slot = x.slot;
@@ -711,12 +750,11 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
                     }
                 }
                 if (valid && half == 0) {
-                    const float at = mc == -INFINITY ? 0.f : mc;
                     if (!whole) {
-                        a.part_ml[prow] = make_float2(mc, l);
+                        a.part_ml[prow] = make_float2(m, l);
                     } else {
-                        if (a.lse) a.lse[row] = some ? (at + log2f(l)) * kLn2 : -INFINITY;
-                        if (a.stats) a.stats[row] = at + log2f(l);
+                        if (a.lse) a.lse[row] = some ? (exponent_of(m, scale) + log2f(l)) * kLn2 : -INFINITY;
+                        if (a.stats) a.stats[row] = exponent_of(m, scale) + log2f(l);
                     }
                 }
             }
@@ -750,17 +788,17 @@ constexpr int kJoinWarps = 8, kJoinEach = 2;   // of a block, rows of a warp
 template <int kJoinSplit>
 __host__ __device__ constexpr int join_rows() { return kJoinSplit > 1 ? kJoinWarps : kJoinEach * kJoinWarps; }   // of a block
 
-// The results of row rr of query tile t: acc / total, its maximum.
+// The results of row rr of query tile t: acc / total, its maximum, the factor of its scores.
 __device__ __forceinline__ void joined_row(const AttendArgs &a, const JoinUnit &x, int tok, int rr, int lane, float4 acc, float total,
-                                           float at) {
+                                           float m, float scale) {
     const bool some = x.limit + tok >= 0;
     const float vs = a.c.v_scale ? kv::load(a.c.v_scale + x.h) : 1.f, inv = vs / total;
     const int64_t out = (x.row + tok) * (a.G * a.c.H) + x.h * a.G + rr % a.G;
     *reinterpret_cast<uint2 *>(a.o + out * kD + lane * 4) =
         some ? make_uint2(float2_to_bf16x2(acc.x * inv, acc.y * inv), float2_to_bf16x2(acc.z * inv, acc.w * inv)) : make_uint2(0, 0);
     if (lane == 0) {
-        if (a.lse) a.lse[out] = some ? (at + log2f(total)) * kLn2 : -INFINITY;
-        if (a.stats) a.stats[out] = at + log2f(total);
+        if (a.lse) a.lse[out] = some ? (exponent_of(m, scale) + log2f(total)) * kLn2 : -INFINITY;
+        if (a.stats) a.stats[out] = exponent_of(m, scale) + log2f(total);
     }
 }
 
@@ -771,13 +809,13 @@ __device__ __forceinline__ void add_part(float4 &acc, float w, const float4 &v) 
     acc.w += w * v.w;
 }
 
-// The sum over parts s, s + split, .. of a row, by a warp; `at`: the maximum over all parts.
-__device__ __forceinline__ void join_parts(const AttendArgs &a, int cta, int parts, int row, int s, int split, int lane, float4 *acc,
-                                           float *total, float *at) {
+// The sum over parts s, s + split, .. of a row, by a warp; `most`: the maximum over all parts.
+__device__ __forceinline__ void join_parts(const AttendArgs &a, int cta, int parts, int row, int s, int split, int lane, float scale,
+                                           float4 *acc, float *total, float *most) {
     float top = -INFINITY;
     for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_ml[part_slot(cta, p) * kRows + row].x);
     for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    *at = top == -INFINITY ? 0.f : top;
+    *most = top;
     *total = 0.f;
     *acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p0 = s; p0 < parts; p0 += 32 * split) {   // lane l has the statistics of the l-th of these
@@ -785,7 +823,7 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, int cta, int par
         const int mine = p0 + lane * split;
         if (mine < parts) {
             const float2 ml = a.part_ml[part_slot(cta, mine) * kRows + row];
-            f = ml.x == -INFINITY ? 0.f : tc::ex2(ml.x - *at);
+            f = part_factor(ml.x, top, scale);
             l = ml.y * f;
         }
         for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -806,7 +844,7 @@ __device__ __forceinline__ int token_of(const AttendArgs &a, const JoinUnit &x, 
 
 // Rows [row0, row0 + kJoinEach) of a unit in kParts parts, by a warp that has all of their loads in flight.
 template <int kParts>
-__device__ __forceinline__ void join_rows_at_once(const AttendArgs &a, const JoinUnit &x, int cta, int row0, int lane) {
+__device__ __forceinline__ void join_rows_at_once(const AttendArgs &a, const JoinUnit &x, int cta, int row0, int lane, float scale) {
     float2 ml[kJoinEach][kParts];
     float4 v[kJoinEach][kParts];
 #pragma unroll
@@ -825,15 +863,14 @@ __device__ __forceinline__ void join_rows_at_once(const AttendArgs &a, const Joi
         float top = -INFINITY, total = 0.f;
 #pragma unroll
         for (int p = 0; p < kParts; ++p) top = fmaxf(top, ml[e][p].x);
-        const float at = top == -INFINITY ? 0.f : top;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int p = 0; p < kParts; ++p) {
-            const float f = ml[e][p].x == -INFINITY ? 0.f : tc::ex2(ml[e][p].x - at);
+            const float f = part_factor(ml[e][p].x, top, scale);
             total += ml[e][p].y * f;
             add_part(acc, f, v[e][p]);
         }
-        joined_row(a, x, tok, (row0 + e) % kTile, lane, acc, total, at);
+        joined_row(a, x, tok, (row0 + e) % kTile, lane, acc, total, top, scale);
     }
 }
 
@@ -843,15 +880,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kJoinSplit) paged_combine_ke
     const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const JoinUnit x = static_cast<const JoinUnit *>(a.joins)[cta];
     if (x.parts == 0) return;
+    const float scale = exponent_scale(a, x.h);
     if constexpr (kJoinSplit > 1) {
         __shared__ float4 sums[kJoinWarps][kJoinSplit][32];
         __shared__ float totals[kJoinWarps][kJoinSplit];
         const int k = warp / kJoinSplit, s = warp % kJoinSplit, row = blockIdx.y * join_rows<kJoinSplit>() + k, tok = token_of(a, x, row);
-        float at = 0.f;
+        float top = -INFINITY;
         if (tok >= 0) {
             float4 acc;
             float total;
-            join_parts(a, cta, x.parts, row, s, kJoinSplit, lane, &acc, &total, &at);
+            join_parts(a, cta, x.parts, row, s, kJoinSplit, lane, scale, &acc, &total, &top);
             sums[k][s][lane] = acc;
             if (lane == 0) totals[k][s] = total;
         }
@@ -861,19 +899,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps * kJoinSplit) paged_combine_ke
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kJoinSplit; ++i) add_part(acc, 1.f, sums[k][i][lane]), total += totals[k][i];
-        joined_row(a, x, tok, row % kTile, lane, acc, total, at);
+        joined_row(a, x, tok, row % kTile, lane, acc, total, top, scale);
     } else {
         const int row0 = blockIdx.y * join_rows<1>() + warp * kJoinEach;
-        if (x.parts == 2) return join_rows_at_once<2>(a, x, cta, row0, lane);
-        if (x.parts == 3) return join_rows_at_once<3>(a, x, cta, row0, lane);
-        if (x.parts == 4) return join_rows_at_once<4>(a, x, cta, row0, lane);
+        if (x.parts == 2) return join_rows_at_once<2>(a, x, cta, row0, lane, scale);
+        if (x.parts == 3) return join_rows_at_once<3>(a, x, cta, row0, lane, scale);
+        if (x.parts == 4) return join_rows_at_once<4>(a, x, cta, row0, lane, scale);
         for (int row = row0; row < row0 + kJoinEach; ++row) {
             const int tok = token_of(a, x, row);
             if (tok < 0) continue;
             float4 acc;
-            float total, at;
-            join_parts(a, cta, x.parts, row, 0, 1, lane, &acc, &total, &at);
-            joined_row(a, x, tok, row % kTile, lane, acc, total, at);
+            float total, top;
+            join_parts(a, cta, x.parts, row, 0, 1, lane, scale, &acc, &total, &top);
+            joined_row(a, x, tok, row % kTile, lane, acc, total, top, scale);
         }
     }
 }

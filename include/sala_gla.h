@@ -512,7 +512,8 @@ int sala_gla_kv_append(const sala_kv_cache *cache, const void *k, int64_t k_stri
  *   accumulate  nonzero: adds p_j, summed over the call's new tokens and the query heads of the group, to
  *               the weights of place j (the cache needs weights). The order of the sum is fixed.
  *   Hq          a multiple of num_kv_heads, at most 128 query heads on one
- * Scores, statistics and sums are fp32; p is rounded to bf16 for the product with v. Scratch comes from
+ * Scores, statistics and sums are fp32; p is rounded to bf16 for the product with v. Scores of any size count by their
+ * differences, down to the roundings of fp32 (of q.k, and 2^-22 of a difference). Scratch comes from
  * the library's stream-ordered pool (as sala_gla_chunk_fwd). A device-side wait that gives up (2 s)
  * records SALA_ERR_TIMEOUT in the status word.
  * Errors: SALA_ERR_INVALID_ARG, SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED, SALA_ERR_CUDA.
