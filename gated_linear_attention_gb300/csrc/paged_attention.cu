@@ -131,6 +131,8 @@ __device__ __forceinline__ float part_factor(float m, float top, float scale) {
 }
 // c m of a row's maximum, 0 where it has none
 __device__ __forceinline__ float exponent_of(float m, float scale) { return m == -INFINITY ? 0.f : m * scale; }
+// log sum exp in units of the scores, for the accumulated weights: below c it would lose the score's own bits
+__device__ __forceinline__ float score_lse(float m, float l, float scale) { return m + log2f(l) / scale; }
 
 // The 16-lane forms of tensor memory accesses: lanes l and l + 16 of the warp take the same row, 32 columns apart (or
 // OFF apart, for a store).
@@ -754,7 +756,7 @@ __global__ void __launch_bounds__(Shape<E4M3, kQ, kSplit>::kThreads, 1)
                         a.part_ml[prow] = make_float2(m, l);
                     } else {
                         if (a.lse) a.lse[row] = some ? (exponent_of(m, scale) + log2f(l)) * kLn2 : -INFINITY;
-                        if (a.stats) a.stats[row] = exponent_of(m, scale) + log2f(l);
+                        if (a.stats) a.stats[row] = score_lse(m, l, scale);
                     }
                 }
             }
@@ -798,7 +800,7 @@ __device__ __forceinline__ void joined_row(const AttendArgs &a, const JoinUnit &
         some ? make_uint2(float2_to_bf16x2(acc.x * inv, acc.y * inv), float2_to_bf16x2(acc.z * inv, acc.w * inv)) : make_uint2(0, 0);
     if (lane == 0) {
         if (a.lse) a.lse[out] = some ? (exponent_of(m, scale) + log2f(total)) * kLn2 : -INFINITY;
-        if (a.stats) a.stats[out] = exponent_of(m, scale) + log2f(total);
+        if (a.stats) a.stats[out] = score_lse(m, total, scale);
     }
 }
 

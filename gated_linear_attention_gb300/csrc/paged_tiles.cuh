@@ -344,7 +344,7 @@ struct AttendArgs {
     void *joins, *weight_joins;   // [CTAs] units that several CTAs share
     float *part_o;       // [2 * CTAs, 256, 128] partial O
     float2 *part_ml;     // [2 * CTAs, 256] its maximum (in units of the scores) and sum
-    float *stats;        // [T, Hq] log2 of each row's sum of exponentials, or null
+    float *stats;        // [T, Hq] log of each row's sum of exponentials, in units of the scores, or null
     float *part_w;       // [2 * CTAs, 128] partial sums of weights
     uint16_t *o;
     float *lse;

@@ -1,10 +1,13 @@
 // The attention weight that each cached token received, added to its running sum.
 //
-// Runs after the attention, when every row's y = log2 sum 2^(c s) is known (c = scale * k_scale * log2 e):
-//     weights[j] += sum over the rows r that see j of  2^(c k_j.q_r - y_r)
+// Runs after the attention, when every row's z = m + log2(sum 2^(c (s - m))) / c is known (c = scale * k_scale * log2 e, m its
+// largest score):
+//     weights[j] += sum over the rows r that see j of  2^(c (k_j.q_r - z_r))
+// z in units of the scores keeps their bits: z >= m also after rounding, so that no weight passes 1, however large the
+// scores (with c z held instead, the products' roundings alone are a factor of 2 from |c z| = 2^24 on).
 // The scores are made again, transposed: S^T = K Q^T (tcgen05, 128 places x 128 rows). A place is then a lane of
-// tensor memory and its sum over the rows a thread's own, without shuffles or atomics, in a fixed order. y is the same
-// for all lanes: it enters as one more step of the product, columns of ones beside K and -y / c as three bf16 terms (24
+// tensor memory and its sum over the rows a thread's own, without shuffles or atomics, in a fixed order. z is the same
+// for all lanes: it enters as one more step of the product, columns of ones beside K and -z as three bf16 terms (24
 // bits) beside Q, so that an element costs a multiplication, an exp2 and an addition. (Read from shared memory
 // instead, it competed with the operands of the products: 7 query tiles on 6007 places 295 us.)
 //
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         for (uint32_t j = qt > Layout::kQueries ? qt - Layout::kQueries : 0; j < qt; ++j)
             tc::mbar_wait(&bar.q_full[j % Layout::kQueries], (j / Layout::kQueries) & 1, tck::kWaitNs);
     } else if (warp == kStatsWarp && !idle) {
-        // ---- the columns beside Q: -y / c of each row ------------------------------------------------------
+        // ---- the columns beside Q: -z of each row ------------------------------------------------------
         uint32_t qt = 0;
         const int Hq = a.G * c.H;
         Item x;
@@ -227,7 +230,6 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         do {
             ok = take(x);
             if (!ok) break;
-            const float inv = -1.f / (a.scale * (c.k_scale ? kv::load(c.k_scale + x.h) : 1.f) * kLog2e);
             float next[4];
             auto fetch = [&](int q) {   // rows 32 e + lane of query tile q
                 const int rows = min(a.TB, x.ntok - q * a.TB) * a.G;
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 uint8_t *aux = smem + Layout::kAuxAt + s * kAuxBytes;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float v = y[e] * inv;
+                    const float v = -y[e];
                     const float hi = __bfloat162float(__float2bfloat16_rn(v));
                     const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
                     *reinterpret_cast<uint4 *>(aux + aux_at(32 * e + lane, 0)) =

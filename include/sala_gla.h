@@ -513,7 +513,9 @@ int sala_gla_kv_append(const sala_kv_cache *cache, const void *k, int64_t k_stri
  *               the weights of place j (the cache needs weights). The order of the sum is fixed.
  *   Hq          a multiple of num_kv_heads, at most 128 query heads on one
  * Scores, statistics and sums are fp32; p is rounded to bf16 for the product with v. Scores of any size count by their
- * differences, down to the roundings of fp32 (of q.k, and 2^-22 of a difference). Scratch comes from
+ * differences, down to the roundings of fp32 (of q.k, and 2^-22 of a difference). Accumulated weights are relative to
+ * exp(lse) with its rounding, 2^-23 |lse|; where that is large (equal largest scores beside |lse| > 2^20) a weight may be too
+ * large by the number of such scores, but never above 1. Scratch comes from
  * the library's stream-ordered pool (as sala_gla_chunk_fwd). A device-side wait that gives up (2 s)
  * records SALA_ERR_TIMEOUT in the status word.
  * Errors: SALA_ERR_INVALID_ARG, SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED, SALA_ERR_CUDA.

@@ -7,7 +7,9 @@ ties. What remains, with c = scale * k_scale * log2 e (relative error d <= 4 * 2
     c m is common to all of a row but for maxima that grew, by 2^8 at least, and so leaves 2 * 1024 * 2^-24 * 2^-8. Times log 2: 2^-15.
   - exp2 2^-21; sums of n positive terms in chains of at most 128 + n / 128: E = 2^-15 + 2^-21 + (128 + n / 128) 2^-24 of a weight's
     numerator or of their sum. o: as in test_gpu_paged_attention.py, with this E.
-  - lse = (c m + log2 sum) log 2: E and its roundings (c's, the product, the sum, log 2, the product) 6 * 2^-24 |lse|."""
+  - lse = (c m + log2 sum) log 2: E and its roundings (c's, the product, the sum, log 2, the product) 6 * 2^-24 |lse|.
+  - accumulated weights go by z = m + log2(sum) / c, rounded: a relative error of |lse| 2^-23 beside 2 E. Where that is large the
+    rounding still leaves m <= z <= m + 2 log2(sum) / c: a weight lies between p / sum and p * sum."""
 import math
 
 import pytest
@@ -63,28 +65,35 @@ def test_scales(kind, k_scale, T, Hq, H, lens):
     for scale in SCALES:
         c, q = _whole_numbers(lens, T, Hq, H, kind, k_scale, seed=T)
         g, r = on_gpu(c), on_cpu(c)
-        o, lse = sala_gla.paged_attention(q.cuda(), g, scale)
+        o, lse = sala_gla.paged_attention(q.cuda(), g, scale, accumulate=True)
         assert sala_gla.get_device_status() == 0
         exact = float(torch.tensor(scale, dtype=torch.float32))
-        ro, rlse, mass, _, _, _ = _exact(r, q, exact)
+        ro, rlse, mass, sums, low, high = _exact(r, q, exact)
         E = 2.0 ** -15 + 2.0 ** -21 + (128 + max(lens) / 128) * 2.0 ** -24
         err = (o.cpu().double() - ro).abs()
         assert bool((err <= (2.0 ** -8 + 2 * E + 2.0 ** -16) * mass + 2.0 ** -8 * ro.abs()).all()), (scale, float(err.max()))
         err = (lse.cpu().double() - rlse).abs()
         assert bool((err <= E + 6 * 2.0 ** -24 * rlse.abs()).all()), (scale, float(err.max()))
+        w, rows = g.weights.cpu().double(), T * Hq // H
+        e = 2 * E + 2.0 ** -21 + rows * 2.0 ** -23
+        assert bool((w >= low * (1 - e) - 1e-30).all()) and bool((w <= high * (1 + e) + 1e-30).all()), scale
+        off = float(rlse.abs().max()) * 2.0 ** -23
+        if off < 0.1:
+            assert bool(((w - sums).abs() <= (e + 2 * off) * sums + 1e-30).all()), (scale, float((w - sums).abs().max()))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("T,L", [(1, 2500), (7, 700), (40, 300)])
 @pytest.mark.parametrize("scale", [1e6, 1e9, 1e18])
 def test_largest_score_is_all_that_counts(kind, T, L, scale):
-    """Scores with roundings, at most 128 * 2^-24 sum |q k|: rows whose largest score leads by more give that place's values."""
+    """Scores with roundings, at most 128 * 2^-24 sum |q k|: rows whose largest score leads by more give that place's values,
+    and no weight passes the number of rows."""
     from gated_linear_attention_gb300 import sala_gla
     c = make_cache([L], 32, 1, kind, seed=T, weights=True)
     c["weights"].zero_()
     q, _ = new_tokens([T], 8, seed=2, size=2.0)
     g, r = on_gpu(c), on_cpu(c)
-    o, lse = sala_gla.paged_attention(q[None].cuda(), g, scale)
+    o, lse = sala_gla.paged_attention(q[None].cuda(), g, scale, accumulate=True)
     assert sala_gla.get_device_status() == 0
     ks, vs = r.rows(r.k, r.k_scale, 0, 0, L), r.rows(r.v, r.v_scale, 0, 0, L)
     checked = 0
@@ -101,3 +110,4 @@ def test_largest_score_is_all_that_counts(kind, T, L, scale):
                 assert abs(float(lse[0, t, h]) - scale * float(top[h, 0])) <= scale * float(bound[h]) + 6 * 2.0 ** -24 * scale * float(top[h, 0])
     assert checked > 4
     assert bool(o.isfinite().all()) and bool(lse.isfinite().all())
+    assert float(g.weights.max()) <= 8 * T and float(g.weights.min()) >= 0 and float(g.weights.sum()) >= checked
