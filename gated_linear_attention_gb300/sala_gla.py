@@ -8,6 +8,7 @@ this module raises: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -601,8 +602,10 @@ class KvCache:
     them; k_scale, v_scale: fp32 [Hkv] (e4m3 only, None: 1); weights: fp32 [num_pages, Hkv, page_size],
     the running attention weights that eviction goes by, or None. Holds the tensors, copies nothing;
     their contents (lengths, tables, pages) may change between calls, ``kv_lens`` and ``block_table``
-    may be replaced by :meth:`with_requests`."""
-    __slots__ = ("k_pages", "v_pages", "block_table", "kv_lens", "k_scale", "v_scale", "weights", "N", "H", "_c", "_ref")
+    may be replaced by :meth:`with_requests`. A tensor that is assigned to one of the attributes is checked with the
+    others as here, and the calls from then on go by it."""
+    _TENSORS = ("k_pages", "v_pages", "block_table", "kv_lens", "k_scale", "v_scale", "weights")
+    __slots__ = (*("_" + n for n in _TENSORS), "_N", "_H", "_c", "_ref")
 
     def __init__(self, k_pages, v_pages, block_table, kv_lens, k_scale=None, v_scale=None, weights=None):
         if not isinstance(k_pages, torch.Tensor):
@@ -630,8 +633,8 @@ class KvCache:
         if weights is not None:
             _need(weights, "weights", torch.float32, (P, H, S))
         _one_device(k_pages, v_pages, block_table, kv_lens, k_scale, v_scale, weights)
-        self.k_pages, self.v_pages, self.block_table, self.kv_lens = k_pages, v_pages, block_table, kv_lens
-        self.k_scale, self.v_scale, self.weights, self.N, self.H = k_scale, v_scale, weights, N, H
+        self._k_pages, self._v_pages, self._block_table, self._kv_lens = k_pages, v_pages, block_table, kv_lens
+        self._k_scale, self._v_scale, self._weights, self._N, self._H = k_scale, v_scale, weights, N, H
         self._c = KvCacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scale), _ptr(v_scale), _ptr(weights),
                                 block_table.data_ptr(), kv_lens.data_ptr(), P, W, S, H,
                                 SALA_KV_BF16 if bf16 else SALA_KV_E4M3)
@@ -640,6 +643,18 @@ class KvCache:
     def with_requests(self, block_table, kv_lens):
         """The same pages with another batch's table and lengths."""
         return KvCache(self.k_pages, self.v_pages, block_table, kv_lens, self.k_scale, self.v_scale, self.weights)
+
+    def _tensor(name):
+        held = operator.attrgetter("_" + name)
+
+        def assign(self, value):
+            if value is not held(self):   # it is after an operation in place: cache.kv_lens += 1
+                KvCache.__init__(self, *(value if n == name else getattr(self, n) for n in KvCache._TENSORS))
+        return property(held, assign)
+
+    k_pages, v_pages, block_table, kv_lens, k_scale, v_scale, weights = map(_tensor, _TENSORS)
+    N, H = (property(operator.attrgetter(n)) for n in ("_N", "_H"))
+    del _tensor
 
 
 def _one_device(*tensors):
