@@ -786,6 +786,9 @@ int sala_gla_state_pool_compact(void *pool, int32_t dtype, int64_t L, int64_t P,
 }
 
 namespace {
+// Places of a request: kernels count them in 32 bits, and step past the last one by what a block takes at once.
+constexpr int64_t kMaxPlaces = int64_t(1) << 30;
+
 bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 // What the entry points of a paged cache have in common: its sizes, types and pointers, and the
@@ -797,7 +800,7 @@ int check_kv(const sala_kv_cache *cache, const int64_t *cu, int64_t N, int64_t T
     if (k.page_size < 16 || k.page_size > 256 || (k.page_size & (k.page_size - 1))) return SALA_ERR_INVALID_ARG;
     if (k.num_kv_heads < 1 || k.num_kv_heads > 65535 || k.num_pages < 1 || k.table_width < 1) return SALA_ERR_INVALID_ARG;
     // places and (page, head) rows are counted in 32 bits, bytes in 64
-    if (k.num_pages >= kMaxRows / k.num_kv_heads || k.table_width >= kMaxRows / k.page_size) return SALA_ERR_INVALID_ARG;
+    if (k.num_pages >= kMaxRows / k.num_kv_heads || k.table_width > kMaxPlaces / k.page_size) return SALA_ERR_INVALID_ARG;
     if (N > (int64_t(1) << 20) / 4 || (N > 0 && T > (kMaxRows - 1) / (cu ? 1 : N)) || k.num_kv_heads > (kMaxRows - 1) / (N + 1))
         return SALA_ERR_INVALID_ARG;
     if (!k.k_pages || !k.v_pages || (N > 0 && (!k.block_table || !k.kv_lens))) return SALA_ERR_INVALID_ARG;
@@ -923,7 +926,7 @@ int sala_gla_kv_evict(const sala_kv_cache *cache, int64_t budget, int64_t sinks,
     KvArgs c;
     if (const int e = check_kv(cache, nullptr, N, 0, &c)) return e;
     if (budget < 1 || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks || budget >= kMaxRows ||
-        !c.weights)
+        (kept && budget > kMaxPlaces) || !c.weights)
         return SALA_ERR_INVALID_ARG;
     if (N == 0) return SALA_OK;
     if (!aligned4(new_lens) || !aligned4(kept)) return SALA_ERR_MISALIGNED;

@@ -457,7 +457,8 @@ int sala_gla_state_pool_compact(void *pool, int32_t dtype, int64_t L, int64_t P,
  *                     its T_n new tokens have the places kv_lens[n] - T_n .. kv_lens[n] - 1. Tokens whose
  *                     place is negative have none: they are not stored and attend to nothing (a padding
  *                     row of a batch has kv_lens[n] = 0).
- *   page_size         16, 32, 64, 128 or 256
+ *   page_size         16, 32, 64, 128 or 256; table_width * page_size at most 2^30
+ * N is at most 2^18 in the calls below.
  * A length below 0 or above table_width * page_size is recorded as SALA_ERR_BAD_INDEX and taken as 0; a
  * page outside [0, num_pages) is recorded as SALA_ERR_BAD_INDEX and the outputs of its request are then
  * unspecified (no access leaves the tensors). Requests may share pages (a common prefix) in calls
@@ -535,7 +536,7 @@ int sala_gla_paged_attention(const sala_kv_cache *cache, const void *q, int64_t 
  *             of a model share it).
  *   kept      int32 [N, num_kv_heads, budget] output, the former places of the tokens now at 0, 1, ..
  *             (then -1), or NULL
- *   budget    >= 1;  sinks, recent >= 0 with sinks + recent <= budget
+ *   budget    >= 1, below 2^31, with `kept` at most 2^30;  sinks, recent >= 0 with sinks + recent <= budget
  * Errors: SALA_ERR_INVALID_ARG (also without weights), SALA_ERR_MISALIGNED, SALA_ERR_UNSUPPORTED,
  * SALA_ERR_CUDA.
  */
