@@ -12,10 +12,11 @@ namespace {
 constexpr int kThreads = 256, kTokens = 8;
 
 // x / s, correctly rounded where an e4m3 value comes of it (Markstein: with r the correctly rounded 1 / s, one correction
-// q + (x - q s) r of q = x r rounds correctly). What lies past 2^10 is clamped anyway; infinities and NaN stay.
+// q - (q s - x) r of q = x r rounds correctly). What lies past 2^10 is clamped anyway; infinities and NaN stay, and so does a zero's
+// sign (with x - q s it would not: sums of zeros of both signs are +0).
 __device__ __forceinline__ float divided(float x, float s, float r) {
     const float q = x * r;
-    return fabsf(q) <= 1024.f ? fmaf(fmaf(-q, s, x), r, q) : q;
+    return fabsf(q) <= 1024.f ? fmaf(-fmaf(q, s, -x), r, q) : q;
 }
 
 template <bool E4M3>
