@@ -59,7 +59,9 @@ struct Barriers {
     uint64_t k_full[3], k_empty[3], q_full[3], q_empty[3], raw_full[5], raw_empty[5];
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t s_full[kGroups], s_free[kGroups];
-    uint64_t part_full[kGroups], part_free[kGroups];
+    // Partial sums, from group b to group a: [a][b]. (With one barrier for a sender a collector an item ahead of it would pass by
+    // the parity of the phase before the sender's last.) Sums of a group that are read.
+    uint64_t part_full[kGroups][kGroups], part_free[kGroups];
     uint64_t drain;
 };
 
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         for (int i = 0; i < kGroups; ++i) {
             tc::mbar_init(&bar.s_full[i], 1);
             tc::mbar_init(&bar.s_free[i], 4);
-            tc::mbar_init(&bar.part_full[i], 4);
+            for (int from = 0; from < kGroups; ++from) tc::mbar_init(&bar.part_full[i][from], 4);
             tc::mbar_init(&bar.part_free[i], 4);
         }
         tc::mbar_init(&bar.drain, 1);
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
         const int g = warp >> 2, r = threadIdx.x & (kTile - 1);
         const uint32_t ts = tmem + g * kTile + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         uint32_t tile = 0, done = 0;             // score tiles of the CTA, of this group
-        uint32_t sent = 0, flips = 0;             // partial sums handed over; parity of every group's, a bit each
+        uint32_t sent = 0, flips = 0;             // partial sums handed over; parity of those from each group, a bit each
         bool ok = true;
         Item x{};
         float scale = 0.f;
@@ -440,10 +442,6 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 continue;
             }
             tile += m;
-            const uint32_t before = flips;
-#pragma unroll
-            for (int o = 1; o < kGroups; ++o)
-                if (o < m) flips ^= 1u << ((owner + o) & (kGroups - 1));
             if (mine >= m) continue;
             Weight w;
             if (mine == 0) w = look(p);
@@ -456,15 +454,16 @@ __global__ void __launch_bounds__(Shape<E4M3>::kThreads, 1)
                 parts[g][r] = total;
                 ++sent;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.part_full[g]);
+                if (lane == 0) mbar_arrive(&bar.part_full[owner][g]);
                 continue;
             }
 #pragma unroll
             for (int o = 1; o < kGroups; ++o) {
                 if (o >= m) break;
                 const int from = (g + o) & (kGroups - 1);
-                ok = wait_warp(&bar.part_full[from], (before >> from) & 1, aborted, status);
+                ok = wait_warp(&bar.part_full[g][from], (flips >> from) & 1, aborted, status);
                 if (!ok) break;
+                flips ^= 1u << from;
                 total += parts[from][r];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.part_free[from]);
