@@ -3,7 +3,9 @@
 // A warp takes eight tokens of one head: lanes 0-15 their keys, 16-31 their values, 16 bytes each. The loads of k and v
 // need only the tokens' numbers and are issued first; meanwhile eight lanes find a token's request (a binary search
 // of the offsets) and page each. (One token a warp, the chain of lookups bounded the kernel: 40 k tokens into e4m3 pages
-// took 28 us; now 10.2 us, 62 MB at 6.1 TB/s. One token takes 2.2 us, a launch.)
+// took 28 us. Now 10.1 us where the 62 MB stay in L2, and 14.9 us a call on tokens that come from memory, 4.2 TB/s, with
+// half of the issue slots and a third of the memory's rate in use: each warp's chain of lookups comes before its stores. One
+// token takes 2.1 us, a launch.)
 #include "kv_cache.cuh"
 
 namespace sala {

@@ -11,8 +11,9 @@
 // blocks may write block b once every thread has read it: the sources of later blocks lie at or behind their own
 // destinations, past everything written so far. Blocks depend on each other only within a (request, head, array,
 // slice of the row), so keys, values, weights and slices of a row are CTAs of their own. Its bytes bound it where there
-// are many requests: 96 of 8192 places to 4096, 816 MB, both kernels in 138 us on pages read for the first time. Loads
-// of the block after next held in registers left room for fewer CTAs (286 us), a ring of bulk copies in shared memory 314 us.
+// are many requests: 96 of 8192 places to 4096, 816 MB, both kernels in 138 to 142 us a call among calls on other caches, 179
+// to 197 us on the same cache again and again (25 of them the selection). Loads of the block after next held in registers left
+// room for fewer CTAs (286 us of the latter kind), a ring of bulk copies in shared memory 314 us.
 #include "kv_cache.cuh"
 
 namespace sala {

@@ -23,12 +23,13 @@
 // widen them (exactly) to bf16.
 //
 // Bounds, at 32 query heads on 2 key/value heads. 256 requests of one token on up to 12288 bf16 places: the cache's 2.15 GB,
-// 318 us = 6.8 TB/s, a copy's rate. A chunk of 4096 tokens on 32768 places: 2.06 TFLOP in 1240 us = 1660 TFLOP/s, the products at
-// the clock that the power limit leaves (a library product 1695). A softmax thread has 96 registers and 64 scores: what is not
-// needed between a tile's scores and its weights stays out of registers there, which took 120 us off the chunk. 61 requests with
-// 5 tokens on 8192 e4m3 places: 84 us against 40 for its bytes; the tiles pass shared memory three times more (read and
-// stored by the widening, read by the product). fp16 tiles, cheaper to widen, took longer (the queries then need a scale
-// for each row to stay in range). One token on 4001 places: 14 us of launch, split, one tile a CTA and join.
+// 316 to 321 us = 6.7 TB/s, a copy's rate. A chunk of 4096 tokens on 32768 places: 2.06 TFLOP in 1240 us by itself = 1660 TFLOP/s, the
+// products at the clock that the power limit leaves (a library product 1695); calls in a row, with the join of its ends, take 1300 to
+// 1360 us, 1510 to 1580 TFLOP/s. A softmax thread has 96 registers and 64 scores: what is not needed between a tile's scores and its
+// weights stays out of registers there, which took 120 us off the chunk. 61 requests with 5 tokens on 8192 e4m3 places: 88 us against
+// 38 for its bytes, and 256 requests of one token on up to 12288 such places 275 us against 159; the tiles pass shared memory three
+// times more (read and stored by the widening, read by the product). fp16 tiles, cheaper to widen, took longer (the queries then
+// need a scale for each row to stay in range). One token on 4001 places: 15 us of launch, split, one tile a CTA and join.
 //
 // What is masked never enters: scores are replaced, not added to, and V is cleared in the rows behind the unit's
 // last place (0 times a NaN there would be NaN). Rows of V that some tokens of the unit see and others do not are
@@ -48,9 +49,8 @@ constexpr int kMmaWarp = 16, kLoadWarp = 17, kValueWarp = 18;
 constexpr uint32_t kS0 = 0, kO0 = 256;           // tensor memory columns: S (and P over it) of the groups, then O
 constexpr float kRescale = 8.f;                  // growth of the maximum (log2) that rescales O
 // c m beyond which the scores' differences are taken before the factor c. Below it the rounding of c m is 2^-14 at most, no more than
-// those of such scores themselves. (Taken in the
-// usual way's registers they made a chunk of 1320 us 30 to 70 us longer; as a way of their own 12, and 256 requests on up to 1000
-// places with 8 key/value heads 127 -> 134 us.)
+// those of such scores themselves. (As the only way they took a chunk of 4096 tokens on 32768 places from 1316 to 1365 us; as a way of
+// their own beside the usual one to 1330, and 256 requests on up to 1000 places with 8 key/value heads from 127 to 134.)
 constexpr float kFar = 1024.f;
 constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128, 0, 0), kIdO = tc::idesc_bf16_f32(128, 128, 0, 1);
 
@@ -1040,9 +1040,9 @@ cudaError_t launch_paged_attention(const KvArgs &c, const void *q, int64_t q_str
     const int Q = c.T > c.N * a.TB ? 2 : 1;
     // A warp issues its lanes' boxes one after another, and the 16 of a bf16 tile in pages of 16 places (8 of an e4m3 tile) bound the
     // kernel: a second warp then loads the values. Pages of 16 and the two warps: a chunk of 2048 tokens on 16384 places
-    // 424 -> 350 us, 128 requests of one token on up to 12288 places 196 -> 171 (e4m3 180 -> 147), but 256 on up to 120 places
-    // and 8 key/value heads 53.6 -> 57.7, as the values wait for the item. In pages of 32 the same chunk 348 -> 358 and the
-    // requests 167 -> 171 (e4m3 150 -> 147): one warp.
+    // 456 -> 348 us, 128 requests of one token on up to 12288 places 207 -> 181 (e4m3 195 -> 151), 256 on up to 1000 places and 8
+    // key/value heads 161 -> 135, but on up to 120 places 55 -> 62, as the values wait for the item. In pages of 32 the same
+    // chunk 352 -> 354 and the requests 172 -> 173 (e4m3 160 -> 150): one warp.
     const bool split = c.S < 32;
     Maps maps;
     cudaError_t e;
